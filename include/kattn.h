@@ -86,7 +86,11 @@ enum kattn_p_mode {
                                           affected outputs are not written (fast
                                           mode) or are NaN (exact mode) */
 #define KATTN_DEVERR_BAD_PAGE 0x4u     /* kattn_decode_paged: a block-table entry
-                                          outside [0, cap_rows / page_rows) */
+                                          outside [0, cap_rows / page_rows); the page
+                                          operations: also a reference count that
+                                          does not match the table */
+#define KATTN_DEVERR_NO_PAGES 0x8u     /* kattn_reserve_pages, kattn_fork_sequences:
+                                          the pool has too few free pages */
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* kattn_status_string(int status);
@@ -375,7 +379,175 @@ int kattn_expf_constants(double* out68);
 int kattn_hash_rows(const void* data, int64_t n_rows, int64_t row_bytes, int64_t row_stride_bytes,
                     uint64_t* hashes, void* stream);
 
-/* Read (and clear) the device error word of a decode workspace.  Copies 4
+/* ------------------------------------------- differential attention -- */
+/* Decode attention by the difference of two softmax maps over the same int8
+ * cache.  kv planes and query heads come in pairs: with g = Hq / Hkv and
+ * H = Hq / 2 differential heads, head i reads the plane pair p = i / g, that
+ * is the planes 2p and 2p + 1, and for column j of sequence b
+ *   s_a,t = ((float)(q8[2i+a] . k8[2p+a][t]) * (qs[2i+a] * k_scale[2p+a][t])) * sm_scale
+ *   V_t   = (v_scale[2p][t] * v[2p][t], v_scale[2p+1][t] * v[2p+1][t])    (256 channels)
+ *   out[b][j][i][:] = sum_t softmax(s_0)_t V_t - lam * sum_t softmax(s_1)_t V_t
+ * over the keys t < ctx_len[b] + j, with q8, qs the absmax/127 quantization of
+ * q[b][j][2i + a] as in kattn_decode.  The weights stay in float32: a P rounded
+ * to 8 bits would leave the rounding error of what the two maps share.
+ * lam: float32, [H] (lam_per_row = 0: one value per head, e.g. the learned
+ *   weight of a layer) or [B][M][H] (lam_per_row = 1: one per row).
+ * Hkv must be even.  q: float32 [B][M][Hq][d], d = 128.
+ * out: float32 [B][M][Hq / 2][256].
+ * row_start, ctx_len, max_ctx, sm_scale, the cache layouts and the limits on
+ * M, g * M and B as in kattn_decode; a sequence that breaks the row_start /
+ * ctx_len rule gets NaN outputs and KATTN_DEVERR_BAD_SEQUENCE.
+ * Deterministic; the bytes of out[b][j][i] depend only on that row's own keys,
+ * so column j equals an M = 1 call with ctx_len + j, in any batch.
+ * workspace: kattn_diff_workspace_size(B, M, Hq, max_ctx) bytes, 256-byte
+ * aligned; its first 256 bytes zeroed before the first call, and shared only
+ * by calls that are ordered on the GPU, as a decode workspace.  Two kernels on
+ * `stream` at most; capturable in a CUDA graph once a first call on the device
+ * has run outside capture. */
+size_t kattn_diff_workspace_size(int B, int M, int Hq, int max_ctx);
+int kattn_decode_diff(const float* q, const int8_t* k, const float* k_scale, const int8_t* v,
+                      const float* v_scale, const int64_t* row_start, const int32_t* ctx_len,
+                      const float* lam, int lam_per_row, int B, int M, int Hq, int Hkv, int d,
+                      int cap_rows, int max_ctx, float sm_scale, float* out, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* kattn_decode_diff over a paged cache: block_table, max_pages, page_rows and
+ * the device-side checks as in kattn_decode_paged.  out equals, byte for byte,
+ * kattn_decode_diff on a cache that holds the same rows contiguously. */
+int kattn_decode_diff_paged(const float* q, const int8_t* k, const float* k_scale,
+                            const int8_t* v, const float* v_scale, const int32_t* block_table,
+                            int max_pages, int page_rows, const int32_t* ctx_len,
+                            const float* lam, int lam_per_row, int B, int M, int Hq, int Hkv,
+                            int d, int cap_rows, int max_ctx, float sm_scale, float* out,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------- norm with 8-bit output -- */
+enum kattn_dtype { KATTN_F32 = 0, KATTN_BF16 = 1, KATTN_F16 = 2 };
+enum kattn_code { KATTN_INT8 = 0, KATTN_E4M3 = 1 };
+
+/* Residual addition, root-mean-square norm and quantization of rows.  For each
+ * row r < rows of width d:
+ *   h     = x[r]                                      without a residual, or
+ *   h     = round_to_type(x[r] + residual[r]), stored in residual_out[r]
+ *   z_i   = h_i * weight_i                            (one float32 rounding)
+ *   s0    = f32(max |z_i|) / 127  (e4m3: / 448)       (IEEE division), the
+ *           maximum over the row (group = 0) or over each run of 128 channels
+ *           (group = 128)
+ *   codes = clamp(rint_half_even(z_i / s0), -127, 127), or e4m3(z_i / s0)
+ *           (nearest even, saturating at 448); 0 where s0 = 0
+ *   scale = s0 / sqrt(mean(h^2) + eps)
+ * so codes * scale is the norm h / rms(h) * weight in 8 bits.  The codes are
+ * the quantization formula of kattn_quantize_kv applied to z; they do not
+ * depend on the rounding of the mean.
+ * x, weight, residual, residual_out: elements of x_type (a kattn_dtype); the
+ *   sums are float32.  Rows of x and residual at strides x_stride and
+ *   res_stride elements (>= d); residual_out has rows at res_out_stride and may
+ *   be the residual itself (the same pointer and stride).  residual and
+ *   residual_out are both NULL or both given.
+ * codes: [rows][d] bytes (int8 or e4m3 by code_type); scales: float32 [rows] or
+ *   [rows][d / 128] (group = 128, which needs d % 128 == 0).
+ * Alignment: each array to its element.  (16-byte vectors are used where the
+ * pointers, strides and d allow it.)  The outputs must not overlap x, weight
+ * or each other.  1 <= d <= 2^24.  rows == 0 is a no-op.  Deterministic. */
+int kattn_rms_norm_quant(const void* x, const void* residual, const void* weight, int x_type,
+                         int64_t rows, int d, int64_t x_stride, int64_t res_stride,
+                         int64_t res_out_stride, float eps, int group, int code_type,
+                         void* residual_out, void* codes, float* scales, void* stream);
+
+/* ----------------------------------------------- pages of a cache -- */
+/* The pages of a paged cache, managed on the device.  A pool of n_pages pages
+ * (cap_rows = n_pages * page_rows) has ref_count, int32 [n_pages]: how many
+ * block-table entries name the page; a page of count 0 is free.  block_table,
+ * int32 [n_slots][max_pages], holds a row of pages for each slot (a sequence);
+ * an entry below 0 is unused.  A page that several rows name (a common prompt)
+ * must not be written; kattn_fork_sequences gives a child a copy of the page
+ * that it will write next.  One table serves the caches of all layers: the
+ * page operations move numbers, kattn_copy_pages moves the rows of one cache.
+ *
+ * Every operation is asynchronous on `stream`, allocates nothing and gives the
+ * same result on every run: free pages are taken in ascending order.  Lists
+ * (seqs, parents, children, lens, src, dst) are int32 arrays on the device, so
+ * they are checked there; what a check finds is set in the workspace's error
+ * word (kattn_get_device_status).  A list has at most n_slots entries.
+ *   KATTN_DEVERR_BAD_SEQUENCE  a slot outside [0, n_slots), a slot that a list
+ *     names again (the first place counts; to free a slot twice is no error),
+ *     or lens out of range: that entry of the list is skipped;
+ *   KATTN_DEVERR_BAD_PAGE      a page outside the pool, or a count that would
+ *     fall below 0: that page is skipped;
+ *   KATTN_DEVERR_NO_PAGES      see the operation.
+ * workspace: kattn_page_workspace_size(n_slots, n_pages) bytes, 256-byte
+ * aligned, all of it zeroed before the first call.  It may be reused by calls
+ * ordered on the GPU, for the same or smaller sizes; calls that share it and
+ * overlap on the GPU race. */
+size_t kattn_page_workspace_size(int n_slots, int n_pages);
+
+/* Gives each slot seqs[i], i < n, pages for lens[i] rows: those of its first
+ * ceil(lens[i] / page_rows) table entries that are unused get free pages with
+ * count 1, in the order of the list and then of the entries.  If the pool has
+ * fewer free pages than all of them need together, no page is given to any
+ * slot and KATTN_DEVERR_NO_PAGES is set.  0 <= lens[i] <= max_pages * page_rows. */
+int kattn_reserve_pages(int32_t* block_table, int n_slots, int max_pages, int32_t* ref_count,
+                        int n_pages, int page_rows, const int32_t* seqs, const int32_t* lens,
+                        int n, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Ends the sequences of the slots seqs[i]: every page that the row names loses
+ * one reference, and the row's entries become -1.  A row that is already empty
+ * is left as it is. */
+int kattn_free_sequences(int32_t* block_table, int n_slots, int max_pages, int32_t* ref_count,
+                         int n_pages, const int32_t* seqs, int n, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* Branches sequences: slot children[i] becomes a copy of the first lens[i] rows
+ * of slot parents[i].  Whatever the child held is released first (as
+ * kattn_free_sequences).  It then shares the parent's full pages (their counts
+ * rise), and if lens[i] ends inside a page it gets a free page of its own for
+ * the rest: src[i] and dst[i] are the pages to copy with kattn_copy_pages, -1
+ * and -1 if there is nothing to copy.  Its other entries become -1.
+ * A pair is skipped, with src[i] = dst[i] = -1 and its child left as it was, if
+ * a slot is out of range, the child is also a parent of this call or was named
+ * before, lens[i] is outside [0, max_pages * page_rows], or the parent does not
+ * hold lens[i] rows (KATTN_DEVERR_BAD_SEQUENCE; KATTN_DEVERR_BAD_PAGE for an
+ * entry outside the pool).  Where the free pages (with those just released) do
+ * not suffice, the first pairs of the list get theirs; the children of the
+ * others are left empty and KATTN_DEVERR_NO_PAGES is set. */
+int kattn_fork_sequences(int32_t* block_table, int n_slots, int max_pages, int32_t* ref_count,
+                         int n_pages, int page_rows, const int32_t* parents,
+                         const int32_t* children, const int32_t* lens, int n, int32_t* src,
+                         int32_t* dst, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Plans the moves that bring the live pages (count > 0) to the front of the
+ * pool.  With n_live live pages, the k-th free page below n_live takes the
+ * k-th live page at or above it, in ascending order:
+ *   src[k], dst[k]  the moves, for kattn_copy_pages; the rest of the two arrays
+ *                   (n_pages / 2 entries each, at least 1) is -1;
+ *   counts          int32 [2]: n_live and the number of moves;
+ *   table_out, ref_out   the table and counts after the moves.  They may be the
+ *                   inputs themselves (in place), or other arrays: then a
+ *                   decode step in flight can go on with the old table until
+ *                   the copies are done (no destination is a live page).
+ * Table entries outside the pool are kept (KATTN_DEVERR_BAD_PAGE for those at
+ * or above n_pages). */
+int kattn_compact_pages(const int32_t* block_table, int n_slots, int max_pages,
+                        const int32_t* ref_count, int n_pages, int32_t* table_out,
+                        int32_t* ref_out, int32_t* src, int32_t* dst, int32_t* counts,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Copies pages of one cache: the page_rows rows of page src[i] to page dst[i],
+ * in every plane of k, v (int8 [Hkv][cap_rows][128]) and k_scale, v_scale
+ * (float32 [Hkv][cap_rows]).  Entries with src[i] or dst[i] below 0 are skipped;
+ * an entry outside the pool is skipped and sets KATTN_DEVERR_BAD_PAGE.  count:
+ * NULL, or an int32 on the device: only the first min(n, *count) entries are
+ * taken.  A source may be named several times; a destination must be named
+ * once, and must not be a source of the same call (the copies run side by
+ * side).  page_rows and cap_rows as in kattn_decode_paged; k, v 16-byte
+ * aligned, scales 16-byte aligned.  workspace: at least 256 bytes (only its
+ * error word is used). */
+int kattn_copy_pages(int8_t* k, float* k_scale, int8_t* v, float* v_scale, int Hkv, int d,
+                     int cap_rows, int page_rows, const int32_t* src, const int32_t* dst, int n,
+                     const int32_t* count, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/* Read (and clear) the device error word of a workspace.  Copies 4
  * bytes to the host and waits for `stream`.  *device_err receives the
  * KATTN_DEVERR_* bits set by calls since the last read. */
 int kattn_get_device_status(void* workspace, size_t workspace_bytes,

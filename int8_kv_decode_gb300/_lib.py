@@ -56,6 +56,26 @@ SIGNATURES = {
                                       c_void_p, c_void_p, c_void_p]),
     "kattn_expf_constants": (c_int, [ctypes.POINTER(ctypes.c_double)]),
     "kattn_hash_rows": (c_int, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p]),
+    "kattn_diff_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int]),
+    "kattn_decode_diff": (c_int, [c_void_p] * 8 + [c_int] * 8 + [c_float, c_void_p, c_void_p,
+                                                                 c_size_t, c_void_p]),
+    "kattn_decode_diff_paged": (c_int, [c_void_p] * 6 + [c_int, c_int, c_void_p, c_void_p]
+                                + [c_int] * 8 + [c_float, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "kattn_rms_norm_quant": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int64, c_int, c_int64,
+                                     c_int64, c_int64, c_float, c_int, c_int, c_void_p, c_void_p,
+                                     c_void_p, c_void_p]),
+    "kattn_page_workspace_size": (c_size_t, [c_int, c_int]),
+    "kattn_reserve_pages": (c_int, [c_void_p, c_int, c_int, c_void_p, c_int, c_int, c_void_p,
+                                    c_void_p, c_int, c_void_p, c_size_t, c_void_p]),
+    "kattn_free_sequences": (c_int, [c_void_p, c_int, c_int, c_void_p, c_int, c_void_p, c_int,
+                                     c_void_p, c_size_t, c_void_p]),
+    "kattn_fork_sequences": (c_int, [c_void_p, c_int, c_int, c_void_p, c_int, c_int, c_void_p,
+                                     c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p,
+                                     c_size_t, c_void_p]),
+    "kattn_compact_pages": (c_int, [c_void_p, c_int, c_int, c_void_p, c_int, c_void_p, c_void_p,
+                                    c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "kattn_copy_pages": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
+                                 c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_size_t, c_void_p]),
     "kattn_get_device_status": (c_int, [c_void_p, c_size_t, ctypes.POINTER(c_int), c_void_p]),
 }
 

@@ -19,6 +19,7 @@ P_MODES = {"f32": 0, "bf16": 1, "e4m3": 2, "e4m3x448": 3, "e4m3x256": 4, "e4m3di
 DEVERR_BAD_SEQUENCE = 0x1
 DEVERR_TIMEOUT = 0x2
 DEVERR_BAD_PAGE = 0x4
+DEVERR_NO_PAGES = 0x8
 
 
 def _stream(device) -> int:
@@ -416,8 +417,346 @@ def qk_scores_debug(q, k, k_scale, row_start, ctx_len, max_ctx: int, *, scores=N
     return (scores, q_i8, q_scale) if want_q else scores
 
 
+# ------------------------------------------------ differential attention --
+
+def _need_all(device, specs):
+    """Checks of several tensors on one device: (tensor, dtype, name, ndim) each."""
+    for t, dtype, name, ndim in specs:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.device != device or not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.dim() != ndim:
+            raise ValueError(f"{name} must have {ndim} dimensions")
+
+
+def _launch(name, device, *args):
+    """One library call on torch's current stream of `device`, which need not
+    be the current device."""
+    fn = getattr(_lib.load(), name)
+    if device.index == torch.cuda.current_device():
+        _lib.check(name, fn(*args, _stream(device)))
+    else:
+        with torch.cuda.device(device):
+            _lib.check(name, fn(*args, _stream(device)))
+
+
+def diff_workspace_size(B: int, M: int, Hq: int, max_ctx: int) -> int:
+    return int(_lib.load().kattn_diff_workspace_size(B, M, Hq, max_ctx))
+
+
+def alloc_diff_workspace(B: int, M: int, Hq: int, max_ctx: int, device="cuda") -> torch.Tensor:
+    """A zeroed workspace for decode_diff (allocated by torch, not the library)."""
+    n = diff_workspace_size(B, M, Hq, max_ctx)
+    if n == 0:
+        raise ValueError("invalid sizes for a differential decode workspace")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _diff_args(q, k, k_scale, v, v_scale, ctx_len, max_ctx, lam, out, workspace, extra):
+    """Checks and defaults that decode_diff and decode_diff_paged share."""
+    if not isinstance(q, torch.Tensor) or not isinstance(lam, torch.Tensor):
+        raise TypeError("q and lam must be torch tensors")
+    _need_all(q.device, [(q, torch.float32, "q", 4), (k, torch.int8, "k", 3),
+                         (v, torch.int8, "v", 3), (k_scale, torch.float32, "k_scale", 2),
+                         (v_scale, torch.float32, "v_scale", 2),
+                         (ctx_len, torch.int32, "ctx_len", 1),
+                         (lam, torch.float32, "lam", lam.dim())] + extra)
+    B, M, Hq, d = q.shape
+    Hkv, cap, dk = k.shape
+    if v.shape != k.shape or k_scale.shape != (Hkv, cap) or v_scale.shape != (Hkv, cap) or dk != d:
+        raise ValueError("k/v/scales shapes disagree")
+    if Hkv < 2 or Hkv % 2 or Hq % Hkv:
+        raise ValueError("kv planes come in pairs, and Hq must be a multiple of Hkv")
+    if ctx_len.shape[0] != B:
+        raise ValueError("ctx_len must have B entries")
+    if not 0 < max_ctx < 2 ** 30:
+        raise ValueError("max_ctx out of range")
+    H = Hq // 2
+    per_row = lam.dim() == 3
+    if lam.shape != ((B, M, H) if per_row else (H,)):
+        raise ValueError("lam must have shape [Hq/2] or [B][M][Hq/2]")
+    if out is None:
+        out = torch.empty((B, M, H, 2 * d), dtype=torch.float32, device=q.device)
+    else:
+        _need_all(q.device, [(out, torch.float32, "out", 4)])
+        if out.shape != (B, M, H, 2 * d):
+            raise ValueError("out must have shape [B][M][Hq/2][256]")
+    if workspace is None:
+        workspace = (alloc_diff_workspace(B, M, Hq, max_ctx, q.device) if B else
+                     torch.zeros(256, dtype=torch.uint8, device=q.device))
+    else:
+        _need_all(q.device, [(workspace, torch.uint8, "workspace", 1)])
+    return B, M, Hq, Hkv, d, cap, int(per_row), out, workspace
+
+
+def decode_diff(q, k, k_scale, v, v_scale, row_start, ctx_len, max_ctx: int, lam, *, out=None,
+                sm_scale: float = 0.0, workspace=None):
+    """Differential decode attention; returns out [B][M][Hq/2][256] float32.
+
+    Head i of the Hq/2 differential heads is softmax_1 V - lam softmax_2 V: its
+    two maps come from query heads 2i, 2i+1 and key planes 2p, 2p+1, its V is
+    the 256 channels of value planes 2p, 2p+1, with p = i // (Hq / Hkv).
+    lam: float32 [Hq/2], or [B][M][Hq/2] for one value per row.  q and the cache
+    as in decode(); Hkv even.  workspace: a zeroed uint8 tensor of
+    diff_workspace_size(...) bytes, allocated here with torch if None.
+    (kattn_decode_diff)
+    """
+    B, M, Hq, Hkv, d, cap, per_row, out, workspace = _diff_args(
+        q, k, k_scale, v, v_scale, ctx_len, max_ctx, lam, out, workspace,
+        [(row_start, torch.int64, "row_start", 1)])
+    if row_start.shape[0] != B:
+        raise ValueError("row_start must have B entries")
+    _launch("kattn_decode_diff", q.device, q.data_ptr(), k.data_ptr(), k_scale.data_ptr(),
+            v.data_ptr(), v_scale.data_ptr(), row_start.data_ptr(), ctx_len.data_ptr(),
+            lam.data_ptr(), per_row, B, M, Hq, Hkv, d, cap, max_ctx, sm_scale, out.data_ptr(),
+            workspace.data_ptr(), workspace.numel())
+    return out
+
+
+def decode_diff_paged(q, k, k_scale, v, v_scale, block_table, page_rows: int, ctx_len,
+                      max_ctx: int, lam, *, out=None, sm_scale: float = 0.0, workspace=None):
+    """decode_diff() over a paged cache; paging arguments as decode_paged().
+    (kattn_decode_diff_paged)"""
+    B, M, Hq, Hkv, d, cap, per_row, out, workspace = _diff_args(
+        q, k, k_scale, v, v_scale, ctx_len, max_ctx, lam, out, workspace,
+        [(block_table, torch.int32, "block_table", 2)])
+    if block_table.shape[0] != B:
+        raise ValueError("block_table must have B rows")
+    _launch("kattn_decode_diff_paged", q.device, q.data_ptr(), k.data_ptr(), k_scale.data_ptr(),
+            v.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), block_table.shape[1],
+            page_rows, ctx_len.data_ptr(), lam.data_ptr(), per_row, B, M, Hq, Hkv, d, cap, max_ctx,
+            sm_scale, out.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return out
+
+
+# ------------------------------------------------- norm with 8-bit output --
+
+_NORM_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_CODE_TYPES = {torch.int8: 0, torch.float8_e4m3fn: 1}
+
+
+def _rows(t, like, name):
+    """t as rows of its last dimension: (rows, row stride).  2-D tensors may have
+    any row stride, others must be contiguous."""
+    if t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    if t.device != like.device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {like.device}, got {t.device}")
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must have shape {tuple(like.shape)}")
+    d = t.shape[-1]
+    if t.dim() == 2 and (d == 1 or t.stride(1) == 1):
+        return t.shape[0], (t.stride(0) if t.shape[0] > 1 else d)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, or 2-D with a contiguous last dimension")
+    return t.numel() // d, d
+
+
+def rms_norm_quant(x, weight, *, residual=None, residual_out=None, eps: float = 1e-6,
+                   group: int = 0, out=None, out_scale=None, out_dtype=torch.int8):
+    """Residual addition, RMS norm and 8-bit quantization of the rows of x.
+
+    x [..., d] float32, bfloat16 or float16; weight [d] and residual (like x) of
+    the same type.  h = x + residual (rounded to the type) is stored in
+    residual_out (the residual itself if None).  Returns (codes, scales): codes
+    like x in out_dtype (torch.int8 or torch.float8_e4m3fn), scales float32, one
+    per row [...] or per 128 channels [..., d/128] (group = 128), so that codes *
+    scales is h / rms(h) * weight.  (kattn_rms_norm_quant)
+    """
+    if not isinstance(x, torch.Tensor) or not isinstance(weight, torch.Tensor):
+        raise TypeError("x and weight must be torch tensors")
+    if x.dtype not in _NORM_TYPES:
+        raise TypeError(f"x must be float32, bfloat16 or float16, got {x.dtype}")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must have a last dimension of at least 1")
+    rows, xs = _rows(x, x, "x")
+    d = x.shape[-1]
+    _need_all(x.device, [(weight, x.dtype, "weight", 1)])
+    if weight.shape[0] != d:
+        raise ValueError("weight must have one entry per channel")
+    if group not in (0, 128) or (group and d % group):
+        raise ValueError("group must be 0, or 128 for rows of a multiple of 128 channels")
+    rs = ros = d
+    rp = rop = 0
+    if residual is not None:
+        rs = _rows(residual, x, "residual")[1]
+        if residual_out is None:
+            residual_out = residual
+        ros = _rows(residual_out, x, "residual_out")[1]
+        rp, rop = residual.data_ptr(), residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
+    if out.dtype not in _CODE_TYPES:
+        raise TypeError(f"codes must be int8 or float8_e4m3fn, got {out.dtype}")
+    scale_shape = x.shape[:-1] + ((d // group,) if group else ())
+    if out_scale is None:
+        out_scale = torch.empty(scale_shape, dtype=torch.float32, device=x.device)
+    _need_all(x.device, [(out, out.dtype, "out", x.dim()),
+                         (out_scale, torch.float32, "out_scale", out_scale.dim())])
+    if out.shape != x.shape:
+        raise ValueError("out must have the shape of x")
+    if out_scale.numel() != rows * (d // group if group else 1):
+        raise ValueError(f"out_scale must have shape {tuple(scale_shape)}")
+    _launch("kattn_rms_norm_quant", x.device, x.data_ptr(), rp, weight.data_ptr(),
+            _NORM_TYPES[x.dtype], rows, d, xs, rs, ros, eps, group, _CODE_TYPES[out.dtype], rop,
+            out.data_ptr(), out_scale.data_ptr())
+    return out, out_scale
+
+
+# -------------------------------------------------------- page operations --
+
+def page_workspace_size(n_slots: int, n_pages: int) -> int:
+    return int(_lib.load().kattn_page_workspace_size(n_slots, n_pages))
+
+
+def alloc_page_workspace(n_slots: int, n_pages: int, device="cuda") -> torch.Tensor:
+    """A zeroed workspace for the page operations of a table of n_slots rows
+    over a pool of n_pages pages."""
+    n = page_workspace_size(n_slots, n_pages)
+    if n == 0:
+        raise ValueError("invalid sizes for a page workspace")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _page_args(block_table, ref_count, lists, workspace):
+    """Checks that the page operations share; lists: (tensor, name) each, all of
+    one length.  Returns (n_slots, max_pages, n_pages, n, workspace)."""
+    if not isinstance(block_table, torch.Tensor):
+        raise TypeError("block_table must be a torch.Tensor")
+    _need_all(block_table.device,
+              [(block_table, torch.int32, "block_table", 2), (ref_count, torch.int32, "ref_count", 1)]
+              + [(t, torch.int32, name, 1) for t, name in lists])
+    n_slots, max_pages = block_table.shape
+    n_pages = ref_count.shape[0]
+    n = lists[0][0].shape[0] if lists else 0
+    for t, name in lists:
+        if t.shape[0] != n:
+            raise ValueError(f"{name} must have {n} entries")
+    if workspace is None:
+        workspace = alloc_page_workspace(n_slots, n_pages, block_table.device)
+    else:
+        _need_all(block_table.device, [(workspace, torch.uint8, "workspace", 1)])
+    return n_slots, max_pages, n_pages, n, workspace
+
+
+def reserve_pages(block_table, ref_count, seqs, lens, page_rows: int, *, workspace=None) -> None:
+    """Pages from the pool for lens[i] rows of slot seqs[i] (kattn_reserve_pages).
+
+    block_table int32 [n_slots][max_pages] (unused entries below 0), ref_count
+    int32 [n_pages], seqs and lens int32 [n]; both tables are updated in place.
+    """
+    S, mp, P, n, ws = _page_args(block_table, ref_count, [(seqs, "seqs"), (lens, "lens")], workspace)
+    _launch("kattn_reserve_pages", block_table.device, block_table.data_ptr(), S, mp,
+            ref_count.data_ptr(), P, page_rows, seqs.data_ptr(), lens.data_ptr(), n, ws.data_ptr(),
+            ws.numel())
+
+
+def free_sequences(block_table, ref_count, seqs, *, workspace=None) -> None:
+    """Release the pages of the slots seqs (int32 [n]); in place
+    (kattn_free_sequences)."""
+    S, mp, P, n, ws = _page_args(block_table, ref_count, [(seqs, "seqs")], workspace)
+    _launch("kattn_free_sequences", block_table.device, block_table.data_ptr(), S, mp,
+            ref_count.data_ptr(), P, seqs.data_ptr(), n, ws.data_ptr(), ws.numel())
+
+
+def fork_sequences(block_table, ref_count, parents, children, lens, page_rows: int, *, src=None,
+                   dst=None, workspace=None):
+    """Slot children[i] becomes a branch of the first lens[i] rows of slot
+    parents[i]: full pages shared, the last partial one to be copied.  Returns
+    (src, dst), int32 [n], for copy_pages() (kattn_fork_sequences)."""
+    S, mp, P, n, ws = _page_args(
+        block_table, ref_count, [(children, "children"), (parents, "parents"), (lens, "lens")],
+        workspace)
+    dev = block_table.device
+    if src is None:
+        src = torch.empty(n, dtype=torch.int32, device=dev)
+    if dst is None:
+        dst = torch.empty(n, dtype=torch.int32, device=dev)
+    _need_all(dev, [(src, torch.int32, "src", 1), (dst, torch.int32, "dst", 1)])
+    if src.shape[0] != n or dst.shape[0] != n:
+        raise ValueError(f"src and dst must have {n} entries")
+    _launch("kattn_fork_sequences", dev, block_table.data_ptr(), S, mp, ref_count.data_ptr(), P,
+            page_rows, parents.data_ptr(), children.data_ptr(), lens.data_ptr(), n, src.data_ptr(),
+            dst.data_ptr(), ws.data_ptr(), ws.numel())
+    return src, dst
+
+
+def compact_pages(block_table, ref_count, *, table_out=None, ref_out=None, src=None, dst=None,
+                  counts=None, workspace=None):
+    """The moves that bring the live pages to the front of the pool.
+
+    Returns (table_out, ref_out, src, dst, counts): the table and counts after
+    the moves (new tensors unless given; the inputs themselves for an update in
+    place), the moves for copy_pages() (int32 [max(1, n_pages // 2)], -1 past
+    the last), and counts = int32 [n_live, n_moves] (kattn_compact_pages)."""
+    S, mp, P, _, ws = _page_args(block_table, ref_count, [], workspace)
+    dev = block_table.device
+    most = max(1, P // 2)
+    if table_out is None:
+        table_out = torch.empty_like(block_table)
+    if ref_out is None:
+        ref_out = torch.empty_like(ref_count)
+    if src is None:
+        src = torch.empty(most, dtype=torch.int32, device=dev)
+    if dst is None:
+        dst = torch.empty(most, dtype=torch.int32, device=dev)
+    if counts is None:
+        counts = torch.empty(2, dtype=torch.int32, device=dev)
+    _need_all(dev, [(table_out, torch.int32, "table_out", 2), (ref_out, torch.int32, "ref_out", 1),
+                    (src, torch.int32, "src", 1), (dst, torch.int32, "dst", 1),
+                    (counts, torch.int32, "counts", 1)])
+    if table_out.shape != block_table.shape or ref_out.shape != ref_count.shape:
+        raise ValueError("table_out / ref_out must have the shapes of block_table / ref_count")
+    if src.shape[0] != most or dst.shape[0] != most or counts.shape[0] != 2:
+        raise ValueError(f"src and dst must have {most} entries, counts 2")
+    _launch("kattn_compact_pages", dev, block_table.data_ptr(), S, mp, ref_count.data_ptr(), P,
+            table_out.data_ptr(), ref_out.data_ptr(), src.data_ptr(), dst.data_ptr(),
+            counts.data_ptr(), ws.data_ptr(), ws.numel())
+    return table_out, ref_out, src, dst, counts
+
+
+def copy_pages(k, k_scale, v, v_scale, src, dst, page_rows: int, *, count=None,
+               workspace=None) -> None:
+    """Copy page src[i] to page dst[i] in every plane of one cache, k and v
+    [Hkv][cap][128] int8 with their scales [Hkv][cap]; entries below 0 are
+    skipped.  count: an int32 tensor of one entry; only the first min(n, count)
+    moves are made.  workspace: any workspace of the library (its error word
+    takes the checks of the entries); allocated here if None.
+    (kattn_copy_pages)"""
+    if not isinstance(k, torch.Tensor):
+        raise TypeError("k must be a torch.Tensor")
+    dev = k.device
+    specs = [(k, torch.int8, "k", 3), (v, torch.int8, "v", 3),
+             (k_scale, torch.float32, "k_scale", 2), (v_scale, torch.float32, "v_scale", 2),
+             (src, torch.int32, "src", 1), (dst, torch.int32, "dst", 1)]
+    if count is not None:
+        specs.append((count, torch.int32, "count", 1))
+    if workspace is None:
+        workspace = torch.zeros(256, dtype=torch.uint8, device=dev)
+    specs.append((workspace, torch.uint8, "workspace", 1))
+    _need_all(dev, specs)
+    Hkv, cap, d = k.shape
+    if v.shape != k.shape or k_scale.shape != (Hkv, cap) or v_scale.shape != (Hkv, cap):
+        raise ValueError("k/v/scales shapes disagree")
+    if src.shape != dst.shape:
+        raise ValueError("src and dst must have the same length")
+    if count is not None and count.shape[0] != 1:
+        raise ValueError("count must have one entry")
+    _launch("kattn_copy_pages", dev, k.data_ptr(), k_scale.data_ptr(), v.data_ptr(),
+            v_scale.data_ptr(), Hkv, d, cap, page_rows, src.data_ptr(), dst.data_ptr(),
+            src.shape[0], 0 if count is None else count.data_ptr(), workspace.data_ptr(),
+            workspace.numel())
+
+
 def get_device_status(workspace: torch.Tensor) -> int:
-    """Read and clear the device error bits of a decode workspace."""
+    """Read and clear the device error bits of a workspace."""
     _need(workspace, torch.uint8, "workspace", 1)
     lib = _lib.load()
     err = ctypes.c_int(0)

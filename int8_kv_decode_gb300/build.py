@@ -37,6 +37,9 @@ SOURCES = {
     "decode_exact.cu": ["--fmad=false"],
     "expf_constants.cu": ["--fmad=false"],
     "hash_rows.cu": [],
+    "decode_diff.cu": [],
+    "norm_quant.cu": [],
+    "pages.cu": [],
 }
 
 

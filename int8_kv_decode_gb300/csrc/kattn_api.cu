@@ -3,6 +3,7 @@
 #include <cstring>
 
 #include "kattn_internal.cuh"
+#include "ops_internal.cuh"
 
 using namespace kattn;
 
@@ -172,6 +173,85 @@ int run_append(DecodeParams& p, const float* k_new, const float* v_new, const in
   p.vs_w = v_scale;
   const cudaError_t e = launch_decode_fast(p, as_stream(stream));
   return e == cudaSuccess ? KATTN_OK : KATTN_ERR_CUDA;
+}
+
+// The differential decode, once the layout-specific arguments are in p.
+int run_diff(DiffParams& p, const float* q, const int8_t* k, const float* k_scale,
+             const int8_t* v, const float* v_scale, const int32_t* ctx_len, const float* lam,
+             int lam_per_row, int B, int M, int Hq, int Hkv, int cap_rows, int max_ctx,
+             float sm_scale, float* out, void* workspace, size_t workspace_bytes, void* stream) {
+  if (Hkv % 2 != 0 || (lam_per_row != 0 && lam_per_row != 1)) return KATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(sm_scale)) return KATTN_ERR_INVALID_ARG;
+  if (B == 0) return KATTN_OK;
+  if (!v || !v_scale || !lam || !out) return KATTN_ERR_INVALID_ARG;
+  if (!aligned(v, 16) || !aligned(v_scale, 4) || !aligned(lam, 4) || !aligned(out, 16))
+    return KATTN_ERR_MISALIGNED;
+  p.q = q;
+  p.k = k;
+  p.k_scale = k_scale;
+  p.v = v;
+  p.v_scale = v_scale;
+  p.ctx_len = ctx_len;
+  p.lam = lam;
+  p.lam_per_row = lam_per_row;
+  p.out = out;
+  p.B = B;
+  p.M = M;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.g = Hq / Hkv;
+  p.R = p.g * M;
+  p.pairs = Hkv / 2;
+  p.cap_rows = cap_rows;
+  p.max_ctx = max_ctx;
+  p.nwin_max = nsplit_for(max_ctx + M - 1);
+  p.sm_scale = resolve_sm_scale(sm_scale, KATTN_HEAD_DIM);
+  // work units (8 rows of a window and plane pair) are counted in int32
+  if ((int64_t)B * p.nwin_max * p.pairs * ((p.R + 7) / 8) > (int64_t)INT32_MAX / 4)
+    return KATTN_ERR_UNSUPPORTED;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < diff_workspace_bytes(B, M, Hq, max_ctx))
+    return KATTN_ERR_WORKSPACE;
+  set_diff_workspace(p, workspace);
+  return launch_decode_diff(p, as_stream(stream)) == cudaSuccess ? KATTN_OK : KATTN_ERR_CUDA;
+}
+
+// Arguments that the page operations share.
+int check_pages(const void* block_table, int n_slots, int max_pages, const void* ref_count,
+                int n_pages, const void* list, int n, const void* workspace,
+                size_t workspace_bytes) {
+  if (n_slots < 1 || max_pages < 1 || n_pages < 1 || n < 0 || n > n_slots)
+    return KATTN_ERR_INVALID_ARG;
+  if (!block_table || !ref_count || (n > 0 && !list)) return KATTN_ERR_INVALID_ARG;
+  if (!aligned(block_table, 4) || !aligned(ref_count, 4) || !aligned(list, 4))
+    return KATTN_ERR_MISALIGNED;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < page_workspace_bytes(n_slots, n_pages))
+    return KATTN_ERR_WORKSPACE;
+  return KATTN_OK;
+}
+
+// Rows per page: 32 * 2^k, as for the decode, so that every table the page
+// operations make can be decoded.
+int check_page_rows(int page_rows) {
+  if (page_rows < 1) return KATTN_ERR_INVALID_ARG;
+  if (page_rows < kBlockBk || (page_rows & (page_rows - 1)) != 0) return KATTN_ERR_UNSUPPORTED;
+  return KATTN_OK;
+}
+
+PageParams page_params(const int32_t* block_table, int n_slots, int max_pages,
+                       const int32_t* ref_count, int n_pages, int page_rows, int n,
+                       void* workspace) {
+  PageParams p{};
+  p.table = const_cast<int32_t*>(block_table);
+  p.n_slots = n_slots;
+  p.max_pages = max_pages;
+  p.refs = const_cast<int32_t*>(ref_count);
+  p.n_pages = n_pages;
+  p.page_shift = __builtin_ctz((unsigned)page_rows);
+  p.n = n;
+  set_page_workspace(p, workspace);
+  return p;
 }
 
 }  // namespace
@@ -420,6 +500,194 @@ int kattn_hash_rows(const void* data, int64_t n_rows, int64_t row_bytes, int64_t
   const cudaError_t e = launch_hash_rows(data, n_rows, row_bytes, row_stride_bytes, hashes,
                                          as_stream(stream));
   return e == cudaSuccess ? KATTN_OK : KATTN_ERR_CUDA;
+}
+
+size_t kattn_diff_workspace_size(int B, int M, int Hq, int max_ctx) {
+  if (B < 1 || M < 1 || M > KATTN_MAX_M || Hq < 1 || max_ctx < 1) return 0;
+  return diff_workspace_bytes(B, M, Hq, max_ctx);
+}
+
+int kattn_decode_diff(const float* q, const int8_t* k, const float* k_scale, const int8_t* v,
+                      const float* v_scale, const int64_t* row_start, const int32_t* ctx_len,
+                      const float* lam, int lam_per_row, int B, int M, int Hq, int Hkv, int d,
+                      int cap_rows, int max_ctx, float sm_scale, float* out, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  const int st = check_common(q, k, k_scale, row_start, 8, ctx_len, B, M, Hq, Hkv, d, cap_rows,
+                              max_ctx);
+  if (st != KATTN_OK) return st;
+  DiffParams p{};
+  p.row_start = row_start;
+  return run_diff(p, q, k, k_scale, v, v_scale, ctx_len, lam, lam_per_row, B, M, Hq, Hkv, cap_rows,
+                  max_ctx, sm_scale, out, workspace, workspace_bytes, stream);
+}
+
+int kattn_decode_diff_paged(const float* q, const int8_t* k, const float* k_scale,
+                            const int8_t* v, const float* v_scale, const int32_t* block_table,
+                            int max_pages, int page_rows, const int32_t* ctx_len,
+                            const float* lam, int lam_per_row, int B, int M, int Hq, int Hkv,
+                            int d, int cap_rows, int max_ctx, float sm_scale, float* out,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_common(q, k, k_scale, block_table, 4, ctx_len, B, M, Hq, Hkv, d, cap_rows,
+                        max_ctx);
+  if (st != KATTN_OK) return st;
+  st = check_paging(max_pages, page_rows, cap_rows);
+  if (st != KATTN_OK) return st;
+  DiffParams p{};
+  p.block_table = block_table;
+  p.max_pages = max_pages;
+  p.page_shift = __builtin_ctz((unsigned)page_rows);
+  p.n_pages = cap_rows / page_rows;
+  return run_diff(p, q, k, k_scale, v, v_scale, ctx_len, lam, lam_per_row, B, M, Hq, Hkv, cap_rows,
+                  max_ctx, sm_scale, out, workspace, workspace_bytes, stream);
+}
+
+int kattn_rms_norm_quant(const void* x, const void* residual, const void* weight, int x_type,
+                         int64_t rows, int d, int64_t x_stride, int64_t res_stride,
+                         int64_t res_out_stride, float eps, int group, int code_type,
+                         void* residual_out, void* codes, float* scales, void* stream) {
+  if (x_type < KATTN_F32 || x_type > KATTN_F16) return KATTN_ERR_INVALID_ARG;
+  if (code_type != KATTN_INT8 && code_type != KATTN_E4M3) return KATTN_ERR_INVALID_ARG;
+  if (rows < 0 || d < 1 || d > (1 << 24) || !std::isfinite(eps) || eps < 0.0f)
+    return KATTN_ERR_INVALID_ARG;
+  if (group != 0 && group != 128) return KATTN_ERR_UNSUPPORTED;
+  if (group != 0 && d % group != 0) return KATTN_ERR_INVALID_ARG;
+  if (x_stride < d) return KATTN_ERR_INVALID_ARG;
+  if ((residual == nullptr) != (residual_out == nullptr)) return KATTN_ERR_INVALID_ARG;
+  if (residual && (res_stride < d || res_out_stride < d)) return KATTN_ERR_INVALID_ARG;
+  if (residual && residual == residual_out && res_stride != res_out_stride)
+    return KATTN_ERR_INVALID_ARG;
+  if (rows > INT32_MAX) return KATTN_ERR_UNSUPPORTED;     // one grid axis
+  if (rows == 0) return KATTN_OK;
+  if (!x || !weight || !codes || !scales) return KATTN_ERR_INVALID_ARG;
+  const size_t e = x_type == KATTN_F32 ? 4 : 2;
+  if (!aligned(x, e) || !aligned(weight, e) || !aligned(residual, e) || !aligned(residual_out, e) ||
+      !aligned(scales, 4))
+    return KATTN_ERR_MISALIGNED;
+  NormParams p{};
+  p.x = x;
+  p.residual = residual;
+  p.weight = weight;
+  p.residual_out = residual_out;
+  p.codes = static_cast<uint8_t*>(codes);
+  p.scales = scales;
+  p.rows = rows;
+  p.x_stride = x_stride;
+  p.res_stride = res_stride;
+  p.res_out_stride = res_out_stride;
+  p.d = d;
+  p.group = group ? group : d;
+  p.eps = eps;
+  return launch_rms_norm_quant(p, x_type, code_type, as_stream(stream)) == cudaSuccess
+             ? KATTN_OK
+             : KATTN_ERR_CUDA;
+}
+
+size_t kattn_page_workspace_size(int n_slots, int n_pages) {
+  if (n_slots < 1 || n_pages < 1) return 0;
+  return page_workspace_bytes(n_slots, n_pages);
+}
+
+int kattn_reserve_pages(int32_t* block_table, int n_slots, int max_pages, int32_t* ref_count,
+                        int n_pages, int page_rows, const int32_t* seqs, const int32_t* lens,
+                        int n, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_pages(block_table, n_slots, max_pages, ref_count, n_pages, seqs, n, workspace,
+                       workspace_bytes);
+  if (st == KATTN_OK) st = check_page_rows(page_rows);
+  if (st != KATTN_OK) return st;
+  if (n == 0) return KATTN_OK;
+  if (!lens) return KATTN_ERR_INVALID_ARG;
+  if (!aligned(lens, 4)) return KATTN_ERR_MISALIGNED;
+  PageParams p = page_params(block_table, n_slots, max_pages, ref_count, n_pages, page_rows, n,
+                             workspace);
+  p.seqs = seqs;
+  p.lens = lens;
+  return launch_reserve_pages(p, as_stream(stream)) == cudaSuccess ? KATTN_OK : KATTN_ERR_CUDA;
+}
+
+int kattn_free_sequences(int32_t* block_table, int n_slots, int max_pages, int32_t* ref_count,
+                         int n_pages, const int32_t* seqs, int n, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  const int st = check_pages(block_table, n_slots, max_pages, ref_count, n_pages, seqs, n,
+                             workspace, workspace_bytes);
+  if (st != KATTN_OK) return st;
+  if (n == 0) return KATTN_OK;
+  PageParams p = page_params(block_table, n_slots, max_pages, ref_count, n_pages, 1, n, workspace);
+  p.seqs = seqs;
+  return launch_free_sequences(p, as_stream(stream)) == cudaSuccess ? KATTN_OK : KATTN_ERR_CUDA;
+}
+
+int kattn_fork_sequences(int32_t* block_table, int n_slots, int max_pages, int32_t* ref_count,
+                         int n_pages, int page_rows, const int32_t* parents,
+                         const int32_t* children, const int32_t* lens, int n, int32_t* src,
+                         int32_t* dst, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_pages(block_table, n_slots, max_pages, ref_count, n_pages, children, n, workspace,
+                       workspace_bytes);
+  if (st == KATTN_OK) st = check_page_rows(page_rows);
+  if (st != KATTN_OK) return st;
+  if (n == 0) return KATTN_OK;
+  if (!parents || !lens || !src || !dst) return KATTN_ERR_INVALID_ARG;
+  if (!aligned(parents, 4) || !aligned(lens, 4) || !aligned(src, 4) || !aligned(dst, 4))
+    return KATTN_ERR_MISALIGNED;
+  PageParams p = page_params(block_table, n_slots, max_pages, ref_count, n_pages, page_rows, n,
+                             workspace);
+  p.seqs = children;
+  p.parents = parents;
+  p.lens = lens;
+  p.src = src;
+  p.dst = dst;
+  return launch_fork_sequences(p, as_stream(stream)) == cudaSuccess ? KATTN_OK : KATTN_ERR_CUDA;
+}
+
+int kattn_compact_pages(const int32_t* block_table, int n_slots, int max_pages,
+                        const int32_t* ref_count, int n_pages, int32_t* table_out,
+                        int32_t* ref_out, int32_t* src, int32_t* dst, int32_t* counts,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  const int st = check_pages(block_table, n_slots, max_pages, ref_count, n_pages, nullptr, 0,
+                             workspace, workspace_bytes);
+  if (st != KATTN_OK) return st;
+  if (!table_out || !ref_out || !src || !dst || !counts) return KATTN_ERR_INVALID_ARG;
+  if (!aligned(table_out, 4) || !aligned(ref_out, 4) || !aligned(src, 4) || !aligned(dst, 4) ||
+      !aligned(counts, 4))
+    return KATTN_ERR_MISALIGNED;
+  PageParams p = page_params(block_table, n_slots, max_pages, ref_count, n_pages, 1, 0, workspace);
+  p.table_out = table_out;
+  p.ref_out = ref_out;
+  p.src = src;
+  p.dst = dst;
+  p.counts = counts;
+  return launch_compact_pages(p, as_stream(stream)) == cudaSuccess ? KATTN_OK : KATTN_ERR_CUDA;
+}
+
+int kattn_copy_pages(int8_t* k, float* k_scale, int8_t* v, float* v_scale, int Hkv, int d,
+                     int cap_rows, int page_rows, const int32_t* src, const int32_t* dst, int n,
+                     const int32_t* count, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  if (Hkv < 1 || cap_rows < 1 || n < 0) return KATTN_ERR_INVALID_ARG;
+  if (d != KATTN_HEAD_DIM) return KATTN_ERR_UNSUPPORTED;
+  const int st = check_page_rows(page_rows);
+  if (st != KATTN_OK) return st;
+  if (cap_rows % page_rows != 0) return KATTN_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < 256) return KATTN_ERR_WORKSPACE;
+  if (n == 0) return KATTN_OK;
+  if (!k || !k_scale || !v || !v_scale || !src || !dst) return KATTN_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_scale, 16) || !aligned(v_scale, 16) ||
+      !aligned(src, 4) || !aligned(dst, 4) || !aligned(count, 4))
+    return KATTN_ERR_MISALIGNED;
+  CopyParams p{};
+  p.k = k;
+  p.v = v;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.Hkv = Hkv;
+  p.cap_rows = cap_rows;
+  p.page_rows = page_rows;
+  p.n_pages = cap_rows / page_rows;
+  p.n = n;
+  p.src = src;
+  p.dst = dst;
+  p.count = count;
+  p.err = static_cast<uint32_t*>(workspace);
+  return launch_copy_pages(p, as_stream(stream)) == cudaSuccess ? KATTN_OK : KATTN_ERR_CUDA;
 }
 
 int kattn_get_device_status(void* workspace, size_t workspace_bytes, int* device_err,

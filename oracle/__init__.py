@@ -26,6 +26,9 @@ Modules:
                 float32 emulation
   hashdump   -- FNV-1a 64 row hashes and the first differing row (§3.4's
                 parity-dump method)
+  diff       -- differential decode attention over pairs of heads and planes
+  norm       -- residual addition, RMS norm and 8-bit row quantization
+  pages      -- reserving, freeing, forking and compacting a cache's pages
 
 Parity unpinned:
   * the absolute accuracy of the rounded-P modes against the infinitely
@@ -37,4 +40,5 @@ Parity unpinned:
     held to it only through the end-to-end tolerances and exact mode).
 """
 
-from . import quant, rounding, expf_tang, attention, hashdump  # noqa: F401
+from . import (quant, rounding, expf_tang, attention, hashdump, diff, norm,  # noqa: F401
+               pages)

@@ -1,0 +1,307 @@
+"""Differential decode attention on the GPU against the float64 oracle.
+
+Tolerance, per channel: |error| <= 2^-17 * (sum w_0 |V| + |lam| sum w_1 |V|).
+The query codes, the integer scores and the float32 score are the oracle's own,
+so the error is that of the weights and sums, all relative to the terms added:
+the exponential (2 ulp, and its argument rounded twice: x e^-x is at most 0.37,
+so below 2^-23 of the largest weight), numerator and row sum; the weight times
+scale held in 22 bits (2^-22); at most 8 tensor-core additions of 16 keys to a
+128-key span, each off by up to 2^-22; 4 rescalings of a span, 3 + 2 roundings
+of the span merge, 32 + 10 of the window merge (2^-24 each); the division, the
+product with lam and the difference (3 * 2^-24).  The sum is below
+(8 + 1 + 4) * 2^-22 + 60 * 2^-24 < 2^-17.
+"""
+
+import numpy as np
+import pytest
+
+import oracle
+from synth.paging import page_layout, paged_copy
+
+TOL = 2.0 ** -17
+
+
+def inputs(B, M, Hq, Hkv, ctx, seed=0, per_row=False, q_gain=2.0, outliers=False):
+    """Host arrays of a ragged contiguous cache with random rows between the
+    sequences."""
+    r = np.random.default_rng(seed)
+    ctx = np.asarray([ctx] * B if np.isscalar(ctx) else ctx, np.int32)
+    gaps = r.integers(0, 4, B)
+    n = ctx.astype(np.int64) + M - 1 + gaps
+    start = np.concatenate([[0], np.cumsum(n)[:-1]]).astype(np.int64)
+    cap = int(n.sum())
+    x = {"ctx": ctx, "start": start, "cap": cap, "M": M,
+         "q": (q_gain * r.standard_normal((B, M, Hq, 128))).astype(np.float32)}
+    for name in ("k", "v"):
+        rows = r.standard_normal((cap, Hkv, 128)).astype(np.float32)
+        if outliers:
+            rows[:, :, r.integers(0, 128, 4)] *= 20
+        x[name + "8"], x[name + "s"] = oracle.quant.quantize_kv(rows)
+    H = Hq // 2
+    x["lam"] = r.uniform(-0.5, 1.2, (B, M, H) if per_row else (H,)).astype(np.float32)
+    return x
+
+
+def device(x):
+    import torch
+    return {n: torch.from_numpy(np.ascontiguousarray(a)).cuda() for n, a in x.items()
+            if isinstance(a, np.ndarray)}
+
+
+def run(x, t=None, **kw):
+    import int8_kv_decode_gb300 as K
+    t = t or device(x)
+    return K.decode_diff(t["q"], t["k8"], t["ks"], t["v8"], t["vs"], t["start"], t["ctx"],
+                         int(x["ctx"].max()), t["lam"], **kw)
+
+
+def expected(x, **kw):
+    rows = [np.arange(int(c) + x["M"] - 1) + s for c, s in zip(x["ctx"], x["start"])]
+    return oracle.diff.decode(x["q"], x["k8"], x["ks"], x["v8"], x["vs"], rows, x["ctx"], x["lam"],
+                              **kw)
+
+
+def check(got, want, mass):
+    err = np.abs(got.astype(np.float64) - want)
+    assert np.all(np.isfinite(got))
+    worst = (err / np.maximum(mass, 1e-30)).max()
+    assert worst <= TOL, worst
+
+
+def bits(t):
+    return t.cpu().numpy().view(np.uint32)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+gpu = pytest.mark.gpu
+
+
+@gpu
+@pytest.mark.parametrize("B,M,Hq,Hkv,ctx", [
+    (1, 1, 2, 2, 1),                      # one key, one head
+    (1, 1, 8, 2, 2),
+    (3, 1, 8, 2, [31, 32, 33]),           # the 32-key block's edges
+    (3, 2, 6, 2, [127, 128, 129]),        # the 128-key span's edges, GQA 3
+    (4, 3, 8, 4, [511, 512, 513, 510]),   # the 512-key window's edges, drafts across it
+    (2, 8, 16, 2, [5, 700]),              # 8 columns, 64 rows per map
+    (2, 5, 32, 4, [1500, 1025]),
+    (1, 1, 32, 4, 5000),
+    (5, 1, 10, 2, [1, 2000, 64, 600, 3]),  # GQA 5
+    (2, 4, 64, 4, [300, 900]),            # 64 rows per map
+    (1, 1, 4, 2, 40000),                  # more than 64 windows
+])
+@pytest.mark.parametrize("per_row", [False, True])
+def test_matches_the_oracle(B, M, Hq, Hkv, ctx, per_row):
+    x = inputs(B, M, Hq, Hkv, ctx, seed=B * 1000 + M * 100 + Hq, per_row=per_row)
+    want, mass = expected(x)
+    check(run(x).cpu().numpy(), want, mass)
+
+
+@gpu
+@pytest.mark.parametrize("seed", range(6))
+def test_random_shapes(seed):
+    r = np.random.default_rng(77 + seed)
+    M, Hkv = int(r.integers(1, 9)), 2 * int(r.integers(1, 4))
+    g = int(r.choice([n for n in range(1, 17) if n * M <= 64]))
+    B = int(r.integers(1, 7))
+    ctx = np.exp(r.uniform(0, np.log(3000), B)).astype(np.int32)
+    x = inputs(B, M, g * Hkv, Hkv, np.maximum(ctx, 1), seed=seed, per_row=bool(seed % 2))
+    want, mass = expected(x, sm_scale=0.05)
+    check(run(x, sm_scale=0.05).cpu().numpy(), want, mass)
+
+
+@gpu
+def test_outlier_channels_and_large_scores():
+    x = inputs(2, 2, 16, 2, [700, 90], seed=5, outliers=True, q_gain=8.0)
+    want, mass = expected(x)
+    check(run(x).cpu().numpy(), want, mass)
+
+
+@gpu
+def test_zero_and_extreme_scales():
+    # rows of zeros (scale 0), rows with scales 2^-30 of the others and a query of
+    # zeros: the weights are then 1 / L each
+    x = inputs(2, 1, 8, 2, [600, 40], seed=6)
+    x["vs"][:, ::3] = 0
+    x["v8"][:, ::3] = 0
+    x["vs"][:, 1::3] *= np.float32(2.0 ** -30)
+    x["ks"][:, 5] = 0
+    x["q"][0, 0, 2:4] = 0
+    want, mass = expected(x)
+    check(run(x).cpu().numpy(), want, mass)
+
+
+@gpu
+def test_lam_zero_leaves_one_map_and_equal_maps_cancel():
+    import torch
+    x = inputs(2, 2, 8, 2, [200, 65], seed=7)
+    t = device(x)
+    t["lam"].zero_()
+    one = run(x, t)
+    x["lam"][:] = 0
+    want, mass = expected(x)
+    check(one.cpu().numpy(), want, mass)
+    # the same keys and queries on both maps, lam = 1: exactly zero
+    t["q"][:, :, 1::2] = t["q"][:, :, 0::2]
+    t["k8"][1::2], t["ks"][1::2] = t["k8"][0::2], t["ks"][0::2]
+    t["lam"].fill_(1.0)
+    assert torch.count_nonzero(run(x, t)) == 0
+
+
+@gpu
+@pytest.mark.parametrize("M,Hq,Hkv", [(4, 8, 2), (8, 16, 2), (3, 12, 2), (5, 32, 4)])
+def test_column_j_equals_a_single_column_call(M, Hq, Hkv):
+    x = inputs(3, M, Hq, Hkv, [510, 1300, 30], seed=8, per_row=True)
+    t = device(x)
+    full = run(x, t)
+    import int8_kv_decode_gb300 as K
+    for j in range(M):
+        col = K.decode_diff(t["q"][:, j:j + 1].contiguous(), t["k8"], t["ks"], t["v8"], t["vs"],
+                            t["start"], t["ctx"] + j, int(x["ctx"].max()) + j,
+                            t["lam"][:, j:j + 1].contiguous())
+        assert np.array_equal(bits(full[:, j:j + 1]), bits(col)), j
+
+
+@gpu
+def test_bytes_do_not_depend_on_the_batch():
+    x = inputs(40, 1, 16, 2, np.random.default_rng(1).integers(1, 2500, 40), seed=9)
+    t = device(x)
+    full = bits(run(x, t))
+    for b in (0, 7, 39):
+        y = dict(x, ctx=x["ctx"][b:b + 1])
+        one = run(y, {**t, "q": t["q"][b:b + 1], "start": t["start"][b:b + 1], "ctx": t["ctx"][b:b + 1]})
+        assert np.array_equal(full[b:b + 1], bits(one))
+    assert np.array_equal(full, bits(run(x, t)))
+
+
+@gpu
+@pytest.mark.parametrize("P", [32, 64, 256])
+@pytest.mark.parametrize("M,Hq,Hkv,ctx", [(1, 8, 2, [1, 33, 900]), (5, 32, 4, [700, 1, 64]),
+                                          (2, 64, 2, [2000, 513, 40])])
+def test_paged_equals_contiguous_bytes(P, M, Hq, Hkv, ctx):
+    import torch
+    import int8_kv_decode_gb300 as K
+    x = inputs(3, M, Hq, Hkv, ctx, seed=P)
+    t = device(x)
+    want = bits(run(x, t))
+    L = page_layout(x["ctx"], x["start"], M, P, seed=P)
+    kp, ksp, vp, vsp = paged_copy(L, t["k8"], t["ks"], t["v8"], t["vs"], seed=1)
+    bt = torch.from_numpy(L.block_table).cuda()
+    ws = K.alloc_diff_workspace(3, M, Hq, int(max(ctx)))
+    got = K.decode_diff_paged(t["q"], kp, ksp, vp, vsp, bt, P, t["ctx"], int(max(ctx)), t["lam"],
+                              workspace=ws)
+    assert np.array_equal(bits(got), want)
+    assert K.get_device_status(ws) == 0
+
+
+@gpu
+@pytest.mark.parametrize("M,Hq", [(1, 8), (4, 32)])
+def test_bad_sequences_give_nan_and_leave_the_others(M, Hq):
+    import int8_kv_decode_gb300 as K
+    x = inputs(5, M, Hq, 2, [100, 600, 40, 700, 9], seed=11)
+    t = device(x)
+    ws = K.alloc_diff_workspace(5, M, Hq, 700)
+    clean = run(x, t, workspace=ws).cpu().numpy()
+    assert K.get_device_status(ws) == 0
+    t["ctx"][0] = 0                       # no key
+    t["ctx"][2] = 701                     # above max_ctx
+    t["start"][4] = x["cap"] - 3          # past the cache
+    out = run(x, t, workspace=ws).cpu().numpy()
+    assert np.isnan(out[[0, 2, 4]]).all()
+    assert np.array_equal(out[[1, 3]].view(np.uint32), clean[[1, 3]].view(np.uint32))
+    assert K.get_device_status(ws) == K.DEVERR_BAD_SEQUENCE
+    assert K.get_device_status(ws) == 0
+
+
+@gpu
+def test_bad_table_entries_are_flagged():
+    import torch
+    import int8_kv_decode_gb300 as K
+    x = inputs(3, 1, 8, 2, [300, 700, 64], seed=12)
+    t = device(x)
+    L = page_layout(x["ctx"], x["start"], 1, 64, seed=2)
+    kp, ksp, vp, vsp = paged_copy(L, t["k8"], t["ks"], t["v8"], t["vs"])
+    bt = torch.from_numpy(L.block_table).cuda()
+    ws = K.alloc_diff_workspace(3, 1, 8, 700)
+
+    def go(table):
+        return K.decode_diff_paged(t["q"], kp, ksp, vp, vsp, table, 64, t["ctx"], 700, t["lam"],
+                                   workspace=ws).cpu().numpy()
+    clean = go(bt)
+    bad = bt.clone()
+    bad[1, 3], bad[1, 10] = L.n_pages, -7
+    out = go(bad)
+    assert np.array_equal(out[[0, 2]].view(np.uint32), clean[[0, 2]].view(np.uint32))
+    assert np.isfinite(out[1]).all()
+    assert K.get_device_status(ws) == K.DEVERR_BAD_PAGE
+    narrow = go(bt[:, :5].contiguous())
+    assert np.isnan(narrow[1]).all() and np.isfinite(narrow[[0, 2]]).all()
+    assert K.get_device_status(ws) == K.DEVERR_BAD_SEQUENCE
+
+
+@gpu
+def test_graph_replay_side_stream_and_two_calls_at_once():
+    import torch
+    import int8_kv_decode_gb300 as K
+    x, y = inputs(4, 2, 16, 2, [900, 30, 513, 64], seed=13), inputs(2, 1, 8, 2, [2000, 5], seed=14)
+    a, b = device(x), device(y)
+    wa, wb = bits(run(x, a)), bits(run(y, b))
+    ws = K.alloc_diff_workspace(4, 2, 16, 900)
+    out = torch.empty((4, 2, 8, 256), device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run(x, a, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(x, a, out=out, workspace=ws)
+    for _ in range(3):
+        out.zero_()
+        with torch.cuda.stream(s):        # another call, its own workspace, meanwhile
+            other = run(y, b)
+        g.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(bits(out), wa) and np.array_equal(bits(other), wb)
+    q2 = torch.randn_like(a["q"])         # new inputs in the captured buffers
+    a["q"].copy_(q2)
+    g.replay()
+    torch.cuda.synchronize()
+    assert np.array_equal(bits(out), bits(run(x, a)))
+
+
+@gpu
+def test_many_short_sequences():
+    r = np.random.default_rng(3)
+    x = inputs(3000, 1, 4, 2, r.integers(1, 40, 3000), seed=15)
+    t = device(x)
+    got = run(x, t).cpu().numpy()
+    pick = [0, 1, 1499, 2999]
+    rows = [np.arange(int(x["ctx"][b])) + x["start"][b] for b in pick]
+    want, mass = oracle.diff.decode(x["q"][pick], x["k8"], x["ks"], x["v8"], x["vs"], rows,
+                                    x["ctx"][pick], x["lam"])
+    check(got[pick], want, mass)
+
+
+@gpu
+def test_offsets_past_32_bits():
+    # a cache of 2^24 + rows per plane: byte offsets of plane 1 pass 2^31, the
+    # sequence sits at the very end
+    import torch
+    import int8_kv_decode_gb300 as K
+    x = inputs(1, 1, 4, 2, [700], seed=16)
+    want = bits(run(x))
+    t = device(x)
+    cap = (1 << 24) + 4096
+    big = {n: torch.zeros((2, cap, 128), dtype=torch.int8, device="cuda") for n in ("k8", "v8")}
+    big.update({n: torch.zeros((2, cap), device="cuda") for n in ("ks", "vs")})
+    for n in big:
+        big[n][:, cap - 700:] = t[n][:, :700]
+    got = K.decode_diff(t["q"], big["k8"], big["ks"], big["v8"], big["vs"], t["start"] + (cap - 700),
+                        t["ctx"], 700, t["lam"])
+    assert np.array_equal(bits(got), want)
