@@ -450,11 +450,14 @@ def diff_workspace_size(B: int, M: int, Hq: int, max_ctx: int) -> int:
 
 
 def alloc_diff_workspace(B: int, M: int, Hq: int, max_ctx: int, device="cuda") -> torch.Tensor:
-    """A zeroed workspace for decode_diff (allocated by torch, not the library)."""
+    """A workspace for decode_diff with its header zeroed (allocated by torch, not
+    the library)."""
     n = diff_workspace_size(B, M, Hq, max_ctx)
     if n == 0:
         raise ValueError("invalid sizes for a differential decode workspace")
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
 
 
 def _diff_args(q, k, k_scale, v, v_scale, ctx_len, max_ctx, lam, out, workspace, extra):
@@ -502,8 +505,9 @@ def decode_diff(q, k, k_scale, v, v_scale, row_start, ctx_len, max_ctx: int, lam
     two maps come from query heads 2i, 2i+1 and key planes 2p, 2p+1, its V is
     the 256 channels of value planes 2p, 2p+1, with p = i // (Hq / Hkv).
     lam: float32 [Hq/2], or [B][M][Hq/2] for one value per row.  q and the cache
-    as in decode(); Hkv even.  workspace: a zeroed uint8 tensor of
-    diff_workspace_size(...) bytes, allocated here with torch if None.
+    as in decode(); Hkv even.  workspace: a uint8 tensor of
+    diff_workspace_size(...) bytes, its first 256 zeroed before its first use,
+    allocated here with torch if None.
     (kattn_decode_diff)
     """
     B, M, Hq, Hkv, d, cap, per_row, out, workspace = _diff_args(

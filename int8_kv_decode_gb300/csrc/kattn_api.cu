@@ -204,11 +204,8 @@ int run_diff(DiffParams& p, const float* q, const int8_t* k, const float* k_scal
   p.pairs = Hkv / 2;
   p.cap_rows = cap_rows;
   p.max_ctx = max_ctx;
-  p.nwin_max = nsplit_for(max_ctx + M - 1);
   p.sm_scale = resolve_sm_scale(sm_scale, KATTN_HEAD_DIM);
-  // work units (8 rows of a window and plane pair) are counted in int32
-  if ((int64_t)B * p.nwin_max * p.pairs * ((p.R + 7) / 8) > (int64_t)INT32_MAX / 4)
-    return KATTN_ERR_UNSUPPORTED;
+  if (diff_units(p) > (int64_t)INT32_MAX / 4) return KATTN_ERR_UNSUPPORTED;   // counted in int32
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < diff_workspace_bytes(B, M, Hq, max_ctx))
     return KATTN_ERR_WORKSPACE;

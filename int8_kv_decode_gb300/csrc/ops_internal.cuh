@@ -28,6 +28,7 @@ struct DiffParams {
   int nwin_max;                 // windows of the longest sequence
   float sm_scale;
 };
+int64_t diff_units(const DiffParams& p);          // work units, at most
 size_t diff_workspace_bytes(int B, int M, int Hq, int max_ctx);
 void set_diff_workspace(DiffParams& p, void* workspace);
 cudaError_t launch_decode_diff(const DiffParams& p, cudaStream_t stream);
