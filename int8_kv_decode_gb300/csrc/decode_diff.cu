@@ -17,33 +17,64 @@
 namespace kattn {
 namespace {
 
-// Every warp works on its own: it takes a unit (sequence, window, plane pair,
-// row group), streams the window's rows through its own ring and writes the
-// window's partial.  No warp waits for another, so a stall of one is covered by
-// the others.  Windows sit at fixed key positions, so the bytes of a row depend
-// on its own keys alone.
+// ------------------------------------------------------------------ split
+// Two warps work on a unit (sequence, window, plane pair, row group).  Warp a
+// owns map a and plane a: it streams the rows of key plane 2p + a and value
+// plane 2p + a through its own ring, scores its key plane and takes the softmax
+// weights of map a; the two exchange their weights through shared memory, once
+// per block; then each sums its 128 value channels for both maps, so every
+// value is converted to f16 once.  (One warp for both planes takes 255
+// registers, 8 warps an SM: 193 us on the serving case against this form's
+// 12 warps.)  The pairs do not wait for one another.  Windows sit at fixed key
+// positions, so the bytes of a row depend on its own keys alone.
 constexpr int kWindow = 256;
 constexpr int kWinBlocks = kWindow / kBlockBk;    // 8: lane e < 8 holds the row of block e
-constexpr int kWarps = 4;
-constexpr int kStageBytes = 2 * kBlockBytes;      // the K (or V) rows of both planes of a block
-constexpr int kMaxGroups = 512;                   // entries of the prefix over sequences
+constexpr int kPairs = 2;                         // pairs of warps in a block
+constexpr int kThreads = kPairs * 64;
+constexpr int kStages = 3;                        // 4 KB each: K, V, K, V, ... of one plane
+constexpr uint32_t kLastStage = (kStages - 1) * kBlockBytes;
+constexpr int kMaxGroups = 256;                   // entries of the prefix over sequences
 constexpr int kQStride = kD + 16;                 // bytes between query rows (spread over banks)
+// The running maximum that the weights refer to moves only when a block's maximum
+// exceeds it by more than kLag: most blocks then rescale nothing.  Weights stay
+// below e^kLag < 2^6.
+constexpr float kLag = 4.0f;
 
 __host__ __device__ inline int diff_windows(int keys) { return (keys + kWindow - 1) / kWindow; }
 __host__ __device__ inline int diff_stride(int R) { return 2 * R * (2 * kD + 2); }   // floats
 
-// Tiles of 8 query rows: T = 2, one tile per map; T = 1, up to 4 rows, those of
-// map 0 in rows 0..3 of the tile and those of map 1 in rows 4..7.
+// What the warps of a pair hand over per block: the weights of both maps, as the
+// second product's operand takes them (two keys of a row side by side), and the
+// factors of the rows where a reference moved (kMoved).
+template <int T>
+struct Exchange {
+  float w[T][kBlockBk / 2][8][2];
+  float alpha[2][8];                              // of each map's rows
+  int info[2];                                    // per warp: kFailed | kMoved
+};
+constexpr int kFailed = 1, kMoved = 2;
+
+struct DiffItem {
+  int b, pair, w, rg, ctx, row0;                  // b < 0: none
+};
+
 template <int T>
 struct __align__(1024) DiffSmem {
-  static constexpr int kStages = T == 1 ? 2 : 3;
-  uint8_t ring[kWarps][kStages][kStageBytes];
-  float scale[kWarps][4][kBlockBk];               // ks of both planes, vs of both planes
-  uint8_t q[kWarps][T * 8 * kQStride];
-  float qs[kWarps][T * 8];
-  uint64_t full[kWarps][kStages];
+  static constexpr int kExBytes = (int)sizeof(Exchange<T>);
+  uint8_t ring[kPairs][2][kStages][kBlockBytes];
+  alignas(16) Exchange<T> ex[kPairs][2];                      // by block parity
+  alignas(16) float vs[kPairs][2][kBlockBk];                  // v_scale of the block
+  float row_sum[kPairs][2][8];                    // of a sequence that ends in its window
+  // What a warp needs once per block or item is kept here, not in registers (the
+  // accumulators take half of the 128 that four blocks an SM leave a thread).
+  alignas(16) uint8_t q[kPairs][2][8 * kQStride];
+  float qs[kPairs][2][8];
+  float up[kPairs][2][8];                         // 2^E of the operand's rows
+  DiffItem item[kPairs][2][2];                    // the current and the next, by parity
+  uint64_t full[kPairs][2][kStages];
   int prefix[kMaxGroups + 1];
-  int warp_total[kWarps];
+  int ctx[kMaxGroups], row0[kMaxGroups];          // of each sequence (up to kMaxGroups)
+  int warp_total[kThreads / 32];
 };
 
 __device__ __forceinline__ bool diff_valid(const DiffParams& p, int b, int ctx) {
@@ -53,16 +84,17 @@ __device__ __forceinline__ bool diff_valid(const DiffParams& p, int b, int ctx) 
   return ((keys + (1 << p.page_shift) - 1) >> p.page_shift) <= (int64_t)p.max_pages;
 }
 
-struct DiffItem {
-  int b, pair, w, rg, ctx, row0;                  // b < 0: none
-};
-
-// Row (in a plane) of block e = lane of the item's window; lanes past the window hold 0.
-__device__ __forceinline__ int block_row(const DiffParams& p, const DiffItem& it, int lane) {
+// Row (in a plane) of block e = lane of the item's window, in two steps: the
+// table entry is loaded well before it is looked at.  Lanes past the window hold 0.
+__device__ __forceinline__ int row_entry(const DiffParams& p, const DiffItem& it, int lane) {
   const int key = it.w * kWindow + lane * kBlockBk;
   if (it.b < 0 || lane >= kWinBlocks || key >= it.ctx + p.M - 1) return 0;
   if (p.block_table == nullptr) return it.row0 + key;
-  int page = __ldg(p.block_table + (int64_t)it.b * p.max_pages + (key >> p.page_shift));
+  return __ldg(p.block_table + (int64_t)it.b * p.max_pages + (key >> p.page_shift));
+}
+__device__ __forceinline__ int row_of_entry(const DiffParams& p, const DiffItem& it, int page, int lane) {
+  if (p.block_table == nullptr) return page;
+  const int key = it.w * kWindow + lane * kBlockBk;
   if ((unsigned)page >= (unsigned)p.n_pages) {
     atomicOr(p.err_word, KATTN_DEVERR_BAD_PAGE);
     page = 0;
@@ -70,42 +102,123 @@ __device__ __forceinline__ int block_row(const DiffParams& p, const DiffItem& it
   return (page << p.page_shift) | (key & ((1 << p.page_shift) - 1));
 }
 
-// Online-softmax update of one tile over a block; s0 / s1 hold the scores of the
-// two 16-key halves in the MMA layout and return the weights.
-__device__ __forceinline__ void diff_softmax(float (&s0)[4], float (&s1)[4], float (&m_run)[2],
-                                             float (&l_run)[2], float (&alpha)[2], bool& rescale) {
-  float mnew[2];
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p));
+}
+
+// warp_quantize_row's result for a row already loaded (lane: elements 4 lane ..),
+// without its four divisions: x * (1 / s) is off by less than 3.1e-5 (|x / s| <=
+// 127; 1/s, the product and the quotient's own rounding 2^-24 each), so its
+// nearest integer is that of the division unless it lies closer than 1e-4 to a
+// half; those, and scales whose reciprocal may overflow, divide.
+__device__ __forceinline__ uint32_t quantize_loaded_row(float4 x, float* scale_out) {
+  const float amax = warp_max(fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
+  const float s = quant_scale(amax);
+  *scale_out = s;
+  const float inv = __frcp_rn(s);
+  const float magic = 12582912.0f;                // 1.5 * 2^23: the sum's low byte is the integer
+  const float t[4] = {__fmul_rn(x.x, inv), __fmul_rn(x.y, inv), __fmul_rn(x.z, inv), __fmul_rn(x.w, inv)};
+  uint32_t r[4];
+  float far = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    float bm = fmaxf(fmaxf(s0[e], s0[2 + e]), fmaxf(s1[e], s1[2 + e]));
-    bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
-    bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
-    bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 16));
-    mnew[e] = fmaxf(m_run[e], bm);
+  for (int i = 0; i < 4; ++i) {
+    const float y = __fadd_rn(t[i], magic);
+    far = fmaxf(far, fabsf(__fsub_rn(t[i], __fsub_rn(y, magic))));
+    r[i] = __float_as_uint(y);
   }
-  const float2 l2e = make_float2(kLog2e, kLog2e);
-  const float2 mn = make_float2(mnew[0], mnew[1]);
-  const bool live0 = mnew[0] != -INFINITY, live1 = mnew[1] != -INFINITY;
-  const float2 da = f2_mul(f2_sub(make_float2(m_run[0], m_run[1]), mn), l2e);
-  alpha[0] = live0 ? fast_exp2(da.x) : 1.0f;
-  alpha[1] = live1 ? fast_exp2(da.y) : 1.0f;
-  rescale |= (alpha[0] != 1.0f) | (alpha[1] != 1.0f);
-  m_run[0] = mnew[0];
-  m_run[1] = mnew[1];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const float2 d0 = f2_mul(f2_sub(make_float2(s0[2 * k], s0[2 * k + 1]), mn), l2e);
-    const float2 d1 = f2_mul(f2_sub(make_float2(s1[2 * k], s1[2 * k + 1]), mn), l2e);
-    s0[2 * k] = live0 ? fast_exp2(d0.x) : 0.0f;
-    s0[2 * k + 1] = live1 ? fast_exp2(d0.y) : 0.0f;
-    s1[2 * k] = live0 ? fast_exp2(d1.x) : 0.0f;
-    s1[2 * k + 1] = live1 ? fast_exp2(d1.y) : 0.0f;
+  if (far > 0.4999f || !(s > 1e-30f))
+    return pack_i8x4(quant_one(x.x, s), quant_one(x.y, s), quant_one(x.z, s), quant_one(x.w, s));
+  return __byte_perm(__byte_perm(r[0], r[1], 0x0040u), __byte_perm(r[2], r[3], 0x0040u), 0x5410u);
+}
+
+// Shared memory by 32-bit address and immediate offset: the block loop's addresses
+// are lane constants plus a stage or buffer offset.
+template <int kOff>
+__device__ __forceinline__ uint4 lds128a(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4+%5];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr), "n"(kOff)
+               : "memory");
+  return v;
+}
+template <int kOff>
+__device__ __forceinline__ float2 lds64a(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2+%3];\n"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(addr), "n"(kOff)
+               : "memory");
+  return v;
+}
+template <int kOff>
+__device__ __forceinline__ float lds32a(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1+%2];\n" : "=f"(v) : "r"(addr), "n"(kOff) : "memory");
+  return v;
+}
+template <int kOff>
+__device__ __forceinline__ void sts32(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0+%1], %2;\n" ::"r"(addr), "n"(kOff), "f"(v) : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t addr, float2 v) {
+  asm volatile("st.shared.v2.f32 [%0], {%1,%2};\n" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit elements, transposed: thread (g, c) gets elements
+// [rows 2c, 2c + 1][column g] of matrix i in r[i]; lane 8 i + r gives the address
+// of row r of matrix i.
+template <int kOff>
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4+%5];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr), "n"(kOff)
+               : "memory");
+}
+
+// kBlockBk rows of a plane into a stage, 128-byte swizzle.
+__device__ __forceinline__ void load_stage(uint32_t dst, const CUtensorMap* map, int row,
+                                           uint32_t bar, uint64_t policy) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar),
+               "r"((uint32_t)kBlockBytes)
+               : "memory");
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3}], [%4], %5;\n" ::"r"(dst), "l"(map), "r"(0), "r"(row), "r"(bar),
+      "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ bool bar_try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// Whether the stage's copy landed, for the whole warp; the wait is bounded.
+__device__ __forceinline__ bool stage_ready(uint32_t bar, uint32_t parity) {
+  for (uint32_t it = 0; it < kSpinLimit; ++it)
+    if (__all_sync(0xffffffffu, bar_try_wait(bar, parity))) return true;
+  return false;
+}
+
+// The row's reference moves to the block's maximum bm where that exceeds its
+// threshold; alpha: the factor of what is summed up so far.
+__device__ __forceinline__ void move_reference(float bm, float& m_run, float& m_move, float& alpha) {
+  if (bm > m_move) {
+    const float m = __fmul_rn(bm, kLog2e);
+    // (nothing is summed up yet where the threshold was -inf)
+    if (m_move != -INFINITY) alpha = fast_exp2(__fsub_rn(m_run, m));
+    m_run = m;
+    m_move = __fadd_rn(bm, kLag);
   }
-  const float2 sum = f2_add(f2_add(make_float2(s0[0], s0[1]), make_float2(s0[2], s0[3])),
-                            f2_add(make_float2(s1[0], s1[1]), make_float2(s1[2], s1[3])));
-  const float2 l = f2_fma(make_float2(l_run[0], l_run[1]), make_float2(alpha[0], alpha[1]), sum);
-  l_run[0] = l.x;
-  l_run[1] = l.y;
 }
 
 // out = o_0 / l_0 - lam * (o_1 / l_1), each operation rounded on its own, here and
@@ -114,21 +227,22 @@ __device__ __forceinline__ float diff_out(float o0, float l0, float o1, float l1
   return __fsub_rn(__fdiv_rn(o0, l0), __fmul_rn(lam, __fdiv_rn(o1, l1)));
 }
 
+// T: tiles of 8 query rows on the value side.  T = 2: 8 rows of each map, a tile
+// per map.  T = 1: 4 rows of each map in one tile, map 0 in rows 0..3.
 template <int T>
-__global__ void __launch_bounds__(kWarps * 32, T == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, 3)
 diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
   using Smem = DiffSmem<T>;
-  constexpr int kStages = Smem::kStages;
-  constexpr int kRows = T * 8;
   constexpr int kUnitRows = T == 1 ? 4 : 8;       // rows of each map in a unit
   extern __shared__ unsigned char smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int wp = warp >> 1, a = warp & 1;         // the pair of warps; the warp's map and plane
   const int g = lane >> 2, c = lane & 3;
   const int M = p.M, R = p.R, H = p.Hq / 2;
   const int nrg = (R + kUnitRows - 1) / kUnitRows;
-  uint64_t* full = sm.full[warp];
+  uint64_t* full = sm.full[wp][a];
   if (lane == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -138,19 +252,20 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
   const int gs = (p.B + kMaxGroups - 1) / kMaxGroups;
   const int ng = (p.B + gs - 1) / gs;
   const int per_win = p.pairs * nrg;
-  auto units_of = [&](int b) -> int {
-    const int ctx = p.ctx_len[b];
+  auto units_of = [&](int b, int ctx) -> int {
     return diff_valid(p, b, ctx) ? diff_windows(ctx + M - 1) * per_win : 0;
   };
-  for (int i = tid; i < kMaxGroups; i += kWarps * 32) {
-    int n = 0;
+  for (int i = tid; i < kMaxGroups; i += kThreads) {
+    int n = 0, ctx = 0;
     if (i < ng)
-      for (int b = i * gs; b < min(p.B, i * gs + gs); ++b) n += units_of(b);
+      for (int b = i * gs; b < min(p.B, i * gs + gs); ++b) n += units_of(b, ctx = p.ctx_len[b]);
     sm.prefix[i] = n;
+    sm.ctx[i] = ctx;
+    sm.row0[i] = gs == 1 && i < ng && p.block_table == nullptr ? (int)p.row_start[i] : 0;
   }
   __syncthreads();
   {
-    constexpr int kPer = kMaxGroups / (kWarps * 32);
+    constexpr int kPer = kMaxGroups / kThreads;
     int n[kPer], run = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -167,28 +282,28 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
     __syncthreads();
     int base = incl - run;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
+    for (int w = 0; w < kThreads / 32; ++w)
       if (w < warp) base += sm.warp_total[w];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       sm.prefix[tid * kPer + i] = base;
       base += n[i];
     }
-    if (tid == kWarps * 32 - 1) sm.prefix[kMaxGroups] = base;
+    if (tid == kThreads - 1) sm.prefix[kMaxGroups] = base;
   }
   // ---- the rows of sequences that break the rules
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     if (diff_valid(p, b, p.ctx_len[b])) continue;
     float* o = p.out + (int64_t)b * M * H * 2 * kD;
-    for (int64_t i = tid; i < (int64_t)M * H * 2 * kD; i += kWarps * 32)
+    for (int64_t i = tid; i < (int64_t)M * H * 2 * kD; i += kThreads)
       o[i] = __int_as_float(0x7fc00000);
     if (tid == 0) atomicOr(p.err_word, KATTN_DEVERR_BAD_SEQUENCE);
   }
   __syncthreads();
   griddep_launch_dependents();
   const int total = sm.prefix[kMaxGroups];
-  const int G = gridDim.x * kWarps;
-  int t = warp * gridDim.x + blockIdx.x;          // neighbouring units on different SMs
+  const int G = gridDim.x * kPairs;
+  int t = wp * gridDim.x + blockIdx.x;            // neighbouring units on different SMs
   if (t >= total) return;
 
   auto find = [&](int u) -> DiffItem {
@@ -200,16 +315,21 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
       if (sm.prefix[mid] <= u) lo = mid;
       else hi = mid;
     }
-    int r = u - sm.prefix[lo], b = lo * gs;
-    if (gs > 1)
-      for (int n; r >= (n = units_of(b)); ++b) r -= n;
-    it.b = b;
+    int r = u - sm.prefix[lo];
+    it.b = lo;
+    it.ctx = sm.ctx[lo];
+    it.row0 = sm.row0[lo];
+    if (gs > 1) {
+      int b = lo * gs;
+      for (int n; r >= (n = units_of(b, p.ctx_len[b])); ++b) r -= n;
+      it.b = b;
+      it.ctx = p.ctx_len[b];
+      it.row0 = p.block_table ? 0 : (int)p.row_start[b];
+    }
     it.w = r / per_win;
     r -= it.w * per_win;
     it.pair = r / nrg;
     it.rg = r - it.pair * nrg;
-    it.ctx = p.ctx_len[b];
-    it.row0 = p.block_table ? 0 : (int)p.row_start[b];
     return it;
   };
   auto blocks_of = [&](const DiffItem& it) -> int {
@@ -217,378 +337,371 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
     return (n + kBlockBk - 1) / kBlockBk;
   };
 
-  DiffItem it0 = find(t), it1 = find(t + G);
-  int row0 = block_row(p, it0, lane), row1 = block_row(p, it1, lane);
+  // rr / g and the query head of unit row rr (rr < 64, g <= 64: exact)
+  const uint32_t ginv = 65536u / (uint32_t)p.g + 1u;
+  auto column = [&](int rr) -> int { return (int)(((uint32_t)rr * ginv) >> 16); };
+
+  DiffItem* items = sm.item[wp][a];
+  int ipar = 0;                                   // parity of the current item
+  auto put = [&](int par, int u) {                // unit u into slot par
+    const DiffItem it = find(u);
+    __syncwarp();
+    if (lane == 0) items[par] = it;
+    __syncwarp();
+  };
+  put(0, t);
+  put(1, t + G);
+  int row0 = row_of_entry(p, items[0], row_entry(p, items[0], lane), lane);
+  int row1 = row_entry(p, items[1], lane);        // an entry until the producer reaches it
 
   // ---- producer: lane 0 issues, every lane keeps the same counters.  Stages
   // go K, V, K, V, ... over this item's blocks, then the next item's.
-  int pnext = 0, pblk = 0, pv = 0, ist = 0, inflight = 0;
-  int pn = blocks_of(it0);
-  const uint64_t policy = nrg > 1 ? l2_evict_normal() : l2_evict_first();
-  auto produce = [&]() {
-    while (inflight < kStages) {
-      if (pblk >= pn) {
-        if (pnext || it1.b < 0) break;
-        pnext = 1;
-        pblk = 0;
-        pn = blocks_of(it1);
-      }
-      const int pair = pnext ? it1.pair : it0.pair;
-      const int row = __shfl_sync(0xffffffffu, pnext ? row1 : row0, pblk) + 2 * pair * p.cap_rows;
-      if (lane == 0) {
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-        mbar_expect_tx(&full[ist], kStageBytes);
-        const CUtensorMap* map = pv ? &maps.v : &maps.k;
-        tma_load_block(sm.ring[warp][ist], map, row, &full[ist], policy);
-        tma_load_block(sm.ring[warp][ist] + kBlockBytes, map, row + p.cap_rows, &full[ist], policy);
-      }
-      pblk += pv;
-      pv ^= 1;
-      ++inflight;
-      ist = ist + 1 == kStages ? 0 : ist + 1;
+  const uint32_t ringb = smem_u32(sm.ring[wp][a][0]), fullb = smem_u32(full);
+  bool pnext = false;
+  int ps = 0, pend = 2 * blocks_of(items[0]), inflight = 0;
+  uint32_t ist = 0;                               // stage to fill, as a byte offset
+  int prow = row0 + (2 * items[0].pair + a) * p.cap_rows;
+  auto reach_next = [&]() {                       // the producer comes to the next item
+    const DiffItem& it = items[ipar ^ 1];
+    row1 = row_of_entry(p, it, row1, lane);
+    ps = 0;
+    pend = 2 * blocks_of(it);
+    prow = row1 + (2 * it.pair + a) * p.cap_rows;
+    if (2 * lane < pend) {                        // its scales, read at its start
+      prefetch_l2(p.k_scale + prow);
+      prefetch_l2(p.v_scale + prow);
     }
   };
-  int cst = 0;
-  uint32_t cph = 0;
+  const uint64_t policy = nrg > 1 ? l2_evict_normal() : l2_evict_first();
+  auto produce = [&]() -> bool {
+    if (ps == pend) {
+      if (pnext || items[ipar ^ 1].b < 0) return false;
+      pnext = true;
+      reach_next();
+    }
+    const int row = __shfl_sync(0xffffffffu, prow, ps >> 1);
+    if (lane == 0) {
+      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+      load_stage(ringb + ist, ps & 1 ? &maps.v : &maps.k, row, fullb + (ist >> 9), policy);
+    }
+    ++ps;
+    ++inflight;
+    ist = ist == kLastStage ? 0 : ist + kBlockBytes;
+    return true;
+  };
+  auto fill = [&]() {
+    while (inflight < kStages && produce()) {
+    }
+  };
+  uint32_t cst = 0, cph = 0;                      // stage to read (byte offset), its parity
   auto consumed = [&]() {
     __syncwarp();
     --inflight;
-    if (++cst == kStages) {
-      cst = 0;
-      cph ^= 1u;
-    }
+    cph ^= cst == kLastStage ? 1u : 0u;
+    cst = cst == kLastStage ? 0 : cst + kBlockBytes;
     produce();
   };
-  produce();
+  fill();
+  bool failed = false;                            // a copy of this warp never arrived
+  // ---- shared-memory addresses of this lane
+  const uint32_t exbase = smem_u32(&sm.ex[wp][0]);
+  uint32_t lex = exbase;                          // exchange buffer of the next block
+  constexpr int kExAlpha = T * 1024, kExInfo = kExAlpha + 64;
+  const uint32_t lk = (uint32_t)swz(g, 2 * c);    // K: rows g, g + 8, ... share the swizzle
+  const uint32_t lv = (uint32_t)((lane & 15) * kD + (((lane >> 4) ^ (lane & 7)) << 4));
+  const uint32_t lvs = smem_u32(sm.vs[wp][a]);
+  const uint32_t lq = smem_u32(&sm.q[wp][a][g * kQStride + 32 * c]);
+  const uint32_t lqs = smem_u32(&sm.qs[wp][a][2 * c]), lup = smem_u32(&sm.up[wp][a][g]);
+  const uint32_t lww = (T == 1 ? 0 : 1024 * a) + ((g >> 1) * 8 + (T == 1 ? 4 * a : 0) + 2 * c) * 8 + (g & 1) * 4;
+  const uint32_t lwr = (c * 8 + g) * 8;
 
   for (;;) {
+    const DiffItem& it0 = items[ipar];
     const int ctx = it0.ctx, s0 = it0.w * kWindow, s1 = min(s0 + kWindow, ctx + M - 1);
-    const int64_t plane = (int64_t)2 * it0.pair * p.cap_rows;
-    const float* ksp = p.k_scale + plane;
-    const float* vsp = p.v_scale + plane;
-    // scales of the window: the values of block 0, and the largest v_scale of
-    // each plane over the keys that every row sees
-    float nx[4], vm[2] = {0.0f, 0.0f};
+    const int plane = (2 * it0.pair + a) * p.cap_rows;
+    // ---- the unit's queries of map a, quantized per row, and the plane's scales:
+    // those of block 0, and the largest v_scale among the keys that every row sees
+    float4 x[kUnitRows];
+#pragma unroll
+    for (int r = 0; r < kUnitRows; ++r) {
+      const int rr = min(it0.rg * kUnitRows + r, R - 1);
+      const int j = column(rr), head = 2 * (it0.pair * p.g + rr - j * p.g) + a;
+      x[r] = __ldg(reinterpret_cast<const float4*>(
+                       p.q + (((int64_t)it0.b * M + j) * p.Hq + head) * kD) + lane);
+    }
+    float nk, nv, vm = 0.0f;                      // scales of the next block's key `lane`
 #pragma unroll
     for (int e = 0; e < kWinBlocks; ++e) {
       const int row = __shfl_sync(0xffffffffu, row0, e) + lane, key = s0 + 32 * e + lane;
-      if (key < s1) {
-        const float a = __ldg(vsp + row), b = __ldg(vsp + p.cap_rows + row);
-        if (key < ctx) {
-          vm[0] = fmaxf(vm[0], a);
-          vm[1] = fmaxf(vm[1], b);
-        }
-        if (e == 0) {
-          nx[2] = a;
-          nx[3] = b;
-        }
-      } else if (e == 0) {
-        nx[2] = nx[3] = 0.0f;
-      }
+      const float v = key < s1 ? __ldg(p.v_scale + plane + row) : 0.0f;
+      if (key < ctx) vm = fmaxf(vm, v);
       if (e == 0) {
-        nx[0] = key < s1 ? __ldg(ksp + row) : 0.0f;
-        nx[1] = key < s1 ? __ldg(ksp + p.cap_rows + row) : 0.0f;
+        nv = v;
+        nk = key < s1 ? __ldg(p.k_scale + plane + row) : 0.0f;
       }
     }
-    // ---- the unit's queries, quantized per row
-    __syncwarp();
-#pragma unroll 4
-    for (int r = 0; r < kRows; ++r) {
-      const int a = T == 1 ? r >> 2 : r >> 3;
-      const int rr = it0.rg * kUnitRows + (T == 1 ? r & 3 : r & 7);
-      uint32_t w = 0;
-      float s = 0.0f;
-      if (rr < R) {
-        const int j = rr / p.g, head = 2 * (it0.pair * p.g + rr % p.g) + a;
-        w = warp_quantize_row(p.q + (((int64_t)it0.b * M + j) * p.Hq + head) * kD, &s);
-      }
-      *reinterpret_cast<uint32_t*>(&sm.q[warp][r * kQStride + 4 * lane]) = w;
-      if (lane == 0) sm.qs[warp][r] = s;
-    }
-    __syncwarp();
-    uint32_t qw[T][8];
-    float qsr[T][2];
 #pragma unroll
-    for (int n = 0; n < T; ++n) {
-      const uint4* src = reinterpret_cast<const uint4*>(&sm.q[warp][(n * 8 + g) * kQStride + 32 * c]);
-      const uint4 lo = src[0], hi = src[1];
-      qw[n][0] = lo.x; qw[n][1] = lo.y; qw[n][2] = lo.z; qw[n][3] = lo.w;
-      qw[n][4] = hi.x; qw[n][5] = hi.y; qw[n][6] = hi.z; qw[n][7] = hi.w;
-      qsr[n][0] = sm.qs[warp][n * 8 + 2 * c];
-      qsr[n][1] = sm.qs[warp][n * 8 + 2 * c + 1];
+    for (int r = 0; r < kUnitRows; ++r) {
+      float s;
+      const uint32_t w = quantize_loaded_row(x[r], &s);
+      const bool in = it0.rg * kUnitRows + r < R;
+      *reinterpret_cast<uint32_t*>(&sm.q[wp][a][r * kQStride + 4 * lane]) = in ? w : 0u;
+      if (lane == 0) sm.qs[wp][a][r] = in ? s : 0.0f;
     }
-    // Draft column of tile rows 2c + e; the rows of both maps share it.
-    int L[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int rr = it0.rg * kUnitRows + (T == 1 ? (2 * c + e) & 3 : 2 * c + e);
-      L[e] = ctx + min(rr / p.g, M - 1);
-    }
-    // Power of two 2^E per plane and row: the largest v_scale among the window's
-    // keys that the row sees, times 2^E, lies in [2^14, 2^15), so that a = p *
-    // v_scale * 2^E stays in f16's normal range down to weights that do not
-    // matter.  upb: of row g (the operand's row); down: 2^-E of rows 2c + e.
-    float upb[2], down[2][2];
+    // Draft column of unit row r of the tile (T = 1: rows 4..7 are those of map 1).
+    auto keys_of = [&](int r) -> int {
+      return ctx + column(min(it0.rg * kUnitRows + (T == 1 ? r & 3 : r), R - 1));
+    };
+    // Power of two 2^E per row: the largest v_scale among the window's keys that
+    // the row sees, times 2^E, lies in [2^8, 2^9), so that w * v_scale * 2^E stays
+    // below 2^15 and, down to weights that do not matter, in f16's normal range.
     {
-      float vmax[2][2];
-#pragma unroll
-      for (int pl = 0; pl < 2; ++pl) vmax[pl][0] = vmax[pl][1] = warp_max(vm[pl]);
+      const int r = lane & 7, keys = keys_of(r);  // lane r < 8: row r
+      float vmax = warp_max(vm);
       for (int key = max(ctx, s0); key < s1; ++key) {    // draft keys
         const int row = __shfl_sync(0xffffffffu, row0, (key - s0) >> 5) + ((key - s0) & 31);
-#pragma unroll
-        for (int pl = 0; pl < 2; ++pl) {
-          const float v = __ldg(vsp + pl * (int64_t)p.cap_rows + row);
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (key < L[e]) vmax[pl][e] = fmaxf(vmax[pl][e], v);
-        }
+        const float v = __ldg(p.v_scale + plane + row);
+        if (key < keys) vmax = fmaxf(vmax, v);
       }
-#pragma unroll
-      for (int pl = 0; pl < 2; ++pl) {
-        float up[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int bexp = min(max(268 - (int)((__float_as_uint(vmax[pl][e]) >> 23) & 0xffu), 1), 253);
-          up[e] = __uint_as_float((uint32_t)bexp << 23);
-          down[pl][e] = __uint_as_float((uint32_t)(254 - bexp) << 23);
-        }
-        const float u0 = __shfl_sync(0xffffffffu, up[0], g >> 1);
-        const float u1 = __shfl_sync(0xffffffffu, up[1], g >> 1);
-        upb[pl] = (g & 1) ? u1 : u0;
-      }
+      const int bexp = min(max(262 - (int)((__float_as_uint(vmax) >> 23) & 0xffu), 1), 253);
+      if (lane < 8) sm.up[wp][a][r] = __uint_as_float((uint32_t)bexp << 23);
     }
+    __syncwarp();
 
-    float m_run[T][2], l_run[T][2];
-    float o[2][8][T][4];                          // [plane][m-tile][tile]
+    // Of rows 2c + e: the reference in base 2 (m), the score above which it moves,
+    // and the sum of this thread's weights.
+    float2 m_run = make_float2(0.0f, 0.0f), m_move = make_float2(-INFINITY, -INFINITY);
+    float2 l_run = make_float2(0.0f, 0.0f);
+    float o[8][T][4];                             // [m-tile of 16 channels][tile]
 #pragma unroll
-    for (int n = 0; n < T; ++n)
+    for (int md = 0; md < 8; ++md)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        m_run[n][e] = -INFINITY;
-        l_run[n][e] = 0.0f;
-      }
+      for (int n = 0; n < T; ++n)
 #pragma unroll
-    for (int pl = 0; pl < 2; ++pl)
-#pragma unroll
-      for (int md = 0; md < 8; ++md)
-#pragma unroll
-        for (int n = 0; n < T; ++n)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) o[pl][md][n][u] = 0.0f;
+        for (int u = 0; u < 4; ++u) o[md][n][u] = 0.0f;
 
     const int nb = blocks_of(it0);
-    bool failed = false;
     for (int i = 0; i < nb; ++i) {
       const int t0 = s0 + i * kBlockBk;
-      __syncwarp();
+      float ks4[4];                               // k_scale of keys g + 8q
 #pragma unroll
-      for (int k = 0; k < 4; ++k) sm.scale[warp][k][lane] = nx[k];
+      for (int q = 0; q < 4; ++q) ks4[q] = __shfl_sync(0xffffffffu, nk, g + 8 * q);
+      sts32(lvs + 4 * lane, __float_as_uint(nv));
       {
-        const int row = __shfl_sync(0xffffffffu, row0, min(i + 1, kWinBlocks - 1)) + lane;
-        const bool in = i + 1 < nb && t0 + kBlockBk + lane < s1;
-        nx[0] = in ? __ldg(ksp + row) : 0.0f;
-        nx[1] = in ? __ldg(ksp + p.cap_rows + row) : 0.0f;
-        nx[2] = in ? __ldg(vsp + row) : 0.0f;
-        nx[3] = in ? __ldg(vsp + p.cap_rows + row) : 0.0f;
+        const int row = plane + __shfl_sync(0xffffffffu, row0, i + 1) + lane;   // (lane 8 holds 0)
+        const bool in = t0 + kBlockBk + lane < s1;
+        nk = in ? __ldg(p.k_scale + row) : 0.0f;
+        nv = in ? __ldg(p.v_scale + row) : 0.0f;
       }
-      __syncwarp();
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[cst], cph))) {
-        failed = true;
-        break;
+      uint4 qlo = make_uint4(0, 0, 0, 0), qhi = qlo;
+      float2 qsr = make_float2(0.0f, 0.0f);
+      if (T == 2 || g < 4) {
+        qlo = lds128a<0>(lq);
+        qhi = lds128a<16>(lq);
       }
-      // ---- scores of both maps: sc[tile][half], keys 16 half + g (+ 8), rows 2c + e
-      float sc[T][2][4];
+      if (T == 2 || c < 2) qsr = lds64a<0>(lqs);
+      // ---- scores of map a: sc[half], keys 16 half + g (+ 8), rows 2c + e
+      if (!failed) failed = !stage_ready(fullb + (cst >> 9), cph);
+      float2 sc[2][2];                            // [half][key g | g + 8], rows 2c, 2c + 1
       {
-        const uint8_t* Kt = sm.ring[warp][cst];
-        int acc[T][2][4];
+        const uint32_t k0 = ringb + cst + lk, k1 = k0 ^ 16u;
 #pragma unroll
-        for (int n = 0; n < T; ++n)
+        for (int hf = 0; hf < 2; ++hf) {
+          const uint4 a_lo = hf ? lds128a<2048>(k0) : lds128a<0>(k0);
+          const uint4 a_hi = hf ? lds128a<2048>(k1) : lds128a<0>(k1);
+          const uint4 b_lo = hf ? lds128a<3072>(k0) : lds128a<1024>(k0);
+          const uint4 b_hi = hf ? lds128a<3072>(k1) : lds128a<1024>(k1);
+          int acc[4] = {0, 0, 0, 0}, acc2[4] = {0, 0, 0, 0};
+          mma_i8(acc, a_lo.x, b_lo.x, a_lo.y, b_lo.y, qlo.x, qlo.y);
+          mma_i8(acc2, a_lo.z, b_lo.z, a_lo.w, b_lo.w, qlo.z, qlo.w);
+          mma_i8(acc, a_hi.x, b_hi.x, a_hi.y, b_hi.y, qhi.x, qhi.y);
+          mma_i8(acc2, a_hi.z, b_hi.z, a_hi.w, b_hi.w, qhi.z, qhi.w);
+          // s = (S * (qs * ks)) * sm_scale, rounded as written
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) acc[n][hf][u] = 0;
-#pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const int ra = 16 * hf + g, rb = ra + 8;
-            const uint8_t* B = Kt + a * kBlockBytes;
-            const uint4 a_lo = lds128(B + swz(ra, 2 * c)), a_hi = lds128(B + swz(ra, 2 * c + 1));
-            const uint4 b_lo = lds128(B + swz(rb, 2 * c)), b_hi = lds128(B + swz(rb, 2 * c + 1));
-            const uint32_t wa[8] = {a_lo.x, a_lo.y, a_lo.z, a_lo.w, a_hi.x, a_hi.y, a_hi.z, a_hi.w};
-            const uint32_t wb[8] = {b_lo.x, b_lo.y, b_lo.z, b_lo.w, b_hi.x, b_hi.y, b_hi.z, b_hi.w};
-            // T = 1: the rows of the other map are zero, so both planes add up in one tile
-            const bool mine = T == 2 || (g >> 2) == a;
-            constexpr int kTile1 = T - 1;
-            const int n = T == 1 ? 0 : a;
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-              mma_i8(acc[T == 1 ? 0 : (a ? kTile1 : 0)][hf], wa[2 * s], wb[2 * s], wa[2 * s + 1],
-                     wb[2 * s + 1], mine ? qw[n][2 * s] : 0u, mine ? qw[n][2 * s + 1] : 0u);
+          for (int k2 = 0; k2 < 2; ++k2) {
+            const float ks = ks4[2 * hf + k2];
+            const float2 qk = f2_mul(qsr, make_float2(ks, ks));
+            const float2 S = make_float2(__int2float_rn(acc[2 * k2] + acc2[2 * k2]),
+                                         __int2float_rn(acc[2 * k2 + 1] + acc2[2 * k2 + 1]));
+            sc[hf][k2] = f2_mul(f2_mul(S, qk), make_float2(p.sm_scale, p.sm_scale));
           }
-        consumed();
-        // s = (S * (qs * ks)) * sm_scale; a tile row's map picks the plane of ks
-#pragma unroll
-        for (int n = 0; n < T; ++n) {
-          const float* kss = sm.scale[warp][T == 1 ? c >> 1 : n];
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-            for (int k2 = 0; k2 < 2; ++k2) {
-              const float ks = kss[16 * hf + 8 * k2 + g];
-              const float2 qk = f2_mul(make_float2(qsr[n][0], qsr[n][1]), make_float2(ks, ks));
-              float2 s2 = f2_mul(make_float2(__int2float_rn(acc[n][hf][2 * k2]),
-                                             __int2float_rn(acc[n][hf][2 * k2 + 1])), qk);
-              s2 = f2_mul(s2, make_float2(p.sm_scale, p.sm_scale));
-              sc[n][hf][2 * k2] = s2.x;
-              sc[n][hf][2 * k2 + 1] = s2.y;
-            }
         }
       }
+      if (!failed) consumed();
       if (t0 + kBlockBk > ctx) {                  // keys that some row does not see
 #pragma unroll
-        for (int n = 0; n < T; ++n)
+        for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              if (t0 + 16 * hf + g + 8 * (u >> 1) >= L[u & 1]) sc[n][hf][u] = -INFINITY;
-      }
-      float alpha[T][2];
-      bool rescale = false;
-#pragma unroll
-      for (int n = 0; n < T; ++n)
-        diff_softmax(sc[n][0], sc[n][1], m_run[n], l_run[n], alpha[n], rescale);
-      if (rescale) {
-#pragma unroll
-        for (int pl = 0; pl < 2; ++pl)
-#pragma unroll
-          for (int md = 0; md < 8; ++md)
-#pragma unroll
-            for (int n = 0; n < T; ++n) {
-              const float2 a2 = make_float2(alpha[n][0], alpha[n][1]);
-              const float2 lo = f2_mul(make_float2(o[pl][md][n][0], o[pl][md][n][1]), a2);
-              const float2 hi = f2_mul(make_float2(o[pl][md][n][2], o[pl][md][n][3]), a2);
-              o[pl][md][n][0] = lo.x; o[pl][md][n][1] = lo.y;
-              o[pl][md][n][2] = hi.x; o[pl][md][n][3] = hi.y;
-            }
-      }
-      // ---- the weights in the operand's layout: keys 2c, 2c+1, 2c+8, 2c+9 of the
-      // half, row g
-      float pb[T][2][4];
-#pragma unroll
-      for (int n = 0; n < T; ++n)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const int srcA = 8 * c + (g >> 1), srcB = srcA + 4;
-          float fA[4], fB[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            fA[u] = __shfl_sync(0xffffffffu, sc[n][hf][u], srcA);
-            fB[u] = __shfl_sync(0xffffffffu, sc[n][hf][u], srcB);
+          for (int k2 = 0; k2 < 2; ++k2) {
+            const int key = t0 + 16 * hf + g + 8 * k2;
+            if (key >= keys_of(2 * c)) sc[hf][k2].x = -INFINITY;
+            if (key >= keys_of(2 * c + 1)) sc[hf][k2].y = -INFINITY;
           }
-          const bool odd = g & 1;
-          pb[n][hf][0] = odd ? fA[1] : fA[0];
-          pb[n][hf][1] = odd ? fB[1] : fB[0];
-          pb[n][hf][2] = odd ? fA[3] : fA[2];
-          pb[n][hf][3] = odd ? fB[3] : fB[2];
+      }
+      // ---- weights 2^(s log2 e - m).  A row's reference moves, to the block's
+      // maximum, only where a score exceeds it by more than kLag; only then are
+      // the maxima of the row's 32 keys put together.
+      float2 alpha = make_float2(1.0f, 1.0f);
+      int info = failed ? kFailed : 0;
+      {
+        float2 bm = make_float2(fmaxf(fmaxf(sc[0][0].x, sc[0][1].x), fmaxf(sc[1][0].x, sc[1][1].x)),
+                                fmaxf(fmaxf(sc[0][0].y, sc[0][1].y), fmaxf(sc[1][0].y, sc[1][1].y)));
+        if (__any_sync(0xffffffffu, bm.x > m_move.x || bm.y > m_move.y)) {
+#pragma unroll
+          for (int o2 = 4; o2 <= 16; o2 <<= 1) {
+            bm.x = fmaxf(bm.x, __shfl_xor_sync(0xffffffffu, bm.x, o2));
+            bm.y = fmaxf(bm.y, __shfl_xor_sync(0xffffffffu, bm.y, o2));
+          }
+          move_reference(bm.x, m_run.x, m_move.x, alpha.x);
+          move_reference(bm.y, m_run.y, m_move.y, alpha.y);
+          if (g == 0) sts64(lex + kExAlpha + 32 * a + 8 * c, alpha);
+          if (__any_sync(0xffffffffu, alpha.x != 1.0f || alpha.y != 1.0f)) info |= kMoved;
         }
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[cst], cph))) {
-        failed = true;
-        break;
-      }
-      // ---- P.V: the operand a = p * v_scale * 2^E as f16 hi + lo (22 bits), V exact
+        const float2 l2e = make_float2(kLog2e, kLog2e), mm = make_float2(-m_run.x, -m_run.y);
 #pragma unroll
-      for (int pl = 0; pl < 2; ++pl)
+        for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const uint8_t* Vt = sm.ring[warp][cst] + pl * kBlockBytes;
-          const float* vss = sm.scale[warp][2 + pl] + 16 * hf + 2 * c;
-          const float2 v0 = *reinterpret_cast<const float2*>(vss);
-          const float2 v1 = *reinterpret_cast<const float2*>(vss + 8);
-          const float2 up2 = make_float2(upb[pl], upb[pl]);
-          uint2 bhi[T], blo[T];
-#pragma unroll
-          for (int n = 0; n < T; ++n) {
-            const float2 x = f2_mul(f2_mul(make_float2(pb[n][hf][0], pb[n][hf][1]), v0), up2);
-            const float2 y = f2_mul(f2_mul(make_float2(pb[n][hf][2], pb[n][hf][3]), v1), up2);
-            split_f16x2(x.x, x.y, bhi[n].x, blo[n].x);
-            split_f16x2(y.x, y.y, bhi[n].y, blo[n].y);
+          for (int k2 = 0; k2 < 2; ++k2) {
+            const float2 x2 = f2_fma(sc[hf][k2], l2e, mm);
+            // (a key the row does not see: 2^-inf = 0)
+            sc[hf][k2] = make_float2(fast_exp2(x2.x), fast_exp2(x2.y));
           }
-          const int kr = 16 * hf + 2 * c;
-          const uint4 vw0 = lds128(Vt + swz(kr, g)), vw1 = lds128(Vt + swz(kr + 1, g));
-          const uint4 vw2 = lds128(Vt + swz(kr + 8, g)), vw3 = lds128(Vt + swz(kr + 9, g));
-          const uint32_t w0[4] = {vw0.x, vw0.y, vw0.z, vw0.w}, w1[4] = {vw1.x, vw1.y, vw1.z, vw1.w};
-          const uint32_t w2[4] = {vw2.x, vw2.y, vw2.z, vw2.w}, w3[4] = {vw3.x, vw3.y, vw3.z, vw3.w};
+        l_run = f2_fma(l_run, alpha, f2_add(f2_add(sc[0][0], sc[0][1]), f2_add(sc[1][0], sc[1][1])));
+      }
+      // ---- hand the weights over
+      if (T == 2 || c < 2) {
+        const uint32_t w = lex + lww;
+        sts32<0>(w, sc[0][0].x);
+        sts32<8>(w, sc[0][0].y);
+        sts32<256>(w, sc[0][1].x);
+        sts32<264>(w, sc[0][1].y);
+        sts32<512>(w, sc[1][0].x);
+        sts32<520>(w, sc[1][0].y);
+        sts32<768>(w, sc[1][1].x);
+        sts32<776>(w, sc[1][1].y);
+      }
+      if (lane == 0) sts32(lex + kExInfo + 4 * a, (uint32_t)info);
+      named_sync(1 + wp, 64);
+      const float2 both = lds64a<kExInfo>(lex);
+      const int info0 = __float_as_int(both.x), info1 = __float_as_int(both.y);
+      const uint32_t lexr = lex + lwr, exa = lex + kExAlpha;
+      lex = exbase + exbase + Smem::kExBytes - lex;      // the other buffer
+      if ((info0 | info1) & kFailed) break;       // both warps leave
+      if ((info0 | info1) & kMoved) {
+#pragma unroll
+        for (int n = 0; n < T; ++n) {
+          // the tile's rows 2c, 2c + 1: map n, or (T = 1) map c / 2
+          const int map = T == 1 ? c >> 1 : n, r0 = T == 1 ? 2 * (c & 1) : 2 * c;
+          float2 al = lds64a<0>(exa + 32 * map + 4 * r0);
+          if (!((map ? info1 : info0) & kMoved)) al = make_float2(1.0f, 1.0f);
 #pragma unroll
           for (int md = 0; md < 8; ++md) {
-            const int wi = md >> 1;
-            const uint32_t sel = (md & 1) ? 0x7362u : 0x5140u;
-            const uint32_t t01 = __byte_perm(w0[wi], w1[wi], sel) ^ 0x80808080u;
-            const uint32_t t23 = __byte_perm(w2[wi], w3[wi], sel) ^ 0x80808080u;
-            const uint32_t af[4] = {i8pair_to_h2(t01, 0x4140u), i8pair_to_h2(t01, 0x4342u),
-                                    i8pair_to_h2(t23, 0x4140u), i8pair_to_h2(t23, 0x4342u)};
+            const float2 lo = f2_mul(make_float2(o[md][n][0], o[md][n][1]), al);
+            const float2 hi = f2_mul(make_float2(o[md][n][2], o[md][n][3]), al);
+            o[md][n][0] = lo.x; o[md][n][1] = lo.y; o[md][n][2] = hi.x; o[md][n][3] = hi.y;
+          }
+        }
+      }
+      // ---- P.V: the operand w * v_scale * 2^E as f16 hi + lo (22 bits), V exact
+      const float up = lds32a<0>(lup);
+      const float2 up2 = make_float2(up, up);
+      failed = !stage_ready(fullb + (cst >> 9), cph);
+      // A = V^T.  Row g of m-tile q is channel 16q + 2g, row g + 8 the next one; a
+      // 16-bit element of the stage is two channels of a key, so the transposing
+      // load pairs the keys 2c, 2c + 1 of both channels in a register.  Lane 8i + r
+      // addresses key r (+ 8 if i is odd) of the half, 16-byte chunk q + i / 2.
+      const uint32_t va = ringb + cst + lv;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const float2 v0 = f2_mul(hf ? lds64a<64>(lvs + 8 * c) : lds64a<0>(lvs + 8 * c), up2);
+        const float2 v1 = f2_mul(hf ? lds64a<96>(lvs + 8 * c) : lds64a<32>(lvs + 8 * c), up2);
+        uint2 bhi[T], blo[T];
+#pragma unroll
+        for (int n = 0; n < T; ++n) {
+          const uint32_t w = lexr + 1024 * n;
+          const float2 y0 = f2_mul(hf ? lds64a<512>(w) : lds64a<0>(w), v0);
+          const float2 y1 = f2_mul(hf ? lds64a<768>(w) : lds64a<256>(w), v1);
+          split_f16x2(y0.x, y0.y, bhi[n].x, blo[n].x);
+          split_f16x2(y1.x, y1.y, bhi[n].y, blo[n].y);
+        }
+#pragma unroll
+        for (int q = 0; q < 8; q += 2) {
+          uint32_t vw[4];                         // keys 2c.. and 2c+8.. of tile q, then of tile q + 1
+          if (hf) ldsm_x4_trans<2048>(vw, va ^ (uint32_t)(q << 4));
+          else ldsm_x4_trans<0>(vw, va ^ (uint32_t)(q << 4));
+#pragma unroll
+          for (int d = 0; d < 2; ++d) {
+            // bytes (XOR 0x80) into the mantissa of 1024, less 1152: exact f16
+            const uint32_t t0v = vw[2 * d] ^ 0x80808080u, t1v = vw[2 * d + 1] ^ 0x80808080u;
+            const uint32_t af[4] = {i8pair_to_h2(t0v, 0x4240u), i8pair_to_h2(t0v, 0x4341u),
+                                    i8pair_to_h2(t1v, 0x4240u), i8pair_to_h2(t1v, 0x4341u)};
 #pragma unroll
             for (int n = 0; n < T; ++n) {
-              mma_f16(o[pl][md][n], af, bhi[n]);
-              mma_f16(o[pl][md][n], af, blo[n]);
+              mma_f16(o[q + d][n], af, bhi[n]);
+              mma_f16(o[q + d][n], af, blo[n]);
             }
           }
         }
-      consumed();
+      }
+      if (!failed) consumed();
     }
-    if (failed) {
+    const bool whole = diff_windows(ctx + M - 1) == 1;
+    const int b = it0.b, pair = it0.pair;
+
+    // ---- the window's result
+    float down[2];                                // 2^-E of rows 2c + e
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      down[e] = __uint_as_float((254u << 23) - __float_as_uint(sm.up[wp][a][2 * c + e]));
+      float v = e ? l_run.y : l_run.x;
+      v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 4));
+      v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 8));
+      v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 16));
+      if (e) l_run.y = v;
+      else l_run.x = v;
+    }
+    if (lane == 0) sts32(lex + kExInfo + 4 * a, failed ? (uint32_t)kFailed : 0u);
+    if (whole && g == 0) {
+      sm.row_sum[wp][a][2 * c] = l_run.x;
+      sm.row_sum[wp][a][2 * c + 1] = l_run.y;
+    }
+    named_sync(1 + wp, 64);
+    const float2 both = lds64a<kExInfo>(lex);
+    lex = exbase + exbase + Smem::kExBytes - lex;        // (a warp that runs ahead writes the other)
+    if (__float_as_int(both.x) | __float_as_int(both.y)) {
       // A copy never arrived: flag it, give the copies in flight a bounded chance
       // to land, then leave.
       if (lane == 0) {
         atomicOr(p.err_word, KATTN_DEVERR_TIMEOUT);
         for (int k = 0; k < inflight; ++k) {
-          mbar_wait_bounded(&full[cst], cph);
-          if (++cst == kStages) {
-            cst = 0;
-            cph ^= 1u;
-          }
+          mbar_wait_bounded(&full[cst / kBlockBytes], cph);
+          cph ^= cst == kLastStage ? 1u : 0u;
+          cst = cst == kLastStage ? 0 : cst + kBlockBytes;
         }
       }
       return;
     }
-
-    // ---- the window's result
-#pragma unroll
-    for (int n = 0; n < T; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float v = l_run[n][e];
-        v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 4));
-        v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 8));
-        l_run[n][e] = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 16));
-      }
-    const bool whole = diff_windows(ctx + M - 1) == 1;
-    const int b = it0.b, pair = it0.pair;
     if (whole) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int rr = it0.rg * kUnitRows + (T == 1 ? (2 * c + e) & 3 : 2 * c + e);
+        const int r = T == 1 ? (2 * c + e) & 3 : 2 * c + e, rr = it0.rg * kUnitRows + r;
         const bool in = rr < R && (T == 2 || c < 2);
-        const int j = rr / p.g, i = pair * p.g + rr % p.g;
+        const int j = column(min(rr, R - 1)), i = pair * p.g + min(rr, R - 1) - j * p.g;
         const int64_t row = ((int64_t)b * M + j) * H + i;
         const float lam = in ? p.lam[p.lam_per_row ? row : i] : 0.0f;
-        const float l0 = l_run[0][e];
-        const float l1 = T == 2 ? l_run[T - 1][e] : __shfl_xor_sync(0xffffffffu, l_run[0][e], 2);
+        const float l0 = sm.row_sum[wp][0][r], l1 = sm.row_sum[wp][1][r];
 #pragma unroll
-        for (int pl = 0; pl < 2; ++pl)
-#pragma unroll
-          for (int md = 0; md < 8; ++md) {
-            const float x0 = __fmul_rn(o[pl][md][0][e], down[pl][e]);
-            const float x1 = __fmul_rn(o[pl][md][0][2 + e], down[pl][e]);
-            const float y0 = T == 2 ? __fmul_rn(o[pl][md][T - 1][e], down[pl][e])
-                                    : __shfl_xor_sync(0xffffffffu, x0, 2);
-            const float y1 = T == 2 ? __fmul_rn(o[pl][md][T - 1][2 + e], down[pl][e])
-                                    : __shfl_xor_sync(0xffffffffu, x1, 2);
-            if (in)
-              *reinterpret_cast<float2*>(p.out + row * 2 * kD + pl * kD + 16 * g + 2 * md) =
-                  make_float2(diff_out(x0, l0, y0, l1, lam), diff_out(x1, l0, y1, l1, lam));
-          }
+        for (int md = 0; md < 8; ++md) {
+          const float x0 = __fmul_rn(o[md][0][e], down[e]);
+          const float x1 = __fmul_rn(o[md][0][2 + e], down[e]);
+          const float y0 = T == 2 ? __fmul_rn(o[md][T - 1][e], down[e])
+                                  : __shfl_xor_sync(0xffffffffu, x0, 2);
+          const float y1 = T == 2 ? __fmul_rn(o[md][T - 1][2 + e], down[e])
+                                  : __shfl_xor_sync(0xffffffffu, x1, 2);
+          if (in)
+            *reinterpret_cast<float2*>(p.out + row * 2 * kD + a * kD + 16 * md + 2 * g) =
+                make_float2(diff_out(x0, l0, y0, l1, lam), diff_out(x1, l0, y1, l1, lam));
+        }
       }
     } else {
       float* part = p.partials + (((size_t)b * p.nwin_max + it0.w) * p.pairs + pair) * diff_stride(R);
@@ -596,45 +709,46 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
       for (int n = 0; n < T; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int r = 2 * c + e, a = T == 1 ? r >> 2 : n;
+          const int r = 2 * c + e, map = T == 1 ? r >> 2 : n;
           const int rr = it0.rg * kUnitRows + (T == 1 ? r & 3 : r);
           if (rr >= R) continue;
-          float* dst = part + (size_t)(a * R + rr) * 2 * kD + 16 * g;
+          float* dst = part + (size_t)(map * R + rr) * 2 * kD + a * kD + 2 * g;
 #pragma unroll
-          for (int pl = 0; pl < 2; ++pl)
-#pragma unroll
-            for (int md = 0; md < 8; md += 2)
-              *reinterpret_cast<float4*>(dst + pl * kD + 2 * md) =
-                  make_float4(__fmul_rn(o[pl][md][n][e], down[pl][e]),
-                              __fmul_rn(o[pl][md][n][2 + e], down[pl][e]),
-                              __fmul_rn(o[pl][md + 1][n][e], down[pl][e]),
-                              __fmul_rn(o[pl][md + 1][n][2 + e], down[pl][e]));
-          if (g == 0) {
-            part[(size_t)2 * R * 2 * kD + a * R + rr] = m_run[n][e];
-            part[(size_t)2 * R * 2 * kD + 2 * R + a * R + rr] = l_run[n][e];
-          }
+          for (int md = 0; md < 8; ++md)
+            *reinterpret_cast<float2*>(dst + 16 * md) =
+                make_float2(__fmul_rn(o[md][n][e], down[e]), __fmul_rn(o[md][n][2 + e], down[e]));
         }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int rr = it0.rg * kUnitRows + 2 * c + e;
+        if (g == 0 && rr < R && (T == 2 || c < 2)) {
+          part[(size_t)2 * R * 2 * kD + a * R + rr] = e ? m_run.y : m_run.x;
+          part[(size_t)2 * R * 2 * kD + 2 * R + a * R + rr] = e ? l_run.y : l_run.x;
+        }
+      }
     }
 
     // ---- next item
     t += G;
     if (t >= total) break;
-    it0 = it1;
+    if (!pnext) reach_next();                     // it had nothing left to read ahead
+    pnext = false;
     row0 = row1;
-    it1 = find(t + G);
-    row1 = block_row(p, it1, lane);
-    if (pnext) {
-      pnext = 0;                                  // the producer is already on this item
-    } else {
-      pblk = 0;                                   // it had nothing left to read ahead
-      pn = blocks_of(it0);
+    ipar ^= 1;
+    put(ipar ^ 1, t + G);
+    row1 = row_entry(p, items[ipar ^ 1], lane);
+    if (items[ipar ^ 1].b >= 0) {                 // the next unit's queries (lane: a line of a row)
+      const DiffItem& nx = items[ipar ^ 1];
+      const int rr = min(nx.rg * kUnitRows + min(lane >> 2, kUnitRows - 1), R - 1), j = column(rr);
+      prefetch_l2(p.q + (((int64_t)nx.b * M + j) * p.Hq + 2 * (nx.pair * p.g + rr - j * p.g) + a) * kD +
+                  32 * (lane & 3));
     }
-    produce();
+    fill();
   }
 }
 
 // Joins the windows of a row, one block per (sequence, column, head): warp k sums
-// the windows k, k + 8, ... of both maps with the weights e^(m_s - max m), the
+// the windows k, k + 8, ... of both maps with the weights 2^(m_s - max m), the
 // eight sums are added in order, and the two maps are subtracted.  The order
 // depends on the row's own window count alone.
 constexpr int kMergeWarps = 8;
@@ -683,7 +797,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) diff_merge_kernel(const D
     if (s < ns) {
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
-        w[a] = merge_weight(__ldcg(mcol + s * stride + a * R), mx[a]);
+        w[a] = fast_exp2(__fsub_rn(__ldcg(mcol + s * stride + a * R), mx[a]));
         l[a] = __fmaf_rn(w[a], __ldcg(lcol + s * stride + a * R), l[a]);
       }
     }
@@ -772,13 +886,13 @@ cudaError_t launch_split(const DiffParams& p, const TmaMaps& maps, cudaStream_t 
       return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
       return e;
-    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kWarps * 32, smem)) !=
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, smem)) !=
         cudaSuccess)
       return e;
     slots = sms * (per_sm > 0 ? per_sm : 1);
     if (dev >= 0 && dev < kMaxDevices) slots_cache[dev].store(slots);
   }
-  kern<<<(unsigned)std::min<int64_t>(diff_units(p), slots), kWarps * 32, smem, stream>>>(p, maps);
+  kern<<<(unsigned)std::min<int64_t>(diff_units(p), slots), kThreads, smem, stream>>>(p, maps);
   return cudaGetLastError();
 }
 
