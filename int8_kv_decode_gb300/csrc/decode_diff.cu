@@ -56,6 +56,7 @@ constexpr int kFailed = 1, kMoved = 2;
 
 struct DiffItem {
   int b, pair, w, rg, ctx, row0;                  // b < 0: none
+  int fresh;                                      // other queries than the item before
 };
 
 template <int T>
@@ -73,7 +74,6 @@ struct __align__(1024) DiffSmem {
   DiffItem item[kPairs][2][2];                    // the current and the next, by parity
   uint64_t full[kPairs][2][kStages];
   int prefix[kMaxGroups + 1];
-  int ctx[kMaxGroups], row0[kMaxGroups];          // of each sequence (up to kMaxGroups)
   int warp_total[kThreads / 32];
 };
 
@@ -179,16 +179,17 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t addr) {
                : "memory");
 }
 
-// kBlockBk rows of a plane into a stage, 128-byte swizzle.
-__device__ __forceinline__ void load_stage(uint32_t dst, const CUtensorMap* map, int row,
+// kBlockBk rows of a plane into a stage, 128-byte swizzle, by the lane with issue
+// set (predicated, so that the warp does not branch).  The stage was read by every
+// lane before: their loads have returned, as products that took them were issued.
+__device__ __forceinline__ void load_stage(bool issue, uint32_t dst, const CUtensorMap* map, int row,
                                            uint32_t bar, uint64_t policy) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar),
-               "r"((uint32_t)kBlockBytes)
-               : "memory");
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%2, %3}], [%4], %5;\n" ::"r"(dst), "l"(map), "r"(0), "r"(row), "r"(bar),
-      "l"(policy)
+      "{\n .reg .pred p;\n setp.ne.u32 p, %0, 0;\n"
+      " @p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%5], %7;\n"
+      " @p cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%1], [%2, {%3, %4}], [%5], %6;\n}\n" ::"r"((uint32_t)issue), "r"(dst), "l"(map), "r"(0),
+      "r"(row), "r"(bar), "l"(policy), "r"((uint32_t)kBlockBytes)
       : "memory");
 }
 
@@ -203,10 +204,13 @@ __device__ __forceinline__ bool bar_try_wait(uint32_t bar, uint32_t parity) {
   return done != 0;
 }
 // Whether the stage's copy landed, for the whole warp; the wait is bounded.
-__device__ __forceinline__ bool stage_ready(uint32_t bar, uint32_t parity) {
+__device__ __noinline__ bool stage_wait(uint32_t bar, uint32_t parity) {
   for (uint32_t it = 0; it < kSpinLimit; ++it)
     if (__all_sync(0xffffffffu, bar_try_wait(bar, parity))) return true;
   return false;
+}
+__device__ __forceinline__ bool stage_ready(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, bar_try_wait(bar, parity)) || stage_wait(bar, parity);
 }
 
 // The row's reference moves to the block's maximum bm where that exceeds its
@@ -256,12 +260,10 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
     return diff_valid(p, b, ctx) ? diff_windows(ctx + M - 1) * per_win : 0;
   };
   for (int i = tid; i < kMaxGroups; i += kThreads) {
-    int n = 0, ctx = 0;
+    int n = 0;
     if (i < ng)
-      for (int b = i * gs; b < min(p.B, i * gs + gs); ++b) n += units_of(b, ctx = p.ctx_len[b]);
+      for (int b = i * gs; b < min(p.B, i * gs + gs); ++b) n += units_of(b, p.ctx_len[b]);
     sm.prefix[i] = n;
-    sm.ctx[i] = ctx;
-    sm.row0[i] = gs == 1 && i < ng && p.block_table == nullptr ? (int)p.row_start[i] : 0;
   }
   __syncthreads();
   {
@@ -302,34 +304,50 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
   __syncthreads();
   griddep_launch_dependents();
   const int total = sm.prefix[kMaxGroups];
-  const int G = gridDim.x * kPairs;
-  int t = wp * gridDim.x + blockIdx.x;            // neighbouring units on different SMs
-  if (t >= total) return;
+  // Each pair of warps takes a run of units that follow one another: the windows of
+  // a row group, then the next row group's, so that its queries are read and
+  // quantized once for a run of windows.
+  const int G = gridDim.x * kPairs, worker = wp * gridDim.x + blockIdx.x;
+  int u = (int)((int64_t)worker * total / G);
+  const int u_end = (int)((int64_t)(worker + 1) * total / G);
+  if (u >= u_end) return;
 
-  auto find = [&](int u) -> DiffItem {
-    DiffItem it{-1, 0, 0, 0, 0, 0};
-    if (u >= total) return it;
-    int lo = 0, hi = ng;                          // prefix[lo] <= u < prefix[hi]
+  auto at_sequence = [&](DiffItem& it, int b) {
+    it.b = b;
+    it.ctx = p.ctx_len[b];
+    it.row0 = p.block_table ? 0 : (int)p.row_start[b];
+  };
+  auto find = [&](int i) -> DiffItem {            // unit i < total
+    DiffItem it{};
+    int lo = 0, hi = ng;                          // prefix[lo] <= i < prefix[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (sm.prefix[mid] <= u) lo = mid;
+      if (sm.prefix[mid] <= i) lo = mid;
       else hi = mid;
     }
-    int r = u - sm.prefix[lo];
-    it.b = lo;
-    it.ctx = sm.ctx[lo];
-    it.row0 = sm.row0[lo];
-    if (gs > 1) {
-      int b = lo * gs;
-      for (int n; r >= (n = units_of(b, p.ctx_len[b])); ++b) r -= n;
-      it.b = b;
-      it.ctx = p.ctx_len[b];
-      it.row0 = p.block_table ? 0 : (int)p.row_start[b];
-    }
-    it.w = r / per_win;
-    r -= it.w * per_win;
-    it.pair = r / nrg;
-    it.rg = r - it.pair * nrg;
+    i -= sm.prefix[lo];
+    int b = lo * gs;
+    for (int n; gs > 1 && i >= (n = units_of(b, p.ctx_len[b])); ++b) i -= n;
+    at_sequence(it, b);
+    const int nw = diff_windows(it.ctx + M - 1), run = i / nw;
+    it.w = i - run * nw;
+    it.pair = run / nrg;
+    it.rg = run - it.pair * nrg;
+    it.fresh = 1;
+    return it;
+  };
+  auto after = [&](DiffItem it) -> DiffItem {     // the unit after it (there is one)
+    it.fresh = 0;
+    if (++it.w < diff_windows(it.ctx + M - 1)) return it;
+    it.w = 0;
+    it.fresh = 1;
+    if (++it.rg < nrg) return it;
+    it.rg = 0;
+    if (++it.pair < p.pairs) return it;
+    it.pair = 0;
+    int b = it.b + 1;
+    while (units_of(b, p.ctx_len[b]) == 0) ++b;
+    at_sequence(it, b);
     return it;
   };
   auto blocks_of = [&](const DiffItem& it) -> int {
@@ -343,19 +361,25 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
 
   DiffItem* items = sm.item[wp][a];
   int ipar = 0;                                   // parity of the current item
-  auto put = [&](int par, int u) {                // unit u into slot par
-    const DiffItem it = find(u);
+  auto put = [&](int par, const DiffItem& it) {
     __syncwarp();
     if (lane == 0) items[par] = it;
     __syncwarp();
   };
-  put(0, t);
-  put(1, t + G);
+  auto put_next = [&](int par) {                  // the unit after the other slot's
+    DiffItem it = items[par ^ 1];
+    if (u + 1 < u_end) it = after(it);
+    else it.b = -1;
+    put(par, it);
+  };
+  put(0, find(u));
+  put_next(1);
   int row0 = row_of_entry(p, items[0], row_entry(p, items[0], lane), lane);
   int row1 = row_entry(p, items[1], lane);        // an entry until the producer reaches it
 
-  // ---- producer: lane 0 issues, every lane keeps the same counters.  Stages
-  // go K, V, K, V, ... over this item's blocks, then the next item's.
+  // ---- producer: lane 0 issues, every lane keeps the same counters.  Stages go
+  // over this item's blocks in the order they are read, then the next item's: the
+  // keys of a block come before the values of the one before it.
   const uint32_t ringb = smem_u32(sm.ring[wp][a][0]), fullb = smem_u32(full);
   bool pnext = false;
   int ps = 0, pend = 2 * blocks_of(items[0]), inflight = 0;
@@ -379,11 +403,10 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
       pnext = true;
       reach_next();
     }
-    const int row = __shfl_sync(0xffffffffu, prow, ps >> 1);
-    if (lane == 0) {
-      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-      load_stage(ringb + ist, ps & 1 ? &maps.v : &maps.k, row, fullb + (ist >> 9), policy);
-    }
+    // stage ps of the item's pend = 2 n: K0, K1, V0, K2, V1, ..., V(n-2), V(n-1)
+    const bool last = ps == pend - 1, is_v = last || (ps > 0 && !(ps & 1));
+    const int row = __shfl_sync(0xffffffffu, prow, last ? (ps >> 1) : ((ps + 1) >> 1) - (is_v ? 1 : 0));
+    load_stage(lane == 0, ringb + ist, is_v ? &maps.v : &maps.k, row, fullb + (ist >> 9), policy);
     ++ps;
     ++inflight;
     ist = ist == kLastStage ? 0 : ist + kBlockBytes;
@@ -402,7 +425,6 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
     produce();
   };
   fill();
-  bool failed = false;                            // a copy of this warp never arrived
   // ---- shared-memory addresses of this lane
   const uint32_t exbase = smem_u32(&sm.ex[wp][0]);
   uint32_t lex = exbase;                          // exchange buffer of the next block
@@ -415,19 +437,48 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
   const uint32_t lww = (T == 1 ? 0 : 1024 * a) + ((g >> 1) * 8 + (T == 1 ? 4 * a : 0) + 2 * c) * 8 + (g & 1) * 4;
   const uint32_t lwr = (c * 8 + g) * 8;
 
+  // A copy of this warp never arrived: tell the other warp at its next exchange
+  // (the buffer that it reads then), flag it, and leave.
+  auto drain = [&]() {                            // a bounded chance for the copies in flight to land
+    if (lane == 0)
+      for (int k = 0; k < inflight; ++k) {
+        mbar_wait_bounded(&full[cst / kBlockBytes], cph);
+        cph ^= cst == kLastStage ? 1u : 0u;
+        cst = cst == kLastStage ? 0 : cst + kBlockBytes;
+      }
+  };
+  auto give_up = [&]() {
+    if (lane == 0) {
+      sts32(lex + kExInfo + 4 * a, (uint32_t)kFailed);
+      atomicOr(p.err_word, KATTN_DEVERR_TIMEOUT);
+    }
+    named_sync(1 + wp, 64);
+    drain();
+  };
+
   for (;;) {
     const DiffItem& it0 = items[ipar];
     const int ctx = it0.ctx, s0 = it0.w * kWindow, s1 = min(s0 + kWindow, ctx + M - 1);
     const int plane = (2 * it0.pair + a) * p.cap_rows;
     // ---- the unit's queries of map a, quantized per row, and the plane's scales:
     // those of block 0, and the largest v_scale among the keys that every row sees
-    float4 x[kUnitRows];
+    if (it0.fresh) {
+      float4 x[kUnitRows];
 #pragma unroll
-    for (int r = 0; r < kUnitRows; ++r) {
-      const int rr = min(it0.rg * kUnitRows + r, R - 1);
-      const int j = column(rr), head = 2 * (it0.pair * p.g + rr - j * p.g) + a;
-      x[r] = __ldg(reinterpret_cast<const float4*>(
-                       p.q + (((int64_t)it0.b * M + j) * p.Hq + head) * kD) + lane);
+      for (int r = 0; r < kUnitRows; ++r) {
+        const int rr = min(it0.rg * kUnitRows + r, R - 1);
+        const int j = column(rr), head = 2 * (it0.pair * p.g + rr - j * p.g) + a;
+        x[r] = __ldg(reinterpret_cast<const float4*>(
+                         p.q + (((int64_t)it0.b * M + j) * p.Hq + head) * kD) + lane);
+      }
+#pragma unroll
+      for (int r = 0; r < kUnitRows; ++r) {
+        float s;
+        const uint32_t w = quantize_loaded_row(x[r], &s);
+        const bool in = it0.rg * kUnitRows + r < R;
+        *reinterpret_cast<uint32_t*>(&sm.q[wp][a][r * kQStride + 4 * lane]) = in ? w : 0u;
+        if (lane == 0) sm.qs[wp][a][r] = in ? s : 0.0f;
+      }
     }
     float nk, nv, vm = 0.0f;                      // scales of the next block's key `lane`
 #pragma unroll
@@ -439,14 +490,6 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
         nv = v;
         nk = key < s1 ? __ldg(p.k_scale + plane + row) : 0.0f;
       }
-    }
-#pragma unroll
-    for (int r = 0; r < kUnitRows; ++r) {
-      float s;
-      const uint32_t w = quantize_loaded_row(x[r], &s);
-      const bool in = it0.rg * kUnitRows + r < R;
-      *reinterpret_cast<uint32_t*>(&sm.q[wp][a][r * kQStride + 4 * lane]) = in ? w : 0u;
-      if (lane == 0) sm.qs[wp][a][r] = in ? s : 0.0f;
     }
     // Draft column of unit row r of the tile (T = 1: rows 4..7 are those of map 1).
     auto keys_of = [&](int r) -> int {
@@ -480,6 +523,37 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) o[md][n][u] = 0.0f;
 
+    // Q.K of the next block, started a block ahead: the int8 products are slow (62
+    // cycles of a scheduler's tensor pipe each), and run under the P.V before them.
+    int acc[2][4];
+    auto start_qk = [&]() -> bool {
+      uint4 qlo = make_uint4(0, 0, 0, 0), qhi = qlo;
+      if (T == 2 || g < 4) {
+        qlo = lds128a<0>(lq);
+        qhi = lds128a<16>(lq);
+      }
+      if (!stage_ready(fullb + (cst >> 9), cph)) {
+        give_up();
+        return false;
+      }
+      const uint32_t k0 = ringb + cst + lk, k1 = k0 ^ 16u;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const uint4 a_lo = hf ? lds128a<2048>(k0) : lds128a<0>(k0);
+        const uint4 a_hi = hf ? lds128a<2048>(k1) : lds128a<0>(k1);
+        const uint4 b_lo = hf ? lds128a<3072>(k0) : lds128a<1024>(k0);
+        const uint4 b_hi = hf ? lds128a<3072>(k1) : lds128a<1024>(k1);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) acc[hf][u] = 0;
+        mma_i8(acc[hf], a_lo.x, b_lo.x, a_lo.y, b_lo.y, qlo.x, qlo.y);
+        mma_i8(acc[hf], a_lo.z, b_lo.z, a_lo.w, b_lo.w, qlo.z, qlo.w);
+        mma_i8(acc[hf], a_hi.x, b_hi.x, a_hi.y, b_hi.y, qhi.x, qhi.y);
+        mma_i8(acc[hf], a_hi.z, b_hi.z, a_hi.w, b_hi.w, qhi.z, qhi.w);
+      }
+      consumed();
+      return true;
+    };
+    if (!start_qk()) return;
     const int nb = blocks_of(it0);
     for (int i = 0; i < nb; ++i) {
       const int t0 = s0 + i * kBlockBk;
@@ -493,41 +567,20 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
         nk = in ? __ldg(p.k_scale + row) : 0.0f;
         nv = in ? __ldg(p.v_scale + row) : 0.0f;
       }
-      uint4 qlo = make_uint4(0, 0, 0, 0), qhi = qlo;
+      // ---- scores of map a: sc[half], keys 16 half + g (+ 8), rows 2c + e:
+      // s = (S * (qs * ks)) * sm_scale, rounded as written
       float2 qsr = make_float2(0.0f, 0.0f);
-      if (T == 2 || g < 4) {
-        qlo = lds128a<0>(lq);
-        qhi = lds128a<16>(lq);
-      }
       if (T == 2 || c < 2) qsr = lds64a<0>(lqs);
-      // ---- scores of map a: sc[half], keys 16 half + g (+ 8), rows 2c + e
-      if (!failed) failed = !stage_ready(fullb + (cst >> 9), cph);
       float2 sc[2][2];                            // [half][key g | g + 8], rows 2c, 2c + 1
-      {
-        const uint32_t k0 = ringb + cst + lk, k1 = k0 ^ 16u;
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const uint4 a_lo = hf ? lds128a<2048>(k0) : lds128a<0>(k0);
-          const uint4 a_hi = hf ? lds128a<2048>(k1) : lds128a<0>(k1);
-          const uint4 b_lo = hf ? lds128a<3072>(k0) : lds128a<1024>(k0);
-          const uint4 b_hi = hf ? lds128a<3072>(k1) : lds128a<1024>(k1);
-          int acc[4] = {0, 0, 0, 0}, acc2[4] = {0, 0, 0, 0};
-          mma_i8(acc, a_lo.x, b_lo.x, a_lo.y, b_lo.y, qlo.x, qlo.y);
-          mma_i8(acc2, a_lo.z, b_lo.z, a_lo.w, b_lo.w, qlo.z, qlo.w);
-          mma_i8(acc, a_hi.x, b_hi.x, a_hi.y, b_hi.y, qhi.x, qhi.y);
-          mma_i8(acc2, a_hi.z, b_hi.z, a_hi.w, b_hi.w, qhi.z, qhi.w);
-          // s = (S * (qs * ks)) * sm_scale, rounded as written
+      for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-          for (int k2 = 0; k2 < 2; ++k2) {
-            const float ks = ks4[2 * hf + k2];
-            const float2 qk = f2_mul(qsr, make_float2(ks, ks));
-            const float2 S = make_float2(__int2float_rn(acc[2 * k2] + acc2[2 * k2]),
-                                         __int2float_rn(acc[2 * k2 + 1] + acc2[2 * k2 + 1]));
-            sc[hf][k2] = f2_mul(f2_mul(S, qk), make_float2(p.sm_scale, p.sm_scale));
-          }
+        for (int k2 = 0; k2 < 2; ++k2) {
+          const float ks = ks4[2 * hf + k2];
+          const float2 qk = f2_mul(qsr, make_float2(ks, ks));
+          const float2 S = make_float2(__int2float_rn(acc[hf][2 * k2]), __int2float_rn(acc[hf][2 * k2 + 1]));
+          sc[hf][k2] = f2_mul(f2_mul(S, qk), make_float2(p.sm_scale, p.sm_scale));
         }
-      }
-      if (!failed) consumed();
       if (t0 + kBlockBk > ctx) {                  // keys that some row does not see
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
@@ -542,7 +595,7 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
       // maximum, only where a score exceeds it by more than kLag; only then are
       // the maxima of the row's 32 keys put together.
       float2 alpha = make_float2(1.0f, 1.0f);
-      int info = failed ? kFailed : 0;
+      int info = 0;
       {
         float2 bm = make_float2(fmaxf(fmaxf(sc[0][0].x, sc[0][1].x), fmaxf(sc[1][0].x, sc[1][1].x)),
                                 fmaxf(fmaxf(sc[0][0].y, sc[0][1].y), fmaxf(sc[1][0].y, sc[1][1].y)));
@@ -581,12 +634,16 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
         sts32<776>(w, sc[1][1].y);
       }
       if (lane == 0) sts32(lex + kExInfo + 4 * a, (uint32_t)info);
+      if (i + 1 < nb && !start_qk()) return;
       named_sync(1 + wp, 64);
       const float2 both = lds64a<kExInfo>(lex);
       const int info0 = __float_as_int(both.x), info1 = __float_as_int(both.y);
       const uint32_t lexr = lex + lwr, exa = lex + kExAlpha;
       lex = exbase + exbase + Smem::kExBytes - lex;      // the other buffer
-      if ((info0 | info1) & kFailed) break;       // both warps leave
+      if ((info0 | info1) & kFailed) {            // the other warp has left
+        drain();
+        return;
+      }
       if ((info0 | info1) & kMoved) {
 #pragma unroll
         for (int n = 0; n < T; ++n) {
@@ -605,7 +662,10 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
       // ---- P.V: the operand w * v_scale * 2^E as f16 hi + lo (22 bits), V exact
       const float up = lds32a<0>(lup);
       const float2 up2 = make_float2(up, up);
-      failed = !stage_ready(fullb + (cst >> 9), cph);
+      if (!stage_ready(fullb + (cst >> 9), cph)) {
+        give_up();
+        return;
+      }
       // A = V^T.  Row g of m-tile q is channel 16q + 2g, row g + 8 the next one; a
       // 16-bit element of the stage is two channels of a key, so the transposing
       // load pairs the keys 2c, 2c + 1 of both channels in a register.  Lane 8i + r
@@ -643,7 +703,7 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
           }
         }
       }
-      if (!failed) consumed();
+      consumed();
     }
     const bool whole = diff_windows(ctx + M - 1) == 1;
     const int b = it0.b, pair = it0.pair;
@@ -660,7 +720,7 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
       if (e) l_run.y = v;
       else l_run.x = v;
     }
-    if (lane == 0) sts32(lex + kExInfo + 4 * a, failed ? (uint32_t)kFailed : 0u);
+    if (lane == 0) sts32(lex + kExInfo + 4 * a, 0u);
     if (whole && g == 0) {
       sm.row_sum[wp][a][2 * c] = l_run.x;
       sm.row_sum[wp][a][2 * c + 1] = l_run.y;
@@ -669,16 +729,7 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
     const float2 both = lds64a<kExInfo>(lex);
     lex = exbase + exbase + Smem::kExBytes - lex;        // (a warp that runs ahead writes the other)
     if (__float_as_int(both.x) | __float_as_int(both.y)) {
-      // A copy never arrived: flag it, give the copies in flight a bounded chance
-      // to land, then leave.
-      if (lane == 0) {
-        atomicOr(p.err_word, KATTN_DEVERR_TIMEOUT);
-        for (int k = 0; k < inflight; ++k) {
-          mbar_wait_bounded(&full[cst / kBlockBytes], cph);
-          cph ^= cst == kLastStage ? 1u : 0u;
-          cst = cst == kLastStage ? 0 : cst + kBlockBytes;
-        }
-      }
+      drain();
       return;
     }
     if (whole) {
@@ -729,15 +780,14 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
     }
 
     // ---- next item
-    t += G;
-    if (t >= total) break;
+    if (++u >= u_end) break;
     if (!pnext) reach_next();                     // it had nothing left to read ahead
     pnext = false;
     row0 = row1;
     ipar ^= 1;
-    put(ipar ^ 1, t + G);
+    put_next(ipar ^ 1);
     row1 = row_entry(p, items[ipar ^ 1], lane);
-    if (items[ipar ^ 1].b >= 0) {                 // the next unit's queries (lane: a line of a row)
+    if (items[ipar ^ 1].b >= 0 && items[ipar ^ 1].fresh) {     // its queries (lane: a line of a row)
       const DiffItem& nx = items[ipar ^ 1];
       const int rr = min(nx.rg * kUnitRows + min(lane >> 2, kUnitRows - 1), R - 1), j = column(rr);
       prefetch_l2(p.q + (((int64_t)nx.b * M + j) * p.Hq + 2 * (nx.pair * p.g + rr - j * p.g) + a) * kD +
