@@ -419,30 +419,52 @@ def qk_scores_debug(q, k, k_scale, row_start, ctx_len, max_ctx: int, *, scores=N
 
 # ------------------------------------------------ differential attention --
 
-def _need_all(device, specs):
-    """Checks of several tensors on one device: (tensor, dtype, name, ndim) each."""
-    for t, dtype, name, ndim in specs:
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.device != device or not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if t.dim() != ndim:
-            raise ValueError(f"{name} must have {ndim} dimensions")
+# (the raw handle of torch's current stream: a Stream object costs 2 us more, as
+# much as the launch of a kernel)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_entry = {}          # entry points of the library by name
 
 
-def _launch(name, device, *args):
-    """One library call on torch's current stream of `device`, which need not
-    be the current device."""
-    fn = getattr(_lib.load(), name)
-    if device.index == torch.cuda.current_device():
-        _lib.check(name, fn(*args, _stream(device)))
+def _check(t, dtype, index, name, ndim):
+    """t is a contiguous tensor of the type and dimensions on CUDA device `index`."""
+    try:
+        if t.dtype is dtype and t.get_device() == index >= 0 and t.dim() == ndim and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda or t.get_device() != index:
+        where = f"cuda:{index}" if index >= 0 else "a CUDA device, as the others"
+        raise ValueError(f"{name} must be a CUDA tensor on {where}, got {t.device}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _device_of(t, name):
+    """The CUDA device index of a tensor (-1 on the host)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return t.get_device()
+
+
+def _launch(name, index, *args):
+    """One library call on torch's current stream of device `index`, which need
+    not be the current device."""
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(_lib.load(), name)
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            _lib.check(name, fn(*args, _stream(device)))
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status:
+        _lib.check(name, status)
 
 
 def diff_workspace_size(B: int, M: int, Hq: int, max_ctx: int) -> int:
@@ -460,15 +482,17 @@ def alloc_diff_workspace(B: int, M: int, Hq: int, max_ctx: int, device="cuda") -
     return ws
 
 
-def _diff_args(q, k, k_scale, v, v_scale, ctx_len, max_ctx, lam, out, workspace, extra):
+def _diff_args(q, k, k_scale, v, v_scale, ctx_len, max_ctx, lam, out, workspace):
     """Checks and defaults that decode_diff and decode_diff_paged share."""
-    if not isinstance(q, torch.Tensor) or not isinstance(lam, torch.Tensor):
-        raise TypeError("q and lam must be torch tensors")
-    _need_all(q.device, [(q, torch.float32, "q", 4), (k, torch.int8, "k", 3),
-                         (v, torch.int8, "v", 3), (k_scale, torch.float32, "k_scale", 2),
-                         (v_scale, torch.float32, "v_scale", 2),
-                         (ctx_len, torch.int32, "ctx_len", 1),
-                         (lam, torch.float32, "lam", lam.dim())] + extra)
+    index = _device_of(q, "q")
+    per_row = int(_device_of(lam, "lam") == index and lam.dim() == 3)
+    _check(q, torch.float32, index, "q", 4)
+    _check(k, torch.int8, index, "k", 3)
+    _check(v, torch.int8, index, "v", 3)
+    _check(k_scale, torch.float32, index, "k_scale", 2)
+    _check(v_scale, torch.float32, index, "v_scale", 2)
+    _check(ctx_len, torch.int32, index, "ctx_len", 1)
+    _check(lam, torch.float32, index, "lam", 3 if per_row else 1)
     B, M, Hq, d = q.shape
     Hkv, cap, dk = k.shape
     if v.shape != k.shape or k_scale.shape != (Hkv, cap) or v_scale.shape != (Hkv, cap) or dk != d:
@@ -480,21 +504,20 @@ def _diff_args(q, k, k_scale, v, v_scale, ctx_len, max_ctx, lam, out, workspace,
     if not 0 < max_ctx < 2 ** 30:
         raise ValueError("max_ctx out of range")
     H = Hq // 2
-    per_row = lam.dim() == 3
     if lam.shape != ((B, M, H) if per_row else (H,)):
         raise ValueError("lam must have shape [Hq/2] or [B][M][Hq/2]")
     if out is None:
         out = torch.empty((B, M, H, 2 * d), dtype=torch.float32, device=q.device)
     else:
-        _need_all(q.device, [(out, torch.float32, "out", 4)])
+        _check(out, torch.float32, index, "out", 4)
         if out.shape != (B, M, H, 2 * d):
             raise ValueError("out must have shape [B][M][Hq/2][256]")
     if workspace is None:
         workspace = (alloc_diff_workspace(B, M, Hq, max_ctx, q.device) if B else
                      torch.zeros(256, dtype=torch.uint8, device=q.device))
     else:
-        _need_all(q.device, [(workspace, torch.uint8, "workspace", 1)])
-    return B, M, Hq, Hkv, d, cap, int(per_row), out, workspace
+        _check(workspace, torch.uint8, index, "workspace", 1)
+    return index, B, M, Hq, Hkv, d, cap, per_row, out, workspace
 
 
 def decode_diff(q, k, k_scale, v, v_scale, row_start, ctx_len, max_ctx: int, lam, *, out=None,
@@ -510,12 +533,12 @@ def decode_diff(q, k, k_scale, v, v_scale, row_start, ctx_len, max_ctx: int, lam
     allocated here with torch if None.
     (kattn_decode_diff)
     """
-    B, M, Hq, Hkv, d, cap, per_row, out, workspace = _diff_args(
-        q, k, k_scale, v, v_scale, ctx_len, max_ctx, lam, out, workspace,
-        [(row_start, torch.int64, "row_start", 1)])
+    index, B, M, Hq, Hkv, d, cap, per_row, out, workspace = _diff_args(
+        q, k, k_scale, v, v_scale, ctx_len, max_ctx, lam, out, workspace)
+    _check(row_start, torch.int64, index, "row_start", 1)
     if row_start.shape[0] != B:
         raise ValueError("row_start must have B entries")
-    _launch("kattn_decode_diff", q.device, q.data_ptr(), k.data_ptr(), k_scale.data_ptr(),
+    _launch("kattn_decode_diff", index, q.data_ptr(), k.data_ptr(), k_scale.data_ptr(),
             v.data_ptr(), v_scale.data_ptr(), row_start.data_ptr(), ctx_len.data_ptr(),
             lam.data_ptr(), per_row, B, M, Hq, Hkv, d, cap, max_ctx, sm_scale, out.data_ptr(),
             workspace.data_ptr(), workspace.numel())
@@ -526,12 +549,12 @@ def decode_diff_paged(q, k, k_scale, v, v_scale, block_table, page_rows: int, ct
                       max_ctx: int, lam, *, out=None, sm_scale: float = 0.0, workspace=None):
     """decode_diff() over a paged cache; paging arguments as decode_paged().
     (kattn_decode_diff_paged)"""
-    B, M, Hq, Hkv, d, cap, per_row, out, workspace = _diff_args(
-        q, k, k_scale, v, v_scale, ctx_len, max_ctx, lam, out, workspace,
-        [(block_table, torch.int32, "block_table", 2)])
+    index, B, M, Hq, Hkv, d, cap, per_row, out, workspace = _diff_args(
+        q, k, k_scale, v, v_scale, ctx_len, max_ctx, lam, out, workspace)
+    _check(block_table, torch.int32, index, "block_table", 2)
     if block_table.shape[0] != B:
         raise ValueError("block_table must have B rows")
-    _launch("kattn_decode_diff_paged", q.device, q.data_ptr(), k.data_ptr(), k_scale.data_ptr(),
+    _launch("kattn_decode_diff_paged", index, q.data_ptr(), k.data_ptr(), k_scale.data_ptr(),
             v.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), block_table.shape[1],
             page_rows, ctx_len.data_ptr(), lam.data_ptr(), per_row, B, M, Hq, Hkv, d, cap, max_ctx,
             sm_scale, out.data_ptr(), workspace.data_ptr(), workspace.numel())
@@ -544,21 +567,21 @@ _NORM_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _CODE_TYPES = {torch.int8: 0, torch.float8_e4m3fn: 1}
 
 
-def _rows(t, like, name):
-    """t as rows of its last dimension: (rows, row stride).  2-D tensors may have
-    any row stride, others must be contiguous."""
-    if t.dtype != like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    if t.device != like.device or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on {like.device}, got {t.device}")
-    if t.shape != like.shape:
-        raise ValueError(f"{name} must have shape {tuple(like.shape)}")
-    d = t.shape[-1]
-    if t.dim() == 2 and (d == 1 or t.stride(1) == 1):
-        return t.shape[0], (t.stride(0) if t.shape[0] > 1 else d)
-    if not t.is_contiguous():
+def _row_stride(t, dtype, index, shape, name):
+    """The row stride of t, rows of its last dimension: any for a 2-D tensor, else
+    t is contiguous."""
+    d = shape[-1]
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of x, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    if t.is_contiguous():
+        return d
+    if t.dim() != 2 or (d > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be contiguous, or 2-D with a contiguous last dimension")
-    return t.numel() // d, d
+    return t.stride(0) if shape[0] > 1 else d
 
 
 def rms_norm_quant(x, weight, *, residual=None, residual_out=None, eps: float = 1e-6,
@@ -572,45 +595,55 @@ def rms_norm_quant(x, weight, *, residual=None, residual_out=None, eps: float = 
     per row [...] or per 128 channels [..., d/128] (group = 128), so that codes *
     scales is h / rms(h) * weight.  (kattn_rms_norm_quant)
     """
-    if not isinstance(x, torch.Tensor) or not isinstance(weight, torch.Tensor):
-        raise TypeError("x and weight must be torch tensors")
-    if x.dtype not in _NORM_TYPES:
-        raise TypeError(f"x must be float32, bfloat16 or float16, got {x.dtype}")
-    if x.dim() < 1 or x.shape[-1] < 1:
+    index = _device_of(x, "x")
+    dtype, shape = x.dtype, x.shape
+    x_type = _NORM_TYPES.get(dtype)
+    if x_type is None:
+        raise TypeError(f"x must be float32, bfloat16 or float16, got {dtype}")
+    if len(shape) < 1 or shape[-1] < 1:
         raise ValueError("x must have a last dimension of at least 1")
-    rows, xs = _rows(x, x, "x")
-    d = x.shape[-1]
-    _need_all(x.device, [(weight, x.dtype, "weight", 1)])
+    if index < 0:
+        raise ValueError("x must be a CUDA tensor")
+    d = shape[-1]
+    rows = x.numel() // d
+    groups = 1
+    if group:
+        if group != 128 or d % 128:
+            raise ValueError("group must be 0, or 128 for rows of a multiple of 128 channels")
+        groups = d // 128
+    x_stride = _row_stride(x, dtype, index, shape, "x")
+    _check(weight, dtype, index, "weight", 1)
     if weight.shape[0] != d:
         raise ValueError("weight must have one entry per channel")
-    if group not in (0, 128) or (group and d % group):
-        raise ValueError("group must be 0, or 128 for rows of a multiple of 128 channels")
-    rs = ros = d
-    rp = rop = 0
+    res_stride = res_out_stride = d
+    res_ptr = res_out_ptr = 0
     if residual is not None:
-        rs = _rows(residual, x, "residual")[1]
+        res_stride = _row_stride(residual, dtype, index, shape, "residual")
         if residual_out is None:
-            residual_out = residual
-        ros = _rows(residual_out, x, "residual_out")[1]
-        rp, rop = residual.data_ptr(), residual_out.data_ptr()
+            residual_out, res_out_stride = residual, res_stride
+        else:
+            res_out_stride = _row_stride(residual_out, dtype, index, shape, "residual_out")
+        res_ptr, res_out_ptr = residual.data_ptr(), residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
-    if out.dtype not in _CODE_TYPES:
+        out = torch.empty(shape, dtype=out_dtype, device=x.device)
+    code_type = _CODE_TYPES.get(out.dtype)
+    if code_type is None:
         raise TypeError(f"codes must be int8 or float8_e4m3fn, got {out.dtype}")
-    scale_shape = x.shape[:-1] + ((d // group,) if group else ())
-    if out_scale is None:
-        out_scale = torch.empty(scale_shape, dtype=torch.float32, device=x.device)
-    _need_all(x.device, [(out, out.dtype, "out", x.dim()),
-                         (out_scale, torch.float32, "out_scale", out_scale.dim())])
-    if out.shape != x.shape:
+    _check(out, out.dtype, index, "out", len(shape))
+    if out.shape != shape:
         raise ValueError("out must have the shape of x")
-    if out_scale.numel() != rows * (d // group if group else 1):
-        raise ValueError(f"out_scale must have shape {tuple(scale_shape)}")
-    _launch("kattn_rms_norm_quant", x.device, x.data_ptr(), rp, weight.data_ptr(),
-            _NORM_TYPES[x.dtype], rows, d, xs, rs, ros, eps, group, _CODE_TYPES[out.dtype], rop,
-            out.data_ptr(), out_scale.data_ptr())
+    if out_scale is None:
+        out_scale = torch.empty(shape[:-1] + ((groups,) if group else ()), dtype=torch.float32,
+                                device=x.device)
+    else:
+        _check(out_scale, torch.float32, index, "out_scale", out_scale.dim())
+        if out_scale.numel() != rows * groups:
+            raise ValueError("out_scale must have one entry per scale")
+    _launch("kattn_rms_norm_quant", index, x.data_ptr(), res_ptr, weight.data_ptr(), x_type, rows, d,
+            x_stride, res_stride, res_out_stride, eps, group, code_type, res_out_ptr, out.data_ptr(),
+            out_scale.data_ptr())
     return out, out_scale
 
 
@@ -629,25 +662,29 @@ def alloc_page_workspace(n_slots: int, n_pages: int, device="cuda") -> torch.Ten
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _page_args(block_table, ref_count, lists, workspace):
-    """Checks that the page operations share; lists: (tensor, name) each, all of
-    one length.  Returns (n_slots, max_pages, n_pages, n, workspace)."""
-    if not isinstance(block_table, torch.Tensor):
-        raise TypeError("block_table must be a torch.Tensor")
-    _need_all(block_table.device,
-              [(block_table, torch.int32, "block_table", 2), (ref_count, torch.int32, "ref_count", 1)]
-              + [(t, torch.int32, name, 1) for t, name in lists])
+def _page_args(block_table, ref_count, seqs, name, workspace):
+    """Checks that the page operations share; seqs: the list of slots, or None.
+    Returns (device index, n_slots, max_pages, n_pages, n, workspace)."""
+    index = _device_of(block_table, "block_table")
+    _check(block_table, torch.int32, index, "block_table", 2)
+    _check(ref_count, torch.int32, index, "ref_count", 1)
     n_slots, max_pages = block_table.shape
     n_pages = ref_count.shape[0]
-    n = lists[0][0].shape[0] if lists else 0
-    for t, name in lists:
-        if t.shape[0] != n:
-            raise ValueError(f"{name} must have {n} entries")
+    n = 0
+    if name:
+        _check(seqs, torch.int32, index, name, 1)
+        n = seqs.shape[0]
     if workspace is None:
         workspace = alloc_page_workspace(n_slots, n_pages, block_table.device)
     else:
-        _need_all(block_table.device, [(workspace, torch.uint8, "workspace", 1)])
-    return n_slots, max_pages, n_pages, n, workspace
+        _check(workspace, torch.uint8, index, "workspace", 1)
+    return index, n_slots, max_pages, n_pages, n, workspace
+
+
+def _check_list(t, index, name, n):
+    _check(t, torch.int32, index, name, 1)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} entries")
 
 
 def reserve_pages(block_table, ref_count, seqs, lens, page_rows: int, *, workspace=None) -> None:
@@ -656,8 +693,9 @@ def reserve_pages(block_table, ref_count, seqs, lens, page_rows: int, *, workspa
     block_table int32 [n_slots][max_pages] (unused entries below 0), ref_count
     int32 [n_pages], seqs and lens int32 [n]; both tables are updated in place.
     """
-    S, mp, P, n, ws = _page_args(block_table, ref_count, [(seqs, "seqs"), (lens, "lens")], workspace)
-    _launch("kattn_reserve_pages", block_table.device, block_table.data_ptr(), S, mp,
+    index, S, mp, P, n, ws = _page_args(block_table, ref_count, seqs, "seqs", workspace)
+    _check_list(lens, index, "lens", n)
+    _launch("kattn_reserve_pages", index, block_table.data_ptr(), S, mp,
             ref_count.data_ptr(), P, page_rows, seqs.data_ptr(), lens.data_ptr(), n, ws.data_ptr(),
             ws.numel())
 
@@ -665,8 +703,8 @@ def reserve_pages(block_table, ref_count, seqs, lens, page_rows: int, *, workspa
 def free_sequences(block_table, ref_count, seqs, *, workspace=None) -> None:
     """Release the pages of the slots seqs (int32 [n]); in place
     (kattn_free_sequences)."""
-    S, mp, P, n, ws = _page_args(block_table, ref_count, [(seqs, "seqs")], workspace)
-    _launch("kattn_free_sequences", block_table.device, block_table.data_ptr(), S, mp,
+    index, S, mp, P, n, ws = _page_args(block_table, ref_count, seqs, "seqs", workspace)
+    _launch("kattn_free_sequences", index, block_table.data_ptr(), S, mp,
             ref_count.data_ptr(), P, seqs.data_ptr(), n, ws.data_ptr(), ws.numel())
 
 
@@ -675,18 +713,18 @@ def fork_sequences(block_table, ref_count, parents, children, lens, page_rows: i
     """Slot children[i] becomes a branch of the first lens[i] rows of slot
     parents[i]: full pages shared, the last partial one to be copied.  Returns
     (src, dst), int32 [n], for copy_pages() (kattn_fork_sequences)."""
-    S, mp, P, n, ws = _page_args(
-        block_table, ref_count, [(children, "children"), (parents, "parents"), (lens, "lens")],
-        workspace)
-    dev = block_table.device
+    index, S, mp, P, n, ws = _page_args(block_table, ref_count, children, "children", workspace)
+    _check_list(parents, index, "parents", n)
+    _check_list(lens, index, "lens", n)
     if src is None:
-        src = torch.empty(n, dtype=torch.int32, device=dev)
+        src = torch.empty_like(lens)
+    else:
+        _check_list(src, index, "src", n)
     if dst is None:
-        dst = torch.empty(n, dtype=torch.int32, device=dev)
-    _need_all(dev, [(src, torch.int32, "src", 1), (dst, torch.int32, "dst", 1)])
-    if src.shape[0] != n or dst.shape[0] != n:
-        raise ValueError(f"src and dst must have {n} entries")
-    _launch("kattn_fork_sequences", dev, block_table.data_ptr(), S, mp, ref_count.data_ptr(), P,
+        dst = torch.empty_like(lens)
+    else:
+        _check_list(dst, index, "dst", n)
+    _launch("kattn_fork_sequences", index, block_table.data_ptr(), S, mp, ref_count.data_ptr(), P,
             page_rows, parents.data_ptr(), children.data_ptr(), lens.data_ptr(), n, src.data_ptr(),
             dst.data_ptr(), ws.data_ptr(), ws.numel())
     return src, dst
@@ -700,27 +738,24 @@ def compact_pages(block_table, ref_count, *, table_out=None, ref_out=None, src=N
     the moves (new tensors unless given; the inputs themselves for an update in
     place), the moves for copy_pages() (int32 [max(1, n_pages // 2)], -1 past
     the last), and counts = int32 [n_live, n_moves] (kattn_compact_pages)."""
-    S, mp, P, _, ws = _page_args(block_table, ref_count, [], workspace)
-    dev = block_table.device
+    index, S, mp, P, _, ws = _page_args(block_table, ref_count, None, None, workspace)
     most = max(1, P // 2)
+
+    def array(t, name, like, n):
+        if t is None:
+            return torch.empty(n, dtype=torch.int32, device=like.device)
+        _check_list(t, index, name, n)
+        return t
     if table_out is None:
         table_out = torch.empty_like(block_table)
-    if ref_out is None:
-        ref_out = torch.empty_like(ref_count)
-    if src is None:
-        src = torch.empty(most, dtype=torch.int32, device=dev)
-    if dst is None:
-        dst = torch.empty(most, dtype=torch.int32, device=dev)
-    if counts is None:
-        counts = torch.empty(2, dtype=torch.int32, device=dev)
-    _need_all(dev, [(table_out, torch.int32, "table_out", 2), (ref_out, torch.int32, "ref_out", 1),
-                    (src, torch.int32, "src", 1), (dst, torch.int32, "dst", 1),
-                    (counts, torch.int32, "counts", 1)])
-    if table_out.shape != block_table.shape or ref_out.shape != ref_count.shape:
-        raise ValueError("table_out / ref_out must have the shapes of block_table / ref_count")
-    if src.shape[0] != most or dst.shape[0] != most or counts.shape[0] != 2:
-        raise ValueError(f"src and dst must have {most} entries, counts 2")
-    _launch("kattn_compact_pages", dev, block_table.data_ptr(), S, mp, ref_count.data_ptr(), P,
+    else:
+        _check(table_out, torch.int32, index, "table_out", 2)
+        if table_out.shape != block_table.shape:
+            raise ValueError("table_out must have the shape of block_table")
+    ref_out = array(ref_out, "ref_out", ref_count, P)
+    src, dst = array(src, "src", ref_count, most), array(dst, "dst", ref_count, most)
+    counts = array(counts, "counts", ref_count, 2)
+    _launch("kattn_compact_pages", index, block_table.data_ptr(), S, mp, ref_count.data_ptr(), P,
             table_out.data_ptr(), ref_out.data_ptr(), src.data_ptr(), dst.data_ptr(),
             counts.data_ptr(), ws.data_ptr(), ws.numel())
     return table_out, ref_out, src, dst, counts
@@ -734,29 +769,28 @@ def copy_pages(k, k_scale, v, v_scale, src, dst, page_rows: int, *, count=None,
     moves are made.  workspace: any workspace of the library (its error word
     takes the checks of the entries); allocated here if None.
     (kattn_copy_pages)"""
-    if not isinstance(k, torch.Tensor):
-        raise TypeError("k must be a torch.Tensor")
-    dev = k.device
-    specs = [(k, torch.int8, "k", 3), (v, torch.int8, "v", 3),
-             (k_scale, torch.float32, "k_scale", 2), (v_scale, torch.float32, "v_scale", 2),
-             (src, torch.int32, "src", 1), (dst, torch.int32, "dst", 1)]
-    if count is not None:
-        specs.append((count, torch.int32, "count", 1))
-    if workspace is None:
-        workspace = torch.zeros(256, dtype=torch.uint8, device=dev)
-    specs.append((workspace, torch.uint8, "workspace", 1))
-    _need_all(dev, specs)
+    index = _device_of(k, "k")
+    _check(k, torch.int8, index, "k", 3)
+    _check(v, torch.int8, index, "v", 3)
+    _check(k_scale, torch.float32, index, "k_scale", 2)
+    _check(v_scale, torch.float32, index, "v_scale", 2)
+    _check(src, torch.int32, index, "src", 1)
+    n = src.shape[0]
+    _check_list(dst, index, "dst", n)
     Hkv, cap, d = k.shape
     if v.shape != k.shape or k_scale.shape != (Hkv, cap) or v_scale.shape != (Hkv, cap):
         raise ValueError("k/v/scales shapes disagree")
-    if src.shape != dst.shape:
-        raise ValueError("src and dst must have the same length")
-    if count is not None and count.shape[0] != 1:
-        raise ValueError("count must have one entry")
-    _launch("kattn_copy_pages", dev, k.data_ptr(), k_scale.data_ptr(), v.data_ptr(),
-            v_scale.data_ptr(), Hkv, d, cap, page_rows, src.data_ptr(), dst.data_ptr(),
-            src.shape[0], 0 if count is None else count.data_ptr(), workspace.data_ptr(),
-            workspace.numel())
+    count_ptr = 0
+    if count is not None:
+        _check_list(count, index, "count", 1)
+        count_ptr = count.data_ptr()
+    if workspace is None:
+        workspace = torch.zeros(256, dtype=torch.uint8, device=k.device)
+    else:
+        _check(workspace, torch.uint8, index, "workspace", 1)
+    _launch("kattn_copy_pages", index, k.data_ptr(), k_scale.data_ptr(), v.data_ptr(),
+            v_scale.data_ptr(), Hkv, d, cap, page_rows, src.data_ptr(), dst.data_ptr(), n, count_ptr,
+            workspace.data_ptr(), workspace.numel())
 
 
 def get_device_status(workspace: torch.Tensor) -> int:
