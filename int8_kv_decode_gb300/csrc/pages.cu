@@ -1,9 +1,10 @@
 // The pages of a paged cache: reserving, freeing, forking, compacting, copying.
 //
-// reserve, fork and compact are each one cluster of kCluster blocks: the
-// phases below depend on one another over the whole pool, and the barrier of a
-// cluster costs a fraction of a microsecond where a second launch costs
-// several.  What the blocks hand over goes through the workspace in L2.
+// reserve, fork and compact each plan over the whole pool in phases that depend on
+// one another.  A small pool is planned by one block; a large one by a cluster of
+// kCluster blocks, whose barrier costs a fraction of a microsecond where another
+// launch costs several.  What the blocks hand over goes through the workspace in
+// L2.  Bound by latency: a phase is one or two dependent trips to L2.
 #include <algorithm>
 
 #include "device_common.cuh"
@@ -12,29 +13,30 @@
 namespace kattn {
 namespace {
 
-constexpr int kCluster = 8;                       // blocks of a plan (the portable cluster size)
+constexpr int kCluster = 16;                      // blocks of a large plan
 constexpr int kThreads = 1024;
 constexpr int kWarpsPerBlock = kThreads / 32;
-constexpr int kUnroll = 8;                        // pages a thread looks at per tile
-constexpr int kTile = kThreads * kUnroll;
-static_assert(kUnroll * kWarpsPerBlock == 256, "one counter per thread of the first 8 warps");
+constexpr int kAhead = 8;                         // loads a lane has in flight
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire;\n" ::: "memory");
+// CL: blocks of the plan, 1 or kCluster.
+template <int CL>
+__device__ __forceinline__ void plan_sync() {
+  if constexpr (CL == 1) {
+    __syncthreads();
+  } else {
+    asm volatile("barrier.cluster.arrive.release;\n" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;\n" ::: "memory");
+  }
 }
-__device__ __forceinline__ int cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
-  return (int)r;
+template <int CL>
+__device__ __forceinline__ int plan_rank() {
+  return CL == 1 ? 0 : (int)blockIdx.x;           // the grid is one cluster
 }
 
 __device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
 struct BlockScratch {
   int warp[kWarpsPerBlock];
-  int count[256];
-  int total;
 };
 
 // Sum of v over the block, to every thread.
@@ -70,88 +72,110 @@ __device__ __forceinline__ int block_prefix(int v, BlockScratch& s, int* total) 
 struct Chunk {
   int per, lo, hi;
 };
+template <int CL>
 __device__ __forceinline__ Chunk chunk_of(int n_pages, int rank) {
   Chunk c;
-  c.per = (n_pages + kCluster - 1) / kCluster;
+  c.per = (n_pages + CL - 1) / CL;
   c.lo = min(n_pages, rank * c.per);
   c.hi = min(n_pages, c.lo + c.per);
   return c;
 }
 
-// Ranks of the pages of [lo, hi) for which pick(page, count) holds, in
-// ascending order: put(rank, page, count) is called for each.  Returns how many
-// there are (to every thread).  Per tile, each warp's ballot gives the ranks
-// within 32 pages and a scan over the tile's 256 ballots those between them.
+// Ranks of the pages of [lo, hi) for which pick(page, count) holds, in ascending
+// order: put(rank, page, count) is called for each.  Returns how many there are (to
+// every thread).  Each warp has a run of pages and goes over it twice, once to
+// count (ballots), once, after a scan over the warps, to give the ranks.
 template <typename Pick, typename Put>
 __device__ __forceinline__ int rank_pages(const int32_t* refs, int lo, int hi, BlockScratch& s,
                                           Pick pick, Put put) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int base = 0;
-  for (int t0 = lo; t0 < hi; t0 += kTile) {
-    int c[kUnroll];
-    unsigned bal[kUnroll];
+  const int n = max(0, hi - lo), run = (n + kThreads - 1) / kThreads * 32;
+  const int w0 = min(n, warp * run) + lo, w1 = min(n, warp * run + run) + lo;
+  auto over = [&](auto&& each) {
+    for (int p0 = w0; p0 < w1; p0 += 32 * kAhead) {
+      int c[kAhead];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int p = t0 + u * kThreads + (int)threadIdx.x;
-      c[u] = p < hi ? __ldcg(refs + p) : 0;
+      for (int u = 0; u < kAhead; ++u) {
+        const int p = p0 + 32 * u + lane;
+        c[u] = p < w1 ? __ldcg(refs + p) : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int p = p0 + 32 * u + lane;
+        const bool take = p < w1 && pick(p, c[u]);
+        each(p, c[u], take, __ballot_sync(0xffffffffu, take));
+      }
     }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int p = t0 + u * kThreads + (int)threadIdx.x;
-      bal[u] = __ballot_sync(0xffffffffu, p < hi && pick(p, c[u]));
-    }
-    __syncthreads();                              // the last tile's counters are read
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (lane == 0) s.count[u * kWarpsPerBlock + warp] = __popc(bal[u]);
-    __syncthreads();
-    const int mine = threadIdx.x < 256 ? s.count[threadIdx.x] : 0;
-    int total;
-    const int before = block_prefix(mine, s, &total);
-    if (threadIdx.x < 256) s.count[threadIdx.x] = before;
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (bal[u] >> lane & 1u)
-        put(base + s.count[u * kWarpsPerBlock + warp] + __popc(bal[u] & ((1u << lane) - 1u)),
-            t0 + u * kThreads + (int)threadIdx.x, c[u]);
-    base += total;
-  }
-  return base;
+  };
+  int mine = 0;
+  over([&](int, int, bool, unsigned bal) { mine += __popc(bal); });
+  __syncthreads();
+  if (lane == 0) s.warp[warp] = mine;
+  __syncthreads();
+  const int v = s.warp[lane], total = warp_sum_int(v);
+  int at = warp_sum_int(lane < warp ? v : 0);
+  over([&](int p, int c, bool take, unsigned bal) {
+    if (take) put(at + __popc(bal & ((1u << lane) - 1u)), p, c);
+    at += __popc(bal);
+  });
+  return total;
 }
 
 // Where the entry of rank k lies in a list that each block wrote from its
 // chunk's start on: block c's ranks begin at the sum of the counts before it.
+template <int CL>
 struct Places {
-  int start[kCluster + 1];
+  int start[CL + 1];
   int per;
 };
-__device__ __forceinline__ Places places_of(const int* chunk, int per) {
-  Places p;
+template <int CL>
+__device__ __forceinline__ Places<CL> places_of(const int* chunk, int per) {
+  Places<CL> p;
   p.per = per;
+  int v[CL];
+#pragma unroll
+  for (int c = 0; c < CL; ++c) v[c] = __ldcg(chunk + c);
   p.start[0] = 0;
 #pragma unroll
-  for (int c = 0; c < kCluster; ++c) p.start[c + 1] = p.start[c] + __ldcg(chunk + c);
+  for (int c = 0; c < CL; ++c) p.start[c + 1] = p.start[c] + v[c];
   return p;
 }
-__device__ __forceinline__ int place(const Places& p, int k) {
+template <int CL>
+__device__ __forceinline__ int place(const Places<CL>& p, int k) {
   int at = k;
 #pragma unroll
-  for (int c = 1; c < kCluster; ++c)
+  for (int c = 1; c < CL; ++c)
     if (k >= p.start[c]) at = c * p.per + k - p.start[c];
   return at;
 }
 
-// One reference less on page e of a row (an entry below 0 is unused).
-__device__ __forceinline__ void drop_page(const PageParams& p, int e) {
-  if (e < 0) return;
-  if (e >= p.n_pages) {
-    atomicOr(p.ws.err, KATTN_DEVERR_BAD_PAGE);
-    return;
+// One reference less on each of a lane's pages of a row (an entry below 0 is
+// unused): the subtractions go out together, then their results are looked at.
+template <int N>
+__device__ __forceinline__ void drop_pages(const PageParams& p, const int (&e)[N]) {
+  int before[N];
+  bool outside = false;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const bool in = (unsigned)e[u] < (unsigned)p.n_pages;
+    outside |= e[u] >= p.n_pages;
+    before[u] = in ? atomicSub(p.refs + e[u], 1) : 1;
   }
-  if (atomicSub(p.refs + e, 1) <= 0) {
-    atomicAdd(p.refs + e, 1);
-    atomicOr(p.ws.err, KATTN_DEVERR_BAD_PAGE);
+#pragma unroll
+  for (int u = 0; u < N; ++u)
+    if (before[u] <= 0) {                         // it had none: put it back
+      atomicAdd(p.refs + e[u], 1);
+      outside = true;
+    }
+  if (outside) atomicOr(p.ws.err, KATTN_DEVERR_BAD_PAGE);
+}
+// Entries c0 + 32 u + lane of a row, -1 past the end.
+__device__ __forceinline__ void load_entries(const int32_t* row, int c0, int end, int (&e)[kAhead]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+    const int c = c0 + 32 * u + lane;
+    e[u] = c < end ? __ldcg(row + c) : -1;
   }
 }
 
@@ -164,15 +188,17 @@ __device__ __forceinline__ int pages_for(const PageParams& p, int len) {
 }
 
 // List entries [lo, hi) of block `rank`.
+template <int CL>
 __device__ __forceinline__ void list_range(int n, int rank, int& lo, int& hi) {
-  const int per = (n + kCluster - 1) / kCluster;
+  const int per = (n + CL - 1) / CL;
   lo = min(n, rank * per);
   hi = min(n, lo + per);
 }
 
 // The first list entry that names a slot wins it: claim holds n - i.
+template <int CL>
 __device__ __forceinline__ void claim_slots(const PageParams& p, int rank) {
-  for (int i = rank * kThreads + threadIdx.x; i < p.n; i += kCluster * kThreads) {
+  for (int i = rank * kThreads + threadIdx.x; i < p.n; i += CL * kThreads) {
     const int s = p.seqs[i];
     if ((unsigned)s < (unsigned)p.n_slots) atomicMax(p.ws.claim + s, p.n - i);
   }
@@ -185,37 +211,42 @@ __device__ __forceinline__ bool slot_mine(const PageParams& p, int i, int s) {
 //   1. claims;  2. per list entry the missing pages (one warp each), and the
 //   free pages of the block's chunk in order;  3. the entries' first ranks (a
 //   scan over the list) and the pages of those ranks into the table.
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
-reserve_kernel(const PageParams p) {
+template <int CL>
+__global__ void __launch_bounds__(kThreads) reserve_kernel(const PageParams p) {
   __shared__ BlockScratch s;
   __shared__ int first[kThreads];
-  const int rank = cluster_rank();
+  const int rank = plan_rank<CL>();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  claim_slots(p, rank);
-  cluster_sync();
+  claim_slots<CL>(p, rank);
+  plan_sync<CL>();
   int lo, hi;
-  list_range(p.n, rank, lo, hi);
+  list_range<CL>(p.n, rank, lo, hi);
   for (int i = lo + warp; i < hi; i += kWarpsPerBlock) {
     const int slot = p.seqs[i], len = p.lens[i];
     int miss = 0;
     if (slot_mine(p, i, slot) && len_ok(p, len)) {
       const int need = pages_for(p, len);
       const int32_t* row = p.table + (int64_t)slot * p.max_pages;
-      for (int c = lane; c < need; c += 32) miss += __ldcg(row + c) < 0;
+      for (int c0 = 0; c0 < need; c0 += 32 * kAhead) {
+        int e[kAhead];
+        load_entries(row, c0, need, e);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) miss += c0 + 32 * u + lane < need && e[u] < 0;
+      }
       miss = warp_sum_int(miss);
     } else if (lane == 0) {
       atomicOr(p.ws.err, KATTN_DEVERR_BAD_SEQUENCE);
     }
     if (lane == 0) p.ws.flag[i] = miss;
   }
-  const Chunk ch = chunk_of(p.n_pages, rank);
+  const Chunk ch = chunk_of<CL>(p.n_pages, rank);
   int* list = p.ws.list + ch.lo;
   const int free_here = rank_pages(
       p.refs, ch.lo, ch.hi, s, [](int, int c) { return c == 0; },
       [&](int r, int page, int) { list[r] = page; });
   if (threadIdx.x == 0) p.ws.chunk[rank] = free_here;
-  cluster_sync();
-  const Places pl = places_of(p.ws.chunk, ch.per);
+  plan_sync<CL>();
+  const Places<CL> pl = places_of<CL>(p.ws.chunk, ch.per);
   // pages wanted before this block's entries, and by the whole list
   int64_t before = 0, all = 0;
   for (int i = threadIdx.x; i < p.n; i += kThreads) {
@@ -229,7 +260,7 @@ reserve_kernel(const PageParams p) {
   const int all_hi = block_sum((int)(all >> 20), s), all_lo = block_sum((int)(all & (cap - 1)), s);
   const int bef_hi = block_sum((int)(before >> 20), s), bef_lo = block_sum((int)(before & (cap - 1)), s);
   const int64_t want = (int64_t)all_hi * cap + all_lo;
-  const bool enough = want <= (int64_t)pl.start[kCluster];
+  const bool enough = want <= (int64_t)pl.start[CL];
   if (!enough && rank == 0 && threadIdx.x == 0) atomicOr(p.ws.err, KATTN_DEVERR_NO_PAGES);
   if (enough) {
     int base = (int)((int64_t)bef_hi * cap + bef_lo);
@@ -246,16 +277,22 @@ reserve_kernel(const PageParams p) {
         const int need = pages_for(p, p.lens[i0 + k]);
         int32_t* row = p.table + (int64_t)slot * p.max_pages;
         int at = first[k];
-        for (int c0 = 0; c0 < need; c0 += 32) {
-          const int c = c0 + lane;
-          const bool miss = c < need && __ldcg(row + c) < 0;
-          const unsigned bal = __ballot_sync(0xffffffffu, miss);
-          if (miss) {
-            const int page = __ldcg(p.ws.list + place(pl, at + __popc(bal & ((1u << lane) - 1u))));
-            row[c] = page;
-            p.refs[page] = 1;
+        for (int c0 = 0; c0 < need; c0 += 32 * kAhead) {
+          int e[kAhead];
+          load_entries(row, c0, need, e);
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {      // the pages first, then the stores
+            const bool miss = c0 + 32 * u + lane < need && e[u] < 0;
+            const unsigned bal = __ballot_sync(0xffffffffu, miss);
+            e[u] = miss ? __ldcg(p.ws.list + place(pl, at + __popc(bal & ((1u << lane) - 1u)))) : -1;
+            at += __popc(bal);
           }
-          at += __popc(bal);
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u)
+            if (e[u] >= 0) {
+              row[c0 + 32 * u + lane] = e[u];
+              p.refs[e[u]] = 1;
+            }
         }
       }
       base += total;
@@ -280,7 +317,8 @@ __global__ void __launch_bounds__(256) free_kernel(const PageParams p) {
   int32_t* row = p.table + (int64_t)slot * p.max_pages;
   for (int c = threadIdx.x; c < p.max_pages; c += blockDim.x) {
     if (__ldcg(row + c) == -1) continue;
-    drop_page(p, atomicExch(row + c, -1));
+    const int e[1] = {atomicExch(row + c, -1)};
+    drop_pages(p, e);
   }
 }
 
@@ -290,20 +328,20 @@ __global__ void __launch_bounds__(256) free_kernel(const PageParams p) {
 //   pages in order;  4. the ranks of the pairs that need a page of their own,
 //   and the children's rows.
 // flag: 0 skipped, 1 valid, 2 valid with a page of its own.
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
-fork_kernel(const PageParams p) {
+template <int CL>
+__global__ void __launch_bounds__(kThreads) fork_kernel(const PageParams p) {
   __shared__ BlockScratch s;
   __shared__ int first[kThreads];
-  const int rank = cluster_rank();
+  const int rank = plan_rank<CL>();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  claim_slots(p, rank);
-  for (int i = rank * kThreads + threadIdx.x; i < p.n; i += kCluster * kThreads) {
+  claim_slots<CL>(p, rank);
+  for (int i = rank * kThreads + threadIdx.x; i < p.n; i += CL * kThreads) {
     const int s2 = p.parents[i];
     if ((unsigned)s2 < (unsigned)p.n_slots) p.ws.mark[s2] = 1;
   }
-  cluster_sync();
+  plan_sync<CL>();
   int lo, hi;
-  list_range(p.n, rank, lo, hi);
+  list_range<CL>(p.n, rank, lo, hi);
   const int page_mask = (1 << p.page_shift) - 1;
   for (int i = lo + warp; i < hi; i += kWarpsPerBlock) {
     const int child = p.seqs[i], parent = p.parents[i], len = p.lens[i];
@@ -314,10 +352,14 @@ fork_kernel(const PageParams p) {
       const int need = pages_for(p, len);
       const int32_t* row = p.table + (int64_t)parent * p.max_pages;
       bool absent = false, outside = false;
-      for (int c = lane; c < need; c += 32) {
-        const int e = __ldcg(row + c);
-        absent |= e < 0;
-        outside |= e >= p.n_pages;
+      for (int c0 = 0; c0 < need; c0 += 32 * kAhead) {
+        int e[kAhead];
+        load_entries(row, c0, need, e);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          absent |= c0 + 32 * u + lane < need && e[u] < 0;
+          outside |= e[u] >= p.n_pages;
+        }
       }
       if (__any_sync(0xffffffffu, absent)) err |= KATTN_DEVERR_BAD_SEQUENCE;
       if (__any_sync(0xffffffffu, outside)) err |= KATTN_DEVERR_BAD_PAGE;
@@ -325,22 +367,26 @@ fork_kernel(const PageParams p) {
     }
     if (ok) {
       const int32_t* row = p.table + (int64_t)child * p.max_pages;
-      for (int c = lane; c < p.max_pages; c += 32) drop_page(p, __ldcg(row + c));
+      for (int c0 = 0; c0 < p.max_pages; c0 += 32 * kAhead) {
+        int e[kAhead];
+        load_entries(row, c0, p.max_pages, e);
+        drop_pages(p, e);
+      }
     } else if (lane == 0) {
       atomicOr(p.ws.err, err);
     }
     if (lane == 0) p.ws.flag[i] = !ok ? 0 : (len & page_mask) ? 2 : 1;
   }
-  cluster_sync();
-  const Chunk ch = chunk_of(p.n_pages, rank);
+  plan_sync<CL>();
+  const Chunk ch = chunk_of<CL>(p.n_pages, rank);
   int* list = p.ws.list + ch.lo;
   const int free_here = rank_pages(
       p.refs, ch.lo, ch.hi, s, [](int, int c) { return c == 0; },
       [&](int r, int page, int) { list[r] = page; });
   if (threadIdx.x == 0) p.ws.chunk[rank] = free_here;
-  cluster_sync();
-  const Places pl = places_of(p.ws.chunk, ch.per);
-  const int supply = pl.start[kCluster];
+  plan_sync<CL>();
+  const Places<CL> pl = places_of<CL>(p.ws.chunk, ch.per);
+  const int supply = pl.start[CL];
   int before = 0;
   for (int i = threadIdx.x; i < lo; i += kThreads) before += __ldcg(p.ws.flag + i) == 2;
   int base = block_sum(before, s);
@@ -369,15 +415,15 @@ fork_kernel(const PageParams p) {
             full = 0;
           }
         }
-        for (int c = lane; c < p.max_pages; c += 32) {
-          int e = -1;
-          if (c < full) {
-            e = __ldcg(src + c);
-            atomicAdd(p.refs + e, 1);
-          } else if (c == full && to >= 0) {
-            e = to;
+        for (int c0 = 0; c0 < p.max_pages; c0 += 32 * kAhead) {
+          int e[kAhead];
+          load_entries(src, c0, full, e);
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {
+            const int c = c0 + 32 * u + lane;
+            if (c < full) atomicAdd(p.refs + e[u], 1);
+            if (c < p.max_pages) row[c] = c == full ? to : e[u];
           }
-          row[c] = e;
         }
       }
       if (lane == 0) {
@@ -399,25 +445,25 @@ fork_kernel(const PageParams p) {
 //   and the live pages at or above it, in order;  3. the moves, the counts
 //   after them, and the map of the pages that move.  rewrite_kernel then takes
 //   the table through the map.
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1)
-compact_kernel(const PageParams p) {
+template <int CL>
+__global__ void __launch_bounds__(kThreads) compact_kernel(const PageParams p) {
   __shared__ BlockScratch s;
-  const int rank = cluster_rank();
-  const Chunk ch = chunk_of(p.n_pages, rank);
+  const int rank = plan_rank<CL>();
+  const Chunk ch = chunk_of<CL>(p.n_pages, rank);
   int live = 0;
-  for (int t0 = ch.lo; t0 < ch.hi; t0 += kTile) {
+  for (int t0 = ch.lo; t0 < ch.hi; t0 += kThreads * kAhead) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < kAhead; ++u) {
       const int at = t0 + u * kThreads + (int)threadIdx.x;
       live += at < ch.hi && __ldcg(p.refs + at) > 0;
     }
   }
   live = block_sum(live, s);
   if (threadIdx.x == 0) p.ws.chunk[rank] = live;
-  cluster_sync();
+  plan_sync<CL>();
   int n_live = 0;
 #pragma unroll
-  for (int c = 0; c < kCluster; ++c) n_live += __ldcg(p.ws.chunk + c);
+  for (int c = 0; c < CL; ++c) n_live += __ldcg(p.ws.chunk + c);
   int* holes = p.ws.list + ch.lo;
   int2* movers = p.ws.list2 + ch.lo;
   const int n_holes = rank_pages(
@@ -431,15 +477,15 @@ compact_kernel(const PageParams p) {
       },
       [&](int r, int page, int c) { movers[r] = make_int2(page, c); });
   if (threadIdx.x == 0) {
-    p.ws.chunk[kCluster + rank] = n_holes;
-    p.ws.chunk[2 * kCluster + rank] = n_movers;
+    p.ws.chunk[CL + rank] = n_holes;
+    p.ws.chunk[2 * CL + rank] = n_movers;
   }
-  cluster_sync();
-  const Places ph = places_of(p.ws.chunk + kCluster, ch.per);
-  const Places pm = places_of(p.ws.chunk + 2 * kCluster, ch.per);
-  const int moves = pm.start[kCluster];           // as many as holes
+  plan_sync<CL>();
+  const Places<CL> ph = places_of<CL>(p.ws.chunk + CL, ch.per);
+  const Places<CL> pm = places_of<CL>(p.ws.chunk + 2 * CL, ch.per);
+  const int moves = pm.start[CL];           // as many as holes
   const int slots = max(1, p.n_pages / 2);
-  for (int k = rank * kThreads + threadIdx.x; k < slots; k += kCluster * kThreads) {
+  for (int k = rank * kThreads + threadIdx.x; k < slots; k += CL * kThreads) {
     int from = -1, to = -1;
     if (k < moves) {
       const int2 m = __ldcg(p.ws.list2 + place(pm, k));
@@ -482,16 +528,18 @@ __global__ void __launch_bounds__(256) rewrite_kernel(const PageParams p) {
 }
 
 // ------------------------------------------------------------------- copy
-// One block per (list entry, plane, K or V), in a grid stride.
-__global__ void __launch_bounds__(256) copy_kernel(const CopyParams p) {
+// One block per (list entry, plane), in a grid stride: the page's rows of K and of V
+// are loaded together (four 16-byte loads a thread and step), then stored.  Read
+// once and written once, so the lines are marked to leave the caches first.
+constexpr int kCopyThreads = 256;
+
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p) {
   const int n = p.count ? min(p.n, max(0, *p.count)) : p.n;
-  const int64_t units = (int64_t)n * p.Hkv * 2;
-  const int vecs = p.page_rows * kD / 16;
+  const int64_t units = (int64_t)n * p.Hkv;
+  const int vecs = p.page_rows * kD / 16;         // a multiple of 256 (page_rows >= 32)
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int which = (int)(u & 1);
-    const int64_t ih = u >> 1;
-    const int i = (int)(ih / p.Hkv), h = (int)(ih - (int64_t)i * p.Hkv);
-    const int from = p.src[i], to = p.dst[i];
+    const int i = (int)(u / p.Hkv), h = (int)(u - (int64_t)i * p.Hkv);
+    const int from = __ldg(p.src + i), to = __ldg(p.dst + i);
     if (from < 0 || to < 0) continue;
     if (from >= p.n_pages || to >= p.n_pages) {
       if (threadIdx.x == 0) atomicOr(p.err, KATTN_DEVERR_BAD_PAGE);
@@ -499,12 +547,29 @@ __global__ void __launch_bounds__(256) copy_kernel(const CopyParams p) {
     }
     const int64_t plane = (int64_t)h * p.cap_rows;
     const int64_t a = plane + (int64_t)from * p.page_rows, b = plane + (int64_t)to * p.page_rows;
-    int8_t* x = which ? p.v : p.k;
-    float* y = which ? p.v_scale : p.k_scale;
-    const uint4* xs = reinterpret_cast<const uint4*>(x + a * kD);
-    uint4* xd = reinterpret_cast<uint4*>(x + b * kD);
-    for (int c = threadIdx.x; c < vecs; c += blockDim.x) xd[c] = xs[c];
-    for (int c = threadIdx.x; c < p.page_rows; c += blockDim.x) y[b + c] = y[a + c];
+    const uint4* ks = reinterpret_cast<const uint4*>(p.k + a * kD) + threadIdx.x;
+    const uint4* vs = reinterpret_cast<const uint4*>(p.v + a * kD) + threadIdx.x;
+    uint4* kd = reinterpret_cast<uint4*>(p.k + b * kD) + threadIdx.x;
+    uint4* vd = reinterpret_cast<uint4*>(p.v + b * kD) + threadIdx.x;
+    // the scales: threads of the first half take K's, of the second V's
+    const bool second = threadIdx.x >= kCopyThreads / 2;
+    const int r0 = threadIdx.x & (kCopyThreads / 2 - 1);
+    float* sc = second ? p.v_scale : p.k_scale;
+    for (int r = r0; r < p.page_rows; r += kCopyThreads / 2) sc[b + r] = __ldcs(sc + a + r);
+    int c = 0;
+    for (; c + 2 * kCopyThreads <= vecs; c += 2 * kCopyThreads) {
+      const uint4 k0 = __ldcs(ks + c), k1 = __ldcs(ks + c + kCopyThreads);
+      const uint4 v0 = __ldcs(vs + c), v1 = __ldcs(vs + c + kCopyThreads);
+      __stcs(kd + c, k0);
+      __stcs(kd + c + kCopyThreads, k1);
+      __stcs(vd + c, v0);
+      __stcs(vd + c + kCopyThreads, v1);
+    }
+    if (c < vecs) {
+      const uint4 k0 = __ldcs(ks + c), v0 = __ldcs(vs + c);
+      __stcs(kd + c, k0);
+      __stcs(vd + c, v0);
+    }
   }
 }
 
@@ -543,9 +608,35 @@ void set_page_workspace(PageParams& p, void* workspace) {
   p.ws.list2 = reinterpret_cast<int2*>(ws + w.list2);
 }
 
+// A plan by one block, or by one cluster of kCluster blocks (more than the portable
+// 8, which every GPU of this kind holds).
+template <typename Kernel>
+cudaError_t launch_plan(Kernel one, Kernel many, bool large, const PageParams& p,
+                        cudaStream_t stream) {
+  if (!large) {
+    one<<<1, kThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+  }
+  const cudaError_t e = cudaFuncSetAttribute(many, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kCluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, many, p);
+}
+// One block looks at the counts in passes of 8192 pages, and at 32 list entries at
+// once.
+bool large_plan(const PageParams& p) { return p.n_pages > 16384 || p.n > 64; }
+
 cudaError_t launch_reserve_pages(const PageParams& p, cudaStream_t stream) {
-  reserve_kernel<<<kCluster, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_plan(reserve_kernel<1>, reserve_kernel<kCluster>, large_plan(p), p, stream);
 }
 
 cudaError_t launch_free_sequences(const PageParams& p, cudaStream_t stream) {
@@ -554,13 +645,12 @@ cudaError_t launch_free_sequences(const PageParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_fork_sequences(const PageParams& p, cudaStream_t stream) {
-  fork_kernel<<<kCluster, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_plan(fork_kernel<1>, fork_kernel<kCluster>, large_plan(p), p, stream);
 }
 
 cudaError_t launch_compact_pages(const PageParams& p, cudaStream_t stream) {
-  compact_kernel<<<kCluster, kThreads, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      launch_plan(compact_kernel<1>, compact_kernel<kCluster>, large_plan(p), p, stream);
   if (e != cudaSuccess) return e;
   const int64_t all = (int64_t)p.n_slots * p.max_pages;
   cudaLaunchAttribute attr[1];
@@ -576,8 +666,8 @@ cudaError_t launch_compact_pages(const PageParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_copy_pages(const CopyParams& p, cudaStream_t stream) {
-  const int64_t units = (int64_t)p.n * p.Hkv * 2;
-  copy_kernel<<<(unsigned)std::min<int64_t>(units, 152 * 8), 256, 0, stream>>>(p);
+  const int64_t units = (int64_t)p.n * p.Hkv;
+  copy_kernel<<<(unsigned)std::min<int64_t>(units, 152 * 8), kCopyThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
