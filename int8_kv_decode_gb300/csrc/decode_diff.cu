@@ -797,33 +797,59 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
   }
 }
 
-// Joins the windows of a row, one block per (sequence, column, head): warp k sums
-// the windows k, k + 8, ... of both maps with the weights 2^(m_s - max m), the
-// eight sums are added in order, and the two maps are subtracted.  The order
-// depends on the row's own window count alone.
-constexpr int kMergeWarps = 8;
+// Joins the windows of a row, one block per (sequence, column, head, half of the
+// channels): warp k sums the windows k, k + 8, ... of both maps with the weights
+// 2^(m_s - max m), the eight sums are added in order, and the two maps are
+// subtracted.  The order depends on the row's own window count alone.  Bound by
+// the partials' way out of L2 and the three trips there that depend on one another;
+// the first kFirst windows of a warp are loaded before the maximum is known.
+constexpr int kMergeWarps = 8, kFirst = 2;
 
 __global__ void __launch_bounds__(kMergeWarps * 32, 4) diff_merge_kernel(const DiffParams p) {
-  __shared__ float4 s_o[kMergeWarps][2][2 * kD / 4];
+  __shared__ float4 s_o[kMergeWarps][2][kD / 4];
   __shared__ float s_m[kMergeWarps][2], s_l[kMergeWarps][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int i = blockIdx.x, j = blockIdx.y, b = blockIdx.z;
+  const int i = blockIdx.x >> 1, half = blockIdx.x & 1, j = blockIdx.y, b = blockIdx.z;
   const int ctx = p.ctx_len[b], H = p.Hq / 2, R = p.R;
+  const bool valid = diff_valid(p, b, ctx);
+  const int64_t row = ((int64_t)b * p.M + j) * H + i;
+  const float lam = p.lam[p.lam_per_row ? row : i];
   griddep_wait();                                 // every partial is in place
-  if (!diff_valid(p, b, ctx) || diff_windows(ctx + p.M - 1) == 1) return;
+  if (!valid || diff_windows(ctx + p.M - 1) == 1) return;
   const int ns = diff_windows(ctx + j);
   const int pair = i / p.g, rr = j * p.g + i % p.g;
   const size_t stride = (size_t)p.pairs * diff_stride(R);
   const float* base = p.partials + ((size_t)b * p.nwin_max * p.pairs + pair) * diff_stride(R);
   const float* mcol = base + (size_t)2 * R * 2 * kD + rr;
   const float* lcol = mcol + 2 * R;
-  const float* ocol = base + (size_t)rr * 2 * kD + 4 * lane;
+  const float* ocol = base + (size_t)rr * 2 * kD + half * kD + 4 * lane;
   const size_t map1 = (size_t)R * 2 * kD;
-  // the row's maxima
-  float mx[2] = {-INFINITY, -INFINITY};
-  for (int s = threadIdx.x; s < ns; s += kMergeWarps * 32) {
-    mx[0] = fmaxf(mx[0], __ldcg(mcol + s * stride));
-    mx[1] = fmaxf(mx[1], __ldcg(mcol + s * stride + R));
+  auto ldo = [&](int s, int a) {
+    return __ldcg(reinterpret_cast<const float4*>(ocol + s * stride + a * map1));
+  };
+  // windows warp + 8 n of this warp; lane n weighs window n (n + 32, ...)
+  const int nw = (ns - warp + kMergeWarps - 1) / kMergeWarps;
+  float4 first[kFirst][2];
+#pragma unroll
+  for (int n = 0; n < kFirst; ++n)
+    if (n < nw) {
+      first[n][0] = ldo(warp + kMergeWarps * n, 0);
+      first[n][1] = ldo(warp + kMergeWarps * n, 1);
+    }
+  float m0[2], l0[2];                             // of the lane's first window
+  {
+    const int s = warp + kMergeWarps * lane;
+    const bool in = s < ns;
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      m0[a] = in ? __ldcg(mcol + s * stride + a * R) : -INFINITY;
+      l0[a] = in ? __ldcg(lcol + s * stride + a * R) : 0.0f;
+    }
+  }
+  float mx[2] = {m0[0], m0[1]};                   // the row's maxima
+  for (int n = lane + 32; n < nw; n += 32) {
+    mx[0] = fmaxf(mx[0], __ldcg(mcol + (warp + kMergeWarps * n) * stride));
+    mx[1] = fmaxf(mx[1], __ldcg(mcol + (warp + kMergeWarps * n) * stride + R));
   }
   mx[0] = warp_max(mx[0]);
   mx[1] = warp_max(mx[1]);
@@ -837,62 +863,73 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) diff_merge_kernel(const D
     mx[0] = fmaxf(mx[0], s_m[w][0]);
     mx[1] = fmaxf(mx[1], s_m[w][1]);
   }
-  float4 acc[2][2];                               // [map][128-channel half]
+  float4 acc[2];
   float l[2] = {0.0f, 0.0f};                      // of the windows this lane weighs
-  const int nw = (ns - warp + kMergeWarps - 1) / kMergeWarps;   // windows of this warp
+  auto add = [&](float w, float4 v, float4& x, bool start) {
+    if (start)
+      x = make_float4(__fmul_rn(w, v.x), __fmul_rn(w, v.y), __fmul_rn(w, v.z), __fmul_rn(w, v.w));
+    else
+      x = make_float4(__fmaf_rn(w, v.x, x.x), __fmaf_rn(w, v.y, x.y), __fmaf_rn(w, v.z, x.z),
+                      __fmaf_rn(w, v.w, x.w));
+  };
   for (int n0 = 0; n0 < nw; n0 += 32) {
-    // lane n weighs window warp + 8 (n0 + n)
-    const int s = warp + kMergeWarps * (n0 + lane);
-    float w[2] = {0.0f, 0.0f};
-    if (s < ns) {
+    float w[2];
+    if (n0 > 0) {
+      const int s = warp + kMergeWarps * (n0 + lane);
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
-        w[a] = fast_exp2(__fsub_rn(__ldcg(mcol + s * stride + a * R), mx[a]));
-        l[a] = __fmaf_rn(w[a], __ldcg(lcol + s * stride + a * R), l[a]);
+        m0[a] = s < ns ? __ldcg(mcol + s * stride + a * R) : -INFINITY;
+        l0[a] = s < ns ? __ldcg(lcol + s * stride + a * R) : 0.0f;
       }
     }
-#pragma unroll 4
-    for (int n = 0; n < min(32, nw - n0); ++n) {
-      const float* src = ocol + (size_t)(warp + kMergeWarps * (n0 + n)) * stride;
 #pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        const float wn = __shfl_sync(0xffffffffu, w[a], n);
+    for (int a = 0; a < 2; ++a) {
+      w[a] = fast_exp2(__fsub_rn(m0[a], mx[a]));  // (-inf past the last window: 0)
+      l[a] = __fmaf_rn(w[a], l0[a], l[a]);
+    }
+    const int end = min(32, nw - n0);
+    int n = 0;
+    if (n0 == 0) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(src + a * map1 + h * kD));
-          if (n0 + n == 0)
-            acc[a][h] = make_float4(__fmul_rn(wn, v.x), __fmul_rn(wn, v.y), __fmul_rn(wn, v.z),
-                                    __fmul_rn(wn, v.w));
-          else
-            acc[a][h] = make_float4(__fmaf_rn(wn, v.x, acc[a][h].x), __fmaf_rn(wn, v.y, acc[a][h].y),
-                                    __fmaf_rn(wn, v.z, acc[a][h].z), __fmaf_rn(wn, v.w, acc[a][h].w));
+      for (int k = 0; k < kFirst; ++k)
+        if (k < end) {
+          add(__shfl_sync(0xffffffffu, w[0], k), first[k][0], acc[0], k == 0);
+          add(__shfl_sync(0xffffffffu, w[1], k), first[k][1], acc[1], k == 0);
         }
-      }
+      n = min(kFirst, end);
+    }
+#pragma unroll 4
+    for (; n < end; ++n) {
+      const int s = warp + kMergeWarps * (n0 + n);
+      const float4 v0 = ldo(s, 0), v1 = ldo(s, 1);
+      add(__shfl_sync(0xffffffffu, w[0], n), v0, acc[0], false);
+      add(__shfl_sync(0xffffffffu, w[1], n), v1, acc[1], false);
     }
   }
   if (nw > 0) {
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
-      s_o[warp][a][lane] = acc[a][0];
-      s_o[warp][a][32 + lane] = acc[a][1];
+      s_o[warp][a][lane] = acc[a];
       const float v = warp_sum(l[a]);
       if (lane == 0) s_l[warp][a] = v;
     }
   }
   __syncthreads();
+  if (threadIdx.x >= kD) return;
   const int ch = threadIdx.x;                     // one channel per thread
   float O[2], Ls[2];
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
     O[a] = reinterpret_cast<const float*>(s_o[0][a])[ch];
     Ls[a] = s_l[0][a];
-    for (int w = 1; w < min(ns, kMergeWarps); ++w) {
-      O[a] = __fadd_rn(O[a], reinterpret_cast<const float*>(s_o[w][a])[ch]);
-      Ls[a] = __fadd_rn(Ls[a], s_l[w][a]);
-    }
+#pragma unroll
+    for (int w = 1; w < kMergeWarps; ++w)
+      if (w < ns) {
+        O[a] = __fadd_rn(O[a], reinterpret_cast<const float*>(s_o[w][a])[ch]);
+        Ls[a] = __fadd_rn(Ls[a], s_l[w][a]);
+      }
   }
-  const int64_t row = ((int64_t)b * p.M + j) * H + i;
-  p.out[row * 2 * kD + ch] = diff_out(O[0], Ls[0], O[1], Ls[1], p.lam[p.lam_per_row ? row : i]);
+  p.out[row * 2 * kD + half * kD + ch] = diff_out(O[0], Ls[0], O[1], Ls[1], lam);
 }
 
 // ------------------------------------------------------------------- host
@@ -971,7 +1008,7 @@ cudaError_t launch_decode_diff(const DiffParams& p, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   const cudaError_t e = p.R <= 4 ? launch_split<1>(p, maps, stream) : launch_split<2>(p, maps, stream);
   if (e != cudaSuccess || p.nwin_max <= 1) return e;
-  return launch_pdl(diff_merge_kernel, dim3((unsigned)(p.Hq / 2), (unsigned)p.M, (unsigned)p.B),
+  return launch_pdl(diff_merge_kernel, dim3((unsigned)p.Hq, (unsigned)p.M, (unsigned)p.B),
                     dim3(kMergeWarps * 32), 0, stream, p);
 }
 

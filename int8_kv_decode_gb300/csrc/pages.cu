@@ -13,9 +13,13 @@
 namespace kattn {
 namespace {
 
-constexpr int kCluster = 16;                      // blocks of a large plan
+// Blocks of a large plan: the barrier of a wider cluster costs more, and spreads
+// rows and lists over more warps (512 forks: 8 blocks 19.1 us, 16 blocks 15.6 us;
+// the compaction of 32768 pages, which has neither: 10.0 and 14.5 us).
+constexpr int kCluster = 16, kCompactCluster = 8;
 constexpr int kThreads = 1024;
 constexpr int kWarpsPerBlock = kThreads / 32;
+static_assert(kWarpsPerBlock == 32, "the sums over a block's warps take one per lane");
 constexpr int kAhead = 8;                         // loads a lane has in flight
 
 // CL: blocks of the plan, 1 or kCluster.
@@ -529,8 +533,9 @@ __global__ void __launch_bounds__(256) rewrite_kernel(const PageParams p) {
 
 // ------------------------------------------------------------------- copy
 // One block per (list entry, plane), in a grid stride: the page's rows of K and of V
-// are loaded together (four 16-byte loads a thread and step), then stored.  Read
-// once and written once, so the lines are marked to leave the caches first.
+// are loaded together (four 16-byte loads a thread and step), then stored.  Bound by
+// HBM: 7864 pages of 64 rows and 4 planes (1.06 GB moved) take 173 us, 6.1 TB/s.
+// Streaming cache hints cost 3% (179 us).
 constexpr int kCopyThreads = 256;
 
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p) {
@@ -555,20 +560,20 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p) 
     const bool second = threadIdx.x >= kCopyThreads / 2;
     const int r0 = threadIdx.x & (kCopyThreads / 2 - 1);
     float* sc = second ? p.v_scale : p.k_scale;
-    for (int r = r0; r < p.page_rows; r += kCopyThreads / 2) sc[b + r] = __ldcs(sc + a + r);
+    for (int r = r0; r < p.page_rows; r += kCopyThreads / 2) sc[b + r] = __ldg(sc + a + r);
     int c = 0;
     for (; c + 2 * kCopyThreads <= vecs; c += 2 * kCopyThreads) {
-      const uint4 k0 = __ldcs(ks + c), k1 = __ldcs(ks + c + kCopyThreads);
-      const uint4 v0 = __ldcs(vs + c), v1 = __ldcs(vs + c + kCopyThreads);
-      __stcs(kd + c, k0);
-      __stcs(kd + c + kCopyThreads, k1);
-      __stcs(vd + c, v0);
-      __stcs(vd + c + kCopyThreads, v1);
+      const uint4 k0 = __ldg(ks + c), k1 = __ldg(ks + c + kCopyThreads);
+      const uint4 v0 = __ldg(vs + c), v1 = __ldg(vs + c + kCopyThreads);
+      *(kd + c) = k0;
+      *(kd + c + kCopyThreads) = k1;
+      *(vd + c) = v0;
+      *(vd + c + kCopyThreads) = v1;
     }
     if (c < vecs) {
-      const uint4 k0 = __ldcs(ks + c), v0 = __ldcs(vs + c);
-      __stcs(kd + c, k0);
-      __stcs(vd + c, v0);
+      const uint4 k0 = __ldg(ks + c), v0 = __ldg(vs + c);
+      *(kd + c) = k0;
+      *(vd + c) = v0;
     }
   }
 }
@@ -611,7 +616,7 @@ void set_page_workspace(PageParams& p, void* workspace) {
 // A plan by one block, or by one cluster of kCluster blocks (more than the portable
 // 8, which every GPU of this kind holds).
 template <typename Kernel>
-cudaError_t launch_plan(Kernel one, Kernel many, bool large, const PageParams& p,
+cudaError_t launch_plan(Kernel one, Kernel many, int blocks, bool large, const PageParams& p,
                         cudaStream_t stream) {
   if (!large) {
     one<<<1, kThreads, 0, stream>>>(p);
@@ -621,22 +626,24 @@ cudaError_t launch_plan(Kernel one, Kernel many, bool large, const PageParams& p
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kCluster;
+  attr[0].val.clusterDim.x = blocks;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kCluster);
+  cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, many, p);
 }
-// One block looks at the counts in passes of 8192 pages, and at 32 list entries at
-// once.
+// Where the cluster starts to pay (one block / the cluster, us): reserving for 8
+// slots over 16384 pages 8.4 / 10.1, over 32768 pages 11.2 / 10.5; for 64 slots
+// 9.3 / 9.3; compacting 4096 pages 7.0 / 7.5, 8192 pages 8.7 / 7.4.
 bool large_plan(const PageParams& p) { return p.n_pages > 16384 || p.n > 64; }
+bool large_compaction(const PageParams& p) { return p.n_pages > 4096; }
 
 cudaError_t launch_reserve_pages(const PageParams& p, cudaStream_t stream) {
-  return launch_plan(reserve_kernel<1>, reserve_kernel<kCluster>, large_plan(p), p, stream);
+  return launch_plan(reserve_kernel<1>, reserve_kernel<kCluster>, kCluster, large_plan(p), p, stream);
 }
 
 cudaError_t launch_free_sequences(const PageParams& p, cudaStream_t stream) {
@@ -645,12 +652,13 @@ cudaError_t launch_free_sequences(const PageParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_fork_sequences(const PageParams& p, cudaStream_t stream) {
-  return launch_plan(fork_kernel<1>, fork_kernel<kCluster>, large_plan(p), p, stream);
+  return launch_plan(fork_kernel<1>, fork_kernel<kCluster>, kCluster, large_plan(p), p, stream);
 }
 
 cudaError_t launch_compact_pages(const PageParams& p, cudaStream_t stream) {
   const cudaError_t e =
-      launch_plan(compact_kernel<1>, compact_kernel<kCluster>, large_plan(p), p, stream);
+      launch_plan(compact_kernel<1>, compact_kernel<kCompactCluster>, kCompactCluster,
+                  large_compaction(p), p, stream);
   if (e != cudaSuccess) return e;
   const int64_t all = (int64_t)p.n_slots * p.max_pages;
   cudaLaunchAttribute attr[1];
