@@ -179,17 +179,27 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t addr) {
                : "memory");
 }
 
-// kBlockBk rows of a plane into a stage, 128-byte swizzle, by the lane with issue
-// set (predicated, so that the warp does not branch).  The stage was read by every
-// lane before: their loads have returned, as products that took them were issued.
-__device__ __forceinline__ void load_stage(bool issue, uint32_t dst, const CUtensorMap* map, int row,
+// The first of a chain of products: nothing to add to.
+__device__ __forceinline__ void mma_i8_first(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7},"
+      " {%8,%9}, {%10,%10,%10,%10};\n"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
+}
+
+// kBlockBk rows of a plane into a stage, 128-byte swizzle, by one lane of the warp
+// (predicated, so that the warp does not branch).  The stage was read by every lane
+// before: their loads have returned, as products that took them were issued.
+__device__ __forceinline__ void load_stage(uint32_t dst, const CUtensorMap* map, int row,
                                            uint32_t bar, uint64_t policy) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %0, 0;\n"
-      " @p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%5], %7;\n"
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n"
+      " @p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%4], %6;\n"
       " @p cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%1], [%2, {%3, %4}], [%5], %6;\n}\n" ::"r"((uint32_t)issue), "r"(dst), "l"(map), "r"(0),
-      "r"(row), "r"(bar), "l"(policy), "r"((uint32_t)kBlockBytes)
+      " [%0], [%1, {%2, %3}], [%4], %5;\n}\n" ::"r"(dst), "l"(map), "r"(0), "r"(row), "r"(bar),
+      "l"(policy), "r"((uint32_t)kBlockBytes)
       : "memory");
 }
 
@@ -241,7 +251,8 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
   extern __shared__ unsigned char smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // (broadcast, so that what follows from the warp's number is known to be uniform)
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int wp = warp >> 1, a = warp & 1;         // the pair of warps; the warp's map and plane
   const int g = lane >> 2, c = lane & 3;
   const int M = p.M, R = p.R, H = p.Hq / 2;
@@ -307,7 +318,13 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
   // Each pair of warps takes a run of units that follow one another: the windows of
   // a row group, then the next row group's, so that its queries are read and
   // quantized once for a run of windows.
-  const int G = gridDim.x * kPairs, worker = wp * gridDim.x + blockIdx.x;
+  // Blocks s, s + sms, ... start on the same multiprocessor: their pairs are
+  // numbered one after the other, so that the runs, whose lengths differ by one
+  // unit, add up to the same work on each.  (A numbering by block alone can give one
+  // multiprocessor all the longer runs; with 4 heads per pair 111 us, 109 us so.)
+  const int G = gridDim.x * kPairs;
+  const int per_sm = gridDim.x / p.sms, more = gridDim.x - per_sm * p.sms, on = blockIdx.x % p.sms;
+  const int worker = (on * per_sm + min(on, more) + blockIdx.x / p.sms) * kPairs + wp;
   int u = (int)((int64_t)worker * total / G);
   const int u_end = (int)((int64_t)(worker + 1) * total / G);
   if (u >= u_end) return;
@@ -406,7 +423,7 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
     // stage ps of the item's pend = 2 n: K0, K1, V0, K2, V1, ..., V(n-2), V(n-1)
     const bool last = ps == pend - 1, is_v = last || (ps > 0 && !(ps & 1));
     const int row = __shfl_sync(0xffffffffu, prow, last ? (ps >> 1) : ((ps + 1) >> 1) - (is_v ? 1 : 0));
-    load_stage(lane == 0, ringb + ist, is_v ? &maps.v : &maps.k, row, fullb + (ist >> 9), policy);
+    load_stage(ringb + ist, is_v ? &maps.v : &maps.k, row, fullb + (ist >> 9), policy);
     ++ps;
     ++inflight;
     ist = ist == kLastStage ? 0 : ist + kBlockBytes;
@@ -538,17 +555,20 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
       }
       const uint32_t k0 = ringb + cst + lk, k1 = k0 ^ 16u;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const uint4 a_lo = hf ? lds128a<2048>(k0) : lds128a<0>(k0);
-        const uint4 a_hi = hf ? lds128a<2048>(k1) : lds128a<0>(k1);
-        const uint4 b_lo = hf ? lds128a<3072>(k0) : lds128a<1024>(k0);
-        const uint4 b_hi = hf ? lds128a<3072>(k1) : lds128a<1024>(k1);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) acc[hf][u] = 0;
-        mma_i8(acc[hf], a_lo.x, b_lo.x, a_lo.y, b_lo.y, qlo.x, qlo.y);
-        mma_i8(acc[hf], a_lo.z, b_lo.z, a_lo.w, b_lo.w, qlo.z, qlo.w);
-        mma_i8(acc[hf], a_hi.x, b_hi.x, a_hi.y, b_hi.y, qhi.x, qhi.y);
-        mma_i8(acc[hf], a_hi.z, b_hi.z, a_hi.w, b_hi.w, qhi.z, qhi.w);
+      for (int part = 0; part < 2; ++part) {      // 64 channels each, both halves side by side
+        const uint32_t k = part ? k1 : k0;
+        const uint4 a0 = lds128a<0>(k), b0 = lds128a<1024>(k);
+        const uint4 a1 = lds128a<2048>(k), b1 = lds128a<3072>(k);
+        const uint4 q = part ? qhi : qlo;
+        if (part == 0) {
+          mma_i8_first(acc[0], a0.x, b0.x, a0.y, b0.y, q.x, q.y);
+          mma_i8_first(acc[1], a1.x, b1.x, a1.y, b1.y, q.x, q.y);
+        } else {
+          mma_i8(acc[0], a0.x, b0.x, a0.y, b0.y, q.x, q.y);
+          mma_i8(acc[1], a1.x, b1.x, a1.y, b1.y, q.x, q.y);
+        }
+        mma_i8(acc[0], a0.z, b0.z, a0.w, b0.w, q.z, q.w);
+        mma_i8(acc[1], a1.z, b1.z, a1.w, b1.w, q.z, q.w);
       }
       consumed();
       return true;
@@ -689,18 +709,24 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
           uint32_t vw[4];                         // keys 2c.. and 2c+8.. of tile q, then of tile q + 1
           if (hf) ldsm_x4_trans<2048>(vw, va ^ (uint32_t)(q << 4));
           else ldsm_x4_trans<0>(vw, va ^ (uint32_t)(q << 4));
+          uint32_t af[2][4];
 #pragma unroll
           for (int d = 0; d < 2; ++d) {
             // bytes (XOR 0x80) into the mantissa of 1024, less 1152: exact f16
             const uint32_t t0v = vw[2 * d] ^ 0x80808080u, t1v = vw[2 * d + 1] ^ 0x80808080u;
-            const uint32_t af[4] = {i8pair_to_h2(t0v, 0x4240u), i8pair_to_h2(t0v, 0x4341u),
-                                    i8pair_to_h2(t1v, 0x4240u), i8pair_to_h2(t1v, 0x4341u)};
-#pragma unroll
-            for (int n = 0; n < T; ++n) {
-              mma_f16(o[q + d][n], af, bhi[n]);
-              mma_f16(o[q + d][n], af, blo[n]);
-            }
+            af[d][0] = i8pair_to_h2(t0v, 0x4240u);
+            af[d][1] = i8pair_to_h2(t0v, 0x4341u);
+            af[d][2] = i8pair_to_h2(t1v, 0x4240u);
+            af[d][3] = i8pair_to_h2(t1v, 0x4341u);
           }
+          // (the low parts after the high parts of all: a product waits for the one
+          // before it into the same sum)
+#pragma unroll
+          for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+#pragma unroll
+              for (int n = 0; n < T; ++n) mma_f16(o[q + d][n], af[d], lo ? blo[n] : bhi[n]);
         }
       }
       consumed();
@@ -956,18 +982,19 @@ bool encode_plane_map(CUtensorMap* map, const int8_t* base, int64_t rows) {
 }
 
 template <int T>
-cudaError_t launch_split(const DiffParams& p, const TmaMaps& maps, cudaStream_t stream) {
+cudaError_t launch_split(DiffParams p, const TmaMaps& maps, cudaStream_t stream) {
   const auto kern = diff_split_kernel<T>;
   const int smem = (int)sizeof(DiffSmem<T>) + 1024;     // + alignment slack
   // per device: the CTAs that the GPU holds at once; the shared-memory limit is
   // raised with the first call
-  static std::atomic<int> slots_cache[kMaxDevices];
+  static std::atomic<int> slots_cache[kMaxDevices], sms_cache[kMaxDevices];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  int slots = (dev >= 0 && dev < kMaxDevices) ? slots_cache[dev].load() : 0;
-  if (slots <= 0) {
-    int sms = 0, per_sm = 0;
+  const bool cached = dev >= 0 && dev < kMaxDevices;
+  int slots = cached ? slots_cache[dev].load() : 0, sms = cached ? sms_cache[dev].load() : 0;
+  if (slots <= 0 || sms <= 0) {
+    int per_sm = 0;
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) !=
         cudaSuccess)
       return e;
@@ -977,8 +1004,12 @@ cudaError_t launch_split(const DiffParams& p, const TmaMaps& maps, cudaStream_t 
         cudaSuccess)
       return e;
     slots = sms * (per_sm > 0 ? per_sm : 1);
-    if (dev >= 0 && dev < kMaxDevices) slots_cache[dev].store(slots);
+    if (cached) {
+      slots_cache[dev].store(slots);
+      sms_cache[dev].store(sms);
+    }
   }
+  p.sms = sms;
   kern<<<(unsigned)std::min<int64_t>(diff_units(p), slots), kThreads, smem, stream>>>(p, maps);
   return cudaGetLastError();
 }

@@ -26,6 +26,7 @@ struct DiffParams {
   int pairs;                    // Hkv / 2
   int cap_rows, max_ctx;
   int nwin_max;                 // windows of the longest sequence
+  int sms;                      // multiprocessors of the device
   float sm_scale;
 };
 int64_t diff_units(const DiffParams& p);          // work units, at most

@@ -232,12 +232,13 @@ def test_compaction_moves_the_rows_of_every_sequence():
     assert not p.refs[int(counts[0]):].any()
 
 
-def test_graph_replay_of_a_turnover():
+@pytest.mark.parametrize("n_pages", [100, 20000])
+def test_graph_replay_of_a_turnover(n_pages):
     # free and reserve captured once and replayed: every replay frees what the one
-    # before gave and takes the same pages again
+    # before gave and takes the same pages again (one block, and a cluster)
     import torch
     import int8_kv_decode_gb300 as K
-    p = Pool(16, 8, 100, 32, seed=5)
+    p = Pool(16, 8, n_pages, 32, seed=5)
     p.reserve(list(range(8)), [100] * 8)
     seqs, lens = dev([1, 3, 5, 9]), dev([200, 31, 64, 1])
     K.free_sequences(p.t, p.c, seqs, workspace=p.ws)         # warm-up outside the capture
