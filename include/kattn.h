@@ -396,7 +396,9 @@ int kattn_hash_rows(const void* data, int64_t n_rows, int64_t row_bytes, int64_t
  * out: float32 [B][M][Hq / 2][256].
  * row_start, ctx_len, max_ctx, sm_scale, the cache layouts and the limits on
  * M, g * M and B as in kattn_decode; a sequence that breaks the row_start /
- * ctx_len rule gets NaN outputs and KATTN_DEVERR_BAD_SEQUENCE.
+ * ctx_len rule gets NaN outputs and KATTN_DEVERR_BAD_SEQUENCE.  A bounded wait
+ * for a K/V copy that runs out sets KATTN_DEVERR_TIMEOUT; rows it concerns are
+ * then not written, or unspecified.
  * Deterministic; the bytes of out[b][j][i] depend only on that row's own keys,
  * so column j equals an M = 1 call with ctx_len + j, in any batch.
  * workspace: kattn_diff_workspace_size(B, M, Hq, max_ctx) bytes, 256-byte

@@ -741,20 +741,28 @@ def compact_pages(block_table, ref_count, *, table_out=None, ref_out=None, src=N
     index, S, mp, P, _, ws = _page_args(block_table, ref_count, None, None, workspace)
     most = max(1, P // 2)
 
-    def array(t, name, like, n):
-        if t is None:
-            return torch.empty(n, dtype=torch.int32, device=like.device)
-        _check_list(t, index, name, n)
-        return t
     if table_out is None:
         table_out = torch.empty_like(block_table)
     else:
         _check(table_out, torch.int32, index, "table_out", 2)
         if table_out.shape != block_table.shape:
             raise ValueError("table_out must have the shape of block_table")
-    ref_out = array(ref_out, "ref_out", ref_count, P)
-    src, dst = array(src, "src", ref_count, most), array(dst, "dst", ref_count, most)
-    counts = array(counts, "counts", ref_count, 2)
+    if ref_out is None:
+        ref_out = torch.empty_like(ref_count)
+    else:
+        _check_list(ref_out, index, "ref_out", P)
+    if src is None:
+        src = torch.empty(most, dtype=torch.int32, device=ref_count.device)
+    else:
+        _check_list(src, index, "src", most)
+    if dst is None:
+        dst = torch.empty_like(src)
+    else:
+        _check_list(dst, index, "dst", most)
+    if counts is None:
+        counts = torch.empty(2, dtype=torch.int32, device=ref_count.device)
+    else:
+        _check_list(counts, index, "counts", 2)
     _launch("kattn_compact_pages", index, block_table.data_ptr(), S, mp, ref_count.data_ptr(), P,
             table_out.data_ptr(), ref_out.data_ptr(), src.data_ptr(), dst.data_ptr(),
             counts.data_ptr(), ws.data_ptr(), ws.numel())

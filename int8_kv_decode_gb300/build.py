@@ -136,6 +136,28 @@ def build_exact_timeout_variant(verbose: bool = False) -> str:
     return TIMEOUT_VARIANT_LIB
 
 
+# Test-only builds: a warp of decode_diff.cu finds no further copy ready after
+# `limit` stages, for the maps in the bit mask `maps`, so that a test can check how
+# the two warps of a pair part, with no wait that could block.  Never loaded by the
+# package; only tests/test_gpu_diff_timeout.py loads them.
+def build_diff_timeout_variant(limit: int, maps: int, verbose: bool = False) -> str:
+    """libkattn.so with decode_diff.cu built to run out of copies; returns its path."""
+    build(verbose=verbose)
+    nvcc = nvcc_path()
+    src = os.path.join(CSRC, "decode_diff.cu")
+    obj = os.path.join(BUILD, f"decode_diff_limit{limit}_maps{maps}.o")
+    lib = os.path.join(BUILD, f"libkattn_diff_limit{limit}_maps{maps}.so")
+    if _stale(obj, [src, __file__] + _headers()):
+        _run([nvcc, "-c", src, "-o", obj] + ARCH + COMMON + SOURCES["decode_diff.cu"]
+             + [f"-DKATTN_DIFF_STAGE_LIMIT={limit}", f"-DKATTN_DIFF_STAGE_MAPS={maps}"], verbose)
+    objs = [os.path.join(BUILD, f.replace(".cu", ".o")) for f in SOURCES if f != "decode_diff.cu"]
+    if _stale(lib, objs + [obj]):
+        tmp = lib + ".tmp"
+        _run([nvcc, "-shared", "-o", tmp] + ARCH + objs + [obj, "-cudart", "static"], verbose)
+        os.replace(tmp, lib)
+    return lib
+
+
 if __name__ == "__main__":
     build(force="--force" in sys.argv, verbose=True, ptxas_verbose="-v" in sys.argv)
     print(LIB)

@@ -454,6 +454,17 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
   const uint32_t lww = (T == 1 ? 0 : 1024 * a) + ((g >> 1) * 8 + (T == 1 ? 4 * a : 0) + 2 * c) * 8 + (g & 1) * 4;
   const uint32_t lwr = (c * 8 + g) * 8;
 
+#ifdef KATTN_DIFF_STAGE_LIMIT
+  // Test builds only: a warp of the maps KATTN_DIFF_STAGE_MAPS (a bit each) takes this
+  // many stages, then finds none ready.
+  int taken = 0;
+  auto ready = [&]() {
+    return !((KATTN_DIFF_STAGE_MAPS >> a & 1) && taken++ >= KATTN_DIFF_STAGE_LIMIT) &&
+           stage_ready(fullb + (cst >> 9), cph);
+  };
+#else
+  auto ready = [&]() { return stage_ready(fullb + (cst >> 9), cph); };
+#endif
   // A copy of this warp never arrived: tell the other warp at its next exchange
   // (the buffer that it reads then), flag it, and leave.
   auto drain = [&]() {                            // a bounded chance for the copies in flight to land
@@ -549,7 +560,7 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
         qlo = lds128a<0>(lq);
         qhi = lds128a<16>(lq);
       }
-      if (!stage_ready(fullb + (cst >> 9), cph)) {
+      if (!ready()) {
         give_up();
         return false;
       }
@@ -682,7 +693,7 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
       // ---- P.V: the operand w * v_scale * 2^E as f16 hi + lo (22 bits), V exact
       const float up = lds32a<0>(lup);
       const float2 up2 = make_float2(up, up);
-      if (!stage_ready(fullb + (cst >> 9), cph)) {
+      if (!ready()) {
         give_up();
         return;
       }
