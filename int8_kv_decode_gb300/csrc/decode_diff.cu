@@ -31,8 +31,6 @@ constexpr int kWindow = 256;
 constexpr int kWinBlocks = kWindow / kBlockBk;    // 8: lane e < 8 holds the row of block e
 constexpr int kPairs = 2;                         // pairs of warps in a block
 constexpr int kThreads = kPairs * 64;
-constexpr int kStages = 3;                        // 4 KB each: K, V, K, V, ... of one plane
-constexpr uint32_t kLastStage = (kStages - 1) * kBlockBytes;
 constexpr int kMaxGroups = 256;                   // entries of the prefix over sequences
 constexpr int kQStride = kD + 16;                 // bytes between query rows (spread over banks)
 // The running maximum that the weights refer to moves only when a block's maximum
@@ -59,20 +57,25 @@ struct DiffItem {
   int fresh;                                      // other queries than the item before
 };
 
+// What a warp needs once per block or item is kept here, not in registers (the
+// accumulators take half of the 128 that four blocks an SM leave a thread).
+struct __align__(16) WarpState {
+  float vs[kBlockBk];                             // v_scale of the block
+  float qs[8];
+  float up[8];                                    // 2^E of the operand's rows
+  float row_sum[8];                               // of a sequence that ends in its window
+  uint8_t q[8 * kQStride];
+  int rows[2][kWinBlocks + 2];                    // rows of the blocks, by item slot
+  DiffItem item[2];                               // the current and the next
+};
+
 template <int T>
 struct __align__(1024) DiffSmem {
   static constexpr int kExBytes = (int)sizeof(Exchange<T>);
-  uint8_t ring[kPairs][2][kStages][kBlockBytes];
-  alignas(16) Exchange<T> ex[kPairs][2];                      // by block parity
-  alignas(16) float vs[kPairs][2][kBlockBk];                  // v_scale of the block
-  float row_sum[kPairs][2][8];                    // of a sequence that ends in its window
-  // What a warp needs once per block or item is kept here, not in registers (the
-  // accumulators take half of the 128 that four blocks an SM leave a thread).
-  alignas(16) uint8_t q[kPairs][2][8 * kQStride];
-  float qs[kPairs][2][8];
-  float up[kPairs][2][8];                         // 2^E of the operand's rows
-  DiffItem item[kPairs][2][2];                    // the current and the next, by parity
-  uint64_t full[kPairs][2][kStages];
+  uint8_t ring[kPairs][2][2][kBlockBytes];        // [K|V] of each warp
+  WarpState ws[kPairs][2];
+  alignas(16) Exchange<T> ex[kPairs][2];          // by block parity
+  uint64_t full[kPairs][2][2];
   int prefix[kMaxGroups + 1];
   int warp_total[kThreads / 32];
 };
@@ -244,22 +247,22 @@ __device__ __forceinline__ float diff_out(float o0, float l0, float o1, float l1
 // T: tiles of 8 query rows on the value side.  T = 2: 8 rows of each map, a tile
 // per map.  T = 1: 4 rows of each map in one tile, map 0 in rows 0..3.
 template <int T>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, T == 1 ? 4 : 3)
 diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
   using Smem = DiffSmem<T>;
   constexpr int kUnitRows = T == 1 ? 4 : 8;       // rows of each map in a unit
   extern __shared__ unsigned char smem_raw[];
-  Smem& sm = *reinterpret_cast<Smem*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (offset, not masked: the compiler goes on knowing that this is shared memory)
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw + (0u - smem_u32(smem_raw)) % 1024u);
   // (broadcast, so that what follows from the warp's number is known to be uniform)
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int wp = warp >> 1, a = warp & 1;         // the pair of warps; the warp's map and plane
   const int g = lane >> 2, c = lane & 3;
   const int M = p.M, R = p.R, H = p.Hq / 2;
   const int nrg = (R + kUnitRows - 1) / kUnitRows;
-  uint64_t* full = sm.full[wp][a];
   if (lane == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1);
+    mbar_init(&sm.full[wp][a][0], 1);
+    mbar_init(&sm.full[wp][a][1], 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
 
@@ -376,120 +379,90 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
   const uint32_t ginv = 65536u / (uint32_t)p.g + 1u;
   auto column = [&](int rr) -> int { return (int)(((uint32_t)rr * ginv) >> 16); };
 
-  DiffItem* items = sm.item[wp][a];
-  int ipar = 0;                                   // parity of the current item
-  auto put = [&](int par, const DiffItem& it) {
+  WarpState& ws = sm.ws[wp][a];
+  int ipar = 0;                                   // slot of the current item
+  auto put = [&](int slot, const DiffItem& it) {
     __syncwarp();
-    if (lane == 0) items[par] = it;
+    if (lane == 0) ws.item[slot] = it;
     __syncwarp();
   };
-  auto put_next = [&](int par) {                  // the unit after the other slot's
-    DiffItem it = items[par ^ 1];
+  auto put_next = [&](int slot) {                 // the unit after the other slot's
+    DiffItem it = ws.item[slot ^ 1];
     if (u + 1 < u_end) it = after(it);
     else it.b = -1;
-    put(par, it);
+    put(slot, it);
+  };
+  // The rows of an item's blocks (in the 2-D view of all planes, which is also the
+  // index of their scales), and after the last its successor's first, or -1.
+  auto put_rows = [&](int slot, int entry) {
+    const DiffItem& it = ws.item[slot];
+    const int row = row_of_entry(p, it, entry, lane) + (2 * it.pair + a) * p.cap_rows;
+    const bool in = it.b >= 0 && lane < blocks_of(it);
+    __syncwarp();
+    if (lane < kWinBlocks) ws.rows[slot][lane] = in ? row : -1;
+    if (in) {                                     // its scales, read at its start
+      prefetch_l2(p.k_scale + row);
+      prefetch_l2(p.v_scale + row);
+    }
+    __syncwarp();
   };
   put(0, find(u));
   put_next(1);
-  int row0 = row_of_entry(p, items[0], row_entry(p, items[0], lane), lane);
-  int row1 = row_entry(p, items[1], lane);        // an entry until the producer reaches it
+  put_rows(0, row_entry(p, ws.item[0], lane));
+  int entry = row_entry(p, ws.item[1], lane);     // the next item's, not looked at yet
 
-  // ---- producer: lane 0 issues, every lane keeps the same counters.  Stages go
-  // over this item's blocks in the order they are read, then the next item's: the
-  // keys of a block come before the values of the one before it.
-  const uint32_t ringb = smem_u32(sm.ring[wp][a][0]), fullb = smem_u32(full);
-  bool pnext = false;
-  int ps = 0, pend = 2 * blocks_of(items[0]), inflight = 0;
-  uint32_t ist = 0;                               // stage to fill, as a byte offset
-  int prow = row0 + (2 * items[0].pair + a) * p.cap_rows;
-  auto reach_next = [&]() {                       // the producer comes to the next item
-    const DiffItem& it = items[ipar ^ 1];
-    row1 = row_of_entry(p, it, row1, lane);
-    ps = 0;
-    pend = 2 * blocks_of(it);
-    prow = row1 + (2 * it.pair + a) * p.cap_rows;
-    if (2 * lane < pend) {                        // its scales, read at its start
-      prefetch_l2(p.k_scale + prow);
-      prefetch_l2(p.v_scale + prow);
-    }
-  };
+  // ---- copies: the K rows of a block into one buffer, its V rows into another; a
+  // buffer is refilled with the next block's as soon as its products are issued.
+  const uint32_t lws = smem_u32(&ws), kbuf = smem_u32(sm.ring[wp][a][0]), vbuf = kbuf + kBlockBytes;
+  const uint32_t kbar = smem_u32(sm.full[wp][a]), vbar = kbar + 8;
   const uint64_t policy = nrg > 1 ? l2_evict_normal() : l2_evict_first();
-  auto produce = [&]() -> bool {
-    if (ps == pend) {
-      if (pnext || items[ipar ^ 1].b < 0) return false;
-      pnext = true;
-      reach_next();
-    }
-    // stage ps of the item's pend = 2 n: K0, K1, V0, K2, V1, ..., V(n-2), V(n-1)
-    const bool last = ps == pend - 1, is_v = last || (ps > 0 && !(ps & 1));
-    const int row = __shfl_sync(0xffffffffu, prow, last ? (ps >> 1) : ((ps + 1) >> 1) - (is_v ? 1 : 0));
-    load_stage(ringb + ist, is_v ? &maps.v : &maps.k, row, fullb + (ist >> 9), policy);
-    ++ps;
-    ++inflight;
-    ist = ist == kLastStage ? 0 : ist + kBlockBytes;
-    return true;
-  };
-  auto fill = [&]() {
-    while (inflight < kStages && produce()) {
-    }
-  };
-  uint32_t cst = 0, cph = 0;                      // stage to read (byte offset), its parity
-  auto consumed = [&]() {
-    __syncwarp();
-    --inflight;
-    cph ^= cst == kLastStage ? 1u : 0u;
-    cst = cst == kLastStage ? 0 : cst + kBlockBytes;
-    produce();
-  };
-  fill();
+  load_stage(kbuf, &maps.k, ws.rows[0][0], kbar, policy);
+  load_stage(vbuf, &maps.v, ws.rows[0][0], vbar, policy);
+  uint32_t ph = 0;                                // parity of the block's copies
+  bool k_ahead = false;                           // the next block's K copy is under way
   // ---- shared-memory addresses of this lane
   const uint32_t exbase = smem_u32(&sm.ex[wp][0]);
   uint32_t lex = exbase;                          // exchange buffer of the next block
   constexpr int kExAlpha = T * 1024, kExInfo = kExAlpha + 64;
-  const uint32_t lk = (uint32_t)swz(g, 2 * c);    // K: rows g, g + 8, ... share the swizzle
-  const uint32_t lv = (uint32_t)((lane & 15) * kD + (((lane >> 4) ^ (lane & 7)) << 4));
-  const uint32_t lvs = smem_u32(sm.vs[wp][a]);
-  const uint32_t lq = smem_u32(&sm.q[wp][a][g * kQStride + 32 * c]);
-  const uint32_t lqs = smem_u32(&sm.qs[wp][a][2 * c]), lup = smem_u32(&sm.up[wp][a][g]);
+  constexpr int kVs = offsetof(WarpState, vs), kQs = offsetof(WarpState, qs);
+  constexpr int kUp = offsetof(WarpState, up), kQ = offsetof(WarpState, q);
   const uint32_t lww = (T == 1 ? 0 : 1024 * a) + ((g >> 1) * 8 + (T == 1 ? 4 * a : 0) + 2 * c) * 8 + (g & 1) * 4;
   const uint32_t lwr = (c * 8 + g) * 8;
 
 #ifdef KATTN_DIFF_STAGE_LIMIT
   // Test builds only: a warp of the maps KATTN_DIFF_STAGE_MAPS (a bit each) takes this
-  // many stages, then finds none ready.
+  // many copies, then finds none ready.
   int taken = 0;
-  auto ready = [&]() {
-    return !((KATTN_DIFF_STAGE_MAPS >> a & 1) && taken++ >= KATTN_DIFF_STAGE_LIMIT) &&
-           stage_ready(fullb + (cst >> 9), cph);
+  auto ready = [&](uint32_t bar) {
+    return !((KATTN_DIFF_STAGE_MAPS >> a & 1) && taken++ >= KATTN_DIFF_STAGE_LIMIT) && stage_ready(bar, ph);
   };
 #else
-  auto ready = [&]() { return stage_ready(fullb + (cst >> 9), cph); };
+  auto ready = [&](uint32_t bar) { return stage_ready(bar, ph); };
 #endif
+  // Before a warp leaves early: a bounded chance for its copies in flight to land
+  // (the block's V copy, and its K copy or the next block's).
+  auto drain = [&](bool k_taken) {
+    if (lane != 0) return;
+    mbar_wait_bounded(&sm.full[wp][a][1], ph);
+    if (!k_taken) mbar_wait_bounded(&sm.full[wp][a][0], ph);
+    else if (k_ahead) mbar_wait_bounded(&sm.full[wp][a][0], ph ^ 1u);
+  };
   // A copy of this warp never arrived: tell the other warp at its next exchange
   // (the buffer that it reads then), flag it, and leave.
-  auto drain = [&]() {                            // a bounded chance for the copies in flight to land
-    if (lane == 0)
-      for (int k = 0; k < inflight; ++k) {
-        mbar_wait_bounded(&full[cst / kBlockBytes], cph);
-        cph ^= cst == kLastStage ? 1u : 0u;
-        cst = cst == kLastStage ? 0 : cst + kBlockBytes;
-      }
-  };
-  auto give_up = [&]() {
+  auto give_up = [&](bool k_taken) {
     if (lane == 0) {
       sts32(lex + kExInfo + 4 * a, (uint32_t)kFailed);
       atomicOr(p.err_word, KATTN_DEVERR_TIMEOUT);
     }
     named_sync(1 + wp, 64);
-    drain();
+    drain(k_taken);
   };
 
   for (;;) {
-    const DiffItem& it0 = items[ipar];
-    const int ctx = it0.ctx, s0 = it0.w * kWindow, s1 = min(s0 + kWindow, ctx + M - 1);
-    const int plane = (2 * it0.pair + a) * p.cap_rows;
-    // ---- the unit's queries of map a, quantized per row, and the plane's scales:
-    // those of block 0, and the largest v_scale among the keys that every row sees
+    const DiffItem& it0 = ws.item[ipar];
+    const int nb = blocks_of(it0);
+    const int s1 = min(it0.w * kWindow + kWindow, it0.ctx + M - 1);   // keys [w kWindow, s1)
+    // ---- the unit's queries of map a, quantized per row
     if (it0.fresh) {
       float4 x[kUnitRows];
 #pragma unroll
@@ -504,38 +477,41 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
         float s;
         const uint32_t w = quantize_loaded_row(x[r], &s);
         const bool in = it0.rg * kUnitRows + r < R;
-        *reinterpret_cast<uint32_t*>(&sm.q[wp][a][r * kQStride + 4 * lane]) = in ? w : 0u;
-        if (lane == 0) sm.qs[wp][a][r] = in ? s : 0.0f;
+        *reinterpret_cast<uint32_t*>(&ws.q[r * kQStride + 4 * lane]) = in ? w : 0u;
+        if (lane == 0) ws.qs[r] = in ? s : 0.0f;
       }
     }
-    float nk, nv, vm = 0.0f;                      // scales of the next block's key `lane`
-#pragma unroll
-    for (int e = 0; e < kWinBlocks; ++e) {
-      const int row = __shfl_sync(0xffffffffu, row0, e) + lane, key = s0 + 32 * e + lane;
-      const float v = key < s1 ? __ldg(p.v_scale + plane + row) : 0.0f;
-      if (key < ctx) vm = fmaxf(vm, v);
-      if (e == 0) {
-        nv = v;
-        nk = key < s1 ? __ldg(p.k_scale + plane + row) : 0.0f;
-      }
-    }
-    // Draft column of unit row r of the tile (T = 1: rows 4..7 are those of map 1).
+    // Keys that unit row r of the tile sees (T = 1: rows 4..7 are those of map 1).
     auto keys_of = [&](int r) -> int {
-      return ctx + column(min(it0.rg * kUnitRows + (T == 1 ? r & 3 : r), R - 1));
+      return it0.ctx + column(min(it0.rg * kUnitRows + (T == 1 ? r & 3 : r), R - 1));
     };
-    // Power of two 2^E per row: the largest v_scale among the window's keys that
-    // the row sees, times 2^E, lies in [2^8, 2^9), so that w * v_scale * 2^E stays
-    // below 2^15 and, down to weights that do not matter, in f16's normal range.
+    // ---- the plane's scales: those of block 0, and the largest v_scale among the
+    // keys that every row sees
+    float nk, nv;                                 // scales of the next block's key `lane`
     {
+      const int s0 = it0.w * kWindow;
+      float vm = 0.0f;
+#pragma unroll
+      for (int e = 0; e < kWinBlocks; ++e) {
+        const int key = s0 + 32 * e + lane, at = ws.rows[ipar][e] + lane;
+        const float v = key < s1 ? __ldg(p.v_scale + at) : 0.0f;
+        if (key < it0.ctx) vm = fmaxf(vm, v);
+        if (e == 0) {
+          nv = v;
+          nk = key < s1 ? __ldg(p.k_scale + at) : 0.0f;
+        }
+      }
+      // Power of two 2^E per row: the largest v_scale among the window's keys that the
+      // row sees, times 2^E, lies in [2^8, 2^9), so that w * v_scale * 2^E stays below
+      // 2^15 and, down to weights that do not matter, in f16's normal range.
       const int r = lane & 7, keys = keys_of(r);  // lane r < 8: row r
       float vmax = warp_max(vm);
-      for (int key = max(ctx, s0); key < s1; ++key) {    // draft keys
-        const int row = __shfl_sync(0xffffffffu, row0, (key - s0) >> 5) + ((key - s0) & 31);
-        const float v = __ldg(p.v_scale + plane + row);
+      for (int key = max(it0.ctx, s0); key < s1; ++key) {    // draft keys
+        const float v = __ldg(p.v_scale + ws.rows[ipar][(key - s0) >> 5] + ((key - s0) & 31));
         if (key < keys) vmax = fmaxf(vmax, v);
       }
       const int bexp = min(max(262 - (int)((__float_as_uint(vmax) >> 23) & 0xffu), 1), 253);
-      if (lane < 8) sm.up[wp][a][r] = __uint_as_float((uint32_t)bexp << 23);
+      if (lane < 8) ws.up[r] = __uint_as_float((uint32_t)bexp << 23);
     }
     __syncwarp();
 
@@ -549,70 +525,75 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
 #pragma unroll
       for (int n = 0; n < T; ++n)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) o[md][n][u] = 0.0f;
+        for (int v = 0; v < 4; ++v) o[md][n][v] = 0.0f;
 
-    // Q.K of the next block, started a block ahead: the int8 products are slow (62
-    // cycles of a scheduler's tensor pipe each), and run under the P.V before them.
-    int acc[2][4];
-    auto start_qk = [&]() -> bool {
-      uint4 qlo = make_uint4(0, 0, 0, 0), qhi = qlo;
-      if (T == 2 || g < 4) {
-        qlo = lds128a<0>(lq);
-        qhi = lds128a<16>(lq);
-      }
-      if (!ready()) {
-        give_up();
-        return false;
-      }
-      const uint32_t k0 = ringb + cst + lk, k1 = k0 ^ 16u;
-#pragma unroll
-      for (int part = 0; part < 2; ++part) {      // 64 channels each, both halves side by side
-        const uint32_t k = part ? k1 : k0;
-        const uint4 a0 = lds128a<0>(k), b0 = lds128a<1024>(k);
-        const uint4 a1 = lds128a<2048>(k), b1 = lds128a<3072>(k);
-        const uint4 q = part ? qhi : qlo;
-        if (part == 0) {
-          mma_i8_first(acc[0], a0.x, b0.x, a0.y, b0.y, q.x, q.y);
-          mma_i8_first(acc[1], a1.x, b1.x, a1.y, b1.y, q.x, q.y);
-        } else {
-          mma_i8(acc[0], a0.x, b0.x, a0.y, b0.y, q.x, q.y);
-          mma_i8(acc[1], a1.x, b1.x, a1.y, b1.y, q.x, q.y);
-        }
-        mma_i8(acc[0], a0.z, b0.z, a0.w, b0.w, q.z, q.w);
-        mma_i8(acc[1], a1.z, b1.z, a1.w, b1.w, q.z, q.w);
-      }
-      consumed();
-      return true;
-    };
-    if (!start_qk()) return;
-    const int nb = blocks_of(it0);
     for (int i = 0; i < nb; ++i) {
-      const int t0 = s0 + i * kBlockBk;
+      if (i + 1 == nb) {                          // the next item's rows, its first after this one's last
+        put_rows(ipar ^ 1, entry);
+        if (lane == 0) ws.rows[ipar][nb] = ws.rows[ipar ^ 1][0];
+        __syncwarp();
+      }
+      const int t0 = it0.w * kWindow + i * kBlockBk;
+      const int next = ws.rows[ipar][i + 1];      // row of the block after this one, or -1
       float ks4[4];                               // k_scale of keys g + 8q
 #pragma unroll
       for (int q = 0; q < 4; ++q) ks4[q] = __shfl_sync(0xffffffffu, nk, g + 8 * q);
-      sts32(lvs + 4 * lane, __float_as_uint(nv));
+      sts32<kVs>(lws + 4 * lane, nv);
       {
-        const int row = plane + __shfl_sync(0xffffffffu, row0, i + 1) + lane;   // (lane 8 holds 0)
         const bool in = t0 + kBlockBk + lane < s1;
-        nk = in ? __ldg(p.k_scale + row) : 0.0f;
-        nv = in ? __ldg(p.v_scale + row) : 0.0f;
+        nk = in ? __ldg(p.k_scale + next + lane) : 0.0f;
+        nv = in ? __ldg(p.v_scale + next + lane) : 0.0f;
       }
-      // ---- scores of map a: sc[half], keys 16 half + g (+ 8), rows 2c + e:
-      // s = (S * (qs * ks)) * sm_scale, rounded as written
-      float2 qsr = make_float2(0.0f, 0.0f);
-      if (T == 2 || c < 2) qsr = lds64a<0>(lqs);
-      float2 sc[2][2];                            // [half][key g | g + 8], rows 2c, 2c + 1
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2) {
-          const float ks = ks4[2 * hf + k2];
-          const float2 qk = f2_mul(qsr, make_float2(ks, ks));
-          const float2 S = make_float2(__int2float_rn(acc[hf][2 * k2]), __int2float_rn(acc[hf][2 * k2 + 1]));
-          sc[hf][k2] = f2_mul(f2_mul(S, qk), make_float2(p.sm_scale, p.sm_scale));
+      // ---- Q.K: keys 16 half + g (+ 8), rows 2c + e
+      int acc[2][4];
+      {
+        uint4 qlo = make_uint4(0, 0, 0, 0), qhi = qlo;
+        if (T == 2 || g < 4) {
+          const uint32_t lq = lws + g * kQStride + 32 * c;
+          qlo = lds128a<kQ>(lq);
+          qhi = lds128a<kQ + 16>(lq);
         }
-      if (t0 + kBlockBk > ctx) {                  // keys that some row does not see
+        if (!ready(kbar)) {
+          give_up(false);
+          return;
+        }
+        const uint32_t k0 = kbuf + (uint32_t)swz(g, 2 * c);      // rows g, g + 8, ... share the swizzle
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {    // 64 channels each, both halves side by side
+          const uint32_t k = part ? k0 ^ 16u : k0;
+          const uint4 a0 = lds128a<0>(k), b0 = lds128a<1024>(k);
+          const uint4 a1 = lds128a<2048>(k), b1 = lds128a<3072>(k);
+          const uint4 q = part ? qhi : qlo;
+          if (part == 0) {
+            mma_i8_first(acc[0], a0.x, b0.x, a0.y, b0.y, q.x, q.y);
+            mma_i8_first(acc[1], a1.x, b1.x, a1.y, b1.y, q.x, q.y);
+          } else {
+            mma_i8(acc[0], a0.x, b0.x, a0.y, b0.y, q.x, q.y);
+            mma_i8(acc[1], a1.x, b1.x, a1.y, b1.y, q.x, q.y);
+          }
+          mma_i8(acc[0], a0.z, b0.z, a0.w, b0.w, q.z, q.w);
+          mma_i8(acc[1], a1.z, b1.z, a1.w, b1.w, q.z, q.w);
+        }
+        __syncwarp();
+        k_ahead = next >= 0;
+        if (next >= 0) load_stage(kbuf, &maps.k, next, kbar, policy);
+      }
+      // ---- scores s = (S * (qs * ks)) * sm_scale, rounded as written
+      float2 sc[2][2];                            // [half][key g | g + 8], rows 2c, 2c + 1
+      {
+        float2 qsr = make_float2(0.0f, 0.0f);
+        if (T == 2 || c < 2) qsr = lds64a<kQs>(lws + 8 * c);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+          for (int k2 = 0; k2 < 2; ++k2) {
+            const float ks = ks4[2 * hf + k2];
+            const float2 qk = f2_mul(qsr, make_float2(ks, ks));
+            const float2 S = make_float2(__int2float_rn(acc[hf][2 * k2]), __int2float_rn(acc[hf][2 * k2 + 1]));
+            sc[hf][k2] = f2_mul(f2_mul(S, qk), make_float2(p.sm_scale, p.sm_scale));
+          }
+      }
+      if (t0 + kBlockBk > it0.ctx) {              // keys that some row does not see
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
@@ -665,17 +646,16 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
         sts32<776>(w, sc[1][1].y);
       }
       if (lane == 0) sts32(lex + kExInfo + 4 * a, (uint32_t)info);
-      if (i + 1 < nb && !start_qk()) return;
       named_sync(1 + wp, 64);
       const float2 both = lds64a<kExInfo>(lex);
       const int info0 = __float_as_int(both.x), info1 = __float_as_int(both.y);
       const uint32_t lexr = lex + lwr, exa = lex + kExAlpha;
       lex = exbase + exbase + Smem::kExBytes - lex;      // the other buffer
-      if ((info0 | info1) & kFailed) {            // the other warp has left
-        drain();
-        return;
-      }
-      if ((info0 | info1) & kMoved) {
+      if (info0 | info1) {
+        if ((info0 | info1) & kFailed) {          // the other warp has left
+          drain(true);
+          return;
+        }
 #pragma unroll
         for (int n = 0; n < T; ++n) {
           // the tile's rows 2c, 2c + 1: map n, or (T = 1) map c / 2
@@ -691,21 +671,21 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
         }
       }
       // ---- P.V: the operand w * v_scale * 2^E as f16 hi + lo (22 bits), V exact
-      const float up = lds32a<0>(lup);
+      const float up = lds32a<kUp>(lws + 4 * g);
       const float2 up2 = make_float2(up, up);
-      if (!ready()) {
-        give_up();
+      if (!ready(vbar)) {
+        give_up(true);
         return;
       }
       // A = V^T.  Row g of m-tile q is channel 16q + 2g, row g + 8 the next one; a
-      // 16-bit element of the stage is two channels of a key, so the transposing
+      // 16-bit element of the buffer is two channels of a key, so the transposing
       // load pairs the keys 2c, 2c + 1 of both channels in a register.  Lane 8i + r
       // addresses key r (+ 8 if i is odd) of the half, 16-byte chunk q + i / 2.
-      const uint32_t va = ringb + cst + lv;
+      const uint32_t va = vbuf + (uint32_t)((lane & 15) * kD + (((lane >> 4) ^ (lane & 7)) << 4));
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const float2 v0 = f2_mul(hf ? lds64a<64>(lvs + 8 * c) : lds64a<0>(lvs + 8 * c), up2);
-        const float2 v1 = f2_mul(hf ? lds64a<96>(lvs + 8 * c) : lds64a<32>(lvs + 8 * c), up2);
+        const float2 v0 = f2_mul(hf ? lds64a<kVs + 64>(lws + 8 * c) : lds64a<kVs>(lws + 8 * c), up2);
+        const float2 v1 = f2_mul(hf ? lds64a<kVs + 96>(lws + 8 * c) : lds64a<kVs + 32>(lws + 8 * c), up2);
         uint2 bhi[T], blo[T];
 #pragma unroll
         for (int n = 0; n < T; ++n) {
@@ -720,36 +700,31 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
           uint32_t vw[4];                         // keys 2c.. and 2c+8.. of tile q, then of tile q + 1
           if (hf) ldsm_x4_trans<2048>(vw, va ^ (uint32_t)(q << 4));
           else ldsm_x4_trans<0>(vw, va ^ (uint32_t)(q << 4));
-          uint32_t af[2][4];
 #pragma unroll
           for (int d = 0; d < 2; ++d) {
             // bytes (XOR 0x80) into the mantissa of 1024, less 1152: exact f16
             const uint32_t t0v = vw[2 * d] ^ 0x80808080u, t1v = vw[2 * d + 1] ^ 0x80808080u;
-            af[d][0] = i8pair_to_h2(t0v, 0x4240u);
-            af[d][1] = i8pair_to_h2(t0v, 0x4341u);
-            af[d][2] = i8pair_to_h2(t1v, 0x4240u);
-            af[d][3] = i8pair_to_h2(t1v, 0x4341u);
+            const uint32_t af[4] = {i8pair_to_h2(t0v, 0x4240u), i8pair_to_h2(t0v, 0x4341u),
+                                    i8pair_to_h2(t1v, 0x4240u), i8pair_to_h2(t1v, 0x4341u)};
+#pragma unroll
+            for (int n = 0; n < T; ++n) mma_f16(o[q + d][n], af, bhi[n]);
+#pragma unroll
+            for (int n = 0; n < T; ++n) mma_f16(o[q + d][n], af, blo[n]);
           }
-          // (the low parts after the high parts of all: a product waits for the one
-          // before it into the same sum)
-#pragma unroll
-          for (int lo = 0; lo < 2; ++lo)
-#pragma unroll
-            for (int d = 0; d < 2; ++d)
-#pragma unroll
-              for (int n = 0; n < T; ++n) mma_f16(o[q + d][n], af[d], lo ? blo[n] : bhi[n]);
         }
       }
-      consumed();
+      __syncwarp();
+      if (next >= 0) load_stage(vbuf, &maps.v, next, vbar, policy);
+      ph ^= 1u;
     }
-    const bool whole = diff_windows(ctx + M - 1) == 1;
+    const bool whole = diff_windows(it0.ctx + M - 1) == 1;
     const int b = it0.b, pair = it0.pair;
 
     // ---- the window's result
     float down[2];                                // 2^-E of rows 2c + e
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      down[e] = __uint_as_float((254u << 23) - __float_as_uint(sm.up[wp][a][2 * c + e]));
+      down[e] = __uint_as_float((254u << 23) - __float_as_uint(ws.up[2 * c + e]));
       float v = e ? l_run.y : l_run.x;
       v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 4));
       v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 8));
@@ -757,19 +732,24 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
       if (e) l_run.y = v;
       else l_run.x = v;
     }
-    if (lane == 0) sts32(lex + kExInfo + 4 * a, 0u);
-    if (whole && g == 0) {
-      sm.row_sum[wp][a][2 * c] = l_run.x;
-      sm.row_sum[wp][a][2 * c + 1] = l_run.y;
-    }
-    named_sync(1 + wp, 64);
-    const float2 both = lds64a<kExInfo>(lex);
-    lex = exbase + exbase + Smem::kExBytes - lex;        // (a warp that runs ahead writes the other)
-    if (__float_as_int(both.x) | __float_as_int(both.y)) {
-      drain();
-      return;
-    }
-    if (whole) {
+    if (whole) {                                  // the other map's row sums
+      if (lane == 0) sts32(lex + kExInfo + 4 * a, 0u);
+      if (g == 0) {
+        ws.row_sum[2 * c] = l_run.x;
+        ws.row_sum[2 * c + 1] = l_run.y;
+      }
+      named_sync(1 + wp, 64);
+      const float2 both = lds64a<kExInfo>(lex);
+      lex = exbase + exbase + Smem::kExBytes - lex;      // (a warp that runs ahead writes the other)
+      if (__float_as_int(both.x) | __float_as_int(both.y)) {
+        // the other warp gave up at the last block's V copy: both K and V of the next
+        // block are under way here, if there is one
+        if (lane == 0 && k_ahead) {
+          mbar_wait_bounded(&sm.full[wp][a][0], ph);
+          mbar_wait_bounded(&sm.full[wp][a][1], ph);
+        }
+        return;
+      }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = T == 1 ? (2 * c + e) & 3 : 2 * c + e, rr = it0.rg * kUnitRows + r;
@@ -777,7 +757,7 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
         const int j = column(min(rr, R - 1)), i = pair * p.g + min(rr, R - 1) - j * p.g;
         const int64_t row = ((int64_t)b * M + j) * H + i;
         const float lam = in ? p.lam[p.lam_per_row ? row : i] : 0.0f;
-        const float l0 = sm.row_sum[wp][0][r], l1 = sm.row_sum[wp][1][r];
+        const float l0 = sm.ws[wp][0].row_sum[r], l1 = sm.ws[wp][1].row_sum[r];
 #pragma unroll
         for (int md = 0; md < 8; ++md) {
           const float x0 = __fmul_rn(o[md][0][e], down[e]);
@@ -817,20 +797,19 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
     }
 
     // ---- next item
-    if (++u >= u_end) break;
-    if (!pnext) reach_next();                     // it had nothing left to read ahead
-    pnext = false;
-    row0 = row1;
+    if (++u >= u_end) {
+      named_sync(1 + wp, 64);                     // (for a warp that gave up at the last V copy)
+      return;
+    }
     ipar ^= 1;
     put_next(ipar ^ 1);
-    row1 = row_entry(p, items[ipar ^ 1], lane);
-    if (items[ipar ^ 1].b >= 0 && items[ipar ^ 1].fresh) {     // its queries (lane: a line of a row)
-      const DiffItem& nx = items[ipar ^ 1];
+    entry = row_entry(p, ws.item[ipar ^ 1], lane);
+    if (ws.item[ipar ^ 1].b >= 0 && ws.item[ipar ^ 1].fresh) {   // its queries (lane: a line of a row)
+      const DiffItem& nx = ws.item[ipar ^ 1];
       const int rr = min(nx.rg * kUnitRows + min(lane >> 2, kUnitRows - 1), R - 1), j = column(rr);
       prefetch_l2(p.q + (((int64_t)nx.b * M + j) * p.Hq + 2 * (nx.pair * p.g + rr - j * p.g) + a) * kD +
                   32 * (lane & 3));
     }
-    fill();
   }
 }
 
