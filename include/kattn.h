@@ -478,9 +478,10 @@ int kattn_rms_norm_quant(const void* x, const void* residual, const void* weight
  *     fall below 0: that page is skipped;
  *   KATTN_DEVERR_NO_PAGES      see the operation.
  * workspace: kattn_page_workspace_size(n_slots, n_pages) bytes, 256-byte
- * aligned, all of it zeroed before the first call.  It may be reused by calls
- * ordered on the GPU, for the same or smaller sizes; calls that share it and
- * overlap on the GPU race. */
+ * aligned, all of it zeroed before the first call.  It serves one table and pool:
+ * the calls that use it are ordered on the GPU and have the same n_slots and
+ * n_pages (marks that it keeps at zero between calls lie elsewhere for other
+ * sizes).  Calls that share it and overlap on the GPU race. */
 size_t kattn_page_workspace_size(int n_slots, int n_pages);
 
 /* Gives each slot seqs[i], i < n, pages for lens[i] rows: those of its first

@@ -654,8 +654,8 @@ def page_workspace_size(n_slots: int, n_pages: int) -> int:
 
 
 def alloc_page_workspace(n_slots: int, n_pages: int, device="cuda") -> torch.Tensor:
-    """A zeroed workspace for the page operations of a table of n_slots rows
-    over a pool of n_pages pages."""
+    """A zeroed workspace for the page operations of one table of n_slots rows over
+    one pool of n_pages pages."""
     n = page_workspace_size(n_slots, n_pages)
     if n == 0:
         raise ValueError("invalid sizes for a page workspace")

@@ -98,6 +98,14 @@ def test_strided_rows_and_odd_offsets(dtype, d, stride, offset):
     check(x, w, res, codes, scales, rv, 0)
     rest = rbuf[offset:].view(9, stride)[:, d:]
     assert (rest == 99).all() and (rbuf[:offset] == 99).all()      # nothing between the rows
+    if d % 128 == 0:
+        for t in (torch.int8, torch.float8_e4m3fn):
+            out = torch.empty_like(rv.contiguous())
+            rv.copy_(res)
+            codes, scales = K.rms_norm_quant(xv, w.cuda(), residual=rv, residual_out=out, group=128,
+                                             out_dtype=t)
+            check(x, w, res, codes, scales, out, 128)
+            assert torch.equal(rv.cpu(), res)
 
 
 @pytest.mark.parametrize("group", [0, 128])
