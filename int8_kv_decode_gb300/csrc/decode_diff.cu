@@ -3,7 +3,7 @@
 // for a pair of query heads (2i, 2i + 1), the key planes 2p and 2p + 1 and the
 // 256 value channels of both planes.
 //
-// Two launches: diff_split_kernel reduces windows of kWindow keys, and
+// Two launches: diff_split_kernel reduces windows of the keys, and
 // diff_merge_kernel joins the windows of a row and takes the difference.  A
 // sequence of one window is finished by the first.
 //
@@ -19,7 +19,7 @@
 // With more rows (5 draft columns, 40 rows per map) each group of 8 rows streams
 // the window again, from L2: bound by the steps alone (16 sequences of 1k to 4k
 // keys: split 47 us, the call 62 us).  A single short sequence is bound by latency:
-// about 9 us, and 1.6 us for each of its window's 8 blocks.
+// about 9 us, and 1.6 us for each of a window's 4 or 8 blocks.
 #include "decode_split.cuh"
 #include "ops_internal.cuh"
 
@@ -36,9 +36,15 @@ namespace {
 // sit at fixed key positions, so the bytes of a row depend on its own keys alone.
 // Measured alternatives on the serving case: one warp for both planes (255
 // registers, 8 warps a multiprocessor) took 193 us a call; windows of 128 keys 151
-// us (twice the partials and item starts), of 512 keys the same as 256, but 22 us
-// instead of 19 for a single short sequence.
+// us (twice the partials and item starts), of 512 keys the same as 256, with fewer
+// units to spread.
 constexpr int kWindow = 256;
+// The first kShortKeys keys lie in shorter windows: a short sequence is then spread
+// over more warps, and a long one has only these.  (One sequence of 257 keys: 14.7
+// us a call, 18.8 with one window for them; the first 512 or 1024 keys in windows of
+// 128, or the first 256 in windows of 64, leave that as it is and slow the verify
+// case from 62 to 66, 75 and 75 us.)
+constexpr int kShortWindow = 128, kShortKeys = 256, kShortWindows = kShortKeys / kShortWindow;
 constexpr int kWinBlocks = kWindow / kBlockBk;    // 8: lane e < 8 holds the row of block e
 constexpr int kPairs = 2;                         // pairs of warps in a block
 constexpr int kThreads = kPairs * 64;
@@ -49,7 +55,14 @@ constexpr int kQStride = kD + 16;                 // bytes between query rows (s
 // below e^kLag < 2^6.
 constexpr float kLag = 4.0f;
 
-__host__ __device__ inline int diff_windows(int keys) { return (keys + kWindow - 1) / kWindow; }
+__host__ __device__ inline int diff_windows(int keys) {
+  return keys <= kShortKeys ? (keys + kShortWindow - 1) / kShortWindow
+                            : kShortWindows + (keys - kShortKeys + kWindow - 1) / kWindow;
+}
+__device__ __forceinline__ int window_start(int w) {
+  return w < kShortWindows ? w * kShortWindow : kShortKeys + (w - kShortWindows) * kWindow;
+}
+__device__ __forceinline__ int window_keys(int w) { return w < kShortWindows ? kShortWindow : kWindow; }
 __host__ __device__ inline int diff_stride(int R) { return 2 * R * (2 * kD + 2); }   // floats
 
 // What the warps of a pair hand over per block: the weights of both maps, as the
@@ -101,14 +114,14 @@ __device__ __forceinline__ bool diff_valid(const DiffParams& p, int b, int ctx) 
 // Row (in a plane) of block e = lane of the item's window, in two steps: the
 // table entry is loaded well before it is looked at.  Lanes past the window hold 0.
 __device__ __forceinline__ int row_entry(const DiffParams& p, const DiffItem& it, int lane) {
-  const int key = it.w * kWindow + lane * kBlockBk;
-  if (it.b < 0 || lane >= kWinBlocks || key >= it.ctx + p.M - 1) return 0;
+  const int key = window_start(it.w) + lane * kBlockBk;
+  if (it.b < 0 || lane * kBlockBk >= window_keys(it.w) || key >= it.ctx + p.M - 1) return 0;
   if (p.block_table == nullptr) return it.row0 + key;
   return __ldg(p.block_table + (int64_t)it.b * p.max_pages + (key >> p.page_shift));
 }
 __device__ __forceinline__ int row_of_entry(const DiffParams& p, const DiffItem& it, int page, int lane) {
   if (p.block_table == nullptr) return page;
-  const int key = it.w * kWindow + lane * kBlockBk;
+  const int key = window_start(it.w) + lane * kBlockBk;
   if ((unsigned)page >= (unsigned)p.n_pages) {
     atomicOr(p.err_word, KATTN_DEVERR_BAD_PAGE);
     page = 0;
@@ -385,7 +398,7 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
     return it;
   };
   auto blocks_of = [&](const DiffItem& it) -> int {
-    const int n = min(kWindow, it.ctx + M - 1 - it.w * kWindow);
+    const int n = min(window_keys(it.w), it.ctx + M - 1 - window_start(it.w));
     return (n + kBlockBk - 1) / kBlockBk;
   };
 
@@ -475,7 +488,8 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
   for (;;) {
     const DiffItem& it0 = ws.item[ipar];
     const int nb = blocks_of(it0);
-    const int s1 = min(it0.w * kWindow + kWindow, it0.ctx + M - 1);   // keys [w kWindow, s1)
+    const int s0 = window_start(it0.w);           // the unit's keys: [s0, s1)
+    const int s1 = min(s0 + window_keys(it0.w), it0.ctx + M - 1);
     // ---- the unit's queries of map a, quantized per row
     if (it0.fresh) {
       float4 x[kUnitRows];
@@ -503,7 +517,6 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
     // keys that every row sees
     float nk, nv;                                 // scales of the next block's key `lane`
     {
-      const int s0 = it0.w * kWindow;
       float vm = 0.0f;
 #pragma unroll
       for (int e = 0; e < kWinBlocks; ++e) {
@@ -547,7 +560,7 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
         if (lane == 0) ws.rows[ipar][nb] = ws.rows[ipar ^ 1][0];
         __syncwarp();
       }
-      const int t0 = it0.w * kWindow + i * kBlockBk;
+      const int t0 = s0 + i * kBlockBk;
       const int next = ws.rows[ipar][i + 1];      // row of the block after this one, or -1
       float ks4[4];                               // k_scale of keys g + 8q
 #pragma unroll

@@ -88,8 +88,9 @@ gpu = pytest.mark.gpu
     (1, 1, 2, 2, 1),                      # one key, one head
     (1, 1, 8, 2, 2),
     (3, 1, 8, 2, [31, 32, 33]),           # the 32-key block's edges
-    (3, 2, 6, 2, [127, 128, 129]),        # the 128-key span's edges, GQA 3
-    (4, 3, 8, 4, [511, 512, 513, 510]),   # the 512-key window's edges, drafts across it
+    (3, 2, 6, 2, [127, 128, 129]),        # the first window's edges, GQA 3
+    (4, 3, 8, 4, [511, 512, 513, 510]),   # the 256-key windows' edges, drafts across them
+    (5, 2, 8, 2, [255, 256, 257, 254, 383]),
     (2, 8, 16, 2, [5, 700]),              # 8 columns, 64 rows per map
     (2, 5, 32, 4, [1500, 1025]),
     (1, 1, 32, 4, 5000),
