@@ -5,11 +5,12 @@
 // kCluster blocks, whose barrier costs a fraction of a microsecond where another
 // launch costs several.  What the blocks hand over goes through the workspace in
 // L2.  Bound by latency: a phase is one or two dependent trips to L2.  Measured:
-// reserving for 8 slots of a 4096-page pool 7.1 us, for 512 slots of a 262144-page
-// pool (65k pages taken) 15.4 us; 8 forks 7.5 us, 512 forks of rows up to 512
-// pages 16 to 18 us; planning the compaction of 32768 pages 10.7 us, and 4 us to
-// take a 512 x 512 table through it.
+// reserving for 8 slots of a 4096-page pool 5.9 us, for 512 slots of a 262144-page
+// pool (65k pages taken) 14.5 us; 8 forks 6.5 us, 512 forks of rows up to 512 pages
+// 15.8 us; planning the compaction of 4096 pages 5.2 us, of 32768 pages 9.4 us, and
+// 4 us to take a 512 x 512 table through it.
 #include <algorithm>
+#include <climits>
 
 #include "device_common.cuh"
 #include "ops_internal.cuh"
@@ -18,8 +19,8 @@ namespace kattn {
 namespace {
 
 // Blocks of a large plan: the barrier of a wider cluster costs more, and spreads
-// rows and lists over more warps (512 forks: 8 blocks 19.1 us, 16 blocks 15.6 us;
-// the compaction of 32768 pages, which has neither: 10.0 and 14.5 us).
+// rows and lists over more warps (512 forks: 8 blocks 21.2 us, 16 blocks 15.8 us;
+// the compaction of 32768 pages, which has neither: 9.4 and 14.5 us).
 constexpr int kCluster = 16, kCompactCluster = 8;
 constexpr int kThreads = 1024;
 constexpr int kWarpsPerBlock = kThreads / 32;
@@ -91,41 +92,53 @@ __device__ __forceinline__ Chunk chunk_of(int n_pages, int rank) {
 
 // Ranks of the pages of [lo, hi) for which pick(page, count) holds, in ascending
 // order: put(rank, page, count) is called for each.  Returns how many there are (to
-// every thread).  Each warp has a run of pages and goes over it twice, once to
-// count (ballots), once, after a scan over the warps, to give the ranks.
+// every thread).  Each warp has a run of pages, counts with ballots, and gives the
+// ranks after a scan over the warps.  A run of up to 32 kHeld pages stays in
+// registers in between; a longer one is read again (kHeld 4, 8, 16: the compaction of
+// 32768 pages 9.4, 9.4, 9.7 us, reserving in a pool of 262144 15.1, 14.5, 13.9 us,
+// 512 forks 15.8, 15.8, 16.1 us).
+constexpr int kHeld = 8;
+
 template <typename Pick, typename Put>
 __device__ __forceinline__ int rank_pages(const int32_t* refs, int lo, int hi, BlockScratch& s,
                                           Pick pick, Put put) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = max(0, hi - lo), run = (n + kThreads - 1) / kThreads * 32;
   const int w0 = min(n, warp * run) + lo, w1 = min(n, warp * run + run) + lo;
-  auto over = [&](auto&& each) {
-    for (int p0 = w0; p0 < w1; p0 += 32 * kAhead) {
-      int c[kAhead];
+  int c[kHeld];
+  auto load = [&](int p0) {
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int p = p0 + 32 * u + lane;
-        c[u] = p < w1 ? __ldcg(refs + p) : 0;
-      }
+    for (int u = 0; u < kHeld; ++u) {
+      const int p = p0 + 32 * u + lane;
+      c[u] = p < w1 ? __ldcg(refs + p) : 0;
+    }
+  };
+  auto over = [&](int p0, auto&& each) {
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int p = p0 + 32 * u + lane;
-        const bool take = p < w1 && pick(p, c[u]);
-        each(p, c[u], take, __ballot_sync(0xffffffffu, take));
-      }
+    for (int u = 0; u < kHeld; ++u) {
+      if (p0 + 32 * u >= w1) break;               // (the same for the whole warp)
+      const int p = p0 + 32 * u + lane;
+      const bool take = p < w1 && pick(p, c[u]);
+      each(p, c[u], take, __ballot_sync(0xffffffffu, take));
     }
   };
   int mine = 0;
-  over([&](int, int, bool, unsigned bal) { mine += __popc(bal); });
+  for (int p0 = w0; p0 < w1; p0 += 32 * kHeld) {
+    load(p0);
+    over(p0, [&](int, int, bool, unsigned bal) { mine += __popc(bal); });
+  }
   __syncthreads();
   if (lane == 0) s.warp[warp] = mine;
   __syncthreads();
   const int v = s.warp[lane], total = warp_sum_int(v);
   int at = warp_sum_int(lane < warp ? v : 0);
-  over([&](int p, int c, bool take, unsigned bal) {
-    if (take) put(at + __popc(bal & ((1u << lane) - 1u)), p, c);
-    at += __popc(bal);
-  });
+  for (int p0 = w0; p0 < w1; p0 += 32 * kHeld) {
+    if (w1 - w0 > 32 * kHeld) load(p0);
+    over(p0, [&](int p, int count, bool take, unsigned bal) {
+      if (take) put(at + __popc(bal & ((1u << lane) - 1u)), p, count);
+      at += __popc(bal);
+    });
+  }
   return total;
 }
 
@@ -203,36 +216,115 @@ __device__ __forceinline__ void list_range(int n, int rank, int& lo, int& hi) {
   hi = min(n, lo + per);
 }
 
-// The first list entry that names a slot wins it: claim holds n - i.
+// A slot that a list names again, and a child that is also a parent.  Lists of up to
+// kThreads entries are looked through in shared memory; longer ones leave marks in
+// the workspace, which costs a trip to L2 and a barrier (512 slots reserved: 15.3 us
+// instead of 13.1, the scan over the list below included): the first entry that names
+// a slot wins its claim, n - i.
+struct Lists {
+  int seq[kThreads], parent[kThreads];
+};
+__device__ __forceinline__ bool short_list(const PageParams& p) {
+  return p.n <= kThreads && (int64_t)p.n * p.max_pages < INT32_MAX;
+}
 template <int CL>
-__device__ __forceinline__ void claim_slots(const PageParams& p, int rank) {
+__device__ __forceinline__ void take_lists(const PageParams& p, int rank, Lists& l) {
+  if (short_list(p)) {
+    if ((int)threadIdx.x < p.n) {
+      l.seq[threadIdx.x] = p.seqs[threadIdx.x];
+      if (p.parents) l.parent[threadIdx.x] = p.parents[threadIdx.x];
+    }
+    __syncthreads();
+    return;
+  }
   for (int i = rank * kThreads + threadIdx.x; i < p.n; i += CL * kThreads) {
     const int s = p.seqs[i];
     if ((unsigned)s < (unsigned)p.n_slots) atomicMax(p.ws.claim + s, p.n - i);
+    if (p.parents && (unsigned)p.parents[i] < (unsigned)p.n_slots) p.ws.mark[p.parents[i]] = 1;
+  }
+  plan_sync<CL>();
+}
+// Whether entry i may have slot s (for the whole warp).
+__device__ __forceinline__ bool slot_mine(const PageParams& p, const Lists& l, int i, int s) {
+  if ((unsigned)s >= (unsigned)p.n_slots) return false;
+  if (!short_list(p))
+    return __ldcg(p.ws.claim + s) == p.n - i && !(p.parents && __ldcg(p.ws.mark + s) != 0);
+  const int lane = threadIdx.x & 31;
+  bool taken = false;
+  for (int j = lane; j < i; j += 32) taken |= l.seq[j] == s;
+  if (p.parents)
+    for (int j = lane; j < p.n; j += 32) taken |= l.parent[j] == s;
+  return !__any_sync(0xffffffffu, taken);
+}
+// The marks of this block's entries go back to zero for the next call.
+__device__ __forceinline__ void return_marks(const PageParams& p, int lo, int hi) {
+  if (short_list(p)) return;
+  for (int i = lo + threadIdx.x; i < hi; i += kThreads) {
+    const int s = p.seqs[i];
+    if ((unsigned)s < (unsigned)p.n_slots) p.ws.claim[s] = 0;
+    if (p.parents && (unsigned)p.parents[i] < (unsigned)p.n_slots) p.ws.mark[p.parents[i]] = 0;
   }
 }
-__device__ __forceinline__ bool slot_mine(const PageParams& p, int i, int s) {
-  return (unsigned)s < (unsigned)p.n_slots && __ldcg(p.ws.claim + s) == p.n - i;
+
+// The pages that the list entries want: value(i) of entry i.  Calls each(i, rank of
+// its first page) for this block's entries [lo, hi), a warp each, once enough(all
+// wanted) has said to.
+template <typename Value, typename Enough, typename Each>
+__device__ __forceinline__ void over_wants(const PageParams& p, int lo, int hi, BlockScratch& s,
+                                           int* first, Value value, Enough enough, Each each) {
+  const int warp = threadIdx.x >> 5;
+  if (short_list(p)) {                            // one scan over the whole list
+    int total;
+    const int mine = block_prefix((int)threadIdx.x < p.n ? value(threadIdx.x) : 0, s, &total);
+    first[threadIdx.x] = mine;
+    __syncthreads();
+    if (!enough((int64_t)total)) return;
+    for (int i = lo + warp; i < hi; i += kWarpsPerBlock) each(i, first[i]);
+    return;
+  }
+  // the sums before this block's entries and of the whole list, in 64 bits: 20 low
+  // bits and the rest
+  int64_t before = 0, all = 0;
+  for (int i = threadIdx.x; i < p.n; i += kThreads) {
+    const int m = value(i);
+    all += m;
+    if (i < lo) before += m;
+  }
+  const int low = (1 << 20) - 1;
+  const int64_t want = ((int64_t)block_sum((int)(all >> 20), s) << 20) + block_sum((int)(all & low), s);
+  const int64_t start = ((int64_t)block_sum((int)(before >> 20), s) << 20) + block_sum((int)(before & low), s);
+  if (!enough(want)) return;
+  int base = (int)min(start, (int64_t)INT32_MAX / 2);   // (ranks past the pool are never taken)
+  for (int i0 = lo; i0 < hi; i0 += kThreads) {
+    const int i = i0 + threadIdx.x;
+    int total;
+    const int mine = block_prefix(i < hi ? value(i) : 0, s, &total);
+    __syncthreads();
+    first[threadIdx.x] = base + mine;
+    __syncthreads();
+    for (int k = warp; k < min(kThreads, hi - i0); k += kWarpsPerBlock) each(i0 + k, first[k]);
+    base += total;
+  }
 }
 
 // ---------------------------------------------------------------- reserve
-//   1. claims;  2. per list entry the missing pages (one warp each), and the
-//   free pages of the block's chunk in order;  3. the entries' first ranks (a
-//   scan over the list) and the pages of those ranks into the table.
+//   1. per list entry the missing pages (one warp each), and the free pages of the
+//   block's chunk in order;  2. the entries' first ranks (a scan over the list) and
+//   the pages of those ranks into the table.
 template <int CL>
 __global__ void __launch_bounds__(kThreads) reserve_kernel(const PageParams p) {
   __shared__ BlockScratch s;
+  __shared__ Lists lists;
   __shared__ int first[kThreads];
   const int rank = plan_rank<CL>();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  claim_slots<CL>(p, rank);
-  plan_sync<CL>();
+  take_lists<CL>(p, rank, lists);
   int lo, hi;
   list_range<CL>(p.n, rank, lo, hi);
   for (int i = lo + warp; i < hi; i += kWarpsPerBlock) {
     const int slot = p.seqs[i], len = p.lens[i];
     int miss = 0;
-    if (slot_mine(p, i, slot) && len_ok(p, len)) {
+    if (slot_mine(p, lists, i, slot) && len_ok(p, len)) {
       const int need = pages_for(p, len);
       const int32_t* row = p.table + (int64_t)slot * p.max_pages;
       for (int c0 = 0; c0 < need; c0 += 32 * kAhead) {
@@ -255,36 +347,17 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const PageParams p) {
   if (threadIdx.x == 0) p.ws.chunk[rank] = free_here;
   plan_sync<CL>();
   const Places<CL> pl = places_of<CL>(p.ws.chunk, ch.per);
-  // pages wanted before this block's entries, and by the whole list
-  int64_t before = 0, all = 0;
-  for (int i = threadIdx.x; i < p.n; i += kThreads) {
-    const int m = __ldcg(p.ws.flag + i);
-    all += m;
-    if (i < lo) before += m;
-  }
-  // (a list wants at most what the pool holds, or it gets nothing: the sums are
-  // compared in 64 bits, capped well above any pool)
-  const int cap = 1 << 20;
-  const int all_hi = block_sum((int)(all >> 20), s), all_lo = block_sum((int)(all & (cap - 1)), s);
-  const int bef_hi = block_sum((int)(before >> 20), s), bef_lo = block_sum((int)(before & (cap - 1)), s);
-  const int64_t want = (int64_t)all_hi * cap + all_lo;
-  const bool enough = want <= (int64_t)pl.start[CL];
-  if (!enough && rank == 0 && threadIdx.x == 0) atomicOr(p.ws.err, KATTN_DEVERR_NO_PAGES);
-  if (enough) {
-    int base = (int)((int64_t)bef_hi * cap + bef_lo);
-    for (int i0 = lo; i0 < hi; i0 += kThreads) {
-      const int i = i0 + threadIdx.x;
-      int total;
-      const int mine = block_prefix(i < hi ? __ldcg(p.ws.flag + i) : 0, s, &total);
-      __syncthreads();
-      first[threadIdx.x] = base + mine;
-      __syncthreads();
-      for (int k = warp; k < min(kThreads, hi - i0); k += kWarpsPerBlock) {
-        const int slot = p.seqs[i0 + k];
-        if (__ldcg(p.ws.flag + i0 + k) == 0) continue;
-        const int need = pages_for(p, p.lens[i0 + k]);
-        int32_t* row = p.table + (int64_t)slot * p.max_pages;
-        int at = first[k];
+  over_wants(
+      p, lo, hi, s, first, [&](int i) { return __ldcg(p.ws.flag + i); },
+      [&](int64_t want) {                         // all of them, or none
+        const bool enough = want <= (int64_t)pl.start[CL];
+        if (!enough && rank == 0 && threadIdx.x == 0) atomicOr(p.ws.err, KATTN_DEVERR_NO_PAGES);
+        return enough;
+      },
+      [&](int i, int at) {
+        if (__ldcg(p.ws.flag + i) == 0) return;
+        const int need = pages_for(p, p.lens[i]);
+        int32_t* row = p.table + (int64_t)p.seqs[i] * p.max_pages;
         for (int c0 = 0; c0 < need; c0 += 32 * kAhead) {
           int e[kAhead];
           load_entries(row, c0, need, e);
@@ -302,15 +375,8 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const PageParams p) {
               p.refs[e[u]] = 1;
             }
         }
-      }
-      base += total;
-    }
-  }
-  // the claims go back to zero for the next call
-  for (int i = lo + threadIdx.x; i < hi; i += kThreads) {
-    const int slot = p.seqs[i];
-    if ((unsigned)slot < (unsigned)p.n_slots) p.ws.claim[slot] = 0;
-  }
+      });
+  return_marks(p, lo, hi);
 }
 
 // ------------------------------------------------------------------- free
@@ -331,30 +397,24 @@ __global__ void __launch_bounds__(256) free_kernel(const PageParams p) {
 }
 
 // ------------------------------------------------------------------- fork
-//   1. claims of the children, marks of the parents;  2. per pair (one warp
-//   each) the checks, and the release of what a valid child held;  3. the free
-//   pages in order;  4. the ranks of the pairs that need a page of their own,
-//   and the children's rows.
+//   1. per pair (one warp each) the checks, and the release of what a valid child
+//   held;  2. the free pages in order;  3. the ranks of the pairs that need a page of
+//   their own, and the children's rows.
 // flag: 0 skipped, 1 valid, 2 valid with a page of its own.
 template <int CL>
 __global__ void __launch_bounds__(kThreads) fork_kernel(const PageParams p) {
   __shared__ BlockScratch s;
+  __shared__ Lists lists;
   __shared__ int first[kThreads];
   const int rank = plan_rank<CL>();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  claim_slots<CL>(p, rank);
-  for (int i = rank * kThreads + threadIdx.x; i < p.n; i += CL * kThreads) {
-    const int s2 = p.parents[i];
-    if ((unsigned)s2 < (unsigned)p.n_slots) p.ws.mark[s2] = 1;
-  }
-  plan_sync<CL>();
+  take_lists<CL>(p, rank, lists);
   int lo, hi;
   list_range<CL>(p.n, rank, lo, hi);
   const int page_mask = (1 << p.page_shift) - 1;
   for (int i = lo + warp; i < hi; i += kWarpsPerBlock) {
     const int child = p.seqs[i], parent = p.parents[i], len = p.lens[i];
-    bool ok = slot_mine(p, i, child) && (unsigned)parent < (unsigned)p.n_slots && len_ok(p, len);
-    if (ok) ok = __ldcg(p.ws.mark + child) == 0;
+    bool ok = slot_mine(p, lists, i, child) && (unsigned)parent < (unsigned)p.n_slots && len_ok(p, len);
     unsigned err = ok ? 0u : KATTN_DEVERR_BAD_SEQUENCE;
     if (ok) {
       const int need = pages_for(p, len);
@@ -395,57 +455,44 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PageParams p) {
   plan_sync<CL>();
   const Places<CL> pl = places_of<CL>(p.ws.chunk, ch.per);
   const int supply = pl.start[CL];
-  int before = 0;
-  for (int i = threadIdx.x; i < lo; i += kThreads) before += __ldcg(p.ws.flag + i) == 2;
-  int base = block_sum(before, s);
-  for (int i0 = lo; i0 < hi; i0 += kThreads) {
-    const int i = i0 + threadIdx.x;
-    int total;
-    const int mine = block_prefix(i < hi && __ldcg(p.ws.flag + i) == 2 ? 1 : 0, s, &total);
-    __syncthreads();
-    first[threadIdx.x] = base + mine;
-    __syncthreads();
-    for (int k = warp; k < min(kThreads, hi - i0); k += kWarpsPerBlock) {
-      const int flag = __ldcg(p.ws.flag + i0 + k);
-      int from = -1, to = -1;
-      if (flag != 0) {
-        const int child = p.seqs[i0 + k], parent = p.parents[i0 + k], len = p.lens[i0 + k];
-        int full = len >> p.page_shift;
-        int32_t* row = p.table + (int64_t)child * p.max_pages;
-        const int32_t* src = p.table + (int64_t)parent * p.max_pages;
-        if (flag == 2) {
-          if (first[k] < supply) {
-            from = __ldcg(src + full);
-            to = __ldcg(p.ws.list + place(pl, first[k]));
-            if (lane == 0) p.refs[to] = 1;
-          } else {                                // no page left: the child stays empty
-            if (lane == 0) atomicOr(p.ws.err, KATTN_DEVERR_NO_PAGES);
-            full = 0;
+  over_wants(
+      p, lo, hi, s, first, [&](int i) { return (int)(__ldcg(p.ws.flag + i) == 2); },
+      [](int64_t) { return true; },
+      [&](int i, int at) {
+        const int flag = __ldcg(p.ws.flag + i);
+        int from = -1, to = -1;
+        if (flag != 0) {
+          const int child = p.seqs[i], parent = p.parents[i], len = p.lens[i];
+          int full = len >> p.page_shift;
+          int32_t* row = p.table + (int64_t)child * p.max_pages;
+          const int32_t* src = p.table + (int64_t)parent * p.max_pages;
+          if (flag == 2) {
+            if (at < supply) {
+              from = __ldcg(src + full);
+              to = __ldcg(p.ws.list + place(pl, at));
+            } else {                              // no page left: the child stays empty
+              if (lane == 0) atomicOr(p.ws.err, KATTN_DEVERR_NO_PAGES);
+              full = 0;
+            }
           }
-        }
-        for (int c0 = 0; c0 < p.max_pages; c0 += 32 * kAhead) {
-          int e[kAhead];
-          load_entries(src, c0, full, e);
+          for (int c0 = 0; c0 < p.max_pages; c0 += 32 * kAhead) {
+            int e[kAhead];
+            load_entries(src, c0, full, e);
 #pragma unroll
-          for (int u = 0; u < kAhead; ++u) {
-            const int c = c0 + 32 * u + lane;
-            if (c < full) atomicAdd(p.refs + e[u], 1);
-            if (c < p.max_pages) row[c] = c == full ? to : e[u];
+            for (int u = 0; u < kAhead; ++u) {
+              const int c = c0 + 32 * u + lane;
+              if (c < full) atomicAdd(p.refs + e[u], 1);
+              if (c < p.max_pages) row[c] = c == full ? to : e[u];
+            }
           }
+          if (to >= 0 && lane == 0) p.refs[to] = 1;
         }
-      }
-      if (lane == 0) {
-        p.src[i0 + k] = from;
-        p.dst[i0 + k] = to;
-      }
-    }
-    base += total;
-  }
-  for (int i = lo + threadIdx.x; i < hi; i += kThreads) {
-    const int child = p.seqs[i], parent = p.parents[i];
-    if ((unsigned)child < (unsigned)p.n_slots) p.ws.claim[child] = 0;
-    if ((unsigned)parent < (unsigned)p.n_slots) p.ws.mark[parent] = 0;
-  }
+        if (lane == 0) {
+          p.src[i] = from;
+          p.dst[i] = to;
+        }
+      });
+  return_marks(p, lo, hi);
 }
 
 // ---------------------------------------------------------------- compact

@@ -154,6 +154,31 @@ def test_lists_that_break_the_rules():
     p.fork([0, 3], [4, 0], [5, 5])        # child 0 is a parent of the call
 
 
+@pytest.mark.parametrize("m", [64, 65, 1024, 1025, 2100])
+def test_long_lists_that_break_the_rules(m):
+    # slots named again near and far, slots outside, children that are parents of the
+    # call: lists on both sides of each of the plan's limits
+    p = Pool(2100, 6, 30000, 32, seed=m)
+    p.fill(0.3)
+    r = p.r
+    for _ in range(2):
+        seqs = r.permutation(2100)[:m]
+        again = r.integers(1, m, m // 8)
+        seqs[again] = seqs[r.integers(0, again)]
+        seqs[r.integers(0, m, 3)] = [-1, 2100, 2**31 - 1]
+        seqs[-1] = seqs[0]
+        lens = r.integers(0, 6 * 32 + 1, m) // 4
+        lens[r.integers(0, m, 2)] = [-1, 6 * 32 + 1]
+        p.reserve(seqs, lens)
+        slots = r.permutation(2100)
+        children, parents = slots[:m], slots[-(m // 2 + 1):][r.integers(0, m // 2 + 1, m)]
+        children[-1], parents[0] = children[0], children[m // 3]
+        parents[m // 2] = -7
+        held = (p.table[np.clip(parents, 0, 2099)] >= 0).sum(1)
+        p.fork(parents, children, np.maximum(0, held * 32 - r.integers(0, 32, m)))
+        p.free(seqs[:m // 2])
+
+
 def test_damaged_tables_stay_inside_the_pool():
     p = Pool(6, 3, 12, 32)
     p.reserve([0, 1, 2], [96, 64, 32])
