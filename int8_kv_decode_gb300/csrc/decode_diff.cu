@@ -12,13 +12,13 @@
 // side, so with up to 8 rows per map the stream of the cache is the floor, and the
 // split reads each byte once for both maps.  Measured, 64 sequences of 512 to
 // 32768 keys over 64-row pages, 32 query and 4 kv heads (554 MB, 82 us at the
-// measured copy rate): 8 rows per map, split 105 us (5.3 TB/s), the call 125 us; 4
+// measured copy rate): 8 rows per map, split 105 us (5.3 TB/s), the call 121 us; 4
 // rows per map, the call 106 us.  The split at 8 rows is bound by the chain of a
 // block's steps at 12 warps a multiprocessor, no single pipe: tensor 51% busy,
 // issue 35%; with the cache in L2, or without the int8 products, it takes 7% less.
 // With more rows (5 draft columns, 40 rows per map) each group of 8 rows streams
 // the window again, from L2: bound by the steps alone (16 sequences of 1k to 4k
-// keys: split 47 us, the call 62 us).  A single short sequence is bound by latency:
+// keys: split 47 us, the call 56 us).  A single short sequence is bound by latency:
 // about 9 us, and 1.6 us for each of a window's 4 or 8 blocks.
 #include "decode_split.cuh"
 #include "ops_internal.cuh"
@@ -817,8 +817,9 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
       for (int e = 0; e < 2; ++e) {
         const int rr = it0.rg * kUnitRows + 2 * c + e;
         if (g == 0 && rr < R && (T == 2 || c < 2)) {
-          part[(size_t)2 * R * 2 * kD + a * R + rr] = e ? m_run.y : m_run.x;
-          part[(size_t)2 * R * 2 * kD + 2 * R + a * R + rr] = e ? l_run.y : l_run.x;
+          float* ml = part + (size_t)2 * R * 2 * kD + 4 * rr;    // m_0, m_1, l_0, l_1
+          ml[a] = e ? m_run.y : m_run.x;
+          ml[2 + a] = e ? l_run.y : l_run.x;
         }
       }
     }
@@ -840,139 +841,120 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
   }
 }
 
-// Joins the windows of a row, one block per (sequence, column, head, half of the
-// channels): warp k sums the windows k, k + 8, ... of both maps with the weights
-// 2^(m_s - max m), the eight sums are added in order, and the two maps are
-// subtracted.  The order depends on the row's own window count alone.  Bound by
-// the partials' way out of L2 and the three trips there that depend on one another;
-// the first kFirst windows of a warp are loaded before the maximum is known.
-constexpr int kMergeWarps = 8, kFirst = 2;
+// Joins the windows of a row: W warps take a half of its channels.  The windows
+// k, k + 8, ... are summed with the weights 2^(m_s - max m), for k = 0 .. 7; the
+// eight sums are added in order, and the two maps are subtracted.  The order depends
+// on neither W nor other rows.  Bound by the partials' way out of L2 and the trips
+// there that depend on one another (statistics, then 4 W windows a trip): a warp has
+// to have enough windows for its lifetime, and a long row enough warps.  Measured, the
+// call with W = 2, 4, 8: 16 sequences of 1k to 4k keys, 5 columns 56, 58, 62 us (64
+// sequences 183, 191, 210); 64 of up to 32k keys 123, 121, 125 us; 4 of 128k keys
+// 163, 145, 136 us.
+constexpr int kClasses = 8, kBatch = 4;
+template <int W>
+constexpr int merge_halves = W == 8 ? 1 : 2;      // of a row, in a block
 
-__global__ void __launch_bounds__(kMergeWarps * 32, 4) diff_merge_kernel(const DiffParams p) {
-  __shared__ float4 s_o[kMergeWarps][2][kD / 4];
-  __shared__ float s_m[kMergeWarps][2], s_l[kMergeWarps][2];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int i = blockIdx.x >> 1, half = blockIdx.x & 1, j = blockIdx.y, b = blockIdx.z;
+template <int W>
+__global__ void __launch_bounds__(32 * W * merge_halves<W>) diff_merge_kernel(const DiffParams p) {
+  constexpr int kOwn = kClasses / W;              // sums of a warp: k = warp, warp + W, ...
+  static_assert(kBatch % kOwn == 0 && W * kBatch <= 32, "a batch holds whole rounds of the sums");
+  __shared__ float4 s_o[merge_halves<W>][kClasses][2][kD / 4];
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % W, side = (threadIdx.x >> 5) / W;
+  const int i = blockIdx.x * merge_halves<W> >> 1, j = blockIdx.y, b = blockIdx.z;
+  const int half = merge_halves<W> == 2 ? side : blockIdx.x & 1;
   const int ctx = p.ctx_len[b], H = p.Hq / 2, R = p.R;
   const bool valid = diff_valid(p, b, ctx);
   const int64_t row = ((int64_t)b * p.M + j) * H + i;
   const float lam = p.lam[p.lam_per_row ? row : i];
-  griddep_wait();                                 // every partial is in place
-  if (!valid || diff_windows(ctx + p.M - 1) == 1) return;
   const int ns = diff_windows(ctx + j);
   const int pair = i / p.g, rr = j * p.g + i % p.g;
   const size_t stride = (size_t)p.pairs * diff_stride(R);
   const float* base = p.partials + ((size_t)b * p.nwin_max * p.pairs + pair) * diff_stride(R);
-  const float* mcol = base + (size_t)2 * R * 2 * kD + rr;
-  const float* lcol = mcol + 2 * R;
+  const float* mlcol = base + (size_t)2 * R * 2 * kD + 4 * rr;
   const float* ocol = base + (size_t)rr * 2 * kD + half * kD + 4 * lane;
   const size_t map1 = (size_t)R * 2 * kD;
-  auto ldo = [&](int s, int a) {
-    return __ldcg(reinterpret_cast<const float4*>(ocol + s * stride + a * map1));
+  griddep_wait();                                 // every partial is in place
+  if (!valid || diff_windows(ctx + p.M - 1) == 1) return;
+
+  float4 v[kBatch][2];
+  // The warp's n-th window after s0 (s0 a multiple of 4 W): W n + warp.
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int n = 0; n < kBatch; ++n) {
+      const int s = s0 + W * n + warp;
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+        v[n][a] = s < ns ? __ldcg(reinterpret_cast<const float4*>(ocol + s * stride + a * map1))
+                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
   };
-  // windows warp + 8 n of this warp; lane n weighs window n (n + 32, ...)
-  const int nw = (ns - warp + kMergeWarps - 1) / kMergeWarps;
-  float4 first[kFirst][2];
-#pragma unroll
-  for (int n = 0; n < kFirst; ++n)
-    if (n < nw) {
-      first[n][0] = ldo(warp + kMergeWarps * n, 0);
-      first[n][1] = ldo(warp + kMergeWarps * n, 1);
-    }
-  float m0[2], l0[2];                             // of the lane's first window
-  {
-    const int s = warp + kMergeWarps * lane;
-    const bool in = s < ns;
-#pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      m0[a] = in ? __ldcg(mcol + s * stride + a * R) : -INFINITY;
-      l0[a] = in ? __ldcg(lcol + s * stride + a * R) : 0.0f;
-    }
-  }
-  float mx[2] = {m0[0], m0[1]};                   // the row's maxima
-  for (int n = lane + 32; n < nw; n += 32) {
-    mx[0] = fmaxf(mx[0], __ldcg(mcol + (warp + kMergeWarps * n) * stride));
-    mx[1] = fmaxf(mx[1], __ldcg(mcol + (warp + kMergeWarps * n) * stride + R));
+  auto stats = [&](int s) {                       // m_0, m_1, l_0, l_1 of window s
+    return s < ns ? __ldcg(reinterpret_cast<const float4*>(mlcol + s * stride))
+                  : make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
+  };
+  load(0);
+  const float4 st0 = stats(lane);
+  float mx[2] = {st0.x, st0.y};                   // the row's maxima
+  for (int s = lane + 32; s < ns; s += 32) {
+    const float4 st = stats(s);
+    mx[0] = fmaxf(mx[0], st.x);
+    mx[1] = fmaxf(mx[1], st.y);
   }
   mx[0] = warp_max(mx[0]);
   mx[1] = warp_max(mx[1]);
-  if (lane == 0) {
-    s_m[warp][0] = mx[0];
-    s_m[warp][1] = mx[1];
-  }
-  __syncthreads();
+
+  float4 acc[kOwn][2];
 #pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) {
-    mx[0] = fmaxf(mx[0], s_m[w][0]);
-    mx[1] = fmaxf(mx[1], s_m[w][1]);
-  }
-  float4 acc[2];
-  float l[2] = {0.0f, 0.0f};                      // of the windows this lane weighs
-  auto add = [&](float w, float4 v, float4& x, bool start) {
-    if (start)
-      x = make_float4(__fmul_rn(w, v.x), __fmul_rn(w, v.y), __fmul_rn(w, v.z), __fmul_rn(w, v.w));
-    else
-      x = make_float4(__fmaf_rn(w, v.x, x.x), __fmaf_rn(w, v.y, x.y), __fmaf_rn(w, v.z, x.z),
-                      __fmaf_rn(w, v.w, x.w));
-  };
-  for (int n0 = 0; n0 < nw; n0 += 32) {
+  for (int k = 0; k < kOwn; ++k)
+#pragma unroll
+    for (int a = 0; a < 2; ++a) acc[k][a] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float l[2] = {0.0f, 0.0f};
+  for (int s0 = 0; s0 < ns; s0 += 32) {           // lane n weighs window s0 + n
     float w[2];
-    if (n0 > 0) {
-      const int s = warp + kMergeWarps * (n0 + lane);
-#pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        m0[a] = s < ns ? __ldcg(mcol + s * stride + a * R) : -INFINITY;
-        l0[a] = s < ns ? __ldcg(lcol + s * stride + a * R) : 0.0f;
-      }
+    {
+      const float4 st = s0 ? stats(s0 + lane) : st0;
+      w[0] = fast_exp2(__fsub_rn(st.x, mx[0]));   // (-inf past the last window: 0)
+      w[1] = fast_exp2(__fsub_rn(st.y, mx[1]));
+      l[0] = __fmaf_rn(w[0], st.z, l[0]);
+      l[1] = __fmaf_rn(w[1], st.w, l[1]);
     }
+#pragma unroll 1
+    for (int at = 0; at < 32 && s0 + at < ns; at += W * kBatch) {
+      if (s0 + at > 0) load(s0 + at);
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      w[a] = fast_exp2(__fsub_rn(m0[a], mx[a]));  // (-inf past the last window: 0)
-      l[a] = __fmaf_rn(w[a], l0[a], l[a]);
-    }
-    const int end = min(32, nw - n0);
-    int n = 0;
-    if (n0 == 0) {
+      for (int n = 0; n < kBatch; ++n)
 #pragma unroll
-      for (int k = 0; k < kFirst; ++k)
-        if (k < end) {
-          add(__shfl_sync(0xffffffffu, w[0], k), first[k][0], acc[0], k == 0);
-          add(__shfl_sync(0xffffffffu, w[1], k), first[k][1], acc[1], k == 0);
+        for (int a = 0; a < 2; ++a) {
+          const float wn = __shfl_sync(0xffffffffu, w[a], at + W * n + warp);
+          float4& x = acc[n % kOwn][a];
+          x = make_float4(__fmaf_rn(wn, v[n][a].x, x.x), __fmaf_rn(wn, v[n][a].y, x.y),
+                          __fmaf_rn(wn, v[n][a].z, x.z), __fmaf_rn(wn, v[n][a].w, x.w));
         }
-      n = min(kFirst, end);
-    }
-#pragma unroll 4
-    for (; n < end; ++n) {
-      const int s = warp + kMergeWarps * (n0 + n);
-      const float4 v0 = ldo(s, 0), v1 = ldo(s, 1);
-      add(__shfl_sync(0xffffffffu, w[0], n), v0, acc[0], false);
-      add(__shfl_sync(0xffffffffu, w[1], n), v1, acc[1], false);
     }
   }
-  if (nw > 0) {
+  l[0] = warp_sum(l[0]);
+  l[1] = warp_sum(l[1]);
+
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      s_o[warp][a][lane] = acc[a];
-      const float v = warp_sum(l[a]);
-      if (lane == 0) s_l[warp][a] = v;
-    }
-  }
+  for (int k = 0; k < kOwn; ++k)
+#pragma unroll
+    for (int a = 0; a < 2; ++a) s_o[side][k * W + warp][a][lane] = acc[k][a];
   __syncthreads();
-  if (threadIdx.x >= kD) return;
-  const int ch = threadIdx.x;                     // one channel per thread
-  float O[2], Ls[2];
+  if (warp != 0) return;
+  float4 O[2];
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
-    O[a] = reinterpret_cast<const float*>(s_o[0][a])[ch];
-    Ls[a] = s_l[0][a];
+    O[a] = s_o[side][0][a][lane];
 #pragma unroll
-    for (int w = 1; w < kMergeWarps; ++w)
-      if (w < ns) {
-        O[a] = __fadd_rn(O[a], reinterpret_cast<const float*>(s_o[w][a])[ch]);
-        Ls[a] = __fadd_rn(Ls[a], s_l[w][a]);
-      }
+    for (int k = 1; k < kClasses; ++k) {
+      const float4 x = s_o[side][k][a][lane];
+      O[a] = make_float4(__fadd_rn(O[a].x, x.x), __fadd_rn(O[a].y, x.y), __fadd_rn(O[a].z, x.z),
+                         __fadd_rn(O[a].w, x.w));
+    }
   }
-  p.out[row * 2 * kD + half * kD + ch] = diff_out(O[0], Ls[0], O[1], Ls[1], lam);
+  *reinterpret_cast<float4*>(p.out + row * 2 * kD + half * kD + 4 * lane) =
+      make_float4(diff_out(O[0].x, l[0], O[1].x, l[1], lam), diff_out(O[0].y, l[0], O[1].y, l[1], lam),
+                  diff_out(O[0].z, l[0], O[1].z, l[1], lam), diff_out(O[0].w, l[0], O[1].w, l[1], lam));
 }
 
 // ------------------------------------------------------------------- host
@@ -1031,6 +1013,13 @@ cudaError_t launch_split(DiffParams p, const TmaMaps& maps, cudaStream_t stream)
   return cudaGetLastError();
 }
 
+template <int W>
+cudaError_t launch_merge(const DiffParams& p, cudaStream_t stream) {
+  constexpr int kHalves = merge_halves<W>;
+  return launch_pdl(diff_merge_kernel<W>, dim3((unsigned)(p.Hq / kHalves), (unsigned)p.M, (unsigned)p.B),
+                    dim3(32 * W * kHalves), 0, stream, p);
+}
+
 }  // namespace
 
 int64_t diff_units(const DiffParams& p) {
@@ -1056,8 +1045,9 @@ cudaError_t launch_decode_diff(const DiffParams& p, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   const cudaError_t e = p.R <= 4 ? launch_split<1>(p, maps, stream) : launch_split<2>(p, maps, stream);
   if (e != cudaSuccess || p.nwin_max <= 1) return e;
-  return launch_pdl(diff_merge_kernel, dim3((unsigned)p.Hq, (unsigned)p.M, (unsigned)p.B),
-                    dim3(kMergeWarps * 32), 0, stream, p);
+  if (p.nwin_max <= 32) return launch_merge<2>(p, stream);
+  if (p.nwin_max <= 256) return launch_merge<4>(p, stream);
+  return launch_merge<8>(p, stream);
 }
 
 }  // namespace kattn

@@ -183,6 +183,27 @@ def test_bytes_do_not_depend_on_the_batch():
 
 
 @gpu
+@pytest.mark.parametrize("M,Hq", [(1, 8), (5, 16)])
+def test_bytes_do_not_depend_on_max_ctx(M, Hq):
+    # the join of the windows has other shapes for longer limits
+    import int8_kv_decode_gb300 as K
+    x = inputs(4, M, Hq, 2, [300, 5000, 257, 1], seed=10)
+    t = device(x)
+    got = [bits(K.decode_diff(t["q"], t["k8"], t["ks"], t["v8"], t["vs"], t["start"], t["ctx"], limit,
+                              t["lam"]))
+           for limit in (5000, 8190, 8200, 65000, 70000)]
+    for other in got[1:]:
+        assert np.array_equal(got[0], other)
+
+
+@gpu
+def test_a_row_of_more_than_256_windows():
+    x = inputs(2, 2, 4, 2, [70000, 900], seed=11)
+    want, mass = expected(x)
+    check(run(x).cpu().numpy(), want, mass)
+
+
+@gpu
 @pytest.mark.parametrize("P", [32, 64, 256])
 @pytest.mark.parametrize("M,Hq,Hkv,ctx", [(1, 8, 2, [1, 33, 900]), (5, 32, 4, [700, 1, 64]),
                                           (2, 64, 2, [2000, 513, 40])])
