@@ -3,9 +3,10 @@
 // for a pair of query heads (2i, 2i + 1), the key planes 2p and 2p + 1 and the
 // 256 value channels of both planes.
 //
-// Two launches: diff_split_kernel reduces windows of the keys, and
-// diff_merge_kernel joins the windows of a row and takes the difference.  A
-// sequence of one window is finished by the first.
+// Two launches: diff_split_kernel, or diff_tc_kernel for many rows per map and
+// enough windows, reduces windows of the keys; diff_merge_kernel joins the windows
+// of a row and takes the difference.  A sequence of one window is finished by the
+// first.
 //
 // What bounds it: 528 bytes per key and plane pair must come from HBM, for
 // 2 * 128 products per query row and map on the key side and 2 * 256 on the value
@@ -16,12 +17,11 @@
 // rows per map, the call 106 us.  The split at 8 rows is bound by the chain of a
 // block's steps at 12 warps a multiprocessor, no single pipe: tensor 51% busy,
 // issue 35%; with the cache in L2, or without the int8 products, it takes 7% less.
-// With more rows (5 draft columns, 40 rows per map) each group of 8 rows streams
-// the window again, from L2: bound by the steps alone (16 sequences of 1k to 4k
-// keys: split 47 us, the call 56 us).  A single short sequence is bound by latency:
+// With more rows each group of 8 rows streams the window again, from L2: bound by
+// the steps alone (5 draft columns, 40 rows per map, 16 sequences of 1k to 4k keys:
+// split 47 us, the call 56 us).  A single short sequence is bound by latency:
 // about 9 us, and 1.6 us for each of a window's 4 or 8 blocks.
-#include "decode_split.cuh"
-#include "ops_internal.cuh"
+#include "decode_diff_tc.cuh"
 
 namespace kattn {
 namespace {
@@ -32,38 +32,13 @@ namespace {
 // plane 2p + a through its own ring, scores its key plane and takes the softmax
 // weights of map a; the two exchange their weights through shared memory, once
 // per block; then each sums its 128 value channels for both maps, so every
-// value is converted to f16 once.  The pairs do not wait for one another.  Windows
-// sit at fixed key positions, so the bytes of a row depend on its own keys alone.
+// value is converted to f16 once.  The pairs do not wait for one another.
 // Measured alternatives on the serving case: one warp for both planes (255
 // registers, 8 warps a multiprocessor) took 193 us a call; windows of 128 keys 151
 // us (twice the partials and item starts), of 512 keys the same as 256, with fewer
 // units to spread.
-constexpr int kWindow = 256;
-// The first kShortKeys keys lie in shorter windows: a short sequence is then spread
-// over more warps, and a long one has only these.  (One sequence of 257 keys: 14.7
-// us a call, 18.8 with one window for them; the first 512 or 1024 keys in windows of
-// 128, or the first 256 in windows of 64, leave that as it is and slow the verify
-// case from 62 to 66, 75 and 75 us.)
-constexpr int kShortWindow = 128, kShortKeys = 256, kShortWindows = kShortKeys / kShortWindow;
-constexpr int kWinBlocks = kWindow / kBlockBk;    // 8: lane e < 8 holds the row of block e
 constexpr int kPairs = 2;                         // pairs of warps in a block
 constexpr int kThreads = kPairs * 64;
-constexpr int kMaxGroups = 256;                   // entries of the prefix over sequences
-constexpr int kQStride = kD + 16;                 // bytes between query rows (spread over banks)
-// The running maximum that the weights refer to moves only when a block's maximum
-// exceeds it by more than kLag: most blocks then rescale nothing.  Weights stay
-// below e^kLag < 2^6.
-constexpr float kLag = 4.0f;
-
-__host__ __device__ inline int diff_windows(int keys) {
-  return keys <= kShortKeys ? (keys + kShortWindow - 1) / kShortWindow
-                            : kShortWindows + (keys - kShortKeys + kWindow - 1) / kWindow;
-}
-__device__ __forceinline__ int window_start(int w) {
-  return w < kShortWindows ? w * kShortWindow : kShortKeys + (w - kShortWindows) * kWindow;
-}
-__device__ __forceinline__ int window_keys(int w) { return w < kShortWindows ? kShortWindow : kWindow; }
-__host__ __device__ inline int diff_stride(int R) { return 2 * R * (2 * kD + 2); }   // floats
 
 // What the warps of a pair hand over per block: the weights of both maps, as the
 // second product's operand takes them (two keys of a row side by side), and the
@@ -75,11 +50,6 @@ struct Exchange {
   int info[2];                                    // per warp: kFailed | kMoved
 };
 constexpr int kFailed = 1, kMoved = 2;
-
-struct DiffItem {
-  int b, pair, w, rg, ctx, row0;                  // b < 0: none
-  int fresh;                                      // other queries than the item before
-};
 
 // What a warp needs once per block or item is kept here, not in registers (the
 // accumulators take a good part of the 168 that three blocks leave a thread).
@@ -104,116 +74,8 @@ struct __align__(1024) DiffSmem {
   int warp_total[kThreads / 32];
 };
 
-__device__ __forceinline__ bool diff_valid(const DiffParams& p, int b, int ctx) {
-  if (p.block_table == nullptr) return sequence_ok(p.row_start[b], ctx, p.M, p.cap_rows, p.max_ctx);
-  if (ctx < 1 || ctx > p.max_ctx) return false;
-  const int64_t keys = (int64_t)ctx + p.M - 1;
-  return ((keys + (1 << p.page_shift) - 1) >> p.page_shift) <= (int64_t)p.max_pages;
-}
-
-// Row (in a plane) of block e = lane of the item's window, in two steps: the
-// table entry is loaded well before it is looked at.  Lanes past the window hold 0.
-__device__ __forceinline__ int row_entry(const DiffParams& p, const DiffItem& it, int lane) {
-  const int key = window_start(it.w) + lane * kBlockBk;
-  if (it.b < 0 || lane * kBlockBk >= window_keys(it.w) || key >= it.ctx + p.M - 1) return 0;
-  if (p.block_table == nullptr) return it.row0 + key;
-  return __ldg(p.block_table + (int64_t)it.b * p.max_pages + (key >> p.page_shift));
-}
-__device__ __forceinline__ int row_of_entry(const DiffParams& p, const DiffItem& it, int page, int lane) {
-  if (p.block_table == nullptr) return page;
-  const int key = window_start(it.w) + lane * kBlockBk;
-  if ((unsigned)page >= (unsigned)p.n_pages) {
-    atomicOr(p.err_word, KATTN_DEVERR_BAD_PAGE);
-    page = 0;
-  }
-  return (page << p.page_shift) | (key & ((1 << p.page_shift) - 1));
-}
-
 __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p));
-}
-
-// warp_quantize_row's result for a row already loaded (lane: elements 4 lane ..),
-// without its four divisions: x * (1 / s) is off by less than 3.1e-5 (|x / s| <=
-// 127; 1/s, the product and the quotient's own rounding 2^-24 each), so its
-// nearest integer is that of the division unless it lies closer than 1e-4 to a
-// half; those, and scales whose reciprocal may overflow, divide.
-__device__ __forceinline__ uint32_t quantize_loaded_row(float4 x, float* scale_out) {
-  const float amax = warp_max(fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
-  const float s = quant_scale(amax);
-  *scale_out = s;
-  const float inv = __frcp_rn(s);
-  const float magic = 12582912.0f;                // 1.5 * 2^23: the sum's low byte is the integer
-  const float t[4] = {__fmul_rn(x.x, inv), __fmul_rn(x.y, inv), __fmul_rn(x.z, inv), __fmul_rn(x.w, inv)};
-  uint32_t r[4];
-  float far = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float y = __fadd_rn(t[i], magic);
-    far = fmaxf(far, fabsf(__fsub_rn(t[i], __fsub_rn(y, magic))));
-    r[i] = __float_as_uint(y);
-  }
-  if (far > 0.4999f || !(s > 1e-30f))
-    return pack_i8x4(quant_one(x.x, s), quant_one(x.y, s), quant_one(x.z, s), quant_one(x.w, s));
-  return __byte_perm(__byte_perm(r[0], r[1], 0x0040u), __byte_perm(r[2], r[3], 0x0040u), 0x5410u);
-}
-
-// Shared memory by 32-bit address and immediate offset: the block loop's addresses
-// are lane constants plus a stage or buffer offset.
-template <int kOff>
-__device__ __forceinline__ uint4 lds128a(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4+%5];\n"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr), "n"(kOff)
-               : "memory");
-  return v;
-}
-template <int kOff>
-__device__ __forceinline__ float2 lds64a(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2+%3];\n"
-               : "=f"(v.x), "=f"(v.y)
-               : "r"(addr), "n"(kOff)
-               : "memory");
-  return v;
-}
-template <int kOff>
-__device__ __forceinline__ float lds32a(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1+%2];\n" : "=f"(v) : "r"(addr), "n"(kOff) : "memory");
-  return v;
-}
-template <int kOff>
-__device__ __forceinline__ void sts32(uint32_t addr, float v) {
-  asm volatile("st.shared.f32 [%0+%1], %2;\n" ::"r"(addr), "n"(kOff), "f"(v) : "memory");
-}
-__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ void sts64(uint32_t addr, float2 v) {
-  asm volatile("st.shared.v2.f32 [%0], {%1,%2};\n" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
-}
-
-// Four 8 x 8 matrices of 16-bit elements, transposed: thread (g, c) gets elements
-// [rows 2c, 2c + 1][column g] of matrix i in r[i]; lane 8 i + r gives the address
-// of row r of matrix i.
-template <int kOff>
-__device__ __forceinline__ void ldsm_x4_trans(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4+%5];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr), "n"(kOff)
-               : "memory");
-}
-
-// The first of a chain of products: nothing to add to.
-__device__ __forceinline__ void mma_i8_first(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                             uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7},"
-      " {%8,%9}, {%10,%10,%10,%10};\n"
-      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
 }
 
 // kBlockBk rows of a plane into a stage, 128-byte swizzle, by one lane of the warp
@@ -228,44 +90,6 @@ __device__ __forceinline__ void load_stage(uint32_t dst, const CUtensorMap* map,
       " [%0], [%1, {%2, %3}], [%4], %5;\n}\n" ::"r"(dst), "l"(map), "r"(0), "r"(row), "r"(bar),
       "l"(policy), "r"((uint32_t)kBlockBytes)
       : "memory");
-}
-
-__device__ __forceinline__ bool bar_try_wait(uint32_t bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-// Whether the stage's copy landed, for the whole warp; the wait is bounded.
-__device__ __noinline__ bool stage_wait(uint32_t bar, uint32_t parity) {
-  for (uint32_t it = 0; it < kSpinLimit; ++it)
-    if (__all_sync(0xffffffffu, bar_try_wait(bar, parity))) return true;
-  return false;
-}
-__device__ __forceinline__ bool stage_ready(uint32_t bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, bar_try_wait(bar, parity)) || stage_wait(bar, parity);
-}
-
-// The row's reference moves to the block's maximum bm where that exceeds its
-// threshold; alpha: the factor of what is summed up so far.
-__device__ __forceinline__ void move_reference(float bm, float& m_run, float& m_move, float& alpha) {
-  if (bm > m_move) {
-    const float m = __fmul_rn(bm, kLog2e);
-    // (nothing is summed up yet where the threshold was -inf)
-    if (m_move != -INFINITY) alpha = fast_exp2(__fsub_rn(m_run, m));
-    m_run = m;
-    m_move = __fadd_rn(bm, kLag);
-  }
-}
-
-// out = o_0 / l_0 - lam * (o_1 / l_1), each operation rounded on its own, here and
-// in the merge alike.
-__device__ __forceinline__ float diff_out(float o0, float l0, float o1, float l1, float lam) {
-  return __fsub_rn(__fdiv_rn(o0, l0), __fmul_rn(lam, __fdiv_rn(o1, l1)));
 }
 
 // T: tiles of 8 query rows on the value side.  T = 2: 8 rows of each map, a tile
@@ -293,61 +117,13 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
 
-  // ---- units of the sequences before each group of gs sequences
-  const int gs = (p.B + kMaxGroups - 1) / kMaxGroups;
-  const int ng = (p.B + gs - 1) / gs;
-  const int per_win = p.pairs * nrg;
-  auto units_of = [&](int b, int ctx) -> int {
-    return diff_valid(p, b, ctx) ? diff_windows(ctx + M - 1) * per_win : 0;
-  };
-  for (int i = tid; i < kMaxGroups; i += kThreads) {
-    int n = 0;
-    if (i < ng)
-      for (int b = i * gs; b < min(p.B, i * gs + gs); ++b) n += units_of(b, p.ctx_len[b]);
-    sm.prefix[i] = n;
-  }
-  __syncthreads();
-  {
-    constexpr int kPer = kMaxGroups / kThreads;
-    int n[kPer], run = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      n[i] = sm.prefix[tid * kPer + i];
-      run += n[i];
-    }
-    int incl = run;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) sm.warp_total[warp] = incl;
-    __syncthreads();
-    int base = incl - run;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w)
-      if (w < warp) base += sm.warp_total[w];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      sm.prefix[tid * kPer + i] = base;
-      base += n[i];
-    }
-    if (tid == kThreads - 1) sm.prefix[kMaxGroups] = base;
-  }
-  // ---- the rows of sequences that break the rules
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    if (diff_valid(p, b, p.ctx_len[b])) continue;
-    float* o = p.out + (int64_t)b * M * H * 2 * kD;
-    for (int64_t i = tid; i < (int64_t)M * H * 2 * kD; i += kThreads)
-      o[i] = __int_as_float(0x7fc00000);
-    if (tid == 0) atomicOr(p.err_word, KATTN_DEVERR_BAD_SEQUENCE);
-  }
+  const DiffUnits units(p, sm.prefix, nrg, 1);
+  units.count(sm.prefix, sm.warp_total);
+  mark_bad_sequences(p);
   __syncthreads();
   griddep_launch_dependents();
   const int total = sm.prefix[kMaxGroups];
-  // Each pair of warps takes a run of units that follow one another: the windows of
-  // a row group, then the next row group's, so that its queries are read and
-  // quantized once for a run of windows.
+  // Each pair of warps takes a run of units that follow one another.
   // Blocks s, s + sms, ... start on the same multiprocessor: their pairs are
   // numbered one after the other, so that the runs, whose lengths differ by one
   // unit, add up to the same work on each.  (A numbering by block alone can give one
@@ -357,50 +133,8 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
   const int worker = (on * per_sm + min(on, more) + blockIdx.x / p.sms) * kPairs + wp;
   int u = (int)((int64_t)worker * total / G);
   const int u_end = (int)((int64_t)(worker + 1) * total / G);
-  if (u >= u_end) return;
-
-  auto at_sequence = [&](DiffItem& it, int b) {
-    it.b = b;
-    it.ctx = p.ctx_len[b];
-    it.row0 = p.block_table ? 0 : (int)p.row_start[b];
-  };
-  auto find = [&](int i) -> DiffItem {            // unit i < total
-    DiffItem it{};
-    int lo = 0, hi = ng;                          // prefix[lo] <= i < prefix[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (sm.prefix[mid] <= i) lo = mid;
-      else hi = mid;
-    }
-    i -= sm.prefix[lo];
-    int b = lo * gs;
-    for (int n; gs > 1 && i >= (n = units_of(b, p.ctx_len[b])); ++b) i -= n;
-    at_sequence(it, b);
-    const int nw = diff_windows(it.ctx + M - 1), run = i / nw;
-    it.w = i - run * nw;
-    it.pair = run / nrg;
-    it.rg = run - it.pair * nrg;
-    it.fresh = 1;
-    return it;
-  };
-  auto after = [&](DiffItem it) -> DiffItem {     // the unit after it (there is one)
-    it.fresh = 0;
-    if (++it.w < diff_windows(it.ctx + M - 1)) return it;
-    it.w = 0;
-    it.fresh = 1;
-    if (++it.rg < nrg) return it;
-    it.rg = 0;
-    if (++it.pair < p.pairs) return it;
-    it.pair = 0;
-    int b = it.b + 1;
-    while (units_of(b, p.ctx_len[b]) == 0) ++b;
-    at_sequence(it, b);
-    return it;
-  };
-  auto blocks_of = [&](const DiffItem& it) -> int {
-    const int n = min(window_keys(it.w), it.ctx + M - 1 - window_start(it.w));
-    return (n + kBlockBk - 1) / kBlockBk;
-  };
+  DiffItem unit;
+  if (!units.find(&u, u_end, &unit)) return;
 
   // rr / g and the query head of unit row rr (rr < 64, g <= 64: exact)
   const uint32_t ginv = 65536u / (uint32_t)p.g + 1u;
@@ -415,7 +149,7 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
   };
   auto put_next = [&](int slot) {                 // the unit after the other slot's
     DiffItem it = ws.item[slot ^ 1];
-    if (u + 1 < u_end) it = after(it);
+    if (u + 1 < u_end) it = units.after(it);
     else it.b = -1;
     put(slot, it);
   };
@@ -424,7 +158,7 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
   auto put_rows = [&](int slot, int entry) {
     const DiffItem& it = ws.item[slot];
     const int row = row_of_entry(p, it, entry, lane) + (2 * it.pair + a) * p.cap_rows;
-    const bool in = it.b >= 0 && lane < blocks_of(it);
+    const bool in = it.b >= 0 && lane < units.blocks(it);
     __syncwarp();
     if (lane < kWinBlocks) ws.rows[slot][lane] = in ? row : -1;
     if (in) {                                     // its scales, read at its start
@@ -433,7 +167,7 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
     }
     __syncwarp();
   };
-  put(0, find(u));
+  put(0, unit);
   put_next(1);
   put_rows(0, row_entry(p, ws.item[0], lane));
   int entry = row_entry(p, ws.item[1], lane);     // the next item's, not looked at yet
@@ -487,7 +221,7 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
 
   for (;;) {
     const DiffItem& it0 = ws.item[ipar];
-    const int nb = blocks_of(it0);
+    const int nb = units.blocks(it0);
     const int s0 = window_start(it0.w);           // the unit's keys: [s0, s1)
     const int s1 = min(s0 + window_keys(it0.w), it0.ctx + M - 1);
     // ---- the unit's queries of map a, quantized per row
@@ -528,17 +262,13 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
           nk = key < s1 ? __ldg(p.k_scale + at) : 0.0f;
         }
       }
-      // Power of two 2^E per row: the largest v_scale among the window's keys that the
-      // row sees, times 2^E, lies in [2^8, 2^9), so that w * v_scale * 2^E stays below
-      // 2^15 and, down to weights that do not matter, in f16's normal range.
       const int r = lane & 7, keys = keys_of(r);  // lane r < 8: row r
       float vmax = warp_max(vm);
       for (int key = max(it0.ctx, s0); key < s1; ++key) {    // draft keys
         const float v = __ldg(p.v_scale + ws.rows[ipar][(key - s0) >> 5] + ((key - s0) & 31));
         if (key < keys) vmax = fmaxf(vmax, v);
       }
-      const int bexp = min(max(262 - (int)((__float_as_uint(vmax) >> 23) & 0xffu), 1), 253);
-      if (lane < 8) ws.up[r] = __uint_as_float((uint32_t)bexp << 23);
+      if (lane < 8) ws.up[r] = operand_scale(vmax);
     }
     __syncwarp();
 
@@ -584,23 +314,7 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
           give_up(false);
           return;
         }
-        const uint32_t k0 = kbuf + (uint32_t)swz(g, 2 * c);      // rows g, g + 8, ... share the swizzle
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {    // 64 channels each, both halves side by side
-          const uint32_t k = part ? k0 ^ 16u : k0;
-          const uint4 a0 = lds128a<0>(k), b0 = lds128a<1024>(k);
-          const uint4 a1 = lds128a<2048>(k), b1 = lds128a<3072>(k);
-          const uint4 q = part ? qhi : qlo;
-          if (part == 0) {
-            mma_i8_first(acc[0], a0.x, b0.x, a0.y, b0.y, q.x, q.y);
-            mma_i8_first(acc[1], a1.x, b1.x, a1.y, b1.y, q.x, q.y);
-          } else {
-            mma_i8(acc[0], a0.x, b0.x, a0.y, b0.y, q.x, q.y);
-            mma_i8(acc[1], a1.x, b1.x, a1.y, b1.y, q.x, q.y);
-          }
-          mma_i8(acc[0], a0.z, b0.z, a0.w, b0.w, q.z, q.w);
-          mma_i8(acc[1], a1.z, b1.z, a1.w, b1.w, q.z, q.w);
-        }
+        key_products(kbuf + (uint32_t)swz(g, 2 * c), qlo, qhi, acc);
         __syncwarp();
         k_ahead = next >= 0;
         if (next >= 0) load_stage(kbuf, &maps.k, next, kbar, policy);
@@ -610,55 +324,15 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
       {
         float2 qsr = make_float2(0.0f, 0.0f);
         if (T == 2 || c < 2) qsr = lds64a<kQs>(lws + 8 * c);
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-          for (int k2 = 0; k2 < 2; ++k2) {
-            const float ks = ks4[2 * hf + k2];
-            const float2 qk = f2_mul(qsr, make_float2(ks, ks));
-            const float2 S = make_float2(__int2float_rn(acc[hf][2 * k2]), __int2float_rn(acc[hf][2 * k2 + 1]));
-            sc[hf][k2] = f2_mul(f2_mul(S, qk), make_float2(p.sm_scale, p.sm_scale));
-          }
+        scores_of(acc, ks4, qsr, p.sm_scale, sc);
       }
-      if (t0 + kBlockBk > it0.ctx) {              // keys that some row does not see
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-          for (int k2 = 0; k2 < 2; ++k2) {
-            const int key = t0 + 16 * hf + g + 8 * k2;
-            if (key >= keys_of(2 * c)) sc[hf][k2].x = -INFINITY;
-            if (key >= keys_of(2 * c + 1)) sc[hf][k2].y = -INFINITY;
-          }
-      }
-      // ---- weights 2^(s log2 e - m).  A row's reference moves, to the block's
-      // maximum, only where a score exceeds it by more than kLag; only then are
-      // the maxima of the row's 32 keys put together.
+      if (t0 + kBlockBk > it0.ctx)                // keys that some row does not see
+        hide_keys(sc, t0 + g, keys_of(2 * c), keys_of(2 * c + 1));
       float2 alpha = make_float2(1.0f, 1.0f);
       int info = 0;
-      {
-        float2 bm = make_float2(fmaxf(fmaxf(sc[0][0].x, sc[0][1].x), fmaxf(sc[1][0].x, sc[1][1].x)),
-                                fmaxf(fmaxf(sc[0][0].y, sc[0][1].y), fmaxf(sc[1][0].y, sc[1][1].y)));
-        if (__any_sync(0xffffffffu, bm.x > m_move.x || bm.y > m_move.y)) {
-#pragma unroll
-          for (int o2 = 4; o2 <= 16; o2 <<= 1) {
-            bm.x = fmaxf(bm.x, __shfl_xor_sync(0xffffffffu, bm.x, o2));
-            bm.y = fmaxf(bm.y, __shfl_xor_sync(0xffffffffu, bm.y, o2));
-          }
-          move_reference(bm.x, m_run.x, m_move.x, alpha.x);
-          move_reference(bm.y, m_run.y, m_move.y, alpha.y);
-          if (g == 0) sts64(lex + kExAlpha + 32 * a + 8 * c, alpha);
-          if (__any_sync(0xffffffffu, alpha.x != 1.0f || alpha.y != 1.0f)) info |= kMoved;
-        }
-        const float2 l2e = make_float2(kLog2e, kLog2e), mm = make_float2(-m_run.x, -m_run.y);
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-          for (int k2 = 0; k2 < 2; ++k2) {
-            const float2 x2 = f2_fma(sc[hf][k2], l2e, mm);
-            // (a key the row does not see: 2^-inf = 0)
-            sc[hf][k2] = make_float2(fast_exp2(x2.x), fast_exp2(x2.y));
-          }
-        l_run = f2_fma(l_run, alpha, f2_add(f2_add(sc[0][0], sc[0][1]), f2_add(sc[1][0], sc[1][1])));
+      if (block_weights(sc, m_run, m_move, l_run, alpha)) {
+        info = kMoved;
+        if (g == 0) sts64(lex + kExAlpha + 32 * a + 8 * c, alpha);
       }
       // ---- hand the weights over
       if (T == 2 || c < 2) {
@@ -729,10 +403,8 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
           else ldsm_x4_trans<0>(vw, va ^ (uint32_t)(q << 4));
 #pragma unroll
           for (int d = 0; d < 2; ++d) {
-            // bytes (XOR 0x80) into the mantissa of 1024, less 1152: exact f16
-            const uint32_t t0v = vw[2 * d] ^ 0x80808080u, t1v = vw[2 * d + 1] ^ 0x80808080u;
-            const uint32_t af[4] = {i8pair_to_h2(t0v, 0x4240u), i8pair_to_h2(t0v, 0x4341u),
-                                    i8pair_to_h2(t1v, 0x4240u), i8pair_to_h2(t1v, 0x4341u)};
+            uint32_t af[4];
+            value_operand(vw[2 * d], vw[2 * d + 1], af);
 #pragma unroll
             for (int n = 0; n < T; ++n) mma_f16(o[q + d][n], af, bhi[n]);
 #pragma unroll
@@ -751,14 +423,9 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
     float down[2];                                // 2^-E of rows 2c + e
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      down[e] = __uint_as_float((254u << 23) - __float_as_uint(ws.up[2 * c + e]));
-      float v = e ? l_run.y : l_run.x;
-      v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 4));
-      v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 8));
-      v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 16));
-      if (e) l_run.y = v;
-      else l_run.x = v;
+      down[e] = inverse_scale(ws.up[2 * c + e]);
     }
+    l_run = make_float2(row_total(l_run.x), row_total(l_run.y));
     if (whole) {                                  // the other map's row sums
       if (lane == 0) sts32(lex + kExInfo + 4 * a, 0u);
       if (g == 0) {
@@ -1013,6 +680,35 @@ cudaError_t launch_split(DiffParams p, const TmaMaps& maps, cudaStream_t stream)
   return cudaGetLastError();
 }
 
+// Whether diff_tc_kernel takes the call: more than 16 rows per map, and enough windows
+// for the multiprocessors to have several at once.  One window alone takes it longer
+// (14 us against 10), and short sequences have more unit starts than blocks.  The call
+// in us, diff_tc_kernel | row groups, 32 query and 4 kv heads:
+//   sequences x keys, columns       3             5             8
+//    1 x 2k                             27 | 23 (4 columns)
+//    8 x 1k..4k                    34 | 32       41 | 37       59 | 54
+//   12 x 1k..4k                                  43 | 54
+//   16 x 1k..4k                    44 | 47       58 | 56       81 | 79
+//   24 x 1k..4k                                  73 | 78      106 | 112
+//   64 x 1k..4k                   106 | 123     144 | 183     223 | 282
+//   16 x 16k..32k                               311 | 414
+//    1 x 64k                                     78 | 89      116 | 127
+//   90 x 100..500                       57 | 57 (4 columns)   117 | 103
+// (With 16 rows, two groups: 64 x 1k..4k 80 | 84, 16 x 1k..4k 37 | 33.)
+bool many_rows(const DiffParams& p) {
+  static std::atomic<int> sms_cache[kMaxDevices];
+  if (p.R <= 16 || p.nwin_max < 4) return false;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const bool cached = dev >= 0 && dev < kMaxDevices;
+  int sms = cached ? sms_cache[dev].load() : 0;
+  if (sms <= 0) {
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return false;
+    if (cached) sms_cache[dev].store(sms);
+  }
+  return 2 * (int64_t)p.B * p.nwin_max * p.pairs >= 5 * (int64_t)sms;
+}
+
 template <int W>
 cudaError_t launch_merge(const DiffParams& p, cudaStream_t stream) {
   constexpr int kHalves = merge_halves<W>;
@@ -1043,7 +739,9 @@ cudaError_t launch_decode_diff(const DiffParams& p, cudaStream_t stream) {
   const int64_t rows = (int64_t)p.Hkv * p.cap_rows;
   if (!encode_plane_map(&maps.k, p.k, rows) || !encode_plane_map(&maps.v, p.v, rows))
     return cudaErrorInvalidValue;
-  const cudaError_t e = p.R <= 4 ? launch_split<1>(p, maps, stream) : launch_split<2>(p, maps, stream);
+  const cudaError_t e = many_rows(p) ? launch_tc_rows(p, maps, stream)
+                        : p.R <= 4   ? launch_split<1>(p, maps, stream)
+                                     : launch_split<2>(p, maps, stream);
   if (e != cudaSuccess || p.nwin_max <= 1) return e;
   if (p.nwin_max <= 32) return launch_merge<2>(p, stream);
   if (p.nwin_max <= 256) return launch_merge<4>(p, stream);

@@ -203,6 +203,106 @@ def test_a_row_of_more_than_256_windows():
     check(run(x).cpu().numpy(), want, mass)
 
 
+# Many rows per map over many windows have a kernel of their own; the length limit of
+# a call decides (more windows at most), so a small batch reaches it with a large one.
+MANY = 80000
+
+
+@gpu
+@pytest.mark.parametrize("M,Hq", [(1, 34), (3, 16), (3, 14), (4, 16), (3, 26), (5, 16), (6, 16), (5, 22),
+                                  (8, 14), (8, 16)])
+@pytest.mark.parametrize("q_gain", [2.0, 30.0])          # 30: references move in most windows
+def test_many_rows_over_many_windows(M, Hq, q_gain):
+    import int8_kv_decode_gb300 as K
+    x = inputs(4, M, Hq, 2, [1, 300, 1400, 120], seed=M * 100 + Hq, per_row=True, q_gain=q_gain)
+    t = device(x)
+    got = K.decode_diff(t["q"], t["k8"], t["ks"], t["v8"], t["vs"], t["start"], t["ctx"], MANY, t["lam"])
+    if q_gain == 2.0:
+        want, mass = expected(x)
+        check(got.cpu().numpy(), want, mass)
+    assert np.array_equal(bits(got), bits(run(x, t)))
+    for j in (0, M - 1):
+        col = K.decode_diff(t["q"][:, j:j + 1].contiguous(), t["k8"], t["ks"], t["v8"], t["vs"],
+                            t["start"], t["ctx"] + j, 1400 + j, t["lam"][:, j:j + 1].contiguous())
+        assert np.array_equal(bits(got[:, j:j + 1]), bits(col)), j
+
+
+@gpu
+@pytest.mark.parametrize("B,M,Hq,Hkv,top", [(300, 3, 16, 2, 700), (70, 5, 32, 4, 3000), (3, 8, 16, 2, 70000)])
+def test_many_rows_in_more_units_than_blocks(B, M, Hq, Hkv, top):
+    ctx = np.exp(np.random.default_rng(B).uniform(0, np.log(top), B)).astype(np.int32)
+    ctx[:2] = [top, 1]
+    x = inputs(B, M, Hq, Hkv, ctx, seed=B, q_gain=6.0)
+    t = device(x)
+    full = bits(run(x, t))
+    assert np.array_equal(full, bits(run(x, t)))
+    for b in range(0, B, max(1, B // 12)):               # alone: row groups
+        y = dict(x, ctx=np.minimum(x["ctx"][b:b + 1], 70000))
+        one = run(y, {**t, "q": t["q"][b:b + 1], "start": t["start"][b:b + 1], "ctx": t["ctx"][b:b + 1]})
+        assert np.array_equal(full[b:b + 1], bits(one)), b
+
+
+@gpu
+@pytest.mark.parametrize("P", [32, 128])
+def test_many_rows_paged_and_bad_sequences(P):
+    import torch
+    import int8_kv_decode_gb300 as K
+    x = inputs(5, 4, 16, 2, [900, 1, 64, 2000, 31], seed=P)
+    t = device(x)
+    want = bits(run(x, t))
+    L = page_layout(x["ctx"], x["start"], 4, P, seed=P)
+    kp, ksp, vp, vsp = paged_copy(L, t["k8"], t["ks"], t["v8"], t["vs"], seed=1)
+    table = torch.from_numpy(L.block_table).cuda()
+    ws = K.alloc_diff_workspace(5, 4, 16, MANY)
+
+    def paged(ctx, table):
+        return K.decode_diff_paged(t["q"], kp, ksp, vp, vsp, table, P, ctx, MANY, t["lam"], workspace=ws)
+
+    assert np.array_equal(bits(paged(t["ctx"], table)), want)
+    assert K.get_device_status(ws) == 0
+    ctx = t["ctx"].clone()
+    ctx[1], ctx[3] = 0, MANY + 1
+    got = paged(ctx, table)
+    assert torch.isnan(got[[1, 3]]).all()
+    assert np.array_equal(bits(got[[0, 2, 4]]), want[[0, 2, 4]])
+    assert K.get_device_status(ws) == K.DEVERR_BAD_SEQUENCE
+    broken = table.clone()
+    broken[0, 1] = L.n_pages + 7
+    got = paged(t["ctx"], broken)
+    assert K.get_device_status(ws) == K.DEVERR_BAD_PAGE
+    assert np.array_equal(bits(got[1:]), want[1:])
+
+
+@gpu
+def test_many_rows_two_streams_and_a_graph():
+    import torch
+    import int8_kv_decode_gb300 as K
+    x = inputs(6, 5, 16, 2, [3000, 700, 1, 256, 2222, 1500], seed=21)
+    t = device(x)
+    want = bits(run(x, t))
+    args = (t["q"], t["k8"], t["ks"], t["v8"], t["vs"], t["start"], t["ctx"], MANY, t["lam"])
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    spaces = [K.alloc_diff_workspace(6, 5, 16, MANY) for _ in streams]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(4):
+        for s, w in zip(streams, spaces):
+            with torch.cuda.stream(s):
+                outs.append(K.decode_diff(*args, workspace=w))
+    torch.cuda.synchronize()
+    assert all(np.array_equal(bits(o), want) for o in outs)
+    out = torch.empty_like(outs[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        K.decode_diff(*args, out=out, workspace=spaces[0])
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(bits(out), want)
+    assert all(K.get_device_status(w) == 0 for w in spaces)
+
+
 @gpu
 @pytest.mark.parametrize("P", [32, 64, 256])
 @pytest.mark.parametrize("M,Hq,Hkv,ctx", [(1, 8, 2, [1, 33, 900]), (5, 32, 4, [700, 1, 64]),

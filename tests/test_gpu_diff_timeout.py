@@ -40,7 +40,8 @@ def libs():
 
 @pytest.mark.parametrize("variant", range(len(VARIANTS)))
 @pytest.mark.parametrize("B,M,Hq,Hkv,ctx", [(2, 1, 8, 2, [120, 300]), (3, 2, 16, 2, [1500, 100, 600]),
-                                            (30, 1, 16, 2, 9000)])
+                                            (30, 1, 16, 2, 9000), (30, 3, 16, 2, 16000),
+                                            (12, 8, 16, 2, 9000)])
 def test_waits_that_run_out_set_the_bit_and_end(libs, variant, B, M, Hq, Hkv, ctx):
     import torch
     import int8_kv_decode_gb300 as K
