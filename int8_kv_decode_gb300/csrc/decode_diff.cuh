@@ -194,8 +194,8 @@ __device__ __forceinline__ void key_products(uint32_t k0, uint4 qlo, uint4 qhi, 
 #pragma unroll
   for (int part = 0; part < 2; ++part) {          // 64 channels each, both halves side by side
     const uint32_t k = part ? k0 ^ 16u : k0;
-    const uint4 a0 = lds128a<0>(k), b0 = lds128a<1024>(k);
-    const uint4 a1 = lds128a<2048>(k), b1 = lds128a<3072>(k);
+    const uint4 a0 = lds128a<0>(k), b0 = lds128a<8 * kD>(k);
+    const uint4 a1 = lds128a<16 * kD>(k), b1 = lds128a<24 * kD>(k);
     const uint4 q = part ? qhi : qlo;
     if (part == 0) {
       mma_i8_first(acc[0], a0.x, b0.x, a0.y, b0.y, q.x, q.y);
