@@ -250,6 +250,7 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
     // ---- the plane's scales: those of block 0, and the largest v_scale among the
     // keys that every row sees
     float nk, nv;                                 // scales of the next block's key `lane`
+    bool care;                                    // see hide_products
     {
       float vm = 0.0f;
 #pragma unroll
@@ -263,12 +264,15 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
         }
       }
       const int r = lane & 7, keys = keys_of(r);  // lane r < 8: row r
-      float vmax = warp_max(vm);
+      float vmax = warp_max(vm), vall = vmax;
       for (int key = max(it0.ctx, s0); key < s1; ++key) {    // draft keys
         const float v = __ldg(p.v_scale + ws.rows[ipar][(key - s0) >> 5] + ((key - s0) & 31));
         if (key < keys) vmax = fmaxf(vmax, v);
+        vall = max_bits(vall, v);
       }
-      if (lane < 8) ws.up[r] = operand_scale(vmax);
+      const float up = operand_scale(vmax);
+      if (lane < 8) ws.up[r] = up;
+      care = !__all_sync(0xffffffffu, scale_fits(up, vall));
     }
     __syncwarp();
 
@@ -284,138 +288,148 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) o[md][n][v] = 0.0f;
 
-    for (int i = 0; i < nb; ++i) {
-      if (i + 1 == nb) {                          // the next item's rows, its first after this one's last
-        put_rows(ipar ^ 1, entry);
-        if (lane == 0) ws.rows[ipar][nb] = ws.rows[ipar ^ 1][0];
-        __syncwarp();
-      }
-      const int t0 = s0 + i * kBlockBk;
-      const int next = ws.rows[ipar][i + 1];      // row of the block after this one, or -1
-      float ks4[4];                               // k_scale of keys g + 8q
-#pragma unroll
-      for (int q = 0; q < 4; ++q) ks4[q] = __shfl_sync(0xffffffffu, nk, g + 8 * q);
-      sts32<kVs>(lws + 4 * lane, nv);
-      {
-        const bool in = t0 + kBlockBk + lane < s1;
-        nk = in ? __ldg(p.k_scale + next + lane) : 0.0f;
-        nv = in ? __ldg(p.v_scale + next + lane) : 0.0f;
-      }
-      // ---- Q.K: keys 16 half + g (+ 8), rows 2c + e
-      int acc[2][4];
-      {
-        uint4 qlo = make_uint4(0, 0, 0, 0), qhi = qlo;
-        if (T == 2 || g < 4) {
-          const uint32_t lq = lws + g * kQStride + 32 * c;
-          qlo = lds128a<kQ>(lq);
-          qhi = lds128a<kQ + 16>(lq);
+    // The blocks of the unit; false: a copy never arrived, and the warp leaves.
+    auto blocks = [&](auto careful) __attribute__((always_inline)) -> bool {
+      constexpr bool kCare = decltype(careful)::value;
+      for (int i = 0; i < nb; ++i) {
+        if (i + 1 == nb) {                          // the next item's rows, its first after this one's last
+          put_rows(ipar ^ 1, entry);
+          if (lane == 0) ws.rows[ipar][nb] = ws.rows[ipar ^ 1][0];
+          __syncwarp();
         }
-        if (!ready(kbar)) {
-          give_up(false);
-          return;
-        }
-        key_products(kbuf + (uint32_t)swz(g, 2 * c), qlo, qhi, acc);
-        __syncwarp();
-        k_ahead = next >= 0;
-        if (next >= 0) load_stage(kbuf, &maps.k, next, kbar, policy);
-      }
-      // ---- scores s = (S * (qs * ks)) * sm_scale, rounded as written
-      float2 sc[2][2];                            // [half][key g | g + 8], rows 2c, 2c + 1
-      {
-        float2 qsr = make_float2(0.0f, 0.0f);
-        if (T == 2 || c < 2) qsr = lds64a<kQs>(lws + 8 * c);
-        scores_of(acc, ks4, qsr, p.sm_scale, sc);
-      }
-      if (t0 + kBlockBk > it0.ctx)                // keys that some row does not see
-        hide_keys(sc, t0 + g, keys_of(2 * c), keys_of(2 * c + 1));
-      float2 alpha = make_float2(1.0f, 1.0f);
-      int info = 0;
-      if (block_weights(sc, m_run, m_move, l_run, alpha)) {
-        info = kMoved;
-        if (g == 0) sts64(lex + kExAlpha + 32 * a + 8 * c, alpha);
-      }
-      // ---- hand the weights over
-      if (T == 2 || c < 2) {
-        const uint32_t w = lex + lww;
-        sts32<0>(w, sc[0][0].x);
-        sts32<8>(w, sc[0][0].y);
-        sts32<256>(w, sc[0][1].x);
-        sts32<264>(w, sc[0][1].y);
-        sts32<512>(w, sc[1][0].x);
-        sts32<520>(w, sc[1][0].y);
-        sts32<768>(w, sc[1][1].x);
-        sts32<776>(w, sc[1][1].y);
-      }
-      if (lane == 0) sts32(lex + kExInfo + 4 * a, (uint32_t)info);
-      named_sync(1 + wp, 64);
-      const float2 both = lds64a<kExInfo>(lex);
-      const int info0 = __float_as_int(both.x), info1 = __float_as_int(both.y);
-      const uint32_t lexr = lex + lwr, exa = lex + kExAlpha;
-      lex = exbase + exbase + Smem::kExBytes - lex;      // the other buffer
-      if (info0 | info1) {
-        if ((info0 | info1) & kFailed) {          // the other warp has left
-          drain(true);
-          return;
-        }
+        const int t0 = s0 + i * kBlockBk;
+        const int next = ws.rows[ipar][i + 1];      // row of the block after this one, or -1
+        float ks4[4];                               // k_scale of keys g + 8q
 #pragma unroll
-        for (int n = 0; n < T; ++n) {
-          // the tile's rows 2c, 2c + 1: map n, or (T = 1) map c / 2
-          const int map = T == 1 ? c >> 1 : n, r0 = T == 1 ? 2 * (c & 1) : 2 * c;
-          float2 al = lds64a<0>(exa + 32 * map + 4 * r0);
-          if (!((map ? info1 : info0) & kMoved)) al = make_float2(1.0f, 1.0f);
+        for (int q = 0; q < 4; ++q) ks4[q] = __shfl_sync(0xffffffffu, nk, g + 8 * q);
+        sts32<kVs>(lws + 4 * lane, nv);
+        {
+          const bool in = t0 + kBlockBk + lane < s1;
+          nk = in ? __ldg(p.k_scale + next + lane) : 0.0f;
+          nv = in ? __ldg(p.v_scale + next + lane) : 0.0f;
+        }
+        // ---- Q.K: keys 16 half + g (+ 8), rows 2c + e
+        int acc[2][4];
+        {
+          uint4 qlo = make_uint4(0, 0, 0, 0), qhi = qlo;
+          if (T == 2 || g < 4) {
+            const uint32_t lq = lws + g * kQStride + 32 * c;
+            qlo = lds128a<kQ>(lq);
+            qhi = lds128a<kQ + 16>(lq);
+          }
+          if (!ready(kbar)) {
+            give_up(false);
+            return false;
+          }
+          key_products(kbuf + (uint32_t)swz(g, 2 * c), qlo, qhi, acc);
+          __syncwarp();
+          k_ahead = next >= 0;
+          if (next >= 0) load_stage(kbuf, &maps.k, next, kbar, policy);
+        }
+        // ---- scores s = (S * (qs * ks)) * sm_scale, rounded as written
+        float2 sc[2][2];                            // [half][key g | g + 8], rows 2c, 2c + 1
+        {
+          float2 qsr = make_float2(0.0f, 0.0f);
+          if (T == 2 || c < 2) qsr = lds64a<kQs>(lws + 8 * c);
+          scores_of(acc, ks4, qsr, p.sm_scale, sc);
+        }
+        if (t0 + kBlockBk > it0.ctx)                // keys that some row does not see
+          hide_keys(sc, t0 + g, keys_of(2 * c), keys_of(2 * c + 1));
+        float2 alpha = make_float2(1.0f, 1.0f);
+        int info = 0;
+        if (block_weights(sc, m_run, m_move, l_run, alpha)) {
+          info = kMoved;
+          if (g == 0) sts64(lex + kExAlpha + 32 * a + 8 * c, alpha);
+        }
+        // ---- hand the weights over
+        if (T == 2 || c < 2) {
+          const uint32_t w = lex + lww;
+          sts32<0>(w, sc[0][0].x);
+          sts32<8>(w, sc[0][0].y);
+          sts32<256>(w, sc[0][1].x);
+          sts32<264>(w, sc[0][1].y);
+          sts32<512>(w, sc[1][0].x);
+          sts32<520>(w, sc[1][0].y);
+          sts32<768>(w, sc[1][1].x);
+          sts32<776>(w, sc[1][1].y);
+        }
+        if (lane == 0) sts32(lex + kExInfo + 4 * a, (uint32_t)info);
+        named_sync(1 + wp, 64);
+        const float2 both = lds64a<kExInfo>(lex);
+        const int info0 = __float_as_int(both.x), info1 = __float_as_int(both.y);
+        const uint32_t lexr = lex + lwr, exa = lex + kExAlpha;
+        lex = exbase + exbase + Smem::kExBytes - lex;      // the other buffer
+        if (info0 | info1) {
+          if ((info0 | info1) & kFailed) {          // the other warp has left
+            drain(true);
+            return false;
+          }
 #pragma unroll
-          for (int md = 0; md < 8; ++md) {
-            const float2 lo = f2_mul(make_float2(o[md][n][0], o[md][n][1]), al);
-            const float2 hi = f2_mul(make_float2(o[md][n][2], o[md][n][3]), al);
-            o[md][n][0] = lo.x; o[md][n][1] = lo.y; o[md][n][2] = hi.x; o[md][n][3] = hi.y;
+          for (int n = 0; n < T; ++n) {
+            // the tile's rows 2c, 2c + 1: map n, or (T = 1) map c / 2
+            const int map = T == 1 ? c >> 1 : n, r0 = T == 1 ? 2 * (c & 1) : 2 * c;
+            float2 al = lds64a<0>(exa + 32 * map + 4 * r0);
+            if (!((map ? info1 : info0) & kMoved)) al = make_float2(1.0f, 1.0f);
+#pragma unroll
+            for (int md = 0; md < 8; ++md) {
+              const float2 lo = f2_mul(make_float2(o[md][n][0], o[md][n][1]), al);
+              const float2 hi = f2_mul(make_float2(o[md][n][2], o[md][n][3]), al);
+              o[md][n][0] = lo.x; o[md][n][1] = lo.y; o[md][n][2] = hi.x; o[md][n][3] = hi.y;
+            }
           }
         }
-      }
-      // ---- P.V: the operand w * v_scale * 2^E as f16 hi + lo (22 bits), V exact
-      const float up = lds32a<kUp>(lws + 4 * g);
-      const float2 up2 = make_float2(up, up);
-      if (!ready(vbar)) {
-        give_up(true);
-        return;
-      }
-      // A = V^T.  Row g of m-tile q is channel 16q + 2g, row g + 8 the next one; a
-      // 16-bit element of the buffer is two channels of a key, so the transposing
-      // load pairs the keys 2c, 2c + 1 of both channels in a register.  Lane 8i + r
-      // addresses key r (+ 8 if i is odd) of the half, 16-byte chunk q + i / 2.
-      const uint32_t va = vbuf + (uint32_t)((lane & 15) * kD + (((lane >> 4) ^ (lane & 7)) << 4));
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const float2 v0 = f2_mul(hf ? lds64a<kVs + 64>(lws + 8 * c) : lds64a<kVs>(lws + 8 * c), up2);
-        const float2 v1 = f2_mul(hf ? lds64a<kVs + 96>(lws + 8 * c) : lds64a<kVs + 32>(lws + 8 * c), up2);
-        uint2 bhi[T], blo[T];
-#pragma unroll
-        for (int n = 0; n < T; ++n) {
-          const uint32_t w = lexr + 1024 * n;
-          const float2 y0 = f2_mul(hf ? lds64a<512>(w) : lds64a<0>(w), v0);
-          const float2 y1 = f2_mul(hf ? lds64a<768>(w) : lds64a<256>(w), v1);
-          split_f16x2(y0.x, y0.y, bhi[n].x, blo[n].x);
-          split_f16x2(y1.x, y1.y, bhi[n].y, blo[n].y);
+        // ---- P.V: the operand w * v_scale * 2^E as f16 hi + lo (22 bits), V exact
+        const float up = lds32a<kUp>(lws + 4 * g);
+        const float2 up2 = make_float2(up, up);
+        if (!ready(vbar)) {
+          give_up(true);
+          return false;
         }
+        // A = V^T.  Row g of m-tile q is channel 16q + 2g, row g + 8 the next one; a
+        // 16-bit element of the buffer is two channels of a key, so the transposing
+        // load pairs the keys 2c, 2c + 1 of both channels in a register.  Lane 8i + r
+        // addresses key r (+ 8 if i is odd) of the half, 16-byte chunk q + i / 2.
+        const uint32_t va = vbuf + (uint32_t)((lane & 15) * kD + (((lane >> 4) ^ (lane & 7)) << 4));
 #pragma unroll
-        for (int q = 0; q < 8; q += 2) {
-          uint32_t vw[4];                         // keys 2c.. and 2c+8.. of tile q, then of tile q + 1
-          if (hf) ldsm_x4_trans<2048>(vw, va ^ (uint32_t)(q << 4));
-          else ldsm_x4_trans<0>(vw, va ^ (uint32_t)(q << 4));
+        for (int hf = 0; hf < 2; ++hf) {
+          const float2 v0 = f2_mul(hf ? lds64a<kVs + 64>(lws + 8 * c) : lds64a<kVs>(lws + 8 * c), up2);
+          const float2 v1 = f2_mul(hf ? lds64a<kVs + 96>(lws + 8 * c) : lds64a<kVs + 32>(lws + 8 * c), up2);
+          uint2 bhi[T], blo[T];
 #pragma unroll
-          for (int d = 0; d < 2; ++d) {
-            uint32_t af[4];
-            value_operand(vw[2 * d], vw[2 * d + 1], af);
+          for (int n = 0; n < T; ++n) {
+            const uint32_t w = lexr + 1024 * n;
+            const float2 w0 = hf ? lds64a<512>(w) : lds64a<0>(w), w1 = hf ? lds64a<768>(w) : lds64a<256>(w);
+            float2 y0 = f2_mul(w0, v0), y1 = f2_mul(w1, v1);
+            if constexpr (kCare) {
+              hide_products(y0, w0);
+              hide_products(y1, w1);
+            }
+            split_f16x2(y0.x, y0.y, bhi[n].x, blo[n].x);
+            split_f16x2(y1.x, y1.y, bhi[n].y, blo[n].y);
+          }
 #pragma unroll
-            for (int n = 0; n < T; ++n) mma_f16(o[q + d][n], af, bhi[n]);
+          for (int q = 0; q < 8; q += 2) {
+            uint32_t vw[4];                         // keys 2c.. and 2c+8.. of tile q, then of tile q + 1
+            if (hf) ldsm_x4_trans<2048>(vw, va ^ (uint32_t)(q << 4));
+            else ldsm_x4_trans<0>(vw, va ^ (uint32_t)(q << 4));
 #pragma unroll
-            for (int n = 0; n < T; ++n) mma_f16(o[q + d][n], af, blo[n]);
+            for (int d = 0; d < 2; ++d) {
+              uint32_t af[4];
+              value_operand(vw[2 * d], vw[2 * d + 1], af);
+#pragma unroll
+              for (int n = 0; n < T; ++n) mma_f16(o[q + d][n], af, bhi[n]);
+#pragma unroll
+              for (int n = 0; n < T; ++n) mma_f16(o[q + d][n], af, blo[n]);
+            }
           }
         }
+        __syncwarp();
+        if (next >= 0) load_stage(vbuf, &maps.v, next, vbar, policy);
+        ph ^= 1u;
       }
-      __syncwarp();
-      if (next >= 0) load_stage(vbuf, &maps.v, next, vbar, policy);
-      ph ^= 1u;
-    }
+      return true;
+    };
+    if (!(care ? blocks(std::true_type{}) : blocks(std::false_type{}))) return;
     const bool whole = diff_windows(it0.ctx + M - 1) == 1;
     const int b = it0.b, pair = it0.pair;
 

@@ -3,6 +3,8 @@
 // same bytes whichever of them takes it.
 #pragma once
 
+#include <type_traits>
+
 #include "decode_split.cuh"
 #include "ops_internal.cuh"
 
@@ -279,6 +281,22 @@ __device__ __forceinline__ float operand_scale(float vmax) {
 }
 __device__ __forceinline__ float inverse_scale(float up) {
   return __uint_as_float((254u << 23) - __float_as_uint(up));
+}
+// Products weight * v_scale * 2^E of keys that a row may not see: their weight is 0, but
+// 2^E goes by the keys that the row sees, and with a larger scale 2^E may leave float32,
+// where 0 * inf is no number.  Units where that can happen (scale_fits false) take these
+// products in a block loop of their own, so that the others' stays as it is.
+__device__ __forceinline__ void hide_products(float2& y, float2 w) {
+  if (w.x == 0.0f) y.x = 0.0f;
+  if (w.y == 0.0f) y.y = 0.0f;
+}
+// Whether the largest v_scale of the window, hidden keys included, times 2^E is finite.
+__device__ __forceinline__ bool scale_fits(float up, float vall) {
+  return __fmul_rn(vall, up) < INFINITY;
+}
+// The larger of two values >= 0; no number counts as the largest.
+__device__ __forceinline__ float max_bits(float a, float b) {
+  return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
 }
 // Bytes (XOR 0x80) of two keys of two channels into the mantissa of 1024, less 1152:
 // exact f16.  vw: words of the transposing load; af: the operand's rows g and g + 8,

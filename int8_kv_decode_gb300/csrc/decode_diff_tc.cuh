@@ -258,154 +258,168 @@ diff_tc_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
       qhi = make_uint4(q[4], q[5], q[6], q[7]);
     }
     auto keys_of = [&](int r) -> int { return it.ctx + column(min(rg * 8 + r, R - 1)); };
-    // ---- 2^E of the row 2c + odd, for either plane's scales
-    float up[2] = {1.0f, 1.0f};
+    // ---- 2^E of the row 2c + odd, for either plane's scales: lane j takes column j.  Every
+    // warp finds the same `care` (see hide_products): they go through the blocks together.
+    float up[2];
+    bool care = false;
 #pragma unroll
-    for (int pl = 0; pl < 2 && !issuer; ++pl) {
+    for (int pl = 0; pl < 2; ++pl) {
       float vm = 0.0f;
 #pragma unroll
       for (int e = 0; e < kWinBlocks; ++e)
         if (s0 + 32 * e + lane < min(it.ctx, s1)) vm = fmaxf(vm, sm.vs[slot][pl][32 * e + lane]);
-      float vmax = warp_max(vm);
-      const int keys = keys_of(2 * c + odd);
-      for (int key = max(it.ctx, s0); key < s1; ++key)       // draft keys
-        if (key < keys) vmax = fmaxf(vmax, sm.vs[slot][pl][key - s0]);
-      up[pl] = operand_scale(vmax);
-      if (g < 2) sm.down[slot][pl][8 * warp + 2 * c + g] = inverse_scale(up[pl]);
+      float vmax = warp_max(vm), vall = vmax;
+      const int keys = it.ctx + min(lane & 7, M - 1);
+      for (int key = max(it.ctx, s0); key < s1; ++key) {     // draft keys
+        const float v = sm.vs[slot][pl][key - s0];
+        if (key < keys) vmax = fmaxf(vmax, v);
+        vall = max_bits(vall, v);
+      }
+      const float u = operand_scale(vmax);
+      care |= !scale_fits(u, vall);
+      up[pl] = __shfl_sync(0xffffffffu, u, column(min(rg * 8 + 2 * c + odd, R - 1)));
+      if (g < 2 && !issuer) sm.down[slot][pl][8 * warp + 2 * c + g] = inverse_scale(up[pl]);
     }
+    care = __any_sync(0xffffffffu, care);
     float2 m_run = make_float2(0.0f, 0.0f), m_move = make_float2(-INFINITY, -INFINITY);
     float2 l_run = make_float2(0.0f, 0.0f);
 
     const float* const ks0 = &sm.ks[slot][a][g];
-    for (int i = 0; i < nb; ++i, ++gb) {
-      const int t0 = s0 + i * kBlockBk;
-      bool moved = false;
-      if (!issuer) {
-        bool ok = ready(&sm.full[st], ph);
-        const uint32_t ring = smem_u32(sm.ring[st]);
-        int acc[2][4];
-        key_products(ring + a * kBlockBytes + (uint32_t)swz(g, 2 * c), qlo, qhi, acc);
-        float ks4[4];
+    auto blocks = [&](auto careful) __attribute__((always_inline)) {
+      constexpr bool kCare = decltype(careful)::value;
+      for (int i = 0; i < nb; ++i, ++gb) {
+        const int t0 = s0 + i * kBlockBk;
+        bool moved = false;
+        if (!issuer) {
+          bool ok = ready(&sm.full[st], ph);
+          const uint32_t ring = smem_u32(sm.ring[st]);
+          int acc[2][4];
+          key_products(ring + a * kBlockBytes + (uint32_t)swz(g, 2 * c), qlo, qhi, acc);
+          float ks4[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) ks4[q] = ks0[32 * i + 8 * q];
-        float2 sc[2][2];
-        scores_of(acc, ks4, qs, p.sm_scale, sc);
-        if (t0 + kBlockBk > it.ctx) hide_keys(sc, t0 + g, keys_of(2 * c), keys_of(2 * c + 1));
-        float2 alpha = make_float2(1.0f, 1.0f);
-        moved = block_weights(sc, m_run, m_move, l_run, alpha);
-        // ---- the weights of two keys of a row side by side: keys 8q + (g & ~1) and the
-        // next, row 2c + odd
-        float2 w[4];
+          for (int q = 0; q < 4; ++q) ks4[q] = ks0[32 * i + 8 * q];
+          float2 sc[2][2];
+          scores_of(acc, ks4, qs, p.sm_scale, sc);
+          if (t0 + kBlockBk > it.ctx) hide_keys(sc, t0 + g, keys_of(2 * c), keys_of(2 * c + 1));
+          float2 alpha = make_float2(1.0f, 1.0f);
+          moved = block_weights(sc, m_run, m_move, l_run, alpha);
+          // ---- the weights of two keys of a row side by side: keys 8q + (g & ~1) and the
+          // next, row 2c + odd
+          float2 w[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float2 x = sc[q >> 1][q & 1];
-          const float other = __shfl_xor_sync(0xffffffffu, odd ? x.x : x.y, 4);
-          w[q] = odd ? make_float2(other, x.y) : make_float2(x.x, other);
-        }
-        // ---- the MMAs of the block before have read the operands
-        if (commits > waited) {
-          const bool ok_m = stage_ready(smem_u32(&sm.done), (uint32_t)(commits - 1) & 1u);
-          if (ok_m) waited = commits;             // else the exit waits again
-          ok = ok && ok_m;
-          tc_fence_after();
-        }
-        if (!ok) {
-          sm.fail[gb & 1] = gb + 1;
-        } else {
-          uint8_t* const dst = &sm.pb[0][0][0][0] + lane_p;
-          const float* const vs0 = &sm.vs[0][0][0] + slot * 2 * kWindow + 32 * i + (g & 6);
+          for (int q = 0; q < 4; ++q) {
+            const float2 x = sc[q >> 1][q & 1];
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? x.x : x.y, 4);
+            w[q] = odd ? make_float2(other, x.y) : make_float2(x.x, other);
+          }
+          // ---- the MMAs of the block before have read the operands
+          if (commits > waited) {
+            const bool ok_m = stage_ready(smem_u32(&sm.done), (uint32_t)(commits - 1) & 1u);
+            if (ok_m) waited = commits;             // else the exit waits again
+            ok = ok && ok_m;
+            tc_fence_after();
+          }
+          if (!ok) {
+            sm.fail[gb & 1] = gb + 1;
+          } else {
+            uint8_t* const dst = &sm.pb[0][0][0][0] + lane_p;
+            const float* const vs0 = &sm.vs[0][0][0] + slot * 2 * kWindow + 32 * i + (g & 6);
 #pragma unroll
-          for (int pl = 0; pl < 2; ++pl)
+            for (int pl = 0; pl < 2; ++pl)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float2 vs = *reinterpret_cast<const float2*>(vs0 + pl * kWindow + 8 * q);
-              const float2 y = f2_mul(w[q], f2_mul(vs, make_float2(up[pl], up[pl])));
-              uint32_t hi, lo;
-              split_f16x2(y.x, y.y, hi, lo);
-              uint8_t* const to = dst + (pl * 4 + (q >> 1) * 2) * S::kOperand + (q & 1) * 128;
-              *reinterpret_cast<uint32_t*>(to) = hi;
-              *reinterpret_cast<uint32_t*>(to + S::kOperand) = lo;
-            }
-          if (g == 0) *reinterpret_cast<float2*>(&sm.alpha[8 * warp + 2 * c]) = alpha;
-          // ---- V^T: item x = (plane, 16 keys, 32 channels).  Row 16q + g holds channel
-          // 16q + 2g, row 16q + 8 + g the next one.
-          const uint32_t va = ring + 2 * kBlockBytes +
-                              (uint32_t)((lane & 15) * kD + (((lane >> 4) ^ (lane & 7)) << 4));
+              for (int q = 0; q < 4; ++q) {
+                const float2 vs = *reinterpret_cast<const float2*>(vs0 + pl * kWindow + 8 * q);
+                float2 y = f2_mul(w[q], f2_mul(vs, make_float2(up[pl], up[pl])));
+                if constexpr (kCare) hide_products(y, w[q]);
+                uint32_t hi, lo;
+                split_f16x2(y.x, y.y, hi, lo);
+                uint8_t* const to = dst + (pl * 4 + (q >> 1) * 2) * S::kOperand + (q & 1) * 128;
+                *reinterpret_cast<uint32_t*>(to) = hi;
+                *reinterpret_cast<uint32_t*>(to + S::kOperand) = lo;
+              }
+            if (g == 0) *reinterpret_cast<float2*>(&sm.alpha[8 * warp + 2 * c]) = alpha;
+            // ---- V^T: item x = (plane, 16 keys, 32 channels).  Row 16q + g holds channel
+            // 16q + 2g, row 16q + 8 + g the next one.
+            const uint32_t va = ring + 2 * kBlockBytes +
+                                (uint32_t)((lane & 15) * kD + (((lane >> 4) ^ (lane & 7)) << 4));
 #pragma unroll
-          for (int x0 = 0; x0 < 16; x0 += W) {
-            const int x = x0 + warp;              // 8 plane + 4 half + chunk pair
-            if (x0 + W > 16 && x >= 16) break;
-            uint32_t vw[4];
-            ldsm_x4_trans<0>(vw, (va ^ (uint32_t)((x & 3) << 5)) + (x >> 3) * kBlockBytes + ((x >> 2) & 1) * 2048);
-            uint8_t* const to = &sm.vt[0][0][0] + lane_v + x * 1024;
+            for (int x0 = 0; x0 < 16; x0 += W) {
+              const int x = x0 + warp;              // 8 plane + 4 half + chunk pair
+              if (x0 + W > 16 && x >= 16) break;
+              uint32_t vw[4];
+              ldsm_x4_trans<0>(vw, (va ^ (uint32_t)((x & 3) << 5)) + (x >> 3) * kBlockBytes + ((x >> 2) & 1) * 2048);
+              uint8_t* const to = &sm.vt[0][0][0] + lane_v + x * 1024;
 #pragma unroll
-            for (int d = 0; d < 2; ++d) {
-              uint32_t af[4];
-              value_operand(vw[2 * d], vw[2 * d + 1], af);
-              *reinterpret_cast<uint32_t*>(to + d * 512) = af[0];
-              *reinterpret_cast<uint32_t*>(to + d * 512 + 256) = af[1];
-              *reinterpret_cast<uint32_t*>(to + d * 512 + 128) = af[2];
-              *reinterpret_cast<uint32_t*>(to + d * 512 + 384) = af[3];
+              for (int d = 0; d < 2; ++d) {
+                uint32_t af[4];
+                value_operand(vw[2 * d], vw[2 * d + 1], af);
+                *reinterpret_cast<uint32_t*>(to + d * 512) = af[0];
+                *reinterpret_cast<uint32_t*>(to + d * 512 + 256) = af[1];
+                *reinterpret_cast<uint32_t*>(to + d * 512 + 128) = af[2];
+                *reinterpret_cast<uint32_t*>(to + d * 512 + 384) = af[3];
+              }
             }
           }
+          asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        } else if (i == 0) {                        // the next item's rows
+          put_rows(slot ^ 1, nxt, pentry);
         }
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-      } else if (i == 0) {                        // the next item's rows
-        put_rows(slot ^ 1, nxt, pentry);
-      }
-      tc_fence_before();
-      const bool rescale = __syncthreads_or(moved) != 0;
-      if (sm.fail[gb & 1] == gb + 1) {
-        failed = true;
-        break;
-      }
-      if (rescale) {                              // D *= alpha where a reference moved
-        if (warp < kReaders) {
-          tc_fence_after();
+        tc_fence_before();
+        const bool rescale = __syncthreads_or(moved) != 0;
+        if (sm.fail[gb & 1] == gb + 1) {
+          failed = true;
+          return;
+        }
+        if (rescale) {                              // D *= alpha where a reference moved
+          if (warp < kReaders) {
+            tc_fence_after();
 #pragma unroll
-          for (int x = 0; x < 8 / kReaders; ++x)
+            for (int x = 0; x < 8 / kReaders; ++x)
 #pragma unroll 1
-            for (int n = 0; n < S::kRows; n += 16) {
-              const uint32_t at = tlane + (kReaders == 4 ? x : warp >> 2) * S::kPlane + n;
-              float v[16];
-              tc_ld16(at, v);
+              for (int n = 0; n < S::kRows; n += 16) {
+                const uint32_t at = tlane + (kReaders == 4 ? x : warp >> 2) * S::kPlane + n;
+                float v[16];
+                tc_ld16(at, v);
 #pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                const float2 y = f2_mul(make_float2(v[j], v[j + 1]),
-                                        *reinterpret_cast<const float2*>(&sm.alpha[n + j]));
-                v[j] = y.x;
-                v[j + 1] = y.y;
+                for (int j = 0; j < 16; j += 2) {
+                  const float2 y = f2_mul(make_float2(v[j], v[j + 1]),
+                                          *reinterpret_cast<const float2*>(&sm.alpha[n + j]));
+                  v[j] = y.x;
+                  v[j + 1] = y.y;
+                }
+                tc_st16(at, v);
               }
-              tc_st16(at, v);
-            }
-          tc_wait_st();
-          tc_fence_before();
+            tc_wait_st();
+            tc_fence_before();
+          }
+          __syncthreads();
         }
-        __syncthreads();
-      }
-      if (issuer) {
-        if (lane == 0) {
-          tc_fence_after();
+        if (issuer) {
+          if (lane == 0) {
+            tc_fence_after();
 #pragma unroll
-          for (int pl = 0; pl < 2; ++pl)
+            for (int pl = 0; pl < 2; ++pl)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              const uint64_t v = smem_desc(sm.vt[pl][hf]);
-              tc_mma_n(tmem + pl * S::kPlane, v, smem_desc(sm.pb[pl][hf][0]), kIdesc);
-              tc_mma_n(tmem + pl * S::kPlane, v, smem_desc(sm.pb[pl][hf][1]), kIdesc);
-            }
-          tc_commit(&sm.done);
+              for (int hf = 0; hf < 2; ++hf) {
+                const uint64_t v = smem_desc(sm.vt[pl][hf]);
+                tc_mma_n(tmem + pl * S::kPlane, v, smem_desc(sm.pb[pl][hf][0]), kIdesc);
+                tc_mma_n(tmem + pl * S::kPlane, v, smem_desc(sm.pb[pl][hf][1]), kIdesc);
+              }
+            tc_commit(&sm.done);
+          }
+          __syncwarp();
+          while (issued <= gb + kStages && produce()) {}
         }
-        __syncwarp();
-        while (issued <= gb + kStages && produce()) {}
+        ++commits;
+        if (++st == kStages) {
+          st = 0;
+          ph ^= 1u;
+        }
+        if (i == 0 && nxt.b >= 0) copy_scales(slot ^ 1, nxt);
       }
-      ++commits;
-      if (++st == kStages) {
-        st = 0;
-        ph ^= 1u;
-      }
-      if (i == 0 && nxt.b >= 0) copy_scales(slot ^ 1, nxt);
-    }
+    };
+    if (care) blocks(std::true_type{});
+    else blocks(std::false_type{});
     if (failed) break;
 
     // ---- the window's row sums and references

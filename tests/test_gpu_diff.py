@@ -429,3 +429,59 @@ def test_offsets_past_32_bits():
     got = K.decode_diff(t["q"], big["k8"], big["ks"], big["v8"], big["vs"], t["start"] + (cap - 700),
                         t["ctx"], 700, t["lam"])
     assert np.array_equal(bits(got), want)
+
+
+# ------------------------------------------- keys that a column does not see
+
+def columns_alone(x, t, full, limit=None):
+    """Every column of `full` has the bytes of a single-column call (which has no
+    hidden key)."""
+    import int8_kv_decode_gb300 as K
+    for j in range(x["M"]):
+        col = K.decode_diff(t["q"][:, j:j + 1].contiguous(), t["k8"], t["ks"], t["v8"], t["vs"],
+                            t["start"], t["ctx"] + j, limit or int(x["ctx"].max()) + j, t["lam"])
+        assert np.array_equal(bits(full[:, j:j + 1]), bits(col)), j
+
+
+# M, Hq and the limit: up to 4 rows per map, 8 rows and more, and the kernel of many rows
+HIDING = [(2, 4, None), (4, 2, None), (8, 2, None), (2, 16, None), (3, 12, 80000), (8, 16, 80000)]
+
+
+@gpu
+@pytest.mark.parametrize("M,Hq,limit", HIDING)
+def test_large_drafts_behind_zero_or_tiny_rows(M, Hq, limit):
+    # what a column sees in a window is all zeros, or tiny, and a draft key behind it has
+    # a large scale: 2^E of the small scales times the hidden one would leave float32
+    import int8_kv_decode_gb300 as K
+    x = inputs(4, M, Hq, 2, [1, 128, 300, 40], seed=31)
+    at = x["start"]
+    drafts = [np.arange(int(c), int(c) + M - 1) + int(s) for c, s in zip(x["ctx"], at)]
+    x["v8"][:, at[0]], x["vs"][:, at[0]] = 0, 0                     # the only key of column 0
+    x["vs"][:, at[2] + 256:at[2] + 300] = np.float32(2.0 ** -118)
+    x["vs"][:, at[3]:at[3] + 40] = np.float32(2.0 ** -126)
+    for d in drafts:
+        x["vs"][:, d] = 8.0
+    x["v8"][:, drafts[1][0]], x["vs"][:, drafts[1][0]] = 0, 0       # a window begins with a draft of zeros
+    t = device(x)
+    full = K.decode_diff(t["q"], t["k8"], t["ks"], t["v8"], t["vs"], t["start"], t["ctx"],
+                         limit or 300, t["lam"])
+    want, mass = expected(x)
+    check(full.cpu().numpy(), want, mass)
+    columns_alone(x, t, full)
+
+
+@gpu
+@pytest.mark.parametrize("M,Hq,limit", HIDING)
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_a_hidden_scale_that_is_no_number(M, Hq, limit, value):
+    # the last draft key's scales: the columns before the last do not see it
+    import int8_kv_decode_gb300 as K
+    x = inputs(3, M, Hq, 2, [5, 255, 600], seed=32)
+    t = device(x)
+    args = (t["q"], t["k8"], t["ks"], t["v8"], t["vs"], t["start"], t["ctx"], limit or 600, t["lam"])
+    want = bits(K.decode_diff(*args))
+    for b in range(3):
+        last = int(x["start"][b] + x["ctx"][b]) + M - 2
+        t["ks"][:, last] = value
+        t["vs"][:, last] = value
+    assert np.array_equal(bits(K.decode_diff(*args))[:, :M - 1], want[:, :M - 1])
