@@ -388,8 +388,12 @@ int kattn_hash_rows(const void* data, int64_t n_rows, int64_t row_bytes, int64_t
  *   V_t   = (v_scale[2p][t] * v[2p][t], v_scale[2p+1][t] * v[2p+1][t])    (256 channels)
  *   out[b][j][i][:] = sum_t softmax(s_0)_t V_t - lam * sum_t softmax(s_1)_t V_t
  * over the keys t < ctx_len[b] + j, with q8, qs the absmax/127 quantization of
- * q[b][j][2i + a] as in kattn_decode.  The weights stay in float32: a P rounded
- * to 8 bits would leave the rounding error of what the two maps share.
+ * q[b][j][2i + a] as in kattn_decode.  No rounded P is offered: 8 bits would leave
+ * the rounding error of what the two maps share.  The weights are float32; each
+ * product weight * v_scale that multiplies V is held to 22 bits, or to 2^-27 of the
+ * row's largest product in its window of 256 keys if that is coarser (2^-39 where
+ * the v_scales of the window's keys differ by more than a factor of 64).  Weights
+ * below about 2^-126 of the largest are 0.
  * lam: float32, [H] (lam_per_row = 0: one value per head, e.g. the learned
  *   weight of a layer) or [B][M][H] (lam_per_row = 1: one per row).
  * Hkv must be even.  q: float32 [B][M][Hq][d], d = 128.

@@ -56,7 +56,8 @@ constexpr int kFailed = 1, kMoved = 2;
 struct __align__(16) WarpState {
   float vs[kBlockBk];                             // v_scale of the block
   float qs[8];
-  float up[8];                                    // 2^E of the operand's rows
+  float up[8];                                    // 2^E of the operand's rows (1: it follows the products)
+  float mag[2][8], post[2][8], factor[2][8];      // then, per tile: largest product (-1: no such row), 2^E, rescaling
   float row_sum[8];                               // of a sequence that ends in its window
   uint8_t q[8 * kQStride];
   int rows[2][kWinBlocks + 2];                    // rows of the blocks, by item slot
@@ -250,29 +251,34 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
     // ---- the plane's scales: those of block 0, and the largest v_scale among the
     // keys that every row sees
     float nk, nv;                                 // scales of the next block's key `lane`
-    bool care;                                    // see hide_products
+    bool care;                                    // see ScaleRange
     {
-      float vm = 0.0f;
+      const int own = min(it0.ctx, s1), d0 = max(it0.ctx, s0), drafts = s1 - d0;
+      float most = 0.0f, least = INFINITY;
 #pragma unroll
       for (int e = 0; e < kWinBlocks; ++e) {
         const int key = s0 + 32 * e + lane, at = ws.rows[ipar][e] + lane;
         const float v = key < s1 ? __ldg(p.v_scale + at) : 0.0f;
-        if (key < it0.ctx) vm = fmaxf(vm, v);
+        if (key < own) {
+          most = fmaxf(most, v);
+          least = fminf(least, v);
+        }
         if (e == 0) {
           nv = v;
           nk = key < s1 ? __ldg(p.k_scale + at) : 0.0f;
         }
       }
+      float draft = 0.0f;
+      if (lane < drafts) draft = __ldg(p.v_scale + ws.rows[ipar][(d0 + lane - s0) >> 5] + ((d0 + lane - s0) & 31));
       const int r = lane & 7, keys = keys_of(r);  // lane r < 8: row r
-      float vmax = warp_max(vm), vall = vmax;
-      for (int key = max(it0.ctx, s0); key < s1; ++key) {    // draft keys
-        const float v = __ldg(p.v_scale + ws.rows[ipar][(key - s0) >> 5] + ((key - s0) & 31));
-        if (key < keys) vmax = fmaxf(vmax, v);
-        vall = max_bits(vall, v);
+      ScaleRange range = warp_range(most, least);
+      for (int i = 0; i < drafts; ++i) range.add(__shfl_sync(0xffffffffu, draft, i), d0 + i < keys);
+      if (lane < 8) ws.up[r] = range.scale();
+      care = __any_sync(0xffffffffu, range.care());
+      if (care && lane < 8) {
+#pragma unroll
+        for (int n = 0; n < T; ++n) ws.mag[n][r] = range.spread() ? 0.0f : -1.0f;
       }
-      const float up = operand_scale(vmax);
-      if (lane < 8) ws.up[r] = up;
-      care = !__all_sync(0xffffffffu, scale_fits(up, vall));
     }
     __syncwarp();
 
@@ -359,17 +365,49 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
         const int info0 = __float_as_int(both.x), info1 = __float_as_int(both.y);
         const uint32_t lexr = lex + lwr, exa = lex + kExAlpha;
         lex = exbase + exbase + Smem::kExBytes - lex;      // the other buffer
-        if (info0 | info1) {
-          if ((info0 | info1) & kFailed) {          // the other warp has left
+        if (kCare || (info0 | info1)) {
+          if ((info0 | info1) & kFailed) {        // the other warp has left
             drain(true);
             return false;
+          }
+          if constexpr (kCare) {                  // row g of each tile: its largest product, and E
+#pragma unroll
+            for (int n = 0; n < T; ++n) {
+              const uint32_t w = lexr + 1024 * n, v = lws + 8 * c;
+              float m = 0.0f;
+              auto take = [&](float2 w2, float2 v2) {
+                float2 y = f2_mul(w2, v2);
+                hide_products(y, w2);
+                m = fmaxf(m, fmaxf(y.x, y.y));
+              };
+              take(lds64a<0>(w), lds64a<kVs>(v));
+              take(lds64a<256>(w), lds64a<kVs + 32>(v));
+              take(lds64a<512>(w), lds64a<kVs + 64>(v));
+              take(lds64a<768>(w), lds64a<kVs + 96>(v));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+              if (c == 0) {
+                const int map = T == 1 ? g >> 2 : n, r = T == 1 ? g & 3 : g;
+                const float al = (map ? info1 : info0) & kMoved ? lds32a<0>(exa + 32 * map + 4 * r) : 1.0f;
+                float mag = ws.mag[n][g];
+                ws.factor[n][g] = mag < 0.0f ? al : follow_products(m, al, mag);
+                ws.post[n][g] = mag < 0.0f ? 1.0f : product_scale(mag);
+                ws.mag[n][g] = mag;
+              }
+            }
+            __syncwarp();
           }
 #pragma unroll
           for (int n = 0; n < T; ++n) {
             // the tile's rows 2c, 2c + 1: map n, or (T = 1) map c / 2
             const int map = T == 1 ? c >> 1 : n, r0 = T == 1 ? 2 * (c & 1) : 2 * c;
-            float2 al = lds64a<0>(exa + 32 * map + 4 * r0);
-            if (!((map ? info1 : info0) & kMoved)) al = make_float2(1.0f, 1.0f);
+            float2 al;
+            if constexpr (kCare) {
+              al = *reinterpret_cast<const float2*>(&ws.factor[n][2 * c]);
+            } else {
+              al = lds64a<0>(exa + 32 * map + 4 * r0);
+              if (!((map ? info1 : info0) & kMoved)) al = make_float2(1.0f, 1.0f);
+            }
 #pragma unroll
             for (int md = 0; md < 8; ++md) {
               const float2 lo = f2_mul(make_float2(o[md][n][0], o[md][n][1]), al);
@@ -403,6 +441,9 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
             if constexpr (kCare) {
               hide_products(y0, w0);
               hide_products(y1, w1);
+              const float post = ws.post[n][g];
+              y0 = f2_mul(y0, make_float2(post, post));
+              y1 = f2_mul(y1, make_float2(post, post));
             }
             split_f16x2(y0.x, y0.y, bhi[n].x, blo[n].x);
             split_f16x2(y1.x, y1.y, bhi[n].y, blo[n].y);
@@ -429,16 +470,20 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
       }
       return true;
     };
-    if (!(care ? blocks(std::true_type{}) : blocks(std::false_type{}))) return;
+    if (!(!care ? blocks(std::false_type{}) : blocks(std::true_type{}))) return;
     const bool whole = diff_windows(it0.ctx + M - 1) == 1;
     const int b = it0.b, pair = it0.pair;
 
     // ---- the window's result
-    float down[2];                                // 2^-E of rows 2c + e
+    float down[T][2];                             // 2^-E of rows 2c + e
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      down[e] = inverse_scale(ws.up[2 * c + e]);
-    }
+    for (int n = 0; n < T; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float up = ws.up[2 * c + e];
+        if (care) up = __fmul_rn(up, ws.post[n][2 * c + e]);
+        down[n][e] = inverse_scale(up);
+      }
     l_run = make_float2(row_total(l_run.x), row_total(l_run.y));
     if (whole) {                                  // the other map's row sums
       if (lane == 0) sts32(lex + kExInfo + 4 * a, 0u);
@@ -468,11 +513,11 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
         const float l0 = sm.ws[wp][0].row_sum[r], l1 = sm.ws[wp][1].row_sum[r];
 #pragma unroll
         for (int md = 0; md < 8; ++md) {
-          const float x0 = __fmul_rn(o[md][0][e], down[e]);
-          const float x1 = __fmul_rn(o[md][0][2 + e], down[e]);
-          const float y0 = T == 2 ? __fmul_rn(o[md][T - 1][e], down[e])
+          const float x0 = __fmul_rn(o[md][0][e], down[0][e]);
+          const float x1 = __fmul_rn(o[md][0][2 + e], down[0][e]);
+          const float y0 = T == 2 ? __fmul_rn(o[md][T - 1][e], down[T - 1][e])
                                   : __shfl_xor_sync(0xffffffffu, x0, 2);
-          const float y1 = T == 2 ? __fmul_rn(o[md][T - 1][2 + e], down[e])
+          const float y1 = T == 2 ? __fmul_rn(o[md][T - 1][2 + e], down[T - 1][e])
                                   : __shfl_xor_sync(0xffffffffu, x1, 2);
           if (in)
             *reinterpret_cast<float2*>(p.out + row * 2 * kD + a * kD + 16 * md + 2 * g) =
@@ -492,7 +537,7 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
 #pragma unroll
           for (int md = 0; md < 8; ++md)
             *reinterpret_cast<float2*>(dst + 16 * md) =
-                make_float2(__fmul_rn(o[md][n][e], down[e]), __fmul_rn(o[md][n][2 + e], down[e]));
+                make_float2(__fmul_rn(o[md][n][e], down[n][e]), __fmul_rn(o[md][n][2 + e], down[n][e]));
         }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {

@@ -272,31 +272,71 @@ __device__ __forceinline__ float row_total(float v) {
   v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 8));
   return __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, 16));
 }
-// Power of two 2^E per row: the largest v_scale among the window's keys that the row
-// sees, times 2^E, lies in [2^8, 2^9), so that w * v_scale * 2^E stays below 2^15 and,
-// down to weights that do not matter, in f16's normal range.
-__device__ __forceinline__ float operand_scale(float vmax) {
-  const int bexp = min(max(262 - (int)((__float_as_uint(vmax) >> 23) & 0xffu), 1), 253);
+// The operand of the second product is weight * v_scale * 2^E as f16 hi + lo: 22 bits,
+// or steps of 2^-24 below 2^-3.  E per row and plane, for the window:
+//   * the largest v_scale among the keys that the row sees, times 2^E, lies in [2^8,
+//     2^9), so that with weights below 2^6 no product reaches 2^15.  The largest product
+//     is at least the smallest v_scale (the weight of the largest score is 1 or more),
+//     so with scales within a factor of 2^6 a product is held to 22 bits or 2^-27 of
+//     the row's largest;
+//   * where the scales differ by more (or one is 0) the largest scale may belong to a key
+//     of no weight, and the steps would swallow the others.  E then follows the largest
+//     product so far, per map (follow_products), which lies in [2^14, 2^15): 22 bits or
+//     2^-39 of it.
+// Which of them goes by the row's own keys.  (Where every window is of the second kind the
+// calls take 141 us instead of 122, 64 sequences of 512 to 32768 keys, one column, and 183
+// instead of 144, 64 x 1k..4k, 5 columns; one such key per sequence costs 1%.)
+constexpr float kSpread = 0.015625f;              // 2^-6
+__device__ __forceinline__ float power_scale(int top, float v) {    // 2^E: v 2^E in [2^top, 2^(top + 1))
+  const int bexp = min(max(254 + top - (int)((__float_as_uint(v) >> 23) & 0xffu), 1), 253);
   return __uint_as_float((uint32_t)bexp << 23);
 }
+__device__ __forceinline__ float operand_scale(float vmax) { return power_scale(8, vmax); }
 __device__ __forceinline__ float inverse_scale(float up) {
   return __uint_as_float((254u << 23) - __float_as_uint(up));
 }
-// Products weight * v_scale * 2^E of keys that a row may not see: their weight is 0, but
-// 2^E goes by the keys that the row sees, and with a larger scale 2^E may leave float32,
-// where 0 * inf is no number.  Units where that can happen (scale_fits false) take these
-// products in a block loop of their own, so that the others' stays as it is.
+// E that follows the products: 2^E for the largest so far.
+__device__ __forceinline__ float product_scale(float mag) { return power_scale(14, mag); }
+// A block of such a row: m, its largest product; alpha, the factor of what is summed up so
+// far as its reference moved; mag, the largest product so far.  Returns the factor with
+// the step to the new E, a power of two.  (An E that rises makes up for an alpha, so what
+// is summed up stays below 2^31; after alpha = 0 nothing is left of it.)
+__device__ __forceinline__ float follow_products(float m, float alpha, float& mag) {
+  const float was = inverse_scale(product_scale(mag));
+  mag = fmaxf(__fmul_rn(mag, alpha), m);
+  return alpha == 0.0f ? 0.0f : __fmul_rn(alpha, __fmul_rn(product_scale(mag), was));
+}
+// Products weight * v_scale of keys that a row may not see: their weight is 0, but 2^E
+// goes by the keys that the row sees, and with a larger scale 2^E may leave float32, where
+// 0 * inf is no number.
 __device__ __forceinline__ void hide_products(float2& y, float2 w) {
   if (w.x == 0.0f) y.x = 0.0f;
   if (w.y == 0.0f) y.y = 0.0f;
 }
-// Whether the largest v_scale of the window, hidden keys included, times 2^E is finite.
-__device__ __forceinline__ bool scale_fits(float up, float vall) {
-  return __fmul_rn(vall, up) < INFINITY;
-}
-// The larger of two values >= 0; no number counts as the largest.
-__device__ __forceinline__ float max_bits(float a, float b) {
-  return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+// What the scales of a row's keys in the window are: of those it sees the largest and
+// the smallest, and the largest of all (no number counts as the largest).
+struct ScaleRange {
+  float most, least, all;
+  __device__ __forceinline__ void add(float v, bool seen) {
+    if (seen) {
+      most = fmaxf(most, v);
+      least = fminf(least, v);
+    }
+    all = __uint_as_float(max(__float_as_uint(all), __float_as_uint(v)));
+  }
+  __device__ __forceinline__ bool spread() const { return least < __fmul_rn(most, kSpread); }
+  // (times 2^E: 1 where E follows the products, and then a factor of its own)
+  __device__ __forceinline__ float scale() const { return spread() ? 1.0f : operand_scale(most); }
+  // Whether the blocks need care: an E that follows the products, or hidden keys whose
+  // scale times 2^E is not finite.  Such units take an instantiation of the block loop of
+  // their own, so that the others pay nothing.
+  __device__ __forceinline__ bool care() const { return spread() || !(__fmul_rn(all, scale()) < INFINITY); }
+};
+// Over the warp, from each lane's largest and smallest (values >= 0 are ordered as their
+// bits are).
+__device__ __forceinline__ ScaleRange warp_range(float most, float least) {
+  const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+  return {m, __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(least))), m};
 }
 // Bytes (XOR 0x80) of two keys of two channels into the mantissa of 1024, less 1152:
 // exact f16.  vw: words of the transposing load; af: the operand's rows g and g + 8,

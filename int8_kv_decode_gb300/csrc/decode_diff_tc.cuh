@@ -51,8 +51,9 @@ struct __align__(1024) DiffTcSmem {
   uint8_t vt[2][2][kBlockBytes];                  // [plane][16 keys]: V^T as f16, K-major
   uint8_t pb[2][2][2][TcShape<W>::kOperand];      // [plane][16 keys][hi | lo]: P, K-major
   float ks[2][2][kWindow], vs[2][2][kWindow];     // [item slot][plane]: the window's scales
-  float down[2][2][8 * W];                        // [item slot][plane][row]: 2^-E
-  float alpha[8 * W];
+  float down[2][2][8 * W];                        // [item slot][plane][row]: 2^-E (minus the largest product
+                                                  // while E follows it)
+  float alpha[2][8 * W];                          // [plane] where E follows the products, else [0]
   float row_sum[8 * W];                           // of a sequence that ends in its window
   int rows[2][kWinBlocks];                        // [item slot]: rows of the blocks in a plane
   uint64_t full[TcShape<W>::kStages], done;       // a stage's copies landed; the MMAs are done
@@ -258,29 +259,32 @@ diff_tc_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
       qhi = make_uint4(q[4], q[5], q[6], q[7]);
     }
     auto keys_of = [&](int r) -> int { return it.ctx + column(min(rg * 8 + r, R - 1)); };
-    // ---- 2^E of the row 2c + odd, for either plane's scales: lane j takes column j.  Every
-    // warp finds the same `care` (see hide_products): they go through the blocks together.
+    // ---- 2^E of the row 2c + odd, for either plane's scales (with a minus: it follows the
+    // products).  Lane j takes column j, so that every warp finds the same `care` (see
+    // ScaleRange): they go through the blocks together.
     float up[2];
     bool care = false;
 #pragma unroll
     for (int pl = 0; pl < 2; ++pl) {
-      float vm = 0.0f;
+      float most = 0.0f, least = INFINITY;
 #pragma unroll
       for (int e = 0; e < kWinBlocks; ++e)
-        if (s0 + 32 * e + lane < min(it.ctx, s1)) vm = fmaxf(vm, sm.vs[slot][pl][32 * e + lane]);
-      float vmax = warp_max(vm), vall = vmax;
+        if (s0 + 32 * e + lane < min(it.ctx, s1)) {
+          const float v = sm.vs[slot][pl][32 * e + lane];
+          most = fmaxf(most, v);
+          least = fminf(least, v);
+        }
+      ScaleRange range = warp_range(most, least);
       const int keys = it.ctx + min(lane & 7, M - 1);
-      for (int key = max(it.ctx, s0); key < s1; ++key) {     // draft keys
-        const float v = sm.vs[slot][pl][key - s0];
-        if (key < keys) vmax = fmaxf(vmax, v);
-        vall = max_bits(vall, v);
-      }
-      const float u = operand_scale(vmax);
-      care |= !scale_fits(u, vall);
+      for (int key = max(it.ctx, s0); key < s1; ++key) range.add(sm.vs[slot][pl][key - s0], key < keys);
+      care |= range.care();
+      const float u = range.spread() ? -1.0f : range.scale();
       up[pl] = __shfl_sync(0xffffffffu, u, column(min(rg * 8 + 2 * c + odd, R - 1)));
-      if (g < 2 && !issuer) sm.down[slot][pl][8 * warp + 2 * c + g] = inverse_scale(up[pl]);
+      if (g < 2 && !issuer)
+        sm.down[slot][pl][8 * warp + 2 * c + g] = up[pl] < 0.0f ? -0.0f : inverse_scale(up[pl]);
     }
     care = __any_sync(0xffffffffu, care);
+    __syncwarp();
     float2 m_run = make_float2(0.0f, 0.0f), m_move = make_float2(-INFINITY, -INFINITY);
     float2 l_run = make_float2(0.0f, 0.0f);
 
@@ -324,20 +328,54 @@ diff_tc_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
           } else {
             uint8_t* const dst = &sm.pb[0][0][0][0] + lane_p;
             const float* const vs0 = &sm.vs[0][0][0] + slot * 2 * kWindow + 32 * i + (g & 6);
+            auto put = [&](float2 y, int pl, int q) {
+              uint32_t hi, lo;
+              split_f16x2(y.x, y.y, hi, lo);
+              uint8_t* const to = dst + (pl * 4 + (q >> 1) * 2) * S::kOperand + (q & 1) * 128;
+              *reinterpret_cast<uint32_t*>(to) = hi;
+              *reinterpret_cast<uint32_t*>(to + S::kOperand) = lo;
+            };
+            if constexpr (kCare) {                // (state in shared memory: the other loop needs the registers)
+#pragma unroll 1
+              for (int pl = 0; pl < 2; ++pl) {
+                const int row = 8 * warp + 2 * c + odd;
+                const float u = pl ? up[1] : up[0];
+                float mag = -sm.down[slot][pl][row], m = 0.0f;
+                float2 y[4];
 #pragma unroll
-            for (int pl = 0; pl < 2; ++pl)
+                for (int q = 0; q < 4; ++q) {
+                  const float2 vs = *reinterpret_cast<const float2*>(vs0 + pl * kWindow + 8 * q);
+                  y[q] = f2_mul(w[q], f2_mul(vs, make_float2(fabsf(u), fabsf(u))));
+                  hide_products(y[q], w[q]);
+                  m = fmaxf(m, fmaxf(y[q].x, y[q].y));
+                }
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                float f = odd ? alpha.y : alpha.x, post = 1.0f;
+                if (u < 0.0f) {
+                  f = follow_products(m, f, mag);
+                  post = product_scale(mag);
+                }
+                moved = __any_sync(0xffffffffu, moved || f != 1.0f);
+                __syncwarp();                     // (every lane has read the row's state)
+                if (g < 2) {
+                  sm.alpha[pl][row] = f;
+                  sm.down[slot][pl][row] = -mag;
+                }
+                __syncwarp();
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const float2 vs = *reinterpret_cast<const float2*>(vs0 + pl * kWindow + 8 * q);
-                float2 y = f2_mul(w[q], f2_mul(vs, make_float2(up[pl], up[pl])));
-                if constexpr (kCare) hide_products(y, w[q]);
-                uint32_t hi, lo;
-                split_f16x2(y.x, y.y, hi, lo);
-                uint8_t* const to = dst + (pl * 4 + (q >> 1) * 2) * S::kOperand + (q & 1) * 128;
-                *reinterpret_cast<uint32_t*>(to) = hi;
-                *reinterpret_cast<uint32_t*>(to + S::kOperand) = lo;
+                for (int q = 0; q < 4; ++q) put(f2_mul(y[q], make_float2(post, post)), pl, q);
               }
-            if (g == 0) *reinterpret_cast<float2*>(&sm.alpha[8 * warp + 2 * c]) = alpha;
+            } else {
+#pragma unroll
+              for (int pl = 0; pl < 2; ++pl)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const float2 vs = *reinterpret_cast<const float2*>(vs0 + pl * kWindow + 8 * q);
+                  put(f2_mul(w[q], f2_mul(vs, make_float2(up[pl], up[pl]))), pl, q);
+                }
+              if (g == 0) *reinterpret_cast<float2*>(&sm.alpha[0][8 * warp + 2 * c]) = alpha;
+            }
             // ---- V^T: item x = (plane, 16 keys, 32 channels).  Row 16q + g holds channel
             // 16q + 2g, row 16q + 8 + g the next one.
             const uint32_t va = ring + 2 * kBlockBytes +
@@ -377,13 +415,14 @@ diff_tc_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
             for (int x = 0; x < 8 / kReaders; ++x)
 #pragma unroll 1
               for (int n = 0; n < S::kRows; n += 16) {
-                const uint32_t at = tlane + (kReaders == 4 ? x : warp >> 2) * S::kPlane + n;
+                const int pl = kReaders == 4 ? x : warp >> 2;
+                const uint32_t at = tlane + pl * S::kPlane + n;
                 float v[16];
                 tc_ld16(at, v);
 #pragma unroll
                 for (int j = 0; j < 16; j += 2) {
                   const float2 y = f2_mul(make_float2(v[j], v[j + 1]),
-                                          *reinterpret_cast<const float2*>(&sm.alpha[n + j]));
+                                          *reinterpret_cast<const float2*>(&sm.alpha[kCare ? pl : 0][n + j]));
                   v[j] = y.x;
                   v[j + 1] = y.y;
                 }
@@ -418,8 +457,17 @@ diff_tc_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
         if (i == 0 && nxt.b >= 0) copy_scales(slot ^ 1, nxt);
       }
     };
-    if (care) blocks(std::true_type{});
-    else blocks(std::false_type{});
+    if (!care) {
+      blocks(std::false_type{});
+    } else {
+      blocks(std::true_type{});
+#pragma unroll
+      for (int pl = 0; pl < 2; ++pl)
+        if (up[pl] < 0.0f && g < 2 && !issuer) {
+          float& x = sm.down[slot][pl][8 * warp + 2 * c + g];
+          x = inverse_scale(product_scale(-x));
+        }
+    }
     if (failed) break;
 
     // ---- the window's row sums and references

@@ -485,3 +485,121 @@ def test_a_hidden_scale_that_is_no_number(M, Hq, limit, value):
         t["ks"][:, last] = value
         t["vs"][:, last] = value
     assert np.array_equal(bits(K.decode_diff(*args))[:, :M - 1], want[:, :M - 1])
+
+
+# -------------------------------------------- value scales that differ widely
+
+def sink(x, b, key, v_scale, score=68.0):
+    """Key `key` of sequence b takes nearly all of the weight of both maps, with the
+    value scale v_scale and no zero among its values: its score is about `score`, those
+    of the others are within +-10."""
+    r = np.random.default_rng(key)
+    at, Hkv = int(x["start"][b]) + key, x["k8"].shape[0]
+    g = x["q"].shape[2] // Hkv
+    for plane in range(Hkv):
+        base = r.standard_normal(128).astype(np.float32)
+        base *= np.float32(np.sqrt(128.0) / np.linalg.norm(base))
+        heads = 2 * (plane // 2 * g + np.arange(g)) + plane % 2
+        x["q"][b][:, heads] = 2 * base + 0.02 * x["q"][b][:, heads]
+        k = base * np.float32(score / (2 * np.sqrt(128.0)))
+        x["ks"][plane, at] = np.abs(k).max() / np.float32(127)
+        x["k8"][plane, at] = np.rint(k / x["ks"][plane, at])
+    x["v8"][:, at] = r.integers(64, 128, (Hkv, 128)) * r.choice([-1, 1], (Hkv, 128))
+    x["vs"][:, at] = v_scale
+
+
+SPREAD = [(1, 4, None), (4, 2, None), (1, 16, None), (2, 16, None), (3, 12, 80000), (8, 16, 80000)]
+
+
+@gpu
+@pytest.mark.parametrize("M,Hq,limit", SPREAD)
+@pytest.mark.parametrize("down", [5, 7, 20, 34, 60, 100])
+def test_the_weight_on_a_key_of_small_scale(M, Hq, limit, down):
+    # one key has nearly all the weight and a value scale 2^-down of the others': a
+    # product of weight and scale is held relative to the largest product of its row,
+    # not to the largest scale.  First, middle and last key of a window, and a draft key.
+    # The tolerance is the file's: products are off by 2^-22 of themselves, or by 2^-27 of
+    # the row's largest, 256 of them times 127 to the 64 of the sink's own values: 2^-18 of
+    # the mass when all err alike.
+    import int8_kv_decode_gb300 as K
+    ctx = [400, 256, 700, 90, 511]
+    x = inputs(5, M, Hq, 2, ctx, seed=33)
+    small = np.float32(2.0 ** -down / 40)
+    for b, key in enumerate((0, 255, 300, 89, 511 + M - 2)):
+        sink(x, b, key, small)
+    t = device(x)
+    full = K.decode_diff(t["q"], t["k8"], t["ks"], t["v8"], t["vs"], t["start"], t["ctx"], limit or 700,
+                         t["lam"])
+    want, mass = expected(x)
+    check(full.cpu().numpy(), want, mass)
+    columns_alone(x, t, full)
+    assert np.array_equal(bits(full), bits(run(x, t)))
+
+
+@gpu
+@pytest.mark.parametrize("M,Hq,limit", SPREAD)
+def test_the_weight_on_a_value_row_of_zeros(M, Hq, limit):
+    # the same with a value row of zeros: what is left of the sum are weights of about
+    # e^-25, whose exponents are rounded to 2^-19 (the others' bound leaves that room)
+    import int8_kv_decode_gb300 as K
+    x = inputs(3, M, Hq, 2, [200, 256, 600], seed=34)
+    for b, key in enumerate((0, 128, 599)):
+        sink(x, b, key, 0.0, score=25.0)
+        x["v8"][:, int(x["start"][b]) + key] = 0
+    t = device(x)
+    full = K.decode_diff(t["q"], t["k8"], t["ks"], t["v8"], t["vs"], t["start"], t["ctx"], limit or 600,
+                         t["lam"])
+    want, mass = expected(x)
+    check(full.cpu().numpy(), want, mass)
+    columns_alone(x, t, full)
+
+
+@gpu
+@pytest.mark.parametrize("M,Hq,limit", SPREAD)
+@pytest.mark.parametrize("seed", range(4))
+def test_scales_over_the_whole_range(M, Hq, limit, seed):
+    # scales over 2^-60 .. 2^20 and rows of zeros, references that move in most blocks
+    # (weights below 2^-126 are 0, 2^-46 of the sum at most)
+    import int8_kv_decode_gb300 as K
+    x = inputs(4, M, Hq, 2, [33, 129, 900, 300], seed=40 + seed, q_gain=[2.0, 30.0][seed % 2])
+    r = np.random.default_rng(seed)
+    x["vs"] *= (2.0 ** r.integers(-60, 20, x["vs"].shape)).astype(np.float32)
+    zero = r.random(x["vs"].shape) < 0.1
+    x["vs"][zero] = 0
+    x["v8"][zero] = 0
+    x["v8"][(x["v8"] == 0) & ~zero[..., None]] = 1
+    t = device(x)
+    full = K.decode_diff(t["q"], t["k8"], t["ks"], t["v8"], t["vs"], t["start"], t["ctx"], limit or 900,
+                         t["lam"])
+    assert np.isfinite(full.cpu().numpy()).all()
+    columns_alone(x, t, full)
+    # relative to the channel of the largest mass: a channel may be 1 where another is 127
+    want, mass = expected(x)
+    err = np.abs(full.cpu().numpy().astype(np.float64) - want).reshape(4, M, Hq // 2, 2, 128)
+    most = mass.reshape(4, M, Hq // 2, 2, 128).max(-1, keepdims=True)
+    assert (err <= TOL * most).all()
+
+
+@gpu
+@pytest.mark.parametrize("M,Hq,limit", SPREAD)
+@pytest.mark.parametrize("plane", [0, 1])
+def test_one_plane_of_the_two_has_such_a_key(M, Hq, limit, plane):
+    # the two planes of a pair go their own ways, and so do windows and columns
+    import int8_kv_decode_gb300 as K
+    x = inputs(3, M, Hq, 2, [300, 120, 1000], seed=35)
+    other = x["vs"][1 - plane].copy()
+    for b, key in enumerate((0, 119 + M - 1, 700)):
+        sink(x, b, key, np.float32(2.0 ** -30))
+    x["vs"][1 - plane] = other
+    t = device(x)
+    full = K.decode_diff(t["q"], t["k8"], t["ks"], t["v8"], t["vs"], t["start"], t["ctx"], limit or 1000,
+                         t["lam"])
+    want, mass = expected(x)
+    check(full.cpu().numpy(), want, mass)
+    columns_alone(x, t, full)
+    # the other plane's channels are those of a cache without the small scales
+    t["vs"][plane] = t["vs"][1 - plane]
+    same = K.decode_diff(t["q"], t["k8"], t["ks"], t["v8"], t["vs"], t["start"], t["ctx"], limit or 1000,
+                         t["lam"])
+    c = slice(128 * (1 - plane), 128 * (2 - plane))
+    assert np.array_equal(bits(full[..., c].contiguous()), bits(same[..., c].contiguous()))
