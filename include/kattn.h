@@ -453,8 +453,10 @@ enum kattn_code { KATTN_INT8 = 0, KATTN_E4M3 = 1 };
  * codes: [rows][d] bytes (int8 or e4m3 by code_type); scales: float32 [rows] or
  *   [rows][d / 128] (group = 128, which needs d % 128 == 0).
  * Alignment: each array to its element.  (16-byte vectors are used where the
- * pointers, strides and d allow it.)  The outputs must not overlap x, weight
- * or each other.  1 <= d <= 2^24.  rows == 0 is a no-op.  Deterministic. */
+ * pointers, strides and d allow it; they set the order of the float32 sum of
+ * squares, so the last bits of a scale go by d and the alignment of the pointers
+ * and strides, and not by the number of rows.)  The outputs must not overlap x,
+ * weight or each other.  1 <= d <= 2^24.  rows == 0 is a no-op.  Deterministic. */
 int kattn_rms_norm_quant(const void* x, const void* residual, const void* weight, int x_type,
                          int64_t rows, int d, int64_t x_stride, int64_t res_stride,
                          int64_t res_out_stride, float eps, int group, int code_type,

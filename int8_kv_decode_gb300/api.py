@@ -569,7 +569,9 @@ _CODE_TYPES = {torch.int8: 0, torch.float8_e4m3fn: 1}
 
 def _row_stride(t, dtype, index, shape, name):
     """The row stride of t, rows of its last dimension: any for a 2-D tensor, else
-    t is contiguous."""
+    t is contiguous.  A single row keeps the stride of the buffer that it is a slice
+    of: with the pointers it decides the width of the loads, and so the order of the
+    row's sum."""
     d = shape[-1]
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -578,7 +580,7 @@ def _row_stride(t, dtype, index, shape, name):
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}")
     if t.is_contiguous():
-        return d
+        return max(t.stride(0), d) if len(shape) == 2 and shape[0] == 1 else d
     if t.dim() != 2 or (d > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be contiguous, or 2-D with a contiguous last dimension")
     return t.stride(0) if shape[0] > 1 else d
@@ -593,7 +595,8 @@ def rms_norm_quant(x, weight, *, residual=None, residual_out=None, eps: float = 
     residual_out (the residual itself if None).  Returns (codes, scales): codes
     like x in out_dtype (torch.int8 or torch.float8_e4m3fn), scales float32, one
     per row [...] or per 128 channels [..., d/128] (group = 128), so that codes *
-    scales is h / rms(h) * weight.  (kattn_rms_norm_quant)
+    scales is h / rms(h) * weight.  Slices x[i:i+1] (and of the residual) give the
+    bytes that row i has in the whole.  (kattn_rms_norm_quant)
     """
     index = _device_of(x, "x")
     dtype, shape = x.dtype, x.shape
@@ -624,6 +627,8 @@ def rms_norm_quant(x, weight, *, residual=None, residual_out=None, eps: float = 
         else:
             res_out_stride = _row_stride(residual_out, dtype, index, shape, "residual_out")
         res_ptr, res_out_ptr = residual.data_ptr(), residual_out.data_ptr()
+        if res_ptr == res_out_ptr and rows == 1:       # in place, whatever the views' strides say
+            res_out_stride = res_stride
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
     if out is None:

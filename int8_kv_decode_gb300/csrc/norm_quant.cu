@@ -162,8 +162,9 @@ constexpr int kMaxThreads = 512;                  // 128 registers a thread
 
 // TPR threads hold a row, NV vectors of VEC elements each; a block of at least 256
 // threads takes blockDim / TPR rows at a time, in a grid stride, and keeps its part
-// of the weight.  TPR and NV go by d alone (launch_vec), so a row's bytes do not
-// depend on how many rows there are.
+// of the weight.  TPR and NV go by d and VEC, and VEC by d and the alignment of pointers
+// and strides (launch_type): a row's codes depend on nothing else, and its scale, whose sum
+// of squares has an order that follows them, not on how many rows there are.
 template <typename T, int VEC, int NV>
 __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p, const int tpr, const bool e4m3) {
   __shared__ float s_sum[2][32], s_max[2][32];

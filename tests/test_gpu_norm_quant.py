@@ -185,3 +185,48 @@ def test_leading_dimensions_given_outputs_and_graph():
     x3, _, _ = make(0, 64, "float32", False)
     codes, scales = K.rms_norm_quant(x3.cuda(), torch.ones(64).cuda())
     assert codes.shape == (0, 64) and scales.shape == (0,)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d,stride,group", [(256, 257, 0), (256, 257, 128), (255, 255, 0), (256, 256, 0),
+                                            (256, 264, 128), (1024, 1025, 0), (4096, 4100, 0), (4097, 4097, 0)])
+def test_a_row_alone_has_the_bytes_it_has_in_a_batch(dtype, d, stride, group):
+    # a slice of one row keeps the row stride of its buffer
+    import torch
+    import int8_kv_decode_gb300 as K
+    n = 96
+    x, w, res = make(n, d, dtype, True, seed=d + stride)
+
+    def spread(t):
+        view = torch.zeros((n, stride), dtype=t.dtype, device="cuda")[:, :d]
+        view.copy_(t)
+        return view
+    xv, wc, rv = spread(x), w.cuda(), spread(res)
+    out = torch.empty_like(rv)
+    codes, scales = K.rms_norm_quant(xv, wc, residual=rv, residual_out=out, group=group)
+    check(x, w, res, codes, scales, out, group)
+    for i in range(n):
+        c, s = K.rms_norm_quant(xv[i:i + 1], wc, residual=rv[i:i + 1],
+                                residual_out=torch.empty_like(rv[i:i + 1]), group=group)
+        assert torch.equal(c, codes[i:i + 1]) and torch.equal(s, scales[i:i + 1]), i
+
+
+def test_one_row_views_of_any_stride():
+    # a single row whose stride says nothing (a column's transpose, an expanded row), and
+    # the same memory as residual and residual_out through views of different strides
+    import torch
+    import int8_kv_decode_gb300 as K
+    x, w, res = make(1, 256, "bfloat16", True, seed=3)
+    buf = torch.zeros((4, 257), dtype=torch.bfloat16, device="cuda")
+    buf[2, :256] = res[0]
+    for xv in (x.cuda(), x.cuda().reshape(256, 1).t(), x.cuda()[0].expand(1, 256),
+               x.cuda().as_strided((1, 256), (0, 1))):
+        assert xv.shape == (1, 256)
+        rv = buf[2:3, :256]
+        rv.copy_(res)
+        codes, scales = K.rms_norm_quant(xv, w.cuda(), residual=rv, residual_out=rv.view(1, 256))
+        check(x, w, res, codes, scales, rv, 0)
+        rv.copy_(res)
+        codes, scales = K.rms_norm_quant(xv, w.cuda(), residual=rv,
+                                         residual_out=rv.as_strided((1, 256), (256, 1)))
+        check(x, w, res, codes, scales, rv, 0)
