@@ -534,8 +534,9 @@ int kattn_fork_sequences(int32_t* block_table, int n_slots, int max_pages, int32
  *                   inputs themselves (in place), or other arrays: then a
  *                   decode step in flight can go on with the old table until
  *                   the copies are done (no destination is a live page).
- * Table entries outside the pool are kept (KATTN_DEVERR_BAD_PAGE for those at
- * or above n_pages). */
+ * Table entries outside the pool, or of a page that is free by its count, are kept
+ * (KATTN_DEVERR_BAD_PAGE, but for those below 0): after the copies such a page may
+ * hold another sequence's rows. */
 int kattn_compact_pages(const int32_t* block_table, int n_slots, int max_pages,
                         const int32_t* ref_count, int n_pages, int32_t* table_out,
                         int32_t* ref_out, int32_t* src, int32_t* dst, int32_t* counts,

@@ -498,8 +498,8 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PageParams p) {
 // ---------------------------------------------------------------- compact
 //   1. live pages per chunk;  2. with their sum n_live, the free pages below it
 //   and the live pages at or above it, in order;  3. the moves, the counts
-//   after them, and the map of the pages that move.  rewrite_kernel then takes
-//   the table through the map.
+//   after them, and the map of all pages.  rewrite_kernel then takes the table through
+//   the map.
 template <int CL>
 __global__ void __launch_bounds__(kThreads) compact_kernel(const PageParams p) {
   __shared__ BlockScratch s;
@@ -522,7 +522,11 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const PageParams p) {
   int* holes = p.ws.list + ch.lo;
   int2* movers = p.ws.list2 + ch.lo;
   const int n_holes = rank_pages(
-      p.refs, ch.lo, min(ch.hi, n_live), s, [](int, int c) { return c <= 0; },
+      p.refs, ch.lo, min(ch.hi, n_live), s,
+      [&](int page, int c) {
+        p.ws.to[page] = c <= 0 ? -1 : page;       // it stays; no table entry may name a free one
+        return c <= 0;
+      },
       [&](int r, int page, int) { holes[r] = page; });
   const int n_movers = rank_pages(
       p.refs, max(ch.lo, n_live), ch.hi, s,
@@ -568,12 +572,11 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const PageParams p) {
 
 __global__ void __launch_bounds__(256) rewrite_kernel(const PageParams p) {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");   // the moves
-  const int n_live = __ldcg(p.counts);
   const int64_t all = (int64_t)p.n_slots * p.max_pages;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < all;
        i += (int64_t)gridDim.x * blockDim.x) {
     int e = p.table[i];
-    if (e >= n_live) {
+    if (e >= 0) {                                 // (a free page has no place: another's rows move there)
       const int to = e < p.n_pages ? __ldcg(p.ws.to + e) : -1;
       if (to < 0) atomicOr(p.ws.err, KATTN_DEVERR_BAD_PAGE);
       else e = to;

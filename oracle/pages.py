@@ -97,11 +97,10 @@ def compact(table, refs):
     to = dict(zip(movers, holes))
     err, out = 0, table.copy()
     for at, e in np.ndenumerate(table):
-        if e >= n_live:
-            if e in to:
-                out[at] = to[e]
-            else:
-                err |= BAD_PAGE
+        if e >= n or e >= 0 and refs[e] <= 0:
+            err |= BAD_PAGE
+        elif e >= n_live:
+            out[at] = to[e]
     refs_out = np.zeros_like(refs)
     for p in live:
         refs_out[to.get(p, p)] = refs[p]

@@ -298,3 +298,20 @@ def test_unaligned_arrays():
     for a, b in zip(out, want[1:]):
         assert np.array_equal(a.cpu().numpy(), b)
     assert K.get_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("n_pages", [12, 6000])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_compaction_flags_entries_that_name_a_free_page(n_pages, in_place):
+    # a damaged row names a page of count 0 below the live count: another sequence's page
+    # moves there, so the row would answer with that sequence's keys
+    p = Pool(6, 3, n_pages, 32)
+    p.reserve([0, 1, 2], [96, 64, 32])
+    p.free([0])                           # pages 0, 1, 2 are free, 3, 4, 5 move there
+    p.compact(in_place=False)
+    p.reserve([0], [96])
+    p.free([1])                           # live: 2 (slot 2), 3, 4, 5 (slot 0); free: 0, 1
+    p.table[4] = [-1, 1, 4]               # a free page, and one of slot 0's
+    p.sync()
+    p.compact(in_place)
+    assert p.table[4, 1] == 1             # kept, and flagged
