@@ -494,7 +494,8 @@ size_t kattn_page_workspace_size(int n_slots, int n_pages);
  * ceil(lens[i] / page_rows) table entries that are unused get free pages with
  * count 1, in the order of the list and then of the entries.  If the pool has
  * fewer free pages than all of them need together, no page is given to any
- * slot and KATTN_DEVERR_NO_PAGES is set.  0 <= lens[i] <= max_pages * page_rows. */
+ * slot and KATTN_DEVERR_NO_PAGES is set.  0 <= lens[i] <= max_pages * page_rows.
+ * An entry outside the pool among them is kept (KATTN_DEVERR_BAD_PAGE). */
 int kattn_reserve_pages(int32_t* block_table, int n_slots, int max_pages, int32_t* ref_count,
                         int n_pages, int page_rows, const int32_t* seqs, const int32_t* lens,
                         int n, void* workspace, size_t workspace_bytes, void* stream);

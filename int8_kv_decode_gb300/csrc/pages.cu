@@ -327,12 +327,17 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const PageParams p) {
     if (slot_mine(p, lists, i, slot) && len_ok(p, len)) {
       const int need = pages_for(p, len);
       const int32_t* row = p.table + (int64_t)slot * p.max_pages;
+      bool outside = false;
       for (int c0 = 0; c0 < need; c0 += 32 * kAhead) {
         int e[kAhead];
         load_entries(row, c0, need, e);
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) miss += c0 + 32 * u + lane < need && e[u] < 0;
+        for (int u = 0; u < kAhead; ++u) {
+          miss += c0 + 32 * u + lane < need && e[u] < 0;
+          outside |= e[u] >= p.n_pages;
+        }
       }
+      if (outside) atomicOr(p.ws.err, KATTN_DEVERR_BAD_PAGE);
       miss = warp_sum_int(miss);
     } else if (lane == 0) {
       atomicOr(p.ws.err, KATTN_DEVERR_BAD_SEQUENCE);

@@ -38,7 +38,9 @@ def reserve(table, refs, seqs, lens, page_rows):
         if not 0 <= s < len(table) or s in seen or not 0 <= n <= table.shape[1] * page_rows:
             err |= BAD_SEQUENCE
         else:
-            wants += [(s, c) for c in range(-(-int(n) // page_rows)) if table[s, c] < 0]
+            held = table[s, :-(-int(n) // page_rows)]
+            err |= BAD_PAGE if (held >= len(refs)).any() else 0
+            wants += [(s, c) for c in np.flatnonzero(held < 0)]
         seen.add(s)
     pages = np.flatnonzero(refs == 0)
     if len(wants) > len(pages):

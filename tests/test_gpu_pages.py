@@ -315,3 +315,16 @@ def test_compaction_flags_entries_that_name_a_free_page(n_pages, in_place):
     p.sync()
     p.compact(in_place)
     assert p.table[4, 1] == 1             # kept, and flagged
+
+
+@pytest.mark.parametrize("n_pages", [12, 20000])
+def test_reserve_flags_entries_outside_the_pool(n_pages):
+    p = Pool(4, 300, n_pages, 32)
+    p.reserve([0, 1], [64, 32])
+    p.table[0, 1] = n_pages
+    p.table[2, 0] = 2**31 - 1
+    p.sync()
+    p.reserve([1], [64])                  # other rows
+    p.reserve([0], [32])                  # the entry lies past what the length needs
+    p.reserve([0, 3], [96, 32])           # flagged; the others of the row get theirs
+    p.reserve([2], [64])
