@@ -477,6 +477,7 @@ int kattn_rms_norm_quant(const void* x, const void* residual, const void* weight
  * (seqs, parents, children, lens, src, dst) are int32 arrays on the device, so
  * they are checked there; what a check finds is set in the workspace's error
  * word (kattn_get_device_status).  A list has at most n_slots entries.
+ * n_slots, max_pages and n_pages are at most 2^30 each (KATTN_ERR_UNSUPPORTED).
  *   KATTN_DEVERR_BAD_SEQUENCE  a slot outside [0, n_slots), a slot that a list
  *     names again (the first place counts; to free a slot twice is no error),
  *     or lens out of range: that entry of the list is skipped;

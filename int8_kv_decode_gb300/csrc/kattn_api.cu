@@ -219,6 +219,9 @@ int check_pages(const void* block_table, int n_slots, int max_pages, const void*
                 size_t workspace_bytes) {
   if (n_slots < 1 || max_pages < 1 || n_pages < 1 || n < 0 || n > n_slots)
     return KATTN_ERR_INVALID_ARG;
+  // the plans count pages, entries and slots in int32, with up to 2^14 added at the ends
+  constexpr int kMost = 1 << 30;
+  if (n_slots > kMost || max_pages > kMost || n_pages > kMost) return KATTN_ERR_UNSUPPORTED;
   if (!block_table || !ref_count || (n > 0 && !list)) return KATTN_ERR_INVALID_ARG;
   if (!aligned(block_table, 4) || !aligned(ref_count, 4) || !aligned(list, 4))
     return KATTN_ERR_MISALIGNED;

@@ -244,3 +244,16 @@ def test_page_oracle_keeps_its_books():
             _, table, refs, src, dst, counts = oracle.pages.compact(table, refs)
             assert (refs[:counts[0]] > 0).all() and not refs[counts[0]:].any()
         assert np.array_equal(refs, np.bincount(table[table >= 0], minlength=40))
+
+
+# -------------------------------------------------- sizes past the kernels' 32-bit counts
+
+@pytest.mark.parametrize("name,base", [("reserve_pages", RESERVE), ("free_sequences", FREE),
+                                       ("fork_sequences", FORK), ("compact_pages", COMPACT)])
+def test_page_operations_refuse_counts_past_32_bits(lib, name, base):
+    # run on the host alone: the refusal comes before anything is enqueued
+    fn = getattr(lib, "kattn_" + name)
+    ok = dict(base, ws_bytes=BIG)
+    for arg in ("S", "mp", "n_pages"):
+        for size in ((1 << 30) + 1, (1 << 31) - 1):
+            assert call(fn, ok, **{arg: size}) == UNSUPPORTED, (arg, size)
