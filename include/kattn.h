@@ -405,8 +405,8 @@ int kattn_hash_rows(const void* data, int64_t n_rows, int64_t row_bytes, int64_t
  * then not written, or unspecified.
  * Deterministic; the bytes of out[b][j][i] depend only on that row's own keys,
  * so column j equals an M = 1 call with ctx_len + j, in any batch.
- * workspace: kattn_diff_workspace_size(B, M, Hq, max_ctx) bytes, 256-byte
- * aligned; its first 256 bytes zeroed before the first call, and shared only
+ * workspace: kattn_diff_workspace_size(B, M, Hq, max_ctx) bytes (0 for invalid
+ * sizes), 256-byte aligned; its first 256 bytes zeroed before the first call, and shared only
  * by calls that are ordered on the GPU, as a decode workspace.  Two kernels on
  * `stream` at most; capturable in a CUDA graph once a first call on the device
  * has run outside capture. */

@@ -504,6 +504,7 @@ int kattn_hash_rows(const void* data, int64_t n_rows, int64_t row_bytes, int64_t
 
 size_t kattn_diff_workspace_size(int B, int M, int Hq, int max_ctx) {
   if (B < 1 || M < 1 || M > KATTN_MAX_M || Hq < 1 || max_ctx < 1) return 0;
+  if ((int64_t)max_ctx + M - 1 > (int64_t)INT32_MAX / 2) return 0;    // as the call refuses it
   return diff_workspace_bytes(B, M, Hq, max_ctx);
 }
 

@@ -257,3 +257,12 @@ def test_page_operations_refuse_counts_past_32_bits(lib, name, base):
     for arg in ("S", "mp", "n_pages"):
         for size in ((1 << 30) + 1, (1 << 31) - 1):
             assert call(fn, ok, **{arg: size}) == UNSUPPORTED, (arg, size)
+
+
+def test_diff_workspace_size_of_a_limit_that_the_call_refuses(lib):
+    size = lib.kattn_diff_workspace_size
+    top = (1 << 31) - 1
+    for max_ctx, M in ((top, 1), (top, 8), (top - 6, 8), (top // 2 + 1, 1), (top // 2 - 6, 8)):
+        assert size(1, M, 2, max_ctx) == 0, (max_ctx, M)
+        assert call(lib.kattn_decode_diff, DIFF, max_ctx=max_ctx, M=M, ws_bytes=BIG) == INVALID
+    assert size(1, 8, 2, top // 2 - 7) > 0
