@@ -399,7 +399,9 @@ int kattn_hash_rows(const void* data, int64_t n_rows, int64_t row_bytes, int64_t
  * Hkv must be even.  q: float32 [B][M][Hq][d], d = 128.
  * out: float32 [B][M][Hq / 2][256].
  * row_start, ctx_len, max_ctx, sm_scale, the cache layouts and the limits on
- * M, g * M and B as in kattn_decode; a sequence that breaks the row_start /
+ * M, g * M and B as in kattn_decode.  max_ctx also chooses the kernels, so one far
+ * above the lengths costs time (up to 2.3 times, short sequences with 8 columns);
+ * the result is the same.  A sequence that breaks the row_start /
  * ctx_len rule gets NaN outputs and KATTN_DEVERR_BAD_SEQUENCE.  A bounded wait
  * for a K/V copy that runs out sets KATTN_DEVERR_TIMEOUT; rows it concerns are
  * then not written, or unspecified.

@@ -13,14 +13,14 @@
 // side, so with up to 8 rows per map the stream of the cache is the floor, and the
 // split reads each byte once for both maps.  Measured, 64 sequences of 512 to
 // 32768 keys over 64-row pages, 32 query and 4 kv heads (554 MB, 82 us at the
-// measured copy rate): 8 rows per map, split 105 us (5.3 TB/s), the call 121 us; 4
-// rows per map, the call 106 us.  The split at 8 rows is bound by the chain of a
-// block's steps at 12 warps a multiprocessor, no single pipe: tensor 51% busy,
-// issue 35%; with the cache in L2, or without the int8 products, it takes 7% less.
+// measured copy rate): 8 rows per map, split 105 us (5.3 TB/s), the call 122 us; 4
+// rows per map, the call 104 us.  The split at 8 rows is bound by the chain of a
+// block's steps at 12 warps a multiprocessor, no single pipe: tensor 50% busy,
+// issue 37%; with the cache in L2, or without the int8 products, it takes 7% less.
 // With more rows each group of 8 rows streams the window again, from L2: bound by
-// the steps alone (5 draft columns, 40 rows per map, 16 sequences of 1k to 4k keys:
-// split 47 us, the call 56 us).  A single short sequence is bound by latency:
-// about 9 us, and 1.6 us for each of a window's 4 or 8 blocks.
+// the steps alone (2 draft columns, 16 rows per map, 64 sequences of 1k to 4k keys:
+// the call 82 us).  A single short sequence is bound by latency: about 9 us, and 1.6
+// us for each of a window's 4 or 8 blocks.
 #include "decode_diff_tc.cuh"
 
 namespace kattn {
@@ -740,20 +740,32 @@ cudaError_t launch_split(DiffParams p, const TmaMaps& maps, cudaStream_t stream)
 }
 
 // Whether diff_tc_kernel takes the call: more than 16 rows per map, and enough windows
-// for the multiprocessors to have several at once.  One window alone takes it longer
-// (14 us against 10), and short sequences have more unit starts than blocks.  The call
-// in us, diff_tc_kernel | row groups, 32 query and 4 kv heads:
+// for the multiprocessors to have several at once.  One window alone takes it longer,
+// and short sequences have more unit starts than blocks.  The call in us, diff_tc_kernel |
+// row groups (in brackets: the side that the rule takes where it is the slower):
+//   32 query and 4 kv heads
 //   sequences x keys, columns       3             5             8
-//    1 x 2k                             27 | 23 (4 columns)
-//    8 x 1k..4k                    34 | 32       41 | 37       59 | 54
-//   12 x 1k..4k                                  43 | 54
-//   16 x 1k..4k                    44 | 47       58 | 56       81 | 79
-//   24 x 1k..4k                                  73 | 78      106 | 112
-//   64 x 1k..4k                   106 | 123     144 | 183     223 | 282
-//   16 x 16k..32k                               311 | 414
-//    1 x 64k                                     78 | 89      116 | 127
-//   90 x 100..500                       57 | 57 (4 columns)   117 | 103
-// (With 16 rows, two groups: 64 x 1k..4k 80 | 84, 16 x 1k..4k 37 | 33.)
+//    1 x 100                       23 | 16       24 | 16       34 | 16
+//    4 x 1k..4k                    26 | 28       29 | 30       38 | 30
+//    8 x 1k..4k                    33 | 30       39 | 31       56 | 51
+//   12 x 1k..4k                    41 | 31 (tc)  42 | 52       59 | 70
+//   16 x 1k..4k                    43 | 44       54 | 53 (tc)  75 | 76
+//   24 x 1k..4k                    45 | 52       71 | 74      102 | 100 (tc)
+//   64 x 1k..4k                   103 | 121     144 | 177     218 | 279
+//   16 x 16k..32k                 228 | 254     308 | 399     473 | 622
+//    1 x 64k                       76 | 65 (tc)  76 | 88      112 | 124
+//   90 x 100..500                  49 | 49       76 | 70      112 | 100
+//   256 x 100..500                122 | 110     186 | 179     262 | 280 (groups)
+//   5 columns, other heads       16q / 2kv     48q / 6kv     64q / 8kv
+//   16 x 1k..4k                    40 | 32       71 | 76       81 | 98
+//   64 x 1k..4k                    82 | 99      202 | 264     260 | 339
+//   90 x 100..500                  44 | 44      103 | 98      121 | 126 (groups)
+// (With 16 rows, two groups: 64 x 1k..4k 80 | 84, 16 x 1k..4k 37 | 33.)  The windows are
+// counted from max_ctx, as the host does not know the lengths: a limit far above them
+// (131072, as a server's graph may pass) brings short batches here too, and a wider join.
+// Then, 32q / 4kv: 1 x 100, 8 columns 37 us instead of 16; 16 x 1k..4k, 5 columns 60
+// instead of 54 (groups 60); 64 x 1k..4k, 5 columns 170 instead of 144; 90 x 100..500, 8
+// columns 169 instead of 100 (groups 156).
 bool many_rows(const DiffParams& p) {
   static std::atomic<int> sms_cache[kMaxDevices];
   if (p.R <= 16 || p.nwin_max < 4) return false;

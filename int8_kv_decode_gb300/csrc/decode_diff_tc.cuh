@@ -13,12 +13,12 @@
 // reproduces, so a row has the same bytes in either.  The MMAs run beside the next
 // block's scores.
 //
-// What bounds it: the instructions of a block (650 per warp of 8 rows) in the chain
+// What bounds it: the instructions of a block (660 per warp of 8 rows) in the chain
 // scores, weights, operands, with the warps that tensor memory leaves a
 // multiprocessor (2 blocks of 11 at 40 rows): issue 48%, int8 MMA 38% busy.  16
-// sequences of 16k to 32k keys, 5 draft columns, 32 query and 4 kv heads: the call 311
-// us (405 MB, 60 us at the measured copy rate; this kernel 255 us), row groups on
-// mma.sync 414 us.  Tried:
+// sequences of 16k to 32k keys, 5 draft columns, 32 query and 4 kv heads: the call 308
+// us (405 MB, 60 us at the measured copy rate; this kernel 256 us), row groups on
+// mma.sync 399 us.  Tried:
 // mbarriers in place of the block's barrier, so that warps run up to a block apart,
 // the same to 5% slower; one block a multiprocessor with 6 stages 19% slower; the cache
 // in L2, or another L2 policy, the same.
