@@ -282,7 +282,7 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
     }
     __syncwarp();
 
-    // Of rows 2c + e: the reference in base 2 (m), the score above which it moves,
+    // Of rows 2c + e: the reference (m), the score above which it moves,
     // and the sum of this thread's weights.
     float2 m_run = make_float2(0.0f, 0.0f), m_move = make_float2(-INFINITY, -INFINITY);
     float2 l_run = make_float2(0.0f, 0.0f);
@@ -568,7 +568,7 @@ diff_split_kernel(const DiffParams p, const __grid_constant__ TmaMaps maps) {
 }
 
 // Joins the windows of a row: W warps take a half of its channels.  The windows
-// k, k + 8, ... are summed with the weights 2^(m_s - max m), for k = 0 .. 7; the
+// k, k + 8, ... are summed with the weights e^(m_s - max m), for k = 0 .. 7; the
 // eight sums are added in order, and the two maps are subtracted.  The order depends
 // on neither W nor other rows.  Bound by the partials' way out of L2 and the trips
 // there that depend on one another (statistics, then 4 W windows a trip): a warp has
@@ -639,8 +639,8 @@ __global__ void __launch_bounds__(32 * W * merge_halves<W>) diff_merge_kernel(co
     float w[2];
     {
       const float4 st = s0 ? stats(s0 + lane) : st0;
-      w[0] = fast_exp2(__fsub_rn(st.x, mx[0]));   // (-inf past the last window: 0)
-      w[1] = fast_exp2(__fsub_rn(st.y, mx[1]));
+      w[0] = exp_diff(st.x, mx[0]);               // (-inf past the last window: 0)
+      w[1] = exp_diff(st.y, mx[1]);
       l[0] = __fmaf_rn(w[0], st.z, l[0]);
       l[1] = __fmaf_rn(w[1], st.w, l[1]);
     }

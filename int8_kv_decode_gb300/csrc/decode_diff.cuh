@@ -175,11 +175,10 @@ __device__ __forceinline__ bool stage_ready(uint32_t bar, uint32_t parity) {
 // threshold; alpha: the factor of what is summed up so far.
 __device__ __forceinline__ void move_reference(float bm, float& m_run, float& m_move, float& alpha) {
   if (bm > m_move) {
-    const float m = __fmul_rn(bm, kLog2e);
     // (nothing is summed up yet where the threshold was -inf)
-    if (m_move != -INFINITY) alpha = fast_exp2(__fsub_rn(m_run, m));
-    m_run = m;
-    m_move = __fadd_rn(bm, kLag);
+    if (m_move != -INFINITY) alpha = exp_diff(m_run, bm);
+    m_run = bm;
+    m_move = __fadd_rd(bm, kLag);                 // (no more than kLag above, however large the scores)
   }
 }
 
@@ -235,7 +234,8 @@ __device__ __forceinline__ void hide_keys(float2 (&sc)[2][2], int key0, int keys
       if (key >= keys_y) sc[hf][k2].y = -INFINITY;
     }
 }
-// Weights 2^(s log2 e - m) in place of the scores.  A row's reference moves, to the
+// Weights e^(s - m) in place of the scores, the difference first: exact near the largest,
+// where the weights matter, however large the scores are.  A row's reference moves, to the
 // block's maximum, only where a score exceeds it by more than kLag; only then are the
 // maxima of the row's 32 keys put together.  l_run: this thread's weights so far.
 // Returns (to the warp) whether what is summed up so far has to be scaled by alpha.
@@ -254,12 +254,12 @@ __device__ __forceinline__ bool block_weights(float2 (&sc)[2][2], float2& m_run,
     move_reference(bm.y, m_run.y, m_move.y, alpha.y);
     moved = __any_sync(0xffffffffu, alpha.x != 1.0f || alpha.y != 1.0f);
   }
-  const float2 l2e = make_float2(kLog2e, kLog2e), mm = make_float2(-m_run.x, -m_run.y);
+  const float2 l2e = make_float2(kLog2e, kLog2e);
 #pragma unroll
   for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
     for (int k2 = 0; k2 < 2; ++k2) {
-      const float2 x2 = f2_fma(sc[hf][k2], l2e, mm);
+      const float2 x2 = f2_mul(f2_sub(sc[hf][k2], m_run), l2e);
       // (a key the row does not see: 2^-inf = 0)
       sc[hf][k2] = make_float2(fast_exp2(x2.x), fast_exp2(x2.y));
     }

@@ -603,3 +603,33 @@ def test_one_plane_of_the_two_has_such_a_key(M, Hq, limit, plane):
                          t["lam"])
     c = slice(128 * (1 - plane), 128 * (2 - plane))
     assert np.array_equal(bits(full[..., c].contiguous()), bits(same[..., c].contiguous()))
+
+
+# --------------------------------------------------------------- large scores
+
+@gpu
+@pytest.mark.parametrize("M,Hq,limit", SPREAD)
+@pytest.mark.parametrize("size", [1e3, 1e7, 1e8, 3e9, 1e12, 1e20])
+def test_scores_of_any_size(M, Hq, limit, size):
+    # scores are finite float32 values of any size: differences are taken first, where
+    # they are exact near the largest, and a row's weights do not depend on where its
+    # scores lie.  Keys 3, 40, 300 and 555 are the same, so that large scores tie.
+    import int8_kv_decode_gb300 as K
+    x = inputs(3, M, Hq, 2, [600, 45, 1400], seed=36)
+    for b in range(3):
+        at = int(x["start"][b])
+        for key in (40, 300, 555):
+            if key < x["ctx"][b]:
+                x["k8"][:, at + key], x["ks"][:, at + key] = x["k8"][:, at + 3], x["ks"][:, at + 3]
+    x["q"] *= np.float32(np.sqrt(size))
+    x["ks"] *= np.float32(np.sqrt(size))
+    t = device(x)
+    full = K.decode_diff(t["q"], t["k8"], t["ks"], t["v8"], t["vs"], t["start"], t["ctx"], limit or 1400,
+                         t["lam"])
+    got = full.cpu().numpy()
+    want, mass = expected(x)
+    assert np.all(np.isfinite(got))
+    # (a channel may be 0 where all the weight is: relative to the row's largest)
+    most = mass.max(-1, keepdims=True)
+    assert (np.abs(got.astype(np.float64) - want) <= TOL * most).all()
+    columns_alone(x, t, full)
