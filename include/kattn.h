@@ -448,7 +448,8 @@ enum kattn_code { KATTN_INT8 = 0, KATTN_E4M3 = 1 };
  * the quantization formula of kattn_quantize_kv applied to z; they do not
  * depend on the rounding of the mean.
  * x, weight, residual, residual_out: elements of x_type (a kattn_dtype); the
- *   sums are float32.  Rows of x and residual at strides x_stride and
+ *   sums are float32 (so scales are for rows whose squares add up to less than
+ *   2^127 and, with eps = 0, do not vanish; the codes hold anyway).  Rows of x and residual at strides x_stride and
  *   res_stride elements (>= d); residual_out has rows at res_out_stride and may
  *   be the residual itself (the same pointer and stride).  residual and
  *   residual_out are both NULL or both given.
