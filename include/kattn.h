@@ -562,6 +562,144 @@ int kattn_copy_pages(int8_t* k, float* k_scale, int8_t* v, float* v_scale, int H
                      const int32_t* count, void* workspace, size_t workspace_bytes,
                      void* stream);
 
+/* ------------------------------------------------ rotary positions -- */
+/* Angles of rotary positions: table[t][i] = (cos, sin) of the angle t * freq[i], for
+ * the positions t < n_positions and i < rot_dim / 2.  The product, the reduction and
+ * the functions are float64 (a float32 product is off by hundredths of a radian at
+ * position 10^5), rounded once to float32.  freq: float64 [rot_dim / 2] on the device;
+ * scaled positions for long contexts are scaled frequencies.  table: float32
+ * [n_positions][rot_dim / 2][2], 16-byte aligned.  rot_dim: a multiple of 8, up to 128
+ * (else KATTN_ERR_UNSUPPORTED).  n_positions = 0 is a no-op. */
+int kattn_rope_table(const double* freq, int n_positions, int rot_dim, float* table, void* stream);
+
+/* Turns the channels of heads by their row's angles.  With (c_i, s_i) =
+ * table[positions[r]][i], h = rot_dim / 2, and x, y the channels of a head of row r:
+ *   interleaved = 0:  y[i]      = x[i] c_i - x[i + h] s_i,
+ *                     y[i + h]  = x[i + h] c_i + x[i] s_i          for i < h
+ *   interleaved = 1:  y[2i]     = x[2i] c_i - x[2i + 1] s_i,
+ *                     y[2i + 1] = x[2i + 1] c_i + x[2i] s_i        for i < h
+ *   y[i] = x[i] for i >= rot_dim.
+ * Each product and sum is rounded to float32 on its own, the result once to out_type
+ * (x_type or KATTN_F32, kattn_dtypes; as kattn_decode takes float32 queries).
+ * x: row r of head j at x + r * x_stride + j * d, d = 128 (x_stride >= n_heads * d; the
+ * heads may lie among others, as in a fused projection); out likewise, at out_stride.
+ * Strides in elements, multiples of 4; x and out aligned to 4 elements; table as
+ * kattn_rope_table writes it.  out may be x (the same pointer, type and stride), else
+ * they must not overlap.
+ * positions: int32 [n_rows] on the device.  A row of a negative position (padding) is
+ * not written; a position at or past n_positions gives NaN.
+ * n_rows or n_heads 0 is a no-op. */
+int kattn_rope(const void* x, int x_type, int n_rows, int n_heads, int d, int64_t x_stride,
+               const int32_t* positions, const float* table, int n_positions, int rot_dim,
+               int interleaved, void* out, int out_type, int64_t out_stride, void* stream);
+
+/* --------------------------------------------- block-scaled caches -- */
+/* A paged cache whose rows share a scale per block of tokens and head:
+ *   k, v              codes [Hkv][cap_rows][128], int8 or e4m3 (kattn_code, bytes)
+ *   k_scale, v_scale  float32 [Hkv][cap_rows / block_rows]
+ * The value of channel i of row r is code * scale[r / block_rows].  block_rows is 32, 64
+ * or 128 (else KATTN_ERR_UNSUPPORTED) and divides page_rows, which is as in
+ * kattn_decode_paged; so a block lies in one page, and the page operations
+ * above serve such a cache too (its pages are copied by kattn_copy_block_pages).
+ * Key t of sequence b is row block_table[b * max_pages + t / page_rows] * page_rows + t %
+ * page_rows.  k and v 16-byte, the scales 4-byte aligned.  A table row serves keys below
+ * 2^30.  workspace in the calls that take one: at least 256 bytes, 256-byte aligned, the
+ * first 256 zeroed before the first call; only its error word is used
+ * (kattn_decode_blocks needs more).
+ *
+ * Spans: ragged rows of B sequences.  cu_rows: int32 [B + 1] on the device, rising;
+ * rows cu_rows[b] .. cu_rows[b + 1] - 1 of the call's row arrays are the keys start[b],
+ * start[b] + 1, ... of sequence b (start: int32 [B] on the device; a sequence may have
+ * no rows).  n_rows: rows of the arrays; rows that belong to no sequence, such as those
+ * behind cu_rows[B], are neither read nor written.  A sequence whose rows leave [0,
+ * n_rows) or whose keys leave the table's row is skipped (KATTN_DEVERR_BAD_SEQUENCE); a
+ * block whose page is outside the pool is skipped (KATTN_DEVERR_BAD_PAGE).
+ *
+ * Writes new rows of K and V into the cache.  Per sequence, head and block of rows that
+ * it touches, with x the block's new rows (K rotated first, if a table is given: the
+ * rotation of kattn_rope by the key's position, in float32) and top = 127, or 448 for
+ * e4m3:
+ *   s      = max |x| / top                       (IEEE division, over rows and channels)
+ *   if rows of the block before the first new one stay:  s = max(s, the block's scale
+ *            s_old), and where that is larger than s_old the codes c of those rows become
+ *            round(c * (s_old / s))
+ *   codes  = round(x / s), 0 where s = 0;  the block's scale = s
+ * round is to the nearest, ties to even, clamped to +-127, or the nearest e4m3 value,
+ * saturating; every product and quotient is rounded to float32 once.  Rows of the block
+ * behind the last new one are dead: their codes are left as they were, under the new
+ * scale.  (So the codes of a block depend on how its rows came in: a row written under a
+ * small scale is coded again as larger ones follow, each time with half a step of the
+ * new scale.)  A block that several sequences of the call touch, as in a shared page, is
+ * undefined.
+ * k_new, v_new: x_type, row r of head h at + r * k_stride (v_stride) + h * d, each stride >=
+ * n_kv * d; q (may be NULL): [n_rows][Hq][d] at q_stride, turned into q_out at q_out_stride as
+ * kattn_rope does (a skipped sequence's rows become NaN; a row of no sequence is not
+ * written); q_out may be q.  Alignment and strides as in kattn_rope.  table NULL: no
+ * rotation (q must be NULL then, rot_dim and n_positions are ignored); otherwise keys at
+ * or past n_positions make their sequence a bad one.
+ * One launch; bitwise deterministic.  B or n_rows 0 is a no-op. */
+int kattn_append_blocks(const void* k_new, const void* v_new, int x_type, int n_rows, int n_kv, int d,
+                        int64_t k_stride, int64_t v_stride, const int32_t* cu_rows,
+                        const int32_t* start, int B, void* k, float* k_scale, void* v,
+                        float* v_scale, int code_type, int cap_rows, int block_rows,
+                        const int32_t* block_table, int max_pages, int page_rows,
+                        const float* table, int n_positions, int rot_dim, int interleaved,
+                        const void* q, int Hq, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Reads rows back: out_k, out_v [n_rows][Hkv][d] of out_type (a kattn_dtype; 16-byte
+ * aligned, either may be NULL), value = code * scale in float32, rounded once to the type.
+ * Rows of skipped sequences and blocks are not written. */
+int kattn_read_blocks(const void* k, const float* k_scale, const void* v, const float* v_scale,
+                      int code_type, int Hkv, int d, int cap_rows, int block_rows,
+                      const int32_t* block_table, int max_pages, int page_rows,
+                      const int32_t* cu_rows, const int32_t* start, int B, int n_rows, void* out_k,
+                      void* out_v, int out_type, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/* Decode attention over a block-scaled cache, for sequence b, draft column j < M, query
+ * head h of kv head kh = h / g:
+ *   out[b][j][h][:] = sum_t softmax(q . K_t * sm_scale)_t V_t
+ * over the keys t < ctx_len[b] + j, K_t and V_t the values of the cache's rows.  Unlike
+ * kattn_decode the query is not quantized.  q, out: q_type (a kattn_dtype) [B][M][Hq][d],
+ * 16-byte aligned.
+ *   Queries: a row enters scaled by a power of two, its largest element in [2^14, 2^15),
+ *   as f16 (bf16 exact down to 2^-28 of the largest; f16 exact) or, float32, as f16 hi +
+ *   lo (22 bits, or 2^-39 of the largest).  Products are exact, sums float32.
+ *   Weights: relative to the row's reference, held as f16 (11 bits; float32 queries: hi +
+ *   lo, 22 bits) with steps of 2^-33 of the reference's at the smallest, and summed up as
+ *   they are held.  Values, row sums and the output before its one rounding are float32.
+ * ctx_len: int32 [B] on the device.  ctx_len[b] = 0 is an empty slot: its rows are 0, and
+ * nothing of it is read.  Below 0, above max_ctx, or with ceil((ctx_len[b] + M - 1) /
+ * page_rows) > max_pages: NaN and KATTN_DEVERR_BAD_SEQUENCE.  A table entry outside the
+ * pool sets KATTN_DEVERR_BAD_PAGE and reads page 0: the sequence's outputs are then
+ * unspecified.  A bounded wait for a copy that runs out sets KATTN_DEVERR_TIMEOUT; rows it
+ * concerns are then not written, or unspecified.
+ * e4m3 codes that are no numbers, and scales that are not finite, do not reach rows that
+ * see no key of their 32-key step (codes) or block (scales); they are taken as 0 in steps
+ * that some column does not see whole.
+ * Limits on M, g * M, B and sizes, and sm_scale, as in kattn_decode.
+ * Deterministic; the bytes of out[b][j][h] depend only on the row's own query and keys, so
+ * column j equals an M = 1 call with ctx_len + j on the same cache, in any batch.
+ * workspace: kattn_blocks_workspace_size(B, M, Hq, max_ctx) bytes (0 for invalid sizes),
+ * 256-byte aligned, its first 256 bytes zeroed before the first call, and shared only by
+ * calls that are ordered on the GPU.  Two kernels on `stream` at most; capturable in a
+ * CUDA graph once a first call on the device has run outside capture. */
+size_t kattn_blocks_workspace_size(int B, int M, int Hq, int max_ctx);
+int kattn_decode_blocks(const void* q, int q_type, const void* k, const float* k_scale,
+                        const void* v, const float* v_scale, int code_type, int cap_rows,
+                        int block_rows, const int32_t* block_table, int max_pages, int page_rows,
+                        const int32_t* ctx_len, int B, int M, int Hq, int Hkv, int d, int max_ctx,
+                        float sm_scale, void* out, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/* kattn_copy_pages for a block-scaled cache: the rows and scales of page src[i] to page
+ * dst[i] in every plane.  Scales 4-byte aligned; the rest as there. */
+int kattn_copy_block_pages(void* k, float* k_scale, void* v, float* v_scale, int Hkv, int d,
+                           int cap_rows, int page_rows, int block_rows, const int32_t* src,
+                           const int32_t* dst, int n, const int32_t* count, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
 /* Read (and clear) the device error word of a workspace.  Copies 4
  * bytes to the host and waits for `stream`.  *device_err receives the
  * KATTN_DEVERR_* bits set by calls since the last read. */

@@ -76,6 +76,24 @@ SIGNATURES = {
                                     c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "kattn_copy_pages": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
                                  c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "kattn_rope_table": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p]),
+    "kattn_rope": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_int64, c_void_p, c_void_p, c_int,
+                           c_int, c_int, c_void_p, c_int, c_int64, c_void_p]),
+    "kattn_append_blocks": (c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int64, c_int64,
+                                    c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
+                                    c_int, c_int, c_int, c_void_p, c_int, c_int, c_void_p, c_int, c_int,
+                                    c_int, c_void_p, c_int, c_int64, c_void_p, c_int64, c_void_p,
+                                    c_size_t, c_void_p]),
+    "kattn_read_blocks": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
+                                  c_int, c_void_p, c_int, c_int, c_void_p, c_void_p, c_int, c_int,
+                                  c_void_p, c_void_p, c_int, c_void_p, c_size_t, c_void_p]),
+    "kattn_blocks_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int]),
+    "kattn_decode_blocks": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int,
+                                    c_int, c_void_p, c_int, c_int, c_void_p, c_int, c_int, c_int, c_int,
+                                    c_int, c_int, c_float, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "kattn_copy_block_pages": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
+                                       c_int, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_size_t,
+                                       c_void_p]),
     "kattn_get_device_status": (c_int, [c_void_p, c_size_t, ctypes.POINTER(c_int), c_void_p]),
 }
 

@@ -8,6 +8,7 @@ library.  All computation happens in the library's CUDA kernels.
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
@@ -652,6 +653,289 @@ def rms_norm_quant(x, weight, *, residual=None, residual_out=None, eps: float = 
     return out, out_scale
 
 
+# ------------------------------------------------------ rotary positions --
+
+def rope_frequencies(rot_dim: int = 128, base: float = 10000.0, *, linear: float = 1.0,
+                     extend: float = 1.0, parts=None) -> list:
+    """Angle per position of each pair of channels, in float64: base^(-2i / rot_dim).
+
+    For contexts longer than the trained one, at most one of
+      linear = f          every frequency divided by f (positions squeezed);
+      extend = f          the base raised to base * f^(rot_dim / (rot_dim - 2)), so that
+                          the slowest pair is squeezed by f and the fastest not at all;
+      parts = (f, length, slow, fast)
+                          pairs of up to `slow` turns over `length` trained positions are
+                          divided by f, of `fast` turns or more kept, and those between
+                          blended linearly by their turns.
+    """
+    if rot_dim < 8 or rot_dim % 8 or rot_dim > 128:
+        raise ValueError("rot_dim must be a multiple of 8, up to 128")
+    if (linear != 1.0) + (extend != 1.0) + (parts is not None) > 1:
+        raise ValueError("at most one of linear, extend and parts")
+    if not (base > 0 and linear > 0 and extend > 0):
+        raise ValueError("base, linear and extend must be above 0")
+    base = base * extend ** (rot_dim / (rot_dim - 2))
+    freq = [base ** (-i / rot_dim) / linear for i in range(0, rot_dim, 2)]
+    if parts is not None:
+        f, length, slow, fast = parts
+        if not (f > 0 and length > 0 and 0 <= slow < fast):
+            raise ValueError("parts must be (factor, length, slow, fast) with slow < fast")
+        keep = [min(1.0, max(0.0, (length * w / (2 * math.pi) - slow) / (fast - slow))) for w in freq]
+        freq = [w * k + w / f * (1.0 - k) for w, k in zip(freq, keep)]
+    return freq
+
+
+def rope_table(n_positions: int, rot_dim: int = 128, *, frequencies=None, base: float = 10000.0,
+               device="cuda", out=None) -> torch.Tensor:
+    """cos and sin of every position, float32 [n_positions][rot_dim/2][2], for rope() and
+    append_blocks(); angles in float64.  frequencies: rot_dim/2 numbers, those of
+    rope_frequencies(rot_dim, base) if None (kattn_rope_table)."""
+    freq = rope_frequencies(rot_dim, base) if frequencies is None else [float(w) for w in frequencies]
+    if len(freq) != rot_dim // 2:
+        raise ValueError("frequencies must have rot_dim / 2 entries")
+    if out is None:
+        out = torch.empty((n_positions, rot_dim // 2, 2), dtype=torch.float32, device=device)
+    index = _device_of(out, "out")
+    _check(out, torch.float32, index, "out", 3)
+    if out.shape != (n_positions, rot_dim // 2, 2):
+        raise ValueError("out must have shape [n_positions][rot_dim/2][2]")
+    freq = torch.tensor(freq, dtype=torch.float64, device=out.device)
+    _launch("kattn_rope_table", index, freq.data_ptr(), n_positions, rot_dim, out.data_ptr())
+    return out
+
+
+def _heads(t, dtype, index, name, rows=None, heads=None):
+    """The row stride of t [rows][heads][128], whose rows may lie among others."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the others, got {t.device}")
+    if t.dim() != 3 or t.shape[2] != 128:
+        raise ValueError(f"{name} must have shape [rows][heads][128]")
+    n, h, d = t.shape
+    if (rows is not None and n != rows) or (heads is not None and h != heads):
+        raise ValueError(f"{name} must have shape [{rows}][{heads}][128]")
+    if n * h and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
+        raise ValueError(f"the heads of a row of {name} must follow one another")
+    return t.stride(0) if n > 1 else max(h * d, 128)
+
+
+def _angles(table, index):
+    """(pointer, positions, rot_dim) of a table of angles."""
+    _check(table, torch.float32, index, "table", 3)
+    if table.shape[2] != 2:
+        raise ValueError("table must have shape [positions][rot_dim/2][2]")
+    return table.data_ptr(), table.shape[0], 2 * table.shape[1]
+
+
+def rope(x, positions, table, *, interleaved: bool = False, out=None, out_dtype=None):
+    """Turn the heads of x [rows][heads][128] by their row's position (int32 [rows]).
+
+    x: float32, bfloat16 or float16; its rows may be slices of wider ones.  table: of
+    rope_table(); the channels past its rot_dim pass.  interleaved: channels 2i, 2i+1
+    are a pair, else i and i + rot_dim/2.  The result has the type of x or float32
+    (out's, or out_dtype); out may be x.  Rows of negative positions are not written,
+    those past the table are NaN.  (kattn_rope)
+    """
+    index = _device_of(x, "x")
+    x_type = _NORM_TYPES.get(x.dtype)
+    if x_type is None:
+        raise TypeError(f"x must be float32, bfloat16 or float16, got {x.dtype}")
+    x_stride = _heads(x, x.dtype, index, "x")
+    n, h, d = x.shape
+    _check_list(positions, index, "positions", n)
+    if out is None:
+        out = torch.empty((n, h, d), dtype=out_dtype or x.dtype, device=x.device)
+    out_stride = _heads(out, out.dtype, index, "out", n, h)
+    out_type = _NORM_TYPES.get(out.dtype)
+    if out_type is None or (out_type and out_type != x_type):
+        raise TypeError(f"out must be {x.dtype} or float32, got {out.dtype}")
+    table_ptr, n_positions, rot_dim = _angles(table, index)
+    if n == 1 and x.data_ptr() == out.data_ptr():
+        out_stride = x_stride
+    _launch("kattn_rope", index, x.data_ptr(), x_type, n, h, d, x_stride, positions.data_ptr(), table_ptr,
+            n_positions, rot_dim, int(interleaved), out.data_ptr(), out_type, out_stride)
+    return out
+
+
+# -------------------------------------------------- block-scaled caches --
+
+def _block_cache(k, k_scale, v, v_scale, index):
+    """(code type, Hkv, cap, d, block_rows) of a cache with a scale per block and head."""
+    code = _CODE_TYPES.get(k.dtype) if isinstance(k, torch.Tensor) else None
+    if code is None:
+        raise TypeError("k must be a torch.Tensor of int8 or float8_e4m3fn codes")
+    _check(k, k.dtype, index, "k", 3)
+    _check(v, k.dtype, index, "v", 3)
+    _check(k_scale, torch.float32, index, "k_scale", 2)
+    _check(v_scale, torch.float32, index, "v_scale", 2)
+    Hkv, cap, d = k.shape
+    blocks = k_scale.shape[1]
+    if v.shape != k.shape or k_scale.shape != (Hkv, blocks) or v_scale.shape != k_scale.shape \
+            or blocks < 1 or cap % blocks:
+        raise ValueError("k/v/scales shapes disagree")
+    return code, Hkv, cap, d, cap // blocks
+
+
+def _spans(cu_rows, start, block_table, index):
+    _check(block_table, torch.int32, index, "block_table", 2)
+    B = block_table.shape[0]
+    _check_list(start, index, "start", B)
+    _check_list(cu_rows, index, "cu_rows", B + 1)
+    return B
+
+
+def _error_word(workspace, like, index):
+    if workspace is None:
+        return torch.zeros(256, dtype=torch.uint8, device=like.device)
+    _check(workspace, torch.uint8, index, "workspace", 1)
+    return workspace
+
+
+def append_blocks(k_new, v_new, cu_rows, start, k, k_scale, v, v_scale, block_table, page_rows: int, *,
+                  table=None, interleaved: bool = False, q=None, q_out=None, workspace=None):
+    """Write rows of K and V into a block-scaled paged cache; returns q_out.
+
+    k_new, v_new [rows][Hkv][128] (float32, bfloat16 or float16; rows may be slices of
+    wider ones): rows cu_rows[b] .. cu_rows[b+1] are the keys start[b], ... of sequence
+    b (int32 [B+1] and [B]).  k, v [Hkv][cap][128] int8 or float8_e4m3fn, k_scale,
+    v_scale [Hkv][cap/block_rows] float32 (block_rows 32, 64 or 128), block_table int32
+    [B][max_pages].  table (rope_table()): K rows are turned by their key's position
+    before they are coded, and so are the queries q [rows][Hq][128], into q_out (may be
+    q).  workspace: any workspace of the library, for the error bits.
+    (kattn_append_blocks)
+    """
+    index = _device_of(k_new, "k_new")
+    dtype = k_new.dtype
+    x_type = _NORM_TYPES.get(dtype)
+    if x_type is None:
+        raise TypeError(f"k_new must be float32, bfloat16 or float16, got {dtype}")
+    code, Hkv, cap, d, block_rows = _block_cache(k, k_scale, v, v_scale, index)
+    k_stride = _heads(k_new, dtype, index, "k_new", None, Hkv)
+    n = k_new.shape[0]
+    v_stride = _heads(v_new, dtype, index, "v_new", n, Hkv)
+    B = _spans(cu_rows, start, block_table, index)
+    table_ptr = n_positions = rot_dim = q_ptr = q_out_ptr = q_stride = q_out_stride = Hq = 0
+    if table is not None:
+        table_ptr, n_positions, rot_dim = _angles(table, index)
+    if q is not None:
+        if table is None:
+            raise ValueError("q without a table")
+        q_stride = _heads(q, dtype, index, "q", n)
+        Hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((n, Hq, d), dtype=dtype, device=q.device)
+        q_out_stride = _heads(q_out, dtype, index, "q_out", n, Hq)
+        q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
+        if n == 1 and q_ptr == q_out_ptr:
+            q_out_stride = q_stride
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    workspace = _error_word(workspace, k, index)
+    _launch("kattn_append_blocks", index, k_new.data_ptr(), v_new.data_ptr(), x_type, n, Hkv, d, k_stride,
+            v_stride, cu_rows.data_ptr(), start.data_ptr(), B, k.data_ptr(), k_scale.data_ptr(), v.data_ptr(),
+            v_scale.data_ptr(), code, cap, block_rows, block_table.data_ptr(), block_table.shape[1], page_rows,
+            table_ptr, n_positions, rot_dim, int(interleaved), q_ptr, Hq, q_stride, q_out_ptr, q_out_stride,
+            workspace.data_ptr(), workspace.numel())
+    return q_out
+
+
+def read_blocks(k, k_scale, v, v_scale, block_table, page_rows: int, cu_rows, start, n_rows: int, *,
+                out_k=None, out_v=None, dtype=torch.bfloat16, workspace=None):
+    """Rows of a block-scaled cache as values; returns (out_k, out_v), [n_rows][Hkv][128].
+
+    Rows cu_rows[b] .. cu_rows[b+1] of the outputs become the keys start[b], ... of
+    sequence b; n_rows: an upper bound on cu_rows[B]; rows of no sequence are not
+    written.  dtype: float32, bfloat16 or float16.  The rest as append_blocks().
+    (kattn_read_blocks)
+    """
+    index = _device_of(k, "k")
+    code, Hkv, cap, d, block_rows = _block_cache(k, k_scale, v, v_scale, index)
+    B = _spans(cu_rows, start, block_table, index)
+    if n_rows < 0:
+        raise ValueError("n_rows must not be negative")
+    if out_k is not None or out_v is not None:
+        dtype = (out_v if out_k is None else out_k).dtype
+    out_type = _NORM_TYPES.get(dtype)
+    if out_type is None:
+        raise TypeError(f"outputs must be float32, bfloat16 or float16, got {dtype}")
+    shape = (n_rows, Hkv, d)
+    if out_k is None:
+        out_k = torch.empty(shape, dtype=dtype, device=k.device)
+    if out_v is None:
+        out_v = torch.empty(shape, dtype=dtype, device=k.device)
+    _check(out_k, dtype, index, "out_k", 3)
+    _check(out_v, dtype, index, "out_v", 3)
+    if out_k.shape != shape or out_v.shape != shape:
+        raise ValueError("out_k and out_v must have shape [n_rows][Hkv][128]")
+    workspace = _error_word(workspace, k, index)
+    _launch("kattn_read_blocks", index, k.data_ptr(), k_scale.data_ptr(), v.data_ptr(), v_scale.data_ptr(),
+            code, Hkv, d, cap, block_rows, block_table.data_ptr(), block_table.shape[1], page_rows,
+            cu_rows.data_ptr(), start.data_ptr(), B, n_rows, out_k.data_ptr(), out_v.data_ptr(), out_type,
+            workspace.data_ptr(), workspace.numel())
+    return out_k, out_v
+
+
+def blocks_workspace_size(B: int, M: int, Hq: int, max_ctx: int) -> int:
+    return int(_lib.load().kattn_blocks_workspace_size(B, M, Hq, max_ctx))
+
+
+def alloc_blocks_workspace(B: int, M: int, Hq: int, max_ctx: int, device="cuda") -> torch.Tensor:
+    """A workspace for decode_blocks with its header zeroed (allocated by torch, not the
+    library)."""
+    n = blocks_workspace_size(B, M, Hq, max_ctx)
+    if n == 0:
+        raise ValueError("invalid sizes for a block-scaled decode workspace")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def decode_blocks(q, k, k_scale, v, v_scale, block_table, page_rows: int, ctx_len, max_ctx: int, *,
+                  out=None, sm_scale: float = 0.0, workspace=None):
+    """Decode attention over a block-scaled paged cache; returns out like q.
+
+    q [B][M][Hq][128] float32, bfloat16 or float16 (not quantized); column j of sequence
+    b sees the keys t < ctx_len[b] + j (int32 [B]; 0: an empty slot, whose rows are 0).
+    Cache and table as append_blocks().  workspace: a uint8 tensor of
+    blocks_workspace_size(...) bytes, its first 256 zeroed before its first use,
+    allocated here with torch if None.  (kattn_decode_blocks)
+    """
+    index = _device_of(q, "q")
+    q_type = _NORM_TYPES.get(q.dtype)
+    if q_type is None:
+        raise TypeError(f"q must be float32, bfloat16 or float16, got {q.dtype}")
+    _check(q, q.dtype, index, "q", 4)
+    code, Hkv, cap, dk, block_rows = _block_cache(k, k_scale, v, v_scale, index)
+    B, M, Hq, d = q.shape
+    if dk != d or Hkv < 1 or Hq % Hkv:
+        raise ValueError("q must have heads of 128 channels, a multiple of the cache's")
+    _check(block_table, torch.int32, index, "block_table", 2)
+    _check_list(ctx_len, index, "ctx_len", B)
+    if block_table.shape[0] != B:
+        raise ValueError("block_table must have B rows")
+    if not 0 < max_ctx < 2 ** 30:
+        raise ValueError("max_ctx out of range")
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check(out, q.dtype, index, "out", 4)
+        if out.shape != q.shape:
+            raise ValueError("out must have the shape of q")
+    if workspace is None:
+        workspace = (alloc_blocks_workspace(B, M, Hq, max_ctx, q.device) if B else
+                     torch.zeros(256, dtype=torch.uint8, device=q.device))
+    else:
+        _check(workspace, torch.uint8, index, "workspace", 1)
+    _launch("kattn_decode_blocks", index, q.data_ptr(), q_type, k.data_ptr(), k_scale.data_ptr(), v.data_ptr(),
+            v_scale.data_ptr(), code, cap, block_rows, block_table.data_ptr(), block_table.shape[1], page_rows,
+            ctx_len.data_ptr(), B, M, Hq, Hkv, d, max_ctx, sm_scale, out.data_ptr(), workspace.data_ptr(),
+            workspace.numel())
+    return out
+
+
 # -------------------------------------------------------- page operations --
 
 def page_workspace_size(n_slots: int, n_pages: int) -> int:
@@ -781,18 +1065,18 @@ def copy_pages(k, k_scale, v, v_scale, src, dst, page_rows: int, *, count=None,
     skipped.  count: an int32 tensor of one entry; only the first min(n, count)
     moves are made.  workspace: any workspace of the library (its error word
     takes the checks of the entries); allocated here if None.
-    (kattn_copy_pages)"""
+    (kattn_copy_pages)
+    A block-scaled cache (int8 or float8_e4m3fn, scales [Hkv][cap/block_rows])
+    is copied by the same call (kattn_copy_block_pages)."""
     index = _device_of(k, "k")
-    _check(k, torch.int8, index, "k", 3)
-    _check(v, torch.int8, index, "v", 3)
-    _check(k_scale, torch.float32, index, "k_scale", 2)
-    _check(v_scale, torch.float32, index, "v_scale", 2)
+    if k.dtype is not torch.float8_e4m3fn:
+        _check(k, torch.int8, index, "k", 3)
+    _, Hkv, cap, d, block_rows = _block_cache(k, k_scale, v, v_scale, index)
     _check(src, torch.int32, index, "src", 1)
     n = src.shape[0]
     _check_list(dst, index, "dst", n)
-    Hkv, cap, d = k.shape
-    if v.shape != k.shape or k_scale.shape != (Hkv, cap) or v_scale.shape != (Hkv, cap):
-        raise ValueError("k/v/scales shapes disagree")
+    if block_rows == 1 and k.dtype is not torch.int8:
+        raise TypeError("a cache with a scale per row must be int8")
     count_ptr = 0
     if count is not None:
         _check_list(count, index, "count", 1)
@@ -801,9 +1085,14 @@ def copy_pages(k, k_scale, v, v_scale, src, dst, page_rows: int, *, count=None,
         workspace = torch.zeros(256, dtype=torch.uint8, device=k.device)
     else:
         _check(workspace, torch.uint8, index, "workspace", 1)
-    _launch("kattn_copy_pages", index, k.data_ptr(), k_scale.data_ptr(), v.data_ptr(),
-            v_scale.data_ptr(), Hkv, d, cap, page_rows, src.data_ptr(), dst.data_ptr(), n, count_ptr,
-            workspace.data_ptr(), workspace.numel())
+    if block_rows == 1:
+        _launch("kattn_copy_pages", index, k.data_ptr(), k_scale.data_ptr(), v.data_ptr(),
+                v_scale.data_ptr(), Hkv, d, cap, page_rows, src.data_ptr(), dst.data_ptr(), n, count_ptr,
+                workspace.data_ptr(), workspace.numel())
+    else:
+        _launch("kattn_copy_block_pages", index, k.data_ptr(), k_scale.data_ptr(), v.data_ptr(),
+                v_scale.data_ptr(), Hkv, d, cap, page_rows, block_rows, src.data_ptr(), dst.data_ptr(), n,
+                count_ptr, workspace.data_ptr(), workspace.numel())
 
 
 def get_device_status(workspace: torch.Tensor) -> int:

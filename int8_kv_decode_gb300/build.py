@@ -40,6 +40,9 @@ SOURCES = {
     "decode_diff.cu": [],
     "norm_quant.cu": [],
     "pages.cu": [],
+    "rope.cu": [],
+    "blocks.cu": [],
+    "decode_blocks.cu": [],
 }
 
 

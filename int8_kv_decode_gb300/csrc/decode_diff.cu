@@ -684,28 +684,6 @@ __global__ void __launch_bounds__(32 * W * merge_halves<W>) diff_merge_kernel(co
 }
 
 // ------------------------------------------------------------------- host
-// 2-D view [rows][128] of an int8 cache; kBlockBk-row boxes, 128-byte swizzle.
-bool encode_plane_map(CUtensorMap* map, const int8_t* base, int64_t rows) {
-  static const PFN_cuTensorMapEncodeTiled_v12000 enc = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }();
-  if (!enc) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)kD};
-  const cuuint32_t box[2] = {(cuuint32_t)kD, (cuuint32_t)kBlockBk};
-  const cuuint32_t estr[2] = {1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(base), dims, strides,
-             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int T>
 cudaError_t launch_split(DiffParams p, const TmaMaps& maps, cudaStream_t stream) {
   const auto kern = diff_split_kernel<T>;

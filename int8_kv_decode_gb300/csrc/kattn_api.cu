@@ -2,6 +2,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "blocks_internal.cuh"
 #include "kattn_internal.cuh"
 #include "ops_internal.cuh"
 
@@ -252,6 +253,103 @@ PageParams page_params(const int32_t* block_table, int n_slots, int max_pages,
   p.n = n;
   set_page_workspace(p, workspace);
   return p;
+}
+
+// Page copies of a cache whose rows share a scale per block_rows rows (1: a scale each).
+int run_copy(int8_t* k, float* k_scale, int8_t* v, float* v_scale, int Hkv, int d, int cap_rows,
+             int page_rows, int block_rows, const int32_t* src, const int32_t* dst, int n,
+             const int32_t* count, void* workspace, size_t workspace_bytes, void* stream) {
+  const size_t scale_align = block_rows == 1 ? 16 : 4;
+  if (Hkv < 1 || cap_rows < 1 || n < 0) return KATTN_ERR_INVALID_ARG;
+  if (d != KATTN_HEAD_DIM) return KATTN_ERR_UNSUPPORTED;
+  const int st = check_page_rows(page_rows);
+  if (st != KATTN_OK) return st;
+  if (cap_rows % page_rows != 0) return KATTN_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < 256) return KATTN_ERR_WORKSPACE;
+  if (n == 0) return KATTN_OK;
+  if (!k || !k_scale || !v || !v_scale || !src || !dst) return KATTN_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_scale, scale_align) ||
+      !aligned(v_scale, scale_align) ||
+      !aligned(src, 4) || !aligned(dst, 4) || !aligned(count, 4))
+    return KATTN_ERR_MISALIGNED;
+  CopyParams p{};
+  p.k = k;
+  p.v = v;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.Hkv = Hkv;
+  p.cap_rows = cap_rows;
+  p.page_rows = page_rows;
+  p.n_pages = cap_rows / page_rows;
+  p.n = n;
+  p.scale_shift = __builtin_ctz((unsigned)block_rows);
+  p.src = src;
+  p.dst = dst;
+  p.count = count;
+  p.err = static_cast<uint32_t*>(workspace);
+  return launch_copy_pages(p, as_stream(stream)) == cudaSuccess ? KATTN_OK : KATTN_ERR_CUDA;
+}
+
+// ---- block-scaled caches
+int type_size(int type) { return type == KATTN_F32 ? 4 : 2; }
+bool is_dtype(int type) { return type >= KATTN_F32 && type <= KATTN_F16; }
+
+// The cache's own rules (B > 0), and its fields.
+int set_block_cache(BlockCache& c, const void* k, const float* k_scale, const void* v,
+                    const float* v_scale, int code_type, int Hkv, int d, int cap_rows, int block_rows,
+                    const int32_t* block_table, int max_pages, int page_rows) {
+  if (code_type != KATTN_INT8 && code_type != KATTN_E4M3) return KATTN_ERR_INVALID_ARG;
+  if (Hkv < 1 || Hkv > 65535 || cap_rows < 1) return KATTN_ERR_INVALID_ARG;
+  if (d != KATTN_HEAD_DIM) return KATTN_ERR_UNSUPPORTED;
+  if ((int64_t)Hkv * cap_rows > (int64_t)INT32_MAX - 4096) return KATTN_ERR_UNSUPPORTED;
+  const int st = check_paging(max_pages, page_rows, cap_rows);
+  if (st != KATTN_OK) return st;
+  if (block_rows != 32 && block_rows != 64 && block_rows != 128) return KATTN_ERR_UNSUPPORTED;
+  if (page_rows % block_rows != 0) return KATTN_ERR_INVALID_ARG;
+  if (!k || !k_scale || !v || !v_scale || !block_table) return KATTN_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
+      !aligned(block_table, 4))
+    return KATTN_ERR_MISALIGNED;
+  c.k = static_cast<uint8_t*>(const_cast<void*>(k));
+  c.v = static_cast<uint8_t*>(const_cast<void*>(v));
+  c.k_scale = const_cast<float*>(k_scale);
+  c.v_scale = const_cast<float*>(v_scale);
+  c.block_table = block_table;
+  c.Hkv = Hkv;
+  c.cap_rows = cap_rows;
+  c.block_shift = __builtin_ctz((unsigned)block_rows);
+  c.page_shift = __builtin_ctz((unsigned)page_rows);
+  c.n_pages = cap_rows / page_rows;
+  c.max_pages = max_pages;
+  return KATTN_OK;
+}
+
+int set_spans(SpanParams& s, const int32_t* cu_rows, const int32_t* start, int B, int n_rows,
+              void* workspace, size_t workspace_bytes) {
+  if (!cu_rows || !start) return KATTN_ERR_INVALID_ARG;
+  if (!aligned(cu_rows, 4) || !aligned(start, 4)) return KATTN_ERR_MISALIGNED;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < 256) return KATTN_ERR_WORKSPACE;
+  s.cu = cu_rows;
+  s.start = start;
+  s.B = B;
+  s.rows = n_rows;
+  s.err = static_cast<uint32_t*>(workspace);
+  return KATTN_OK;
+}
+
+// Heads of 128 channels at rows of `stride` elements, taken four elements at a time.
+int check_heads(const void* x, int type, int64_t stride, int heads) {
+  if (stride < (int64_t)heads * kD) return KATTN_ERR_INVALID_ARG;
+  if (!x) return KATTN_ERR_INVALID_ARG;
+  if (!aligned(x, 4 * type_size(type)) || stride % 4 != 0) return KATTN_ERR_MISALIGNED;
+  return KATTN_OK;
+}
+
+int check_rope_table(const float* table, int n_positions, int rot_dim, int interleaved) {
+  if (n_positions < 1 || rot_dim < 1 || (interleaved != 0 && interleaved != 1)) return KATTN_ERR_INVALID_ARG;
+  if (rot_dim % 8 != 0 || rot_dim > kD) return KATTN_ERR_UNSUPPORTED;
+  if (!table) return KATTN_ERR_INVALID_ARG;
+  return aligned(table, 16) ? KATTN_OK : KATTN_ERR_MISALIGNED;
 }
 
 }  // namespace
@@ -663,32 +761,174 @@ int kattn_copy_pages(int8_t* k, float* k_scale, int8_t* v, float* v_scale, int H
                      int cap_rows, int page_rows, const int32_t* src, const int32_t* dst, int n,
                      const int32_t* count, void* workspace, size_t workspace_bytes,
                      void* stream) {
-  if (Hkv < 1 || cap_rows < 1 || n < 0) return KATTN_ERR_INVALID_ARG;
+  return run_copy(k, k_scale, v, v_scale, Hkv, d, cap_rows, page_rows, 1, src, dst, n, count,
+                  workspace, workspace_bytes, stream);
+}
+
+int kattn_copy_block_pages(void* k, float* k_scale, void* v, float* v_scale, int Hkv, int d,
+                           int cap_rows, int page_rows, int block_rows, const int32_t* src,
+                           const int32_t* dst, int n, const int32_t* count, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  if (block_rows != 32 && block_rows != 64 && block_rows != 128) return KATTN_ERR_UNSUPPORTED;
+  if (page_rows > 0 && page_rows % block_rows != 0) return KATTN_ERR_INVALID_ARG;
+  return run_copy(static_cast<int8_t*>(k), k_scale, static_cast<int8_t*>(v), v_scale, Hkv, d, cap_rows,
+                  page_rows, block_rows, src, dst, n, count, workspace, workspace_bytes, stream);
+}
+
+int kattn_rope_table(const double* freq, int n_positions, int rot_dim, float* table, void* stream) {
+  if (n_positions < 0 || rot_dim < 1) return KATTN_ERR_INVALID_ARG;
+  if (rot_dim % 8 != 0 || rot_dim > kD) return KATTN_ERR_UNSUPPORTED;
+  if (n_positions == 0) return KATTN_OK;
+  if (!freq || !table) return KATTN_ERR_INVALID_ARG;
+  if (!aligned(freq, 8) || !aligned(table, 16)) return KATTN_ERR_MISALIGNED;
+  const cudaError_t e = launch_rope_table(freq, n_positions, rot_dim / 2, table, as_stream(stream));
+  return e == cudaSuccess ? KATTN_OK : KATTN_ERR_CUDA;
+}
+
+int kattn_rope(const void* x, int x_type, int n_rows, int n_heads, int d, int64_t x_stride,
+               const int32_t* positions, const float* table, int n_positions, int rot_dim,
+               int interleaved, void* out, int out_type, int64_t out_stride, void* stream) {
+  if (!is_dtype(x_type) || (out_type != x_type && out_type != KATTN_F32)) return KATTN_ERR_INVALID_ARG;
+  if (n_rows < 0 || n_heads < 0) return KATTN_ERR_INVALID_ARG;
   if (d != KATTN_HEAD_DIM) return KATTN_ERR_UNSUPPORTED;
-  const int st = check_page_rows(page_rows);
+  if ((int64_t)n_rows * ((n_heads + 3) / 4) > INT32_MAX) return KATTN_ERR_UNSUPPORTED;   // one grid axis
+  if (n_rows == 0 || n_heads == 0) return KATTN_OK;
+  int st = check_rope_table(table, n_positions, rot_dim, interleaved);
+  if (st == KATTN_OK) st = check_heads(x, x_type, x_stride, n_heads);
+  if (st == KATTN_OK) st = check_heads(out, out_type, out_stride, n_heads);
   if (st != KATTN_OK) return st;
-  if (cap_rows % page_rows != 0) return KATTN_ERR_INVALID_ARG;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < 256) return KATTN_ERR_WORKSPACE;
-  if (n == 0) return KATTN_OK;
-  if (!k || !k_scale || !v || !v_scale || !src || !dst) return KATTN_ERR_INVALID_ARG;
-  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_scale, 16) || !aligned(v_scale, 16) ||
-      !aligned(src, 4) || !aligned(dst, 4) || !aligned(count, 4))
-    return KATTN_ERR_MISALIGNED;
-  CopyParams p{};
-  p.k = k;
-  p.v = v;
-  p.k_scale = k_scale;
-  p.v_scale = v_scale;
-  p.Hkv = Hkv;
-  p.cap_rows = cap_rows;
-  p.page_rows = page_rows;
-  p.n_pages = cap_rows / page_rows;
-  p.n = n;
-  p.src = src;
-  p.dst = dst;
-  p.count = count;
-  p.err = static_cast<uint32_t*>(workspace);
-  return launch_copy_pages(p, as_stream(stream)) == cudaSuccess ? KATTN_OK : KATTN_ERR_CUDA;
+  if (x == out && (x_type != out_type || x_stride != out_stride)) return KATTN_ERR_INVALID_ARG;
+  if (!positions) return KATTN_ERR_INVALID_ARG;
+  if (!aligned(positions, 4)) return KATTN_ERR_MISALIGNED;
+  RopeParams p{};
+  p.x = x;
+  p.out = out;
+  p.x_stride = x_stride;
+  p.out_stride = out_stride;
+  p.positions = positions;
+  p.table = table;
+  p.rows = n_rows;
+  p.heads = n_heads;
+  p.n_positions = n_positions;
+  p.half = rot_dim / 2;
+  p.interleaved = interleaved;
+  return launch_rope(p, x_type, out_type, as_stream(stream)) == cudaSuccess ? KATTN_OK : KATTN_ERR_CUDA;
+}
+
+int kattn_append_blocks(const void* k_new, const void* v_new, int x_type, int n_rows, int n_kv, int d,
+                        int64_t k_stride, int64_t v_stride, const int32_t* cu_rows,
+                        const int32_t* start, int B, void* k, float* k_scale, void* v,
+                        float* v_scale, int code_type, int cap_rows, int block_rows,
+                        const int32_t* block_table, int max_pages, int page_rows,
+                        const float* table, int n_positions, int rot_dim, int interleaved,
+                        const void* q, int Hq, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  if (!is_dtype(x_type) || n_rows < 0 || B < 0 || B > 65535) return KATTN_ERR_INVALID_ARG;
+  if (d != KATTN_HEAD_DIM) return KATTN_ERR_UNSUPPORTED;
+  if (B == 0 || n_rows == 0) return KATTN_OK;
+  AppendParams p{};
+  int st = set_block_cache(p.c, k, k_scale, v, v_scale, code_type, n_kv, d, cap_rows, block_rows,
+                           block_table, max_pages, page_rows);
+  if (st == KATTN_OK) st = check_heads(k_new, x_type, k_stride, n_kv);
+  if (st == KATTN_OK) st = check_heads(v_new, x_type, v_stride, n_kv);
+  if (st == KATTN_OK && table) st = check_rope_table(table, n_positions, rot_dim, interleaved);
+  if (st != KATTN_OK) return st;
+  if ((q == nullptr) != (q_out == nullptr) || (q && !table)) return KATTN_ERR_INVALID_ARG;
+  if (q) {
+    if (Hq < 1) return KATTN_ERR_INVALID_ARG;
+    st = check_heads(q, x_type, q_stride, Hq);
+    if (st == KATTN_OK) st = check_heads(q_out, x_type, q_out_stride, Hq);
+    if (st != KATTN_OK) return st;
+    if (q == q_out && q_stride != q_out_stride) return KATTN_ERR_INVALID_ARG;
+  }
+  // one grid axis: the blocks of rows of every plane, and the queries
+  if (((int64_t)n_rows / block_rows + 2 * (int64_t)B) * 2 * n_kv + (int64_t)n_rows * ((Hq + 3) / 4) > INT32_MAX)
+    return KATTN_ERR_UNSUPPORTED;
+  st = set_spans(p.s, cu_rows, start, B, n_rows, workspace, workspace_bytes);
+  if (st != KATTN_OK) return st;
+  p.k_new = k_new;
+  p.v_new = v_new;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q = q;
+  p.q_out = q_out;
+  p.q_stride = q_stride;
+  p.q_out_stride = q_out_stride;
+  p.Hq = Hq;
+  p.table = table;
+  p.n_positions = n_positions;
+  p.half = table ? rot_dim / 2 : 0;
+  p.interleaved = table ? interleaved : 0;
+  const cudaError_t e = launch_append_blocks(p, x_type, code_type, as_stream(stream));
+  return e == cudaSuccess ? KATTN_OK : KATTN_ERR_CUDA;
+}
+
+int kattn_read_blocks(const void* k, const float* k_scale, const void* v, const float* v_scale,
+                      int code_type, int Hkv, int d, int cap_rows, int block_rows,
+                      const int32_t* block_table, int max_pages, int page_rows,
+                      const int32_t* cu_rows, const int32_t* start, int B, int n_rows, void* out_k,
+                      void* out_v, int out_type, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  if (!is_dtype(out_type) || n_rows < 0 || B < 0 || B > 65535) return KATTN_ERR_INVALID_ARG;
+  if (d != KATTN_HEAD_DIM) return KATTN_ERR_UNSUPPORTED;
+  if (B == 0 || n_rows == 0) return KATTN_OK;
+  ReadParams p{};
+  int st = set_block_cache(p.c, k, k_scale, v, v_scale, code_type, Hkv, d, cap_rows, block_rows,
+                           block_table, max_pages, page_rows);
+  if (st != KATTN_OK) return st;
+  if (!out_k && !out_v) return KATTN_ERR_INVALID_ARG;
+  if (!aligned(out_k, 16) || !aligned(out_v, 16)) return KATTN_ERR_MISALIGNED;
+  if (((int64_t)n_rows + 31) / 32 * 2 * Hkv > INT32_MAX) return KATTN_ERR_UNSUPPORTED;
+  st = set_spans(p.s, cu_rows, start, B, n_rows, workspace, workspace_bytes);
+  if (st != KATTN_OK) return st;
+  p.out_k = out_k;
+  p.out_v = out_v;
+  const cudaError_t e = launch_read_blocks(p, code_type, out_type, as_stream(stream));
+  return e == cudaSuccess ? KATTN_OK : KATTN_ERR_CUDA;
+}
+
+size_t kattn_blocks_workspace_size(int B, int M, int Hq, int max_ctx) {
+  if (B < 1 || M < 1 || M > KATTN_MAX_M || Hq < 1 || max_ctx < 1) return 0;
+  if ((int64_t)max_ctx + M - 1 > (int64_t)INT32_MAX / 2) return 0;    // as the call refuses it
+  return block_decode_workspace_bytes(B, M, Hq, max_ctx);
+}
+
+int kattn_decode_blocks(const void* q, int q_type, const void* k, const float* k_scale,
+                        const void* v, const float* v_scale, int code_type, int cap_rows,
+                        int block_rows, const int32_t* block_table, int max_pages, int page_rows,
+                        const int32_t* ctx_len, int B, int M, int Hq, int Hkv, int d, int max_ctx,
+                        float sm_scale, void* out, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  if (!is_dtype(q_type) || B < 0 || B > 65535 || M < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_ctx < 1)
+    return KATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(sm_scale)) return KATTN_ERR_INVALID_ARG;
+  if (d != KATTN_HEAD_DIM || M > KATTN_MAX_M || (Hq / Hkv) * M > KATTN_MAX_ROWS) return KATTN_ERR_UNSUPPORTED;
+  if ((int64_t)max_ctx + M - 1 > (int64_t)INT32_MAX / 2) return KATTN_ERR_INVALID_ARG;
+  if (B == 0) return KATTN_OK;
+  BlockDecodeParams p{};
+  const int st = set_block_cache(p.c, k, k_scale, v, v_scale, code_type, Hkv, d, cap_rows, block_rows,
+                                 block_table, max_pages, page_rows);
+  if (st != KATTN_OK) return st;
+  if (!q || !ctx_len || !out) return KATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(ctx_len, 4)) return KATTN_ERR_MISALIGNED;
+  p.q = q;
+  p.out = out;
+  p.q_type = q_type;
+  p.ctx_len = ctx_len;
+  p.B = B;
+  p.M = M;
+  p.Hq = Hq;
+  p.g = Hq / Hkv;
+  p.R = p.g * M;
+  p.max_ctx = max_ctx;
+  p.sm_scale = resolve_sm_scale(sm_scale, KATTN_HEAD_DIM);
+  if (block_decode_units(p) > (int64_t)INT32_MAX / 4) return KATTN_ERR_UNSUPPORTED;   // counted in int32
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < block_decode_workspace_bytes(B, M, Hq, max_ctx))
+    return KATTN_ERR_WORKSPACE;
+  set_block_decode_workspace(p, workspace);
+  const cudaError_t e = launch_decode_blocks(p, code_type, as_stream(stream));
+  return e == cudaSuccess ? KATTN_OK : KATTN_ERR_CUDA;
 }
 
 int kattn_get_device_status(void* workspace, size_t workspace_bytes, int* device_err,

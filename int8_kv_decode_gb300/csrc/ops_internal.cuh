@@ -85,6 +85,7 @@ struct CopyParams {
   int8_t *k, *v;
   float *k_scale, *v_scale;
   int Hkv, cap_rows, page_rows, n_pages, n;
+  int scale_shift;              // 2^scale_shift rows share a scale
   const int32_t *src, *dst, *count;
   uint32_t* err;
 };

@@ -619,7 +619,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyParams p) 
     const bool second = threadIdx.x >= kCopyThreads / 2;
     const int r0 = threadIdx.x & (kCopyThreads / 2 - 1);
     float* sc = second ? p.v_scale : p.k_scale;
-    for (int r = r0; r < p.page_rows; r += kCopyThreads / 2) sc[b + r] = __ldg(sc + a + r);
+    const int64_t sa = a >> p.scale_shift, sb = b >> p.scale_shift;
+    for (int r = r0; r < p.page_rows >> p.scale_shift; r += kCopyThreads / 2) sc[sb + r] = __ldg(sc + sa + r);
     int c = 0;
     for (; c + 2 * kCopyThreads <= vecs; c += 2 * kCopyThreads) {
       const uint4 k0 = __ldg(ks + c), k1 = __ldg(ks + c + kCopyThreads);

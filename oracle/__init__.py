@@ -29,6 +29,8 @@ Modules:
   diff       -- differential decode attention over pairs of heads and planes
   norm       -- residual addition, RMS norm and 8-bit row quantization
   pages      -- reserving, freeing, forking and compacting a cache's pages
+  blocks     -- rotary positions, and a cache with a scale per block of rows
+                and head: rows written, read and attended to
 
 Parity unpinned:
   * the absolute accuracy of the rounded-P modes against the infinitely
@@ -41,4 +43,4 @@ Parity unpinned:
 """
 
 from . import (quant, rounding, expf_tang, attention, hashdump, diff, norm,  # noqa: F401
-               pages)
+               pages, blocks)
