@@ -5,6 +5,7 @@
 // time: where new rows need a larger scale than the block has, the rows that stay are
 // coded again under the new one, code' = round(code * (s_old / s)).
 #include <algorithm>
+#include <type_traits>
 
 #include "blocks_internal.cuh"
 #include "rope_common.cuh"
@@ -31,19 +32,27 @@ __device__ __forceinline__ int warp_find(int n, int64_t t, int lane, Key key) {
 __device__ __forceinline__ int64_t table_keys(const BlockCache& c) {
   return min((int64_t)c.max_pages << c.page_shift, (int64_t)1 << 30);
 }
-// Whether sequence b's rows lie in the call's and its keys in the table's pages.
-__device__ __forceinline__ bool span_valid(const SpanParams& s, int b, int64_t most) {
+// The rows of sequence b and its first key; whether the rows lie in the call's and the
+// keys in the table's row.
+struct Span {
+  int c0, n, start;
+  bool valid;
+};
+__device__ __forceinline__ Span span_of(const SpanParams& s, int b, int64_t most) {
   const int c0 = __ldg(s.cu + b), c1 = __ldg(s.cu + b + 1), st = __ldg(s.start + b);
-  return c0 >= 0 && c0 <= c1 && c1 <= s.rows && st >= 0 && (int64_t)st + (c1 - c0) <= most;
+  const bool rises = c0 >= 0 && c0 <= c1 && c1 <= s.rows;
+  return {c0, rises ? c1 - c0 : 0, st, rises && st >= 0 && (int64_t)st + (c1 - c0) <= most};
 }
 __device__ __forceinline__ void flag_bad_spans(const SpanParams& s, int64_t most) {
   for (int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; b < s.B; b += (int64_t)gridDim.x * blockDim.x)
-    if (!span_valid(s, (int)b, most)) atomicOr(s.err, KATTN_DEVERR_BAD_SEQUENCE);
+    if (!span_of(s, (int)b, most).valid) atomicOr(s.err, KATTN_DEVERR_BAD_SEQUENCE);
 }
 
-// Row in its plane of key `key` of sequence b; -1 (flagged) where its page is not one.
-__device__ __forceinline__ int row_of_key(const BlockCache& c, uint32_t* err, int b, int key) {
-  const int page = __ldg(c.block_table + (int64_t)b * c.max_pages + (key >> c.page_shift));
+// Row in its plane of key `key`, by its page; -1 (flagged) where that is not one.
+__device__ __forceinline__ int page_of_key(const BlockCache& c, int b, int key) {
+  return __ldg(c.block_table + (int64_t)b * c.max_pages + (key >> c.page_shift));
+}
+__device__ __forceinline__ int row_of_key(const BlockCache& c, uint32_t* err, int page, int key) {
   if ((unsigned)page >= (unsigned)c.n_pages) {
     atomicOr(err, KATTN_DEVERR_BAD_PAGE);
     return -1;
@@ -51,13 +60,32 @@ __device__ __forceinline__ int row_of_key(const BlockCache& c, uint32_t* err, in
   return (page << c.page_shift) | (key & ((1 << c.page_shift) - 1));
 }
 
+// The four codes of a word as float32 values, exact.
+template <bool kE4m3>
+__device__ __forceinline__ void code_values(uint32_t w, float* f) {
+  if constexpr (kE4m3) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * i)), __NV_E4M3);
+      const float2 v = __half22float2(__half2(h));
+      f[2 * i] = v.x;
+      f[2 * i + 1] = v.y;
+    }
+  } else {
+    w ^= 0x80808080u;                             // code + 128 as the low mantissa bits of 2^23
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      f[e] = __fsub_rn(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440u | e)), 8388736.0f);
+  }
+}
+
 // ----------------------------------------------------------------- append
 // One block of threads per (block of rows that a sequence touches, head, K or V): a
-// warp holds 8 of its rows in registers, a lane four channels of each.  The blocks
-// that sequence b touches are the units floor(cu[b] / R) + 2 b + j: at most floor(n / R)
-// + 2 for its n rows, so units of different sequences never meet, and the grid is known
+// warp holds 8 of its rows in registers, two at a time, a lane eight channels of each.  The
+// blocks that sequence b touches are the units floor(cu[b] / R) + 2 b + j: at most floor(n /
+// R) + 2 for its n rows, so units of different sequences never meet, and the grid is known
 // without the lengths.  Queries, if any, are turned by further blocks of threads.
-constexpr int kRowsPerWarp = 8, kQHeads = 4;
+constexpr int kRowsPerWarp = 8;
 
 template <typename T, int kBlock, bool kE4m3, bool kInter>
 __global__ void __launch_bounds__(kBlock * 4) append_kernel(const AppendParams p, const unsigned kv_blocks) {
@@ -67,73 +95,71 @@ __global__ void __launch_bounds__(kBlock * 4) append_kernel(const AppendParams p
   const int R = kBlock;
   int64_t most = table_keys(p.c);
   if (p.table) most = min(most, (int64_t)p.n_positions);
-  flag_bad_spans(p.s, most);
+  if ((int64_t)blockIdx.x * blockDim.x < p.s.B) flag_bad_spans(p.s, most);
 
-  if (blockIdx.x >= kv_blocks) {                  // ---- queries: a warp takes four heads of a row
-    const int groups = (p.Hq + kQHeads - 1) / kQHeads;
+  if (blockIdx.x >= kv_blocks) {                  // ---- queries: a warp takes heads of a row
+    const int groups = (p.Hq + kTurnHeads - 1) / kTurnHeads;
     const int64_t item = (int64_t)(blockIdx.x - kv_blocks) * kWarps + warp;
-    const int row = (int)(item / groups), h0 = (int)(item - (int64_t)row * groups) * kQHeads;
+    const int row = (int)(item / groups), h0 = (int)(item - (int64_t)row * groups) * kTurnHeads;
     if (row >= p.s.rows) return;
-    const int n = min(kQHeads, p.Hq - h0);
-    const T* x = static_cast<const T*>(p.q) + row * p.q_stride + h0 * kD + 4 * lane;
-    T* y = static_cast<T*>(p.q_out) + row * p.q_out_stride + h0 * kD + 4 * lane;
-    Vec<T, 4> raw[kQHeads];
-#pragma unroll
-    for (int i = 0; i < kQHeads; ++i)
-      if (i < n) raw[i] = *reinterpret_cast<const Vec<T, 4>*>(x + i * kD);
-    const int b = warp_find(p.s.B, row, lane, [&](int i) { return (int64_t)__ldg(p.s.cu + i); });
-    if (row < __ldg(p.s.cu + b) || row >= __ldg(p.s.cu + b + 1)) return;     // no sequence's row
-    const bool ok = span_valid(p.s, b, most);
-    const int position = ok ? __ldg(p.s.start + b) + row - __ldg(p.s.cu + b) : 0;
-    const Turn t = load_turn<kInter>(p.table, position, p.half, lane);
-#pragma unroll
-    for (int i = 0; i < kQHeads; ++i) {
-      if (i >= n) break;
-      float f[4];
-      unpack(raw[i], f);
-      turn<kInter>(t, f);
-      if (!ok) f[0] = f[1] = f[2] = f[3] = __int_as_float(0x7fc00000);
-      *reinterpret_cast<Vec<T, 4>*>(y + i * kD) = pack<T, 4>(f);
-    }
+    turn_heads<T, T, kInter>(static_cast<const T*>(p.q) + row * p.q_stride + h0 * kD,
+                             static_cast<T*>(p.q_out) + row * p.q_out_stride + h0 * kD,
+                             min(kTurnHeads, p.Hq - h0), p.table, p.half, lane, [&](bool& know) {
+      const int b = warp_find(p.s.B, row, lane, [&](int i) { return (int64_t)__ldg(p.s.cu + i); });
+      const int c0 = __ldg(p.s.cu + b), c1 = __ldg(p.s.cu + b + 1);
+      const Span s = span_of(p.s, b, most);
+      know = s.valid;
+      return row < c0 || row >= c1 ? -1 : know ? s.start + row - c0 : 0;     // (-1: no sequence's row)
+    });
     return;
   }
 
   // ---- the unit: sequence b, its j-th touched block, head h of K or V
-  const int64_t unit = blockIdx.x / (2 * p.c.Hkv);
-  const int plane = blockIdx.x - (unsigned)unit * (2 * p.c.Hkv);
+  const unsigned unit = blockIdx.x / (2u * p.c.Hkv);
+  const int plane = (int)(blockIdx.x - unit * (2u * p.c.Hkv));
   const bool is_k = plane < p.c.Hkv;
   const int h = is_k ? plane : plane - p.c.Hkv;
   const int b = warp_find(p.s.B, unit, lane, [&](int i) { return (int64_t)(__ldg(p.s.cu + i) / R) + 2 * i; });
-  if (!span_valid(p.s, b, most)) return;
-  const int c0 = __ldg(p.s.cu + b), n = __ldg(p.s.cu + b + 1) - c0, st = __ldg(p.s.start + b);
-  const int64_t j = unit - (c0 / R + 2 * (int64_t)b);
-  if (n == 0 || j < 0 || j > (st + n - 1) / R - st / R) return;
+  const Span span = span_of(p.s, b, most);
+  if (!span.valid || span.n == 0) return;
+  const int st = span.start, n = span.n;
+  const int64_t j = (int64_t)unit - (span.c0 / R + 2 * (int64_t)b);
+  if (j < 0 || j > (st + n - 1) / R - st / R) return;
   const int key0 = (st / R + (int)j) * R;         // the block's keys: [key0, key0 + R)
-  const int row0 = row_of_key(p.c, p.s.err, b, key0);
-  if (row0 < 0) return;
+  const int page = page_of_key(p.c, b, key0);     // (looked at after the rows' loads)
   const int lo = max(st - key0, 0), hi = min(st + n - key0, R);    // its new rows: [lo, hi)
-  uint8_t* codes = (is_k ? p.c.k : p.c.v) + ((int64_t)h * p.c.cap_rows + row0) * kD + 4 * lane;
-  float* scale = (is_k ? p.c.k_scale : p.c.v_scale) + (((int64_t)h * p.c.cap_rows + row0) >> p.c.block_shift);
-  const float was = lo > 0 ? *scale : 0.0f;       // (read by every thread before the barrier below)
 
   const int64_t stride = is_k ? p.k_stride : p.v_stride;
-  const T* x = static_cast<const T*>(is_k ? p.k_new : p.v_new) + (int64_t)h * kD + 4 * lane;
-  const int r0 = warp * kRowsPerWarp;
-  Vec<T, 4> raw[kRowsPerWarp];
+  const bool turns_k = is_k && p.table != nullptr;
+  const int l = lane & 15, side = lane >> 4;
+  const Runs run = lane_runs<kInter>(turns_k ? p.half : 0, l);
+  const T* x = static_cast<const T*>(is_k ? p.k_new : p.v_new) + (int64_t)(span.c0 + key0 - st) * stride + h * kD;
+  const int r0 = warp * kRowsPerWarp;             // row r0 + 2 i + side of the block in step i
+  Vec<T, 4> ra[kRowsPerWarp / 2], rb[kRowsPerWarp / 2];
 #pragma unroll
-  for (int i = 0; i < kRowsPerWarp; ++i) {
-    raw[i] = Vec<T, 4>{};
-    if (r0 + i >= lo && r0 + i < hi)
-      raw[i] = *reinterpret_cast<const Vec<T, 4>*>(x + (int64_t)(c0 + key0 - st + r0 + i) * stride);
+  for (int i = 0; i < kRowsPerWarp / 2; ++i) {
+    const int r = r0 + 2 * i + side;
+    ra[i] = rb[i] = Vec<T, 4>{};
+    if (r >= lo && r < hi) {
+      ra[i] = *reinterpret_cast<const Vec<T, 4>*>(x + r * stride + run.a);
+      rb[i] = *reinterpret_cast<const Vec<T, 4>*>(x + r * stride + run.b);
+    }
   }
-  float f[kRowsPerWarp][4], amax = 0.0f;
+  const int row0 = row_of_key(p.c, p.s.err, page, key0);
+  if (row0 < 0) return;
+  uint8_t* codes = (is_k ? p.c.k : p.c.v) + ((int64_t)h * p.c.cap_rows + row0) * kD;
+  float* scale = (is_k ? p.c.k_scale : p.c.v_scale) + (((int64_t)h * p.c.cap_rows + row0) >> p.c.block_shift);
+  const float was = lo > 0 ? *scale : 0.0f;       // (read by every thread before the barrier below)
+  float fa[kRowsPerWarp / 2][4], fb[kRowsPerWarp / 2][4], amax = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kRowsPerWarp; ++i) {
-    unpack(raw[i], f[i]);
-    if (is_k && p.table && r0 + i >= lo && r0 + i < hi)
-      turn<kInter>(load_turn<kInter>(p.table, key0 + r0 + i, p.half, lane), f[i]);
+  for (int i = 0; i < kRowsPerWarp / 2; ++i) {
+    const int r = r0 + 2 * i + side;
+    unpack(ra[i], fa[i]);
+    unpack(rb[i], fb[i]);
+    if (turns_k && run.turns && r >= lo && r < hi)
+      turn<kInter>(load_angles(p.table, key0 + r, p.half, l), fa[i], fb[i]);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(f[i][e]));
+    for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(fa[i][e]), fabsf(fb[i][e])));
   }
   amax = warp_max_abs(amax);
   if (lane == 0) s_max[warp] = amax;
@@ -144,17 +170,19 @@ __global__ void __launch_bounds__(kBlock * 4) append_kernel(const AppendParams p
   if (threadIdx.x == 0) *scale = s;
   const float inv = __frcp_rn(s);
 #pragma unroll
-  for (int i = 0; i < kRowsPerWarp; ++i) {
-    if (r0 + i < lo || r0 + i >= hi) continue;
-    const Codes<4> c = codes_of(f[i], s, inv, kE4m3);
-    *reinterpret_cast<Codes<4>*>(codes + (r0 + i) * kD) = c;
+  for (int i = 0; i < kRowsPerWarp / 2; ++i) {
+    const int r = r0 + 2 * i + side;
+    if (r < lo || r >= hi) continue;
+    const Codes<4> ca = codes_of(fa[i], s, inv, kE4m3), cb = codes_of(fb[i], s, inv, kE4m3);
+    *reinterpret_cast<Codes<4>*>(codes + r * kD + run.a) = ca;
+    *reinterpret_cast<Codes<4>*>(codes + r * kD + run.b) = cb;
   }
   if (r0 < lo && s > was) {                       // the rows that stay, under the larger scale
     const float by = __fdiv_rn(was, s);
     uint32_t old[kRowsPerWarp];
 #pragma unroll
     for (int i = 0; i < kRowsPerWarp; ++i)
-      old[i] = r0 + i < lo ? *reinterpret_cast<const uint32_t*>(codes + (r0 + i) * kD) : 0u;
+      old[i] = r0 + i < lo ? *reinterpret_cast<const uint32_t*>(codes + (r0 + i) * kD + 4 * lane) : 0u;
 #pragma unroll
     for (int i = 0; i < kRowsPerWarp; ++i) {
       if (r0 + i >= lo) break;
@@ -171,69 +199,81 @@ __global__ void __launch_bounds__(kBlock * 4) append_kernel(const AppendParams p
         }
         w |= (uint32_t)again << (8 * e);
       }
-      *reinterpret_cast<uint32_t*>(codes + (r0 + i) * kD) = w;
+      *reinterpret_cast<uint32_t*>(codes + (r0 + i) * kD + 4 * lane) = w;
     }
   }
 }
 
 // ------------------------------------------------------------------- read
-// A warp takes 32 rows of one head of K or V: eight lanes a row, 16 codes a lane, in
-// steps of four rows; lane i looks row i up first.
+// A warp looks 32 rows up, one a lane, and takes them from one of the 2 Hkv planes of K and
+// V: all their codes are loaded before the first become values.  A lane takes as many codes
+// of a row as make a 16-byte store, so that loads and stores of a row are whole.  The warps
+// of a block take the planes of the same rows, whose values lie side by side.
 template <typename O, bool kE4m3>
-__global__ void __launch_bounds__(256) read_kernel(const ReadParams p) {
+__global__ void __launch_bounds__(256, 4) read_kernel(const ReadParams p) {
+  constexpr int kPer = 16 / sizeof(O), kLanes = kD / kPer;       // codes a lane, lanes a row
+  constexpr int kRows = 32 / kLanes, kLoads = 32 / kRows;        // rows a load, loads
+  using Raw = typename std::conditional<kPer == 8, uint2, uint32_t>::type;
   const int lane = threadIdx.x & 31;
-  const int planes = 2 * p.c.Hkv;
   const int64_t most = table_keys(p.c);
-  flag_bad_spans(p.s, most);
+  if ((int64_t)blockIdx.x * blockDim.x < p.s.B) flag_bad_spans(p.s, most);
+  const int planes = (p.out_k ? p.c.Hkv : 0) + (p.out_v ? p.c.Hkv : 0);
   const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int tile = (int)(item / planes), plane = (int)(item - (int64_t)tile * planes);
   const int64_t first = (int64_t)tile * 32;
   if (first >= p.s.rows) return;
-  const bool is_k = plane < p.c.Hkv;
-  const int h = is_k ? plane : plane - p.c.Hkv;
-  O* out = static_cast<O*>(is_k ? p.out_k : p.out_v);
-  if (!out) return;
+  const bool is_k = p.out_k && plane < p.c.Hkv;
+  const int h = plane - (p.out_k && plane >= p.c.Hkv ? p.c.Hkv : 0);
   const int64_t base = (int64_t)h * p.c.cap_rows;
+
+  // ---- lane i: row first + i.  Its sequence is among those from b0 on; 32 of them are
+  // looked at together.
   int row = -1;
-  float sc = 0.0f;
   {
-    const int64_t r = first + lane;
-    int b = warp_find(p.s.B, first, lane, [&](int i) { return (int64_t)__ldg(p.s.cu + i); });
+    const int b0 = warp_find(p.s.B, first, lane, [&](int i) { return (int64_t)__ldg(p.s.cu + i); });
+    const int r = (int)min(first + lane, (int64_t)INT32_MAX);
+    const int ends = b0 + 1 + lane <= p.s.B ? __ldg(p.s.cu + b0 + 1 + lane) : INT32_MAX;
+    int k = 0;                                    // ends up to the row, by halving
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      const int e = __shfl_sync(0xffffffffu, ends, k + d - 1);
+      if (e <= r) k += d;
+    }
+    if (__shfl_sync(0xffffffffu, ends, k) <= r) ++k;       // (k = 31: none of the 32 is past it)
+    int b = min(b0 + k, p.s.B - 1);
     while (b + 1 < p.s.B && r >= __ldg(p.s.cu + b + 1)) ++b;
-    if (r < p.s.rows && r >= __ldg(p.s.cu + b) && r < __ldg(p.s.cu + b + 1) && span_valid(p.s, b, most)) {
-      row = row_of_key(p.c, p.s.err, b, __ldg(p.s.start + b) + (int)r - __ldg(p.s.cu + b));
-      if (row >= 0) sc = __ldg((is_k ? p.c.k_scale : p.c.v_scale) + ((base + row) >> p.c.block_shift));
+    const Span s = span_of(p.s, b, most);
+    if (first + lane < p.s.rows && s.valid && r >= s.c0 && r < s.c0 + s.n) {
+      const int key = s.start + r - s.c0;
+      row = row_of_key(p.c, p.s.err, page_of_key(p.c, b, key), key);
     }
   }
-  const uint8_t* codes = (is_k ? p.c.k : p.c.v) + base * kD + 16 * (lane & 7);
-  uint4 raw[8];
+  const int col = (lane % kLanes) * kPer, sub = lane / kLanes;
+  const uint8_t* codes = (is_k ? p.c.k : p.c.v) + base * kD + col;
+  Raw raw[kLoads];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int at = __shfl_sync(0xffffffffu, row, 4 * i + (lane >> 3));
-    raw[i] = make_uint4(0, 0, 0, 0);
-    if (at >= 0) raw[i] = __ldg(reinterpret_cast<const uint4*>(codes + (int64_t)at * kD));
+  for (int i = 0; i < kLoads; ++i) {
+    const int at = __shfl_sync(0xffffffffu, row, i * kRows + sub);
+    raw[i] = Raw{};
+    if (at >= 0) raw[i] = __ldg(reinterpret_cast<const Raw*>(codes + (int64_t)at * kD));
   }
+  const float sc = row >= 0 ? __ldg((is_k ? p.c.k_scale : p.c.v_scale) + ((base + row) >> p.c.block_shift)) : 0.0f;
+  O* y = static_cast<O*>(is_k ? p.out_k : p.out_v) + (first * p.c.Hkv + h) * kD + col;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int src = 4 * i + (lane >> 3);
+  for (int i = 0; i < kLoads; ++i) {
+    const int src = i * kRows + sub;
     const float s = __shfl_sync(0xffffffffu, sc, src);
     const bool in = __shfl_sync(0xffffffffu, row, src) >= 0;
-    O* y = out + ((first + src) * p.c.Hkv + h) * kD + 16 * (lane & 7);
-    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-    constexpr int kPer = 16 / sizeof(O);          // values of a 16-byte store
-#pragma unroll
-    for (int v = 0; v < 16; v += kPer) {
-      float f[kPer];
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        const uint8_t byte = (uint8_t)(w[(v + e) / 4] >> (8 * ((v + e) % 4)));
-        float c;
-        if constexpr (kE4m3) c = __half2float(__half(__nv_cvt_fp8_to_halfraw(byte, __NV_E4M3)));
-        else c = (float)(int8_t)byte;
-        f[e] = __fmul_rn(c, s);
-      }
-      if (in) *reinterpret_cast<Vec<O, kPer>*>(y + v) = pack<O, kPer>(f);
+    float f[kPer];
+    if constexpr (kPer == 8) {
+      code_values<kE4m3>(raw[i].x, f);
+      code_values<kE4m3>(raw[i].y, f + 4);
+    } else {
+      code_values<kE4m3>(raw[i], f);
     }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) f[e] = __fmul_rn(f[e], s);
+    if (in) *reinterpret_cast<Vec<O, kPer>*>(y + (int64_t)src * p.c.Hkv * kD) = pack<O, kPer>(f);
   }
 }
 
@@ -243,7 +283,7 @@ cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
   int64_t blocks = kv;
   if (p.q) {
     constexpr int kWarps = kBlock / kRowsPerWarp;
-    const int64_t items = (int64_t)p.s.rows * ((p.Hq + kQHeads - 1) / kQHeads);
+    const int64_t items = (int64_t)p.s.rows * ((p.Hq + kTurnHeads - 1) / kTurnHeads);
     blocks += (items + kWarps - 1) / kWarps;
   }
   if (p.interleaved) append_kernel<T, kBlock, kE4m3, true><<<(unsigned)blocks, kBlock * 4, 0, stream>>>(p, (unsigned)kv);
@@ -264,7 +304,8 @@ cudaError_t launch_append(const AppendParams& p, int code_type, cudaStream_t str
 }
 template <typename O>
 cudaError_t launch_read(const ReadParams& p, int code_type, cudaStream_t stream) {
-  const int64_t items = ((int64_t)p.s.rows + 31) / 32 * 2 * p.c.Hkv;
+  const int planes = (p.out_k ? p.c.Hkv : 0) + (p.out_v ? p.c.Hkv : 0);
+  const int64_t items = ((int64_t)p.s.rows + 31) / 32 * planes;
   const unsigned blocks = (unsigned)((items + 7) / 8);
   if (code_type == KATTN_E4M3) read_kernel<O, true><<<blocks, 256, 0, stream>>>(p);
   else read_kernel<O, false><<<blocks, 256, 0, stream>>>(p);

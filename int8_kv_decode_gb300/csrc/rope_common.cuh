@@ -1,5 +1,5 @@
-// Rotation of a head's channels by their position's angles: four channels a lane, a
-// head of 128 channels a warp.
+// Rotation of a head's channels by their position's angles: sixteen lanes a head, eight
+// channels a lane in two runs of four, so that both channels of a pair are the lane's.
 #pragma once
 
 #include "quant_common.cuh"
@@ -7,64 +7,87 @@
 namespace kattn {
 namespace {
 
-// The angles of a lane's channels 4 lane .. 4 lane + 3, for one position.
-//   half layout: channel i < half turns with channel i + half, by angle i.  half is a
-//     multiple of 4, so the partner's four channels are those of one lane.
-//   interleaved: channels 2i and 2i + 1 turn by angle i.
-struct Turn {
-  float c[4], s[4];
-  int partner;                    // lane of the partner's channels (half layout)
-  bool turns;                     // these channels are rotated
+// Where the two runs of lane l (of 16) begin, and whether its channels are rotated.
+//   half layout: channel i < half turns with channel i + half, by angle i: the runs are
+//     4l and 4l + half.  half is a multiple of 4; the lanes past the last pair hold the
+//     channels behind 2 half.
+//   interleaved: channels 2i and 2i + 1 turn by angle i: eight channels in a row.
+// In both layouts the lane's angles are 4l .. 4l + 3.
+struct Runs {
+  int a, b;
+  bool turns;
 };
 template <bool kInter>
-__device__ __forceinline__ Turn load_turn(const float* __restrict__ table, int position, int half, int lane) {
-  Turn t;
-  const int lanes = half >> 2;                    // that hold the first of each pair (half layout)
-  t.turns = lane < 2 * lanes;
-  t.partner = lane;
-  const float* at = table + (int64_t)position * half * 2;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    t.c[e] = 1.0f;
-    t.s[e] = 0.0f;
-  }
-  if (!t.turns) return t;
-  if constexpr (kInter) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(at) + lane);
-    t.c[0] = t.c[1] = a.x;
-    t.c[2] = t.c[3] = a.z;
-    t.s[0] = -a.y;
-    t.s[1] = a.y;
-    t.s[2] = -a.w;
-    t.s[3] = a.w;
-  } else {
-    const bool first = lane < lanes;
-    t.partner = first ? lane + lanes : lane - lanes;
-    const float4* v = reinterpret_cast<const float4*>(at) + 2 * (first ? lane : lane - lanes);
-    const float4 a = __ldg(v), b = __ldg(v + 1);
-    t.c[0] = a.x;
-    t.c[1] = a.z;
-    t.c[2] = b.x;
-    t.c[3] = b.z;
-    t.s[0] = first ? -a.y : a.y;
-    t.s[1] = first ? -a.w : a.w;
-    t.s[2] = first ? -b.y : b.y;
-    t.s[3] = first ? -b.w : b.w;
-  }
-  return t;
+__device__ __forceinline__ Runs lane_runs(int half, int l) {
+  const int lanes = half >> 2;
+  Runs r;
+  r.turns = l < lanes;
+  r.a = kInter || !r.turns ? 8 * l : 4 * l;       // (8 lanes + 8 (l - lanes) behind the last pair)
+  r.b = kInter || !r.turns ? 8 * l + 4 : 4 * l + half;
+  return r;
 }
 
-// f: the lane's channels, turned in place.  Each product and sum is rounded on its
-// own (a - b s is a + b (-s) to the bit), so that the result, and the 8-bit codes
-// made of it, are those of the formula in float32.
+struct Angles {
+  float2 a[4];                                    // (cos, sin)
+};
+__device__ __forceinline__ Angles load_angles(const float* __restrict__ table, int position, int half, int l) {
+  const float4* at = reinterpret_cast<const float4*>(table + (int64_t)position * half * 2) + 2 * l;
+  const float4 x = __ldg(at), y = __ldg(at + 1);
+  return {{make_float2(x.x, x.y), make_float2(x.z, x.w), make_float2(y.x, y.y), make_float2(y.z, y.w)}};
+}
+
+// A pair (x, y) turned.  Each product and sum is rounded on its own, so that the result,
+// and the 8-bit codes made of it, are those of the formula in float32.
+__device__ __forceinline__ void turn_pair(float& x, float& y, float2 a) {
+  const float u = __fsub_rn(__fmul_rn(x, a.x), __fmul_rn(y, a.y));
+  y = __fadd_rn(__fmul_rn(y, a.x), __fmul_rn(x, a.y));
+  x = u;
+}
 template <bool kInter>
-__device__ __forceinline__ void turn(const Turn& t, float (&f)[4]) {
-  float o[4];
+__device__ __forceinline__ void turn(const Angles& t, float (&a)[4], float (&b)[4]) {
+  if constexpr (kInter) {
+    turn_pair(a[0], a[1], t.a[0]);
+    turn_pair(a[2], a[3], t.a[1]);
+    turn_pair(b[0], b[1], t.a[2]);
+    turn_pair(b[2], b[3], t.a[3]);
+  } else {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) o[e] = kInter ? f[e ^ 1] : __shfl_sync(0xffffffffu, f[e], t.partner);
-  if (!t.turns) return;
+    for (int e = 0; e < 4; ++e) turn_pair(a[e], b[e], t.a[e]);
+  }
+}
+
+// Heads of one row, turned by a warp: the heads 2 i + (lane / 16) below n, all loaded
+// before the first is turned.  x, y: the row's first of these heads.  know: its position
+// has angles (else NaN).
+constexpr int kTurnHeads = 8;
+template <typename T, typename O, bool kInter, typename Position>
+__device__ __forceinline__ void turn_heads(const T* x, O* y, int n, const float* table, int half, int lane,
+                                           Position position) {
+  const int l = lane & 15, side = lane >> 4;
+  const Runs r = lane_runs<kInter>(half, l);
+  Vec<T, 4> ra[kTurnHeads / 2], rb[kTurnHeads / 2];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) f[e] = __fadd_rn(__fmul_rn(f[e], t.c[e]), __fmul_rn(o[e], t.s[e]));
+  for (int i = 0; i < kTurnHeads / 2; ++i)
+    if (2 * i + side < n) {
+      ra[i] = *reinterpret_cast<const Vec<T, 4>*>(x + (2 * i + side) * kD + r.a);
+      rb[i] = *reinterpret_cast<const Vec<T, 4>*>(x + (2 * i + side) * kD + r.b);
+    }
+  bool know;
+  const int at = position(know);                  // (its loads go beside those of the row)
+  if (at < 0) return;
+  Angles t;
+  if (r.turns) t = load_angles(table, at, half, l);
+#pragma unroll
+  for (int i = 0; i < kTurnHeads / 2; ++i) {
+    if (2 * i + side >= n) break;
+    float a[4], b[4];
+    unpack(ra[i], a);
+    unpack(rb[i], b);
+    if (r.turns) turn<kInter>(t, a, b);
+    if (!know) a[0] = a[1] = a[2] = a[3] = b[0] = b[1] = b[2] = b[3] = __int_as_float(0x7fc00000);
+    *reinterpret_cast<Vec<O, 4>*>(y + (2 * i + side) * kD + r.a) = pack<O, 4>(a);
+    *reinterpret_cast<Vec<O, 4>*>(y + (2 * i + side) * kD + r.b) = pack<O, 4>(b);
+  }
 }
 
 }  // namespace
