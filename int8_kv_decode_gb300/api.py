@@ -468,6 +468,25 @@ def _launch(name, index, *args):
         _lib.check(name, status)
 
 
+_plain = None        # the compiled calls (bind.cpp), once loaded
+
+
+def _load_plain():
+    """The module of the calls whose every argument is plainly right; each returns the
+    library's status, or None for a call that the checks here have to look at."""
+    global _plain
+    try:
+        from . import _bind
+    except ImportError as e:
+        raise RuntimeError("the binding module is missing or of another build: build it first "
+                           "(python -c 'import __graft_entry__ as g; g.build()')") from e
+    lib = _lib.load()
+    _bind.setup(*(ctypes.cast(getattr(lib, "kattn_" + n), ctypes.c_void_p).value
+                  for n in ("rope", "append_blocks", "read_blocks", "decode_blocks")))
+    _plain = _bind
+    return _bind
+
+
 def diff_workspace_size(B: int, M: int, Hq: int, max_ctx: int) -> int:
     return int(_lib.load().kattn_diff_workspace_size(B, M, Hq, max_ctx))
 
@@ -739,6 +758,12 @@ def rope(x, positions, table, *, interleaved: bool = False, out=None, out_dtype=
     (out's, or out_dtype); out may be x.  Rows of negative positions are not written,
     those past the table are NaN.  (kattn_rope)
     """
+    if out is not None:
+        status = (_plain or _load_plain()).rope(x, positions, table, interleaved, out)
+        if status is not None:
+            if status:
+                _lib.check("kattn_rope", status)
+            return out
     index = _device_of(x, "x")
     x_type = _NORM_TYPES.get(x.dtype)
     if x_type is None:
@@ -807,6 +832,14 @@ def append_blocks(k_new, v_new, cu_rows, start, k, k_scale, v, v_scale, block_ta
     q).  workspace: any workspace of the library, for the error bits.
     (kattn_append_blocks)
     """
+    if workspace is not None and (q is None or q_out is not None):
+        status = (_plain or _load_plain()).append_blocks(
+            k_new, v_new, cu_rows, start, k, k_scale, v, v_scale, block_table, page_rows, table, interleaved,
+            q, q_out, workspace)
+        if status is not None:
+            if status:
+                _lib.check("kattn_append_blocks", status)
+            return q_out
     index = _device_of(k_new, "k_new")
     dtype = k_new.dtype
     x_type = _NORM_TYPES.get(dtype)
@@ -851,6 +884,13 @@ def read_blocks(k, k_scale, v, v_scale, block_table, page_rows: int, cu_rows, st
     written.  dtype: float32, bfloat16 or float16.  The rest as append_blocks().
     (kattn_read_blocks)
     """
+    if out_k is not None and out_v is not None and workspace is not None:
+        status = (_plain or _load_plain()).read_blocks(
+            k, k_scale, v, v_scale, block_table, page_rows, cu_rows, start, n_rows, out_k, out_v, workspace)
+        if status is not None:
+            if status:
+                _lib.check("kattn_read_blocks", status)
+            return out_k, out_v
     index = _device_of(k, "k")
     code, Hkv, cap, d, block_rows = _block_cache(k, k_scale, v, v_scale, index)
     B = _spans(cu_rows, start, block_table, index)
@@ -903,6 +943,13 @@ def decode_blocks(q, k, k_scale, v, v_scale, block_table, page_rows: int, ctx_le
     blocks_workspace_size(...) bytes, its first 256 zeroed before its first use,
     allocated here with torch if None.  (kattn_decode_blocks)
     """
+    if out is not None and workspace is not None:
+        status = (_plain or _load_plain()).decode_blocks(
+            q, k, k_scale, v, v_scale, block_table, page_rows, ctx_len, max_ctx, out, sm_scale, workspace)
+        if status is not None:
+            if status:
+                _lib.check("kattn_decode_blocks", status)
+            return out
     index = _device_of(q, "q")
     q_type = _NORM_TYPES.get(q.dtype)
     if q_type is None:

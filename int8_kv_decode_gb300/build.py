@@ -83,8 +83,48 @@ def _run(cmd, verbose):
     return r.stdout
 
 
+# The checks and calls of the block-scaled operators in one step from Python (bind.cpp), a
+# module against the torch and Python that run this; the stamp names them.
+BIND = os.path.join(PKG, "_bind.so")
+_STAMP = os.path.join(BUILD, "bind.stamp")
+
+
+def _bind_stamp() -> str:
+    import torch
+    return f"{sys.version} {torch.__version__} {torch.__file__}"
+
+
+def _bind_stale() -> bool:
+    if _stale(BIND, [os.path.join(CSRC, "bind.cpp"), os.path.join(INCLUDE, "kattn.h"), __file__]):
+        return True
+    try:
+        with open(_STAMP, encoding="utf-8") as f:
+            return f.read() != _bind_stamp()
+    except OSError:
+        return True
+
+
+def _build_bind(verbose: bool) -> None:
+    import sysconfig
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    lib = os.path.join(base, "lib")
+    tmp = BIND + ".tmp"
+    cmd = ["g++", "-shared", "-O2", "-std=c++17", "-fPIC", os.path.join(CSRC, "bind.cpp"), "-o", tmp,
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", os.path.join(base, "include"),
+           "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
+           "-lc10"]
+    _run(cmd, verbose)
+    os.replace(tmp, BIND)
+    with open(_STAMP, "w", encoding="utf-8") as f:
+        f.write(_bind_stamp())
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Compile and link libkattn.so; returns its path.  Rebuilds what is stale."""
+    """Compile and link libkattn.so and the binding module; returns the library's path.
+    Rebuilds what is stale."""
     nvcc = nvcc_path()
     os.makedirs(BUILD, exist_ok=True)
     headers = _headers()
@@ -100,9 +140,13 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
     outputs = []
-    if jobs:
-        with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
+    bind = force or _bind_stale()
+    if jobs or bind:
+        with cf.ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
+            binding = ex.submit(_build_bind, verbose) if bind else None
             outputs = list(ex.map(lambda c: _run(c, verbose), jobs))
+            if binding:
+                binding.result()
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + ".tmp"
         _run([nvcc, "-shared", "-o", tmp] + ARCH + objs + ["-cudart", "static"], verbose)
