@@ -75,7 +75,7 @@ struct BlockUnits {
       const int at = tid * kPer + i;
       n[i] = 0;
       if (at < ng)
-        for (int b = at * gs; b < min(p.B, at * gs + gs); ++b) n[i] += of(__ldg(p.ctx_len + b));
+        for (int b = at * gs; b < min(p.B, at * gs + gs); ++b) n[i] += of(__ldcg(p.ctx_len + b));
       run += n[i];
     }
     int incl = run;
@@ -109,10 +109,10 @@ struct BlockUnits {
     }
     int i = at - prefix[lo];
     it.b = lo * gs;
-    it.ctx = __ldg(p.ctx_len + it.b);
+    it.ctx = __ldcg(p.ctx_len + it.b);
     for (int n; i >= (n = of(it.ctx));) {
       i -= n;
-      it.ctx = __ldg(p.ctx_len + ++it.b);
+      it.ctx = __ldcg(p.ctx_len + ++it.b);
     }
     const int nw = windows(it.ctx), run = i / nw;
     it.w = i - run * nw;
@@ -129,7 +129,7 @@ struct BlockUnits {
     if (++it.kh < p.c.Hkv) return it;
     it.kh = 0;
     do {
-      it.ctx = __ldg(p.ctx_len + ++it.b);
+      it.ctx = __ldcg(p.ctx_len + ++it.b);
     } while (!context_valid(p, it.ctx));
     return it;
   }
@@ -208,8 +208,8 @@ __device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], 
 
 // Four elements of a query row as float32.
 __device__ __forceinline__ float4 load_query4(const void* q, int type, int64_t at) {
-  if (type == KATTN_F32) return __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(q) + at));
-  const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(q) + at));
+  if (type == KATTN_F32) return __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(q) + at));
+  const uint2 w = __ldcg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(q) + at));
   if (type == KATTN_BF16)
     return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
                        __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
@@ -232,7 +232,7 @@ __device__ __forceinline__ void store_out2(void* out, int type, int64_t at, floa
 __device__ __forceinline__ void fill_other_rows(const BlockDecodeParams& p) {
   const int64_t n = (int64_t)p.M * p.Hq * kD;
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    const int ctx = __ldg(p.ctx_len + b);
+    const int ctx = __ldcg(p.ctx_len + b);
     if (context_valid(p, ctx)) continue;
     const float v = ctx == 0 ? 0.0f : __int_as_float(0x7fc00000);
     for (int64_t i = 2 * threadIdx.x; i < n; i += 2 * blockDim.x) store_out2(p.out, p.q_type, b * n + i, v, v);
@@ -259,6 +259,7 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (tid == 0) sm.failed = 0;
+  griddep_wait();                                 // what the kernels before wrote is in place
   const BlockUnits units(p, sm.prefix, nrg);
   units.count(sm.prefix, sm.scratch);
   fill_other_rows(p);
@@ -288,7 +289,7 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
   };
   auto entry_of = [&](const BlockItem& x, int steps) -> int {
     if (lane >= steps) return 0;
-    return __ldg(p.c.block_table + (int64_t)x.b * p.c.max_pages + (key_of(x) >> p.c.page_shift));
+    return __ldcg(p.c.block_table + (int64_t)x.b * p.c.max_pages + (key_of(x) >> p.c.page_shift));
   };
   auto row_of = [&](const BlockItem& x, int steps, int page) -> int {
     if (lane >= steps) return 0;
@@ -343,7 +344,7 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
     load_block(vbuf, &maps.v, r, vbar, policy);
     ahead = true;
   }
-  float ks = __ldg(p.c.k_scale + (row >> p.c.block_shift)), vs = __ldg(p.c.v_scale + (row >> p.c.block_shift));
+  float ks = __ldcg(p.c.k_scale + (row >> p.c.block_shift)), vs = __ldcg(p.c.v_scale + (row >> p.c.block_shift));
   BlockItem nx = next_of(it);
   int nb_n = steps_of(nx);
   int entry = entry_of(nx, nb_n);
@@ -360,8 +361,8 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
     }
     // the next item's rows and scales
     const int row_n = row_of(nx, nb_n, entry);
-    const float ks_n = __ldg(p.c.k_scale + (row_n >> p.c.block_shift));
-    const float vs_n = __ldg(p.c.v_scale + (row_n >> p.c.block_shift));
+    const float ks_n = __ldcg(p.c.k_scale + (row_n >> p.c.block_shift));
+    const float vs_n = __ldcg(p.c.v_scale + (row_n >> p.c.block_shift));
     const int first_n = __shfl_sync(0xffffffffu, row_n, 0);
     ahead = nb > 0 && nb_n > 0;
     // keys that the thread's rows 2c, 2c + 1 of each tile see
@@ -673,7 +674,7 @@ __global__ void __launch_bounds__(32 * W) block_merge_kernel(const BlockDecodePa
   __shared__ float4 s_o[kSums][kD / 4];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int head = blockIdx.x, j = blockIdx.y, b = blockIdx.z;
-  const int ctx = __ldg(p.ctx_len + b), R = p.R;
+  const int ctx = __ldcg(p.ctx_len + b), R = p.R;
   const int kh = head / p.g, rr = j * p.g + head - kh * p.g;
   const size_t stride = (size_t)p.c.Hkv * block_stride(R);
   const float* base = p.partials + ((size_t)b * p.nwin_max * p.c.Hkv + kh) * block_stride(R);
@@ -775,8 +776,8 @@ cudaError_t launch_split(BlockDecodeParams p, const TmaMaps& maps, cudaStream_t 
     }
   }
   p.sms = sms;
-  kern<<<(unsigned)std::min<int64_t>(block_decode_units(p), slots), kThreadsB, smem, stream>>>(p, maps);
-  return cudaGetLastError();
+  return launch_pdl(kern, dim3((unsigned)std::min<int64_t>(block_decode_units(p), slots)), dim3(kThreadsB),
+                    (size_t)smem, stream, p, maps);
 }
 template <bool kE4m3>
 cudaError_t launch_split(const BlockDecodeParams& p, const TmaMaps& maps, cudaStream_t stream) {

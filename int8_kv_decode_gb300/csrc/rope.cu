@@ -17,11 +17,12 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeParams p) {
   const int lane = threadIdx.x & 31, groups = (p.heads + kTurnHeads - 1) / kTurnHeads;
   const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int row = (int)(item / groups), h0 = (int)(item - (int64_t)row * groups) * kTurnHeads;
+  griddep_wait();                                 // what the kernels before wrote is in place
   if (row >= p.rows) return;
   turn_heads<T, O, kInter>(static_cast<const T*>(p.x) + row * p.x_stride + h0 * kD,
                            static_cast<O*>(p.out) + row * p.out_stride + h0 * kD, min(kTurnHeads, p.heads - h0),
                            p.table, p.half, lane, [&](bool& know) {
-                             const int position = __ldg(p.positions + row);      // below 0: a padding row
+                             const int position = ld_fresh(p.positions + row);      // below 0: a padding row
                              know = position < p.n_positions;
                              return know ? position : 0;
                            });
@@ -42,9 +43,8 @@ template <typename T, typename O>
 cudaError_t launch_types(const RopeParams& p, cudaStream_t stream) {
   const int64_t items = (int64_t)p.rows * ((p.heads + kTurnHeads - 1) / kTurnHeads);
   const unsigned blocks = (unsigned)((items + kWarps - 1) / kWarps);
-  if (p.interleaved) rope_kernel<T, O, true><<<blocks, kWarps * 32, 0, stream>>>(p);
-  else rope_kernel<T, O, false><<<blocks, kWarps * 32, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(p.interleaved ? rope_kernel<T, O, true> : rope_kernel<T, O, false>, dim3(blocks),
+                    dim3(kWarps * 32), 0, stream, p);
 }
 
 }  // namespace

@@ -30,9 +30,9 @@ __device__ __forceinline__ Runs lane_runs(int half, int l) {
 struct Angles {
   float2 a[4];                                    // (cos, sin)
 };
-__device__ __forceinline__ Angles load_angles(const float* __restrict__ table, int position, int half, int l) {
+__device__ __forceinline__ Angles load_angles(const float* table, int position, int half, int l) {
   const float4* at = reinterpret_cast<const float4*>(table + (int64_t)position * half * 2) + 2 * l;
-  const float4 x = __ldg(at), y = __ldg(at + 1);
+  const float4 x = ld_fresh(at), y = ld_fresh(at + 1);
   return {{make_float2(x.x, x.y), make_float2(x.z, x.w), make_float2(y.x, y.y), make_float2(y.z, y.w)}};
 }
 
