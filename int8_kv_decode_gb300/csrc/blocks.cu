@@ -13,39 +13,52 @@
 namespace kattn {
 namespace {
 
-// The last b in [0, n) whose key(b) is <= t, for keys that rise (0 if there is none),
-// by a whole warp: 32 keys a step.
-template <typename Key>
-__device__ __forceinline__ int warp_find(int n, int64_t t, int lane, Key key) {
-  int lo = 0;
-  while (n > 1) {
-    const int step = (n + 31) >> 5, at = lane * step;
-    const unsigned le = __ballot_sync(0xffffffffu, at < n && key(lo + at) <= t);
-    const int k = max(__popc(le) - 1, 0);
-    lo += k * step;
-    n = min(step, n - k * step);
-  }
-  return lo;
-}
-
 // Keys that a row of the block table can hold (fewer than 2^30: key numbers are 32-bit).
 __device__ __forceinline__ int64_t table_keys(const BlockCache& c) {
   return min((int64_t)c.max_pages << c.page_shift, (int64_t)1 << 30);
 }
-// The rows of sequence b and its first key; whether the rows lie in the call's and the
+// The rows of a sequence and its first key; whether the rows lie in the call's and the
 // keys in the table's row.
 struct Span {
-  int c0, n, start;
+  int b, c0, n, start;
   bool valid;
 };
-__device__ __forceinline__ Span span_of(const SpanParams& s, int b, int64_t most) {
-  const int c0 = ld_fresh(s.cu + b), c1 = ld_fresh(s.cu + b + 1), st = ld_fresh(s.start + b);
+__device__ __forceinline__ Span make_span(const SpanParams& s, int b, int c0, int c1, int start, int64_t most) {
   const bool rises = c0 >= 0 && c0 <= c1 && c1 <= s.rows;
-  return {c0, rises ? c1 - c0 : 0, st, rises && st >= 0 && (int64_t)st + (c1 - c0) <= most};
+  return {b, c0, rises ? c1 - c0 : 0, start, rises && start >= 0 && (int64_t)start + (c1 - c0) <= most};
+}
+__device__ __forceinline__ Span span_of(const SpanParams& s, int b, int64_t most) {
+  return make_span(s, b, ld_fresh(s.cu + b), ld_fresh(s.cu + b + 1), ld_fresh(s.start + b), most);
 }
 __device__ __forceinline__ void flag_bad_spans(const SpanParams& s, int64_t most) {
   for (int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; b < s.B; b += (int64_t)gridDim.x * blockDim.x)
     if (!span_of(s, (int)b, most).valid) atomicOr(s.err, KATTN_DEVERR_BAD_SEQUENCE);
+}
+
+// The last sequence b whose key(b, cu[b]) is <= t, for keys that rise (0 if there is
+// none), by a whole warp: 64 of them a step.  The last step's loads hold its span too, so
+// that a call of up to 64 sequences goes to memory once.
+template <typename Key>
+__device__ __forceinline__ Span find_span(const SpanParams& s, int64_t t, int64_t most, int lane, Key key) {
+  int lo = 0, n = s.B;
+  auto count = [&](int step, int x, int y) {      // those of lo + i step, i < 64, i step < n; x, y: cu of lane, lane + 32
+    const int i = lane * step, j = (lane + 32) * step;
+    return __popc(__ballot_sync(0xffffffffu, i < n && key(lo + i, x) <= t)) +
+           __popc(__ballot_sync(0xffffffffu, j < n && key(lo + j, y) <= t));
+  };
+  while (n > 64) {
+    const int step = (n + 63) >> 6;
+    const int x = ld_fresh(s.cu + min(lo + lane * step, s.B)), y = ld_fresh(s.cu + min(lo + (lane + 32) * step, s.B));
+    const int k = max(count(step, x, y) - 1, 0);
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  const int x = ld_fresh(s.cu + min(lo + lane, s.B)), y = ld_fresh(s.cu + min(lo + lane + 32, s.B));
+  const int sx = ld_fresh(s.start + min(lo + lane, s.B - 1)), sy = ld_fresh(s.start + min(lo + lane + 32, s.B - 1));
+  const int k = max(count(1, x, y) - 1, 0);
+  auto pick = [&](int u, int v, int i) { return i < 32 ? __shfl_sync(0xffffffffu, u, i) : __shfl_sync(0xffffffffu, v, i - 32); };
+  const int c1 = k < 63 ? pick(x, y, k + 1) : ld_fresh(s.cu + lo + 64);
+  return make_span(s, lo + k, pick(x, y, k), c1, pick(sx, sy, k), most);
 }
 
 // Row in its plane of key `key`, by its page; -1 (flagged) where that is not one.
@@ -92,7 +105,7 @@ __global__ void __launch_bounds__(kBlock * 4) append_kernel(const AppendParams p
   constexpr int kWarps = kBlock / kRowsPerWarp;
   __shared__ float s_max[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int R = kBlock;
+  constexpr int R = kBlock;
   // (The kernel that follows is not let in early: its blocks would take the place of this
   // one's.  A row for each of 64 sequences written and read back 10.0 us, with it 13 us.)
   griddep_wait();                                 // what the kernels before wrote is in place
@@ -108,11 +121,9 @@ __global__ void __launch_bounds__(kBlock * 4) append_kernel(const AppendParams p
     turn_heads<T, T, kInter>(static_cast<const T*>(p.q) + row * p.q_stride + h0 * kD,
                              static_cast<T*>(p.q_out) + row * p.q_out_stride + h0 * kD,
                              min(kTurnHeads, p.Hq - h0), p.table, p.half, lane, [&](bool& know) {
-      const int b = warp_find(p.s.B, row, lane, [&](int i) { return (int64_t)ld_fresh(p.s.cu + i); });
-      const int c0 = ld_fresh(p.s.cu + b), c1 = ld_fresh(p.s.cu + b + 1);
-      const Span s = span_of(p.s, b, most);
+      const Span s = find_span(p.s, row, most, lane, [](int, int cu) { return (int64_t)cu; });
       know = s.valid;
-      return row < c0 || row >= c1 ? -1 : know ? s.start + row - c0 : 0;     // (-1: no sequence's row)
+      return row < s.c0 || row >= s.c0 + s.n ? -1 : know ? s.start + row - s.c0 : 0;   // (-1: no sequence's row)
     });
     return;
   }
@@ -122,9 +133,9 @@ __global__ void __launch_bounds__(kBlock * 4) append_kernel(const AppendParams p
   const int plane = (int)(blockIdx.x - unit * (2u * p.c.Hkv));
   const bool is_k = plane < p.c.Hkv;
   const int h = is_k ? plane : plane - p.c.Hkv;
-  const int b = warp_find(p.s.B, unit, lane, [&](int i) { return (int64_t)(ld_fresh(p.s.cu + i) / R) + 2 * i; });
-  const Span span = span_of(p.s, b, most);
+  const Span span = find_span(p.s, unit, most, lane, [](int i, int cu) { return (int64_t)(cu / R) + 2 * i; });
   if (!span.valid || span.n == 0) return;
+  const int b = span.b;
   const int st = span.start, n = span.n;
   const int64_t j = (int64_t)unit - (span.c0 / R + 2 * (int64_t)b);
   if (j < 0 || j > (st + n - 1) / R - st / R) return;
@@ -230,26 +241,32 @@ __global__ void __launch_bounds__(256, 4) read_kernel(const ReadParams p) {
   const int h = plane - (p.out_k && plane >= p.c.Hkv ? p.c.Hkv : 0);
   const int64_t base = (int64_t)h * p.c.cap_rows;
 
-  // ---- lane i: row first + i.  Its sequence is among those from b0 on; 32 of them are
-  // looked at together.
+  // ---- lane i: row first + i.  Its sequence is that of row `first` or one of those that
+  // follow; 32 of them are looked at together.
   int row = -1;
   {
-    const int b0 = warp_find(p.s.B, first, lane, [&](int i) { return (int64_t)ld_fresh(p.s.cu + i); });
+    const int b0 = find_span(p.s, first, most, lane, [](int, int cu) { return (int64_t)cu; }).b;
     const int r = (int)min(first + lane, (int64_t)INT32_MAX);
-    const int ends = b0 + 1 + lane <= p.s.B ? ld_fresh(p.s.cu + b0 + 1 + lane) : INT32_MAX;
-    int k = 0;                                    // ends up to the row, by halving
+    const int at = min(b0 + lane, p.s.B - 1);
+    const int begins = ld_fresh(p.s.cu + at), starts = ld_fresh(p.s.start + at);
+    const int ends = b0 + lane < p.s.B ? ld_fresh(p.s.cu + b0 + lane + 1) : INT32_MAX;
+    int k = 0;                                    // the ends up to the row, by halving
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
       const int e = __shfl_sync(0xffffffffu, ends, k + d - 1);
       if (e <= r) k += d;
     }
-    if (__shfl_sync(0xffffffffu, ends, k) <= r) ++k;       // (k = 31: none of the 32 is past it)
-    int b = min(b0 + k, p.s.B - 1);
-    while (b + 1 < p.s.B && r >= ld_fresh(p.s.cu + b + 1)) ++b;
-    const Span s = span_of(p.s, b, most);
-    if (first + lane < p.s.rows && s.valid && r >= s.c0 && r < s.c0 + s.n) {
+    const int c0 = __shfl_sync(0xffffffffu, begins, k), c1 = __shfl_sync(0xffffffffu, ends, k);
+    const int st = __shfl_sync(0xffffffffu, starts, k);
+    Span s = make_span(p.s, b0 + k, c0, c1, st, most);
+    if (c1 <= r) {                                // (k = 31: further on)
+      int b = b0 + k;
+      while (b + 1 < p.s.B && r >= ld_fresh(p.s.cu + b + 1)) ++b;
+      s = span_of(p.s, b, most);
+    }
+    if (s.b < p.s.B && first + lane < p.s.rows && s.valid && r >= s.c0 && r < s.c0 + s.n) {
       const int key = s.start + r - s.c0;
-      row = row_of_key(p.c, p.s.err, page_of_key(p.c, b, key), key);
+      row = row_of_key(p.c, p.s.err, page_of_key(p.c, s.b, key), key);
     }
   }
   const int col = (lane % kLanes) * kPer, sub = lane / kLanes;
