@@ -205,6 +205,26 @@ def build_diff_timeout_variant(limit: int, maps: int, verbose: bool = False) -> 
     return lib
 
 
+# Likewise for decode_blocks.cu: the warps in the bit mask `warps` of a block of four find no
+# further copy ready after `limit` stages.  Only tests/test_gpu_blocks_timeout.py loads them.
+def build_blocks_timeout_variant(limit: int, warps: int, verbose: bool = False) -> str:
+    """libkattn.so with decode_blocks.cu built to run out of copies; returns its path."""
+    build(verbose=verbose)
+    nvcc = nvcc_path()
+    src = os.path.join(CSRC, "decode_blocks.cu")
+    obj = os.path.join(BUILD, f"decode_blocks_limit{limit}_warps{warps}.o")
+    lib = os.path.join(BUILD, f"libkattn_blocks_limit{limit}_warps{warps}.so")
+    if _stale(obj, [src, __file__] + _headers()):
+        _run([nvcc, "-c", src, "-o", obj] + ARCH + COMMON + SOURCES["decode_blocks.cu"]
+             + [f"-DKATTN_BLOCKS_STAGE_LIMIT={limit}", f"-DKATTN_BLOCKS_STAGE_WARPS={warps}"], verbose)
+    objs = [os.path.join(BUILD, f.replace(".cu", ".o")) for f in SOURCES if f != "decode_blocks.cu"]
+    if _stale(lib, objs + [obj]):
+        tmp = lib + ".tmp"
+        _run([nvcc, "-shared", "-o", tmp] + ARCH + objs + [obj, "-cudart", "static"], verbose)
+        os.replace(tmp, lib)
+    return lib
+
+
 if __name__ == "__main__":
     build(force="--force" in sys.argv, verbose=True, ptxas_verbose="-v" in sys.argv)
     print(LIB)

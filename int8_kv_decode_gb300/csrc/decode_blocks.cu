@@ -5,13 +5,13 @@
 // Two launches: split_kernel reduces windows of the keys, merge_kernel joins the windows
 // of a row.  A sequence of one window is finished by the first.
 //
-// A block of four warps takes a unit: sequence, window of 512 keys, kv head and up to 16 of
-// the rows (query heads x draft columns) that read the head.  Warp w takes the steps of 32
-// keys w, w + 4, ..., so a short window is shared by all four as well, and the warps' sums
-// come together in shared memory: one partial a window.  (A warp per window of 256 keys took
-// 122 us where this takes 96, 64 sequences of 512 to 32768 keys: more partials, larger
-// shares of work per warp.)  A warp's K and V rows come by TMA into a buffer each, refilled
-// for the step that follows as soon as its products are issued.  Per step
+// A block of four warps takes a unit: sequence, window of 512 keys, kv head and T tiles of 8
+// of the rows (query heads x draft columns) that read the head; T = 1 to 5 (unit_tiles).
+// Warp w takes the steps of 32 keys w, w + 4, ..., so a short window is shared by all four as
+// well, and the warps' sums come together in shared memory: one partial a window.  (A warp
+// per window of 256 keys took 122 us where this takes 96, 64 sequences of 512 to 32768 keys:
+// more partials, larger shares of work per warp.)  A warp's K and V rows come by TMA into a
+// buffer each, refilled for the step that follows as soon as its products are issued.  Per step
 //   * S^T = K Q^T on f16 MMAs: the codes are exact in f16, and so are bf16 and f16
 //     queries scaled by a power of two per row (float32 queries as f16 hi + lo, 22 bits),
 //     so the products are exact and the sums float32;
@@ -22,10 +22,25 @@
 //     8 x 8 blocks in registers, to the second product, whose row sums take the weights
 //     as rounded: a weight's rounding then cancels where it dominates;
 //   * O = O + v_scale (V^T P^T): the product of a step starts at zero and enters the
-//     float32 sum with the block's scale, so scales of any range need no care.
-// The K and V codes are converted once for all rows of the unit.
+//     float32 sum with the block's scale, so scales of any range need no care.  From three
+//     tiles on O lies in tensor memory, each lane's columns its own store, read and written
+//     once a step: so the codes are converted once for up to 40 rows, the order of every
+//     row's operations stays that of one tile, and three blocks still fit a multiprocessor.
+//
+// What bounds it.  Up to 8 rows a head, HBM: 64 sequences of 512 to 32768 keys over 64-row
+// pages, 32 query and 4 kv heads (544 MB, 80 us at the measured copy rate): 96 us a call, the
+// split alone 92 (5.9 TB/s), issue 42%.  2 sequences of 128k keys with float32 queries (267
+// MB, 39 us): 55 us, split 52, of which the second MMAs for hi + lo take tensor pipe to 34%.
+// With more rows, issue and the latency of a step's chain at 12 warps a multiprocessor (870
+// instructions a step at T = 2, 320 of them to make f16 of the codes; 1500 at T = 5): 16
+// sequences of 1k to 4k keys, 40 rows a head, 34 us; 64 of them 81 us.  One sequence of 257
+// keys: 6.1 us, latency alone.
+#include <cmath>
+
 #include "blocks_internal.cuh"
 #include "decode_diff.cuh"
+#include "tcgen05_common.cuh"
+
 namespace kattn {
 namespace {
 
@@ -139,12 +154,25 @@ struct BlockUnits {
   }
 };
 
+// Where the sums O of a unit's T tiles of 8 rows are kept: in registers (32 a tile) for one
+// or two tiles, else in tensor memory, a lane's own columns as its own store: per 16
+// channels the first kLow columns of the tiles side by side, then the others.
+template <int T>
+struct Sums {
+  static constexpr bool kTensor = T > 2;
+  static constexpr int kLow = T == 3 ? 8 : 16, kHigh = 4 * T - kLow;
+  // columns allocated, powers of two (with 256 for T = 5 two blocks would have room)
+  enum : int { kFirst = 128, kSecond = T == 5 ? 32 : 0 };
+  static constexpr int kJoin = kTensor ? 1 : T;           // tiles that the warps join at a time
+};
+constexpr int kPerSm = 3;                         // blocks a multiprocessor holds
+
 template <int T, bool kPrecise>
 struct __align__(1024) BlockSmem {
   uint8_t ring[kWarpsB][2][kBlockBytes];                  // [K | V] of each warp
-  // the warps' sums of a unit, in the order of the MMA's registers, with their references
-  // and row sums
-  float4 o[kWarpsB][T][8][32];
+  // the warps' sums of a unit's tiles, in the order of the MMA's registers; their
+  // references and row sums
+  float4 o[kWarpsB][Sums<T>::kJoin][8][32];
   float2 ml[kWarpsB][T][8];
   // f16 queries (hi, and lo): row r's 16-byte chunk of channels 8 i at chunk
   // 4 (i % 4) + i / 4, XOR 4 in odd rows: a lane's loads of its 32 channels spread
@@ -155,7 +183,58 @@ struct __align__(1024) BlockSmem {
   int prefix[kMaxGroups + 1];
   int scratch[kWarpsB];
   int failed;                                             // a warp's copy never arrived
+  uint32_t tensor[2];                                     // tensor memory
 };
+
+// 4, 8 or 16 columns of this warp's lanes of tensor memory.  Loads are in place after
+// tensor_loaded, stores after tc_wait_st.
+template <int N>
+__device__ __forceinline__ void tensor_load(uint32_t at, uint32_t* v) {
+  if constexpr (N == 4) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(at));
+  } else if constexpr (N == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(at));
+  } else {
+    static_assert(N == 16);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(at));
+  }
+}
+template <int N>
+__device__ __forceinline__ void tensor_store(uint32_t at, const uint32_t* v) {
+  if constexpr (N == 4) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(at), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3])
+                 : "memory");
+  } else if constexpr (N == 8) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(at), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    static_assert(N == 16);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n"
+        ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+  }
+}
+template <int N>
+__device__ __forceinline__ void tensor_loaded(uint32_t (&v)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));    // (no use of it comes before)
+}
+__device__ __forceinline__ float2 as_float2(uint32_t x, uint32_t y) {
+  return make_float2(__uint_as_float(x), __uint_as_float(y));
+}
 
 // Rows of 32 keys of a plane into a buffer, by one lane (predicated).
 __device__ __forceinline__ void load_block(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar,
@@ -207,9 +286,8 @@ __device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 // Four elements of a query row as float32.
-__device__ __forceinline__ float4 load_query4(const void* q, int type, int64_t at) {
-  if (type == KATTN_F32) return __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(q) + at));
-  const uint2 w = __ldcg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(q) + at));
+__device__ __forceinline__ float4 query_values(float4 x, int) { return x; }
+__device__ __forceinline__ float4 query_values(uint2 w, int type) {
   if (type == KATTN_BF16)
     return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
                        __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
@@ -243,9 +321,10 @@ __device__ __forceinline__ void fill_other_rows(const BlockDecodeParams& p) {
 // (Blocks a multiprocessor holds: with 4, 128 registers a thread, and T = 1, 99 us instead
 // of 96, 64 sequences of 512 to 32768 keys; one sequence as before.)
 template <int T, bool kE4m3, bool kPrecise>
-__global__ void __launch_bounds__(kThreadsB, 3)
+__global__ void __launch_bounds__(kThreadsB, kPerSm)
 block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps maps) {
   using Smem = BlockSmem<T, kPrecise>;
+  using S = Sums<T>;
   constexpr int kUnitRows = 8 * T, kParts = kPrecise ? 2 : 1;
   extern __shared__ unsigned char smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw + (0u - smem_u32(smem_raw)) % 1024u);
@@ -276,6 +355,17 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
   const int u_end = (int)((int64_t)(worker + 1) * total / G);
   BlockItem it = units.find(u, u_end);
   if (it.b < 0) return;
+  if constexpr (S::kTensor) {
+    if (warp == 0) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&sm.tensor[0])),
+                   "r"((int)S::kFirst));
+      if constexpr (S::kSecond > 0)
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n"
+                     ::"r"(smem_u32(&sm.tensor[1])), "r"((int)S::kSecond));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+    }
+    tc_fence_before();
+  }
 
   const uint32_t ginv = 65536u / (uint32_t)p.g + 1u;      // rr / g for rr < 64
   auto column = [&](int rr) -> int { return (int)(((uint32_t)rr * ginv) >> 16); };
@@ -307,23 +397,27 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
   // that its largest lies in [2^14, 2^15): bf16 elements down to 2^-28 of it are then exact,
   // and sums of products stay in float32.
   auto convert_queries = [&](const BlockItem& x) {
-    float4 v[2 * T];
+    using Raw = typename std::conditional<kPrecise, float4, uint2>::type;
+    Raw v[2 * T];                                 // (all of them on their way at once)
 #pragma unroll
     for (int i = 0; i < 2 * T; ++i) {
       const int rr = x.rg * kUnitRows + warp * 2 * T + i, j = column(min(rr, R - 1));
-      v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (rr < R)
-        v[i] = load_query4(p.q, p.q_type, (((int64_t)x.b * M + j) * p.Hq + x.kh * p.g + rr - j * p.g) * kD + 4 * lane);
+      v[i] = Raw{};
+      if (rr < R) {
+        const int64_t at = (((int64_t)x.b * M + j) * p.Hq + x.kh * p.g + rr - j * p.g) * kD + 4 * lane;
+        v[i] = __ldcg(reinterpret_cast<const Raw*>(static_cast<const char*>(p.q) + at * (kPrecise ? 4 : 2)));
+      }
     }
 #pragma unroll
     for (int i = 0; i < 2 * T; ++i) {
       const int n = (warp * 2 * T + i) >> 3, r = (warp * 2 * T + i) & 7;
-      const float own = fmaxf(fmaxf(fabsf(v[i].x), fabsf(v[i].y)), fmaxf(fabsf(v[i].z), fabsf(v[i].w)));
+      const float4 y = query_values(v[i], p.q_type);
+      const float own = fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w)));
       const float big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(own)));
       const float up = power_scale(14, big);
       uint2 hi, lo;
-      split_f16x2(v[i].x * up, v[i].y * up, hi.x, lo.x);
-      split_f16x2(v[i].z * up, v[i].w * up, hi.y, lo.y);
+      split_f16x2(y.x * up, y.y * up, hi.x, lo.x);
+      split_f16x2(y.z * up, y.w * up, hi.y, lo.y);
       const int chunk = lane >> 1, at = (4 * (chunk & 3) + (chunk >> 2)) ^ (4 * (r & 1));
       reinterpret_cast<uint2*>(&sm.q[n][0][r][at])[lane & 1] = hi;
       if constexpr (kPrecise) reinterpret_cast<uint2*>(&sm.q[n][kParts - 1][r][at])[lane & 1] = lo;
@@ -351,6 +445,38 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
   uint32_t ph = 0;                                // parity of the step's copies
   convert_queries(it);
   __syncthreads();
+  uint32_t low = 0, high = 0;                     // this warp's lanes of tensor memory
+  if constexpr (S::kTensor) {
+    tc_fence_after();
+    low = sm.tensor[0] + ((uint32_t)(32 * warp) << 16);
+    high = S::kSecond > 0 ? sm.tensor[1] + ((uint32_t)(32 * warp) << 16) : low + 8 * S::kLow;
+  }
+  // tile n's four columns of the channels 16 md ..
+  auto columns_of = [&](int md, int n) -> uint32_t {
+    return n < S::kLow / 4 ? low + md * S::kLow + 4 * n : high + md * S::kHigh + 4 * (n - S::kLow / 4);
+  };
+#ifdef KATTN_BLOCKS_STAGE_LIMIT
+  // Test builds only: the warps KATTN_BLOCKS_STAGE_WARPS (a bit each) take this many
+  // copies, then find none ready.
+  int copies = 0;
+  auto ready = [&](uint32_t bar, uint32_t parity) {
+    return !((KATTN_BLOCKS_STAGE_WARPS >> warp & 1) && copies++ >= KATTN_BLOCKS_STAGE_LIMIT) && stage_ready(bar, parity);
+  };
+#else
+  auto ready = [&](uint32_t bar, uint32_t parity) { return stage_ready(bar, parity); };
+#endif
+  auto leave = [&]() {                            // by every warp: the tensor memory is given back
+    if constexpr (S::kTensor) {
+      tc_fence_before();
+      __syncthreads();
+      tc_fence_after();
+      if (warp == 0) {
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(sm.tensor[0]), "r"((int)S::kFirst));
+        if constexpr (S::kSecond > 0)
+          asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(sm.tensor[1]), "r"((int)S::kSecond));
+      }
+    }
+  };
 
   for (;;) {
     const int s0 = it.w * kKeys;
@@ -365,24 +491,34 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
     const float vs_n = __ldcg(p.c.v_scale + (row_n >> p.c.block_shift));
     const int first_n = __shfl_sync(0xffffffffu, row_n, 0);
     ahead = nb > 0 && nb_n > 0;
-    // keys that the thread's rows 2c, 2c + 1 of each tile see
-    int keys[T][2];
-#pragma unroll
-    for (int n = 0; n < T; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        keys[n][e] = it.ctx + column(min(it.rg * kUnitRows + 8 * n + 2 * c + e, R - 1));
+    // keys that the thread's row 2c + e of tile n sees
+    auto keys_of = [&](int n, int e) -> int {
+      return it.ctx + column(min(it.rg * kUnitRows + 8 * n + 2 * c + e, R - 1));
+    };
 
     float2 m[T], l[T];                            // references and row sums of rows 2c, 2c + 1
-    float o[8][T][4];                             // [16 channels][tile]
+    float o[S::kTensor ? 1 : 8][S::kTensor ? 1 : T][4];   // [16 channels][tile]
 #pragma unroll
     for (int n = 0; n < T; ++n) {
       m[n] = make_float2(-INFINITY, -INFINITY);
       l[n] = make_float2(0.0f, 0.0f);
+      if constexpr (!S::kTensor) {
 #pragma unroll
-      for (int md = 0; md < 8; ++md)
+        for (int md = 0; md < 8; ++md)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) o[md][n][v] = 0.0f;
+          for (int v = 0; v < 4; ++v) o[md][n][v] = 0.0f;
+      }
+    }
+    if constexpr (S::kTensor) {
+      uint32_t z[S::kLow];
+#pragma unroll
+      for (int i = 0; i < S::kLow; ++i) z[i] = 0u;
+#pragma unroll
+      for (int md = 0; md < 8; ++md) {
+        tensor_store<S::kLow>(low + md * S::kLow, z);
+        if constexpr (S::kHigh > 0) tensor_store<S::kHigh>(high + md * S::kHigh, z);
+      }
+      tc_wait_st();
     }
     // A copy never arrived: flag it; the block of threads leaves at the next barrier.
     auto give_up = [&]() {
@@ -396,10 +532,12 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
 #pragma unroll 1
     for (int i = 0; i < nb; ++i) {
       const int t0 = s0 + (i * kWarpsB + warp) * kBlockBk;
-      const float ksb = __shfl_sync(0xffffffffu, ks, i), vsb = __shfl_sync(0xffffffffu, vs, i);
+      const float ksb = __shfl_sync(0xffffffffu, ks, i);
+      float vsb = __shfl_sync(0xffffffffu, vs, i);
       const int next = i + 1 < nb ? __shfl_sync(0xffffffffu, row, i + 1) : nb_n > 0 ? first_n : -1;
       const bool edge = t0 + kBlockBk > it.ctx;   // keys that some row does not see
-      if (!stage_ready(kbar, ph)) {
+      if (edge && !(fabsf(vsb) < INFINITY)) vsb = 0.0f;    // (0 * inf would reach rows that see none of them)
+      if (!ready(kbar, ph)) {
         give_up();
         flying = 3;
         break;
@@ -445,7 +583,6 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
       if (next >= 0) load_block(kbuf, &maps.k, next, kbar, policy);
       // ---- weights
       uint2 pf[T][2][kParts];                     // the second product's operand: [half]
-      float2 gain[T];                             // v_scale, for the rows that see a key of the block
 #pragma unroll
       for (int n = 0; n < T; ++n) {
         const float2 f = *reinterpret_cast<const float2*>(&sm.factor[n][2 * c]);
@@ -458,7 +595,7 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
 #pragma unroll
             for (int k2 = 0; k2 < 2; ++k2)
               x[hf][k2] = f2_fma(make_float2(s[n][hf][2 * k2], s[n][hf][2 * k2 + 1]), cf, down);
-          if (edge) hide_keys(x, t0 + g, keys[n][0], keys[n][1]);
+          if (edge) hide_keys(x, t0 + g, keys_of(n, 0), keys_of(n, 1));
         };
         scores(m[n]);                             // (a reference of -inf: +inf, above the limit)
         auto largest = [&]() -> float2 {
@@ -489,11 +626,28 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
           };
           const float2 al = make_float2(move(over.x, top.x, m[n].x), move(over.y, top.y, m[n].y));
           l[n] = f2_mul(l[n], al);
+          if (i == 0) {                           // (nothing is summed up yet)
+          } else if constexpr (S::kTensor) {
+            uint32_t v[32];
 #pragma unroll
-          for (int md = 0; md < 8; ++md) {
-            const float2 a0 = f2_mul(make_float2(o[md][n][0], o[md][n][1]), al);
-            const float2 a1 = f2_mul(make_float2(o[md][n][2], o[md][n][3]), al);
-            o[md][n][0] = a0.x; o[md][n][1] = a0.y; o[md][n][2] = a1.x; o[md][n][3] = a1.y;
+            for (int md = 0; md < 8; ++md) tensor_load<4>(columns_of(md, n), v + 4 * md);
+            tensor_loaded(v);
+#pragma unroll
+            for (int i2 = 0; i2 < 32; i2 += 2) {
+              const float2 a0 = f2_mul(as_float2(v[i2], v[i2 + 1]), al);
+              v[i2] = __float_as_uint(a0.x);
+              v[i2 + 1] = __float_as_uint(a0.y);
+            }
+#pragma unroll
+            for (int md = 0; md < 8; ++md) tensor_store<4>(columns_of(md, n), v + 4 * md);
+            tc_wait_st();
+          } else {
+#pragma unroll
+            for (int md = 0; md < 8; ++md) {
+              const float2 a0 = f2_mul(make_float2(o[md][n][0], o[md][n][1]), al);
+              const float2 a1 = f2_mul(make_float2(o[md][n][2], o[md][n][3]), al);
+              o[md][n][0] = a0.x; o[md][n][1] = a0.y; o[md][n][2] = a1.x; o[md][n][3] = a1.y;
+            }
           }
           scores(m[n]);
         }
@@ -513,8 +667,6 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
                                       transpose8(*reinterpret_cast<const uint32_t*>(&h1)));
           }
         }
-        gain[n] = make_float2(vsb, vsb);
-        if (edge) gain[n] = make_float2(t0 < keys[n][0] ? vsb : 0.0f, t0 < keys[n][1] ? vsb : 0.0f);
         // row sums: a product with ones
         const uint32_t ones[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
         float r[4];
@@ -529,11 +681,12 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
       // ---- O += v_scale V^T P^T.  Row g of m-tile q is channel 16q + 2g, row g + 8 the next
       // one: a 16-bit element of the buffer is two channels of a key, so that the transposing
       // load pairs the keys 2c, 2c + 1 of both channels in a register.
-      if (!stage_ready(vbar, ph)) {
+      if (!ready(vbar, ph)) {
         give_up();
         flying = next >= 0 ? 6 : 2;
         break;
       }
+      const float2 gain = make_float2(vsb, vsb);
       const uint32_t va = vbuf + (uint32_t)((lane & 15) * kD + (((lane >> 4) ^ (lane & 7)) << 4));
 #pragma unroll
       for (int q = 0; q < 8; q += 2) {
@@ -554,52 +707,94 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
             codes_h2<kE4m3, true>(vw[hf][2 * d], a[hf][0], a[hf][1]);
             codes_h2<kE4m3, true>(vw[hf][2 * d + 1], a[hf][2], a[hf][3]);
           }
+          uint32_t ot[S::kTensor ? 4 * T : 1];    // (on their way beside the products)
+          if constexpr (S::kTensor) {
+            tensor_load<S::kLow>(low + (q + d) * S::kLow, ot);
+            if constexpr (S::kHigh > 0) tensor_load<S::kHigh>(high + (q + d) * S::kHigh, ot + S::kLow);
+          }
+          float y[T][4];
 #pragma unroll
           for (int n = 0; n < T; ++n) {
-            float y[4];
-            mma_zero(y, a[0], pf[n][0][0]);
-            mma_f16(y, a[1], pf[n][1][0]);
+            mma_zero(y[n], a[0], pf[n][0][0]);
+            mma_f16(y[n], a[1], pf[n][1][0]);
             if constexpr (kPrecise) {
-              mma_f16(y, a[0], pf[n][0][kParts - 1]);
-              mma_f16(y, a[1], pf[n][1][kParts - 1]);
+              mma_f16(y[n], a[0], pf[n][0][kParts - 1]);
+              mma_f16(y[n], a[1], pf[n][1][kParts - 1]);
             }
-            float* to = o[q + d][n];
-            const float2 r0 = f2_fma(make_float2(y[0], y[1]), gain[n], make_float2(to[0], to[1]));
-            const float2 r1 = f2_fma(make_float2(y[2], y[3]), gain[n], make_float2(to[2], to[3]));
-            to[0] = r0.x; to[1] = r0.y; to[2] = r1.x; to[3] = r1.y;
+          }
+          if constexpr (S::kTensor) tensor_loaded(ot);
+#pragma unroll
+          for (int n = 0; n < T; ++n)
+#pragma unroll
+            for (int v = 0; v < 4; v += 2) {
+              if constexpr (S::kTensor) {
+                uint32_t* to = ot + 4 * n + v;
+                const float2 r = f2_fma(make_float2(y[n][v], y[n][v + 1]), gain, as_float2(to[0], to[1]));
+                to[0] = __float_as_uint(r.x);
+                to[1] = __float_as_uint(r.y);
+              } else {
+                float* to = o[q + d][n] + v;
+                const float2 r = f2_fma(make_float2(y[n][v], y[n][v + 1]), gain, make_float2(to[0], to[1]));
+                to[0] = r.x;
+                to[1] = r.y;
+              }
+            }
+          if constexpr (S::kTensor) {
+            tensor_store<S::kLow>(low + (q + d) * S::kLow, ot);
+            if constexpr (S::kHigh > 0) tensor_store<S::kHigh>(high + (q + d) * S::kHigh, ot + S::kLow);
           }
         }
       }
+      if constexpr (S::kTensor) tc_wait_st();     // (the next step loads them)
       __syncwarp();
       if (next >= 0) load_block(vbuf, &maps.v, next, vbar, policy);
       ph ^= 1u;
     }
 
-    // ---- the warps' sums come together
+    // ---- the warps' sums come together, some tiles at a time
+    const bool whole = block_windows(it.ctx + M - 1) == 1;
+    float* part = p.partials + (((size_t)it.b * p.nwin_max + it.w) * p.c.Hkv + it.kh) * block_stride(R);
 #pragma unroll
-    for (int n = 0; n < T; ++n) {
-#pragma unroll
-      for (int md = 0; md < 8; ++md)
-        sm.o[warp][n][md][lane] = make_float4(o[md][n][0], o[md][n][1], o[md][n][2], o[md][n][3]);
+    for (int n = 0; n < T; ++n)
       if (g == 0) {
         sm.ml[warp][n][2 * c] = make_float2(m[n].x, l[n].x);
         sm.ml[warp][n][2 * c + 1] = make_float2(m[n].y, l[n].y);
       }
-    }
-    __syncthreads();
-    if (sm.failed) {                              // give the copies on their way a bounded chance, and leave
-      if (lane == 0) {
-        if (flying == 0 && ahead) flying = 3;
-        if (flying & 1) mbar_wait_bounded(&sm.full[warp][0], ph);
-        if (flying & 2) mbar_wait_bounded(&sm.full[warp][1], ph);
-        if (flying & 4) mbar_wait_bounded(&sm.full[warp][0], ph ^ 1u);
-      }
-      return;
-    }
-    const bool whole = block_windows(it.ctx + M - 1) == 1;
-    float* part = p.partials + (((size_t)it.b * p.nwin_max + it.w) * p.c.Hkv + it.kh) * block_stride(R);
+#pragma unroll 1
+    for (int n0 = 0; n0 < T; n0 += S::kJoin) {
+      if constexpr (S::kTensor) {
+        uint32_t v[32];
 #pragma unroll
-    for (int n = 0; n < T; ++n) {
+        for (int md = 0; md < 8; ++md) tensor_load<4>(columns_of(md, n0), v + 4 * md);
+        tensor_loaded(v);
+        if (n0 > 0) __syncthreads();              // (the tile before is read)
+#pragma unroll
+        for (int md = 0; md < 8; ++md) {
+          const float2 x = as_float2(v[4 * md], v[4 * md + 1]), y = as_float2(v[4 * md + 2], v[4 * md + 3]);
+          sm.o[warp][0][md][lane] = make_float4(x.x, x.y, y.x, y.y);
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < T; ++n)
+#pragma unroll
+          for (int md = 0; md < 8; ++md)
+            sm.o[warp][n][md][lane] = make_float4(o[md][n][0], o[md][n][1], o[md][n][2], o[md][n][3]);
+      }
+      __syncthreads();
+      if (sm.failed) {                            // give the copies on their way a bounded chance, and leave
+        if (lane == 0) {
+          if (flying == 0 && ahead) flying = 3;
+          if (flying & 1) mbar_wait_bounded(&sm.full[warp][0], ph);
+          if (flying & 2) mbar_wait_bounded(&sm.full[warp][1], ph);
+          if (flying & 4) mbar_wait_bounded(&sm.full[warp][0], ph ^ 1u);
+        }
+        __syncwarp();
+        leave();
+        return;
+      }
+#pragma unroll
+      for (int t = 0; t < S::kJoin; ++t) {
+      const int n = n0 + t;
       // weights 2^(m_w - m) of the warps, for rows 2c and 2c + 1
       float4 st[kWarpsB];                         // m, l of both rows
 #pragma unroll
@@ -621,7 +816,7 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
         const int md = 2 * warp + d;
         float4 x[kWarpsB];
 #pragma unroll
-        for (int w = 0; w < kWarpsB; ++w) x[w] = sm.o[w][n][md][lane];
+        for (int w = 0; w < kWarpsB; ++w) x[w] = sm.o[w][t][md][lane];
         auto join = [&](const float (&wt)[kWarpsB], float a0, float a1, float a2, float a3) {
           return __fadd_rn(__fmaf_rn(wt[1], a1, __fmul_rn(wt[0], a0)), __fmaf_rn(wt[3], a3, __fmul_rn(wt[2], a2)));
         };
@@ -644,8 +839,13 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
       }
     }
 
+    }
+
     // ---- next item
-    if (nx.b < 0) return;
+    if (nx.b < 0) {
+      leave();
+      return;
+    }
     if (nx.b != it.b || nx.kh != it.kh || nx.rg != it.rg) convert_queries(nx);
     it = nx;
     row = row_n;
@@ -752,38 +952,88 @@ __global__ void __launch_bounds__(32 * W) block_merge_kernel(const BlockDecodePa
 }
 
 // ------------------------------------------------------------------- host
+// Units of T tiles that a call has at most.
+int64_t units_of(const BlockDecodeParams& p, int T) {
+  return (int64_t)p.B * block_windows(p.max_ctx + p.M - 1) * p.c.Hkv * ((p.R + 8 * T - 1) / (8 * T));
+}
+
+// Tiles of 8 rows in a unit (1 to 5; float32 queries: to 4), the rows that read a head being
+// dealt into groups of as many.  Large units convert the codes for more rows at once; small
+// ones are more, for the multiprocessors to share.  The choice is the least of an estimate,
+// units a multiprocessor (in thirds, three at a time) times the cost of a unit, 7, 11, 15, 20
+// and 24 us with three of them there (two thirds of that alone), from this table (us a call,
+// bf16 queries, int8 codes, 32 query and 4 kv heads; in brackets what the rule takes):
+//   sequences x keys, columns    at most 1      2       3       4       5 tiles
+//    1 x 100, 8                    [5.0]      6.6     8.2     9.6     9.6
+//    1 x 512, 5                    [8.6]     10.5    13.4    13.4    16.8
+//    1 x 4096, 5                  [10.3]     11.4    14.2    14.3    17.4
+//    4 x 1k..4k, 5                 13.3     [15.9]   18.5    18.4    18.5
+//   16 x 1k..4k, 3                 25.6      27.2   [24.6]   24.6    24.6
+//   16 x 1k..4k, 5                 34.7      35.8    38.3    38.2   [34.3]
+//   16 x 1k..4k, 8                 49.4      40.1    50.9   [46.9]   46.9
+//   64 x 1k..4k, 2                 54.9     [42.1]
+//   64 x 1k..4k, 5                123       108     102     102     [83]
+//   64 x 1k..4k, 8                190       145     149    [130]    130
+//   16 x 16k..32k, 5              277       204     185     186    [150]
+//    1 x 64k, 8                    71       [64]     66      62      62
+//   90 x 100..500, 8               46        39      44     [40]     40
+// (All 64 rows as one unit of 8 tiles, two blocks a multiprocessor: 143 us for 64 x 1k..4k.)
+// Units are counted from max_ctx, as the host does not know the lengths.
+int unit_tiles(const BlockDecodeParams& p) {
+  const int tiles = (p.R + 7) / 8, most = std::min(tiles, p.q_type == KATTN_F32 ? 4 : 5);
+  static const int cost[5] = {7, 11, 15, 20, 24};
+  int best = 1;
+  double least = 0.0;
+  for (int t = 1; t <= most; ++t) {
+    const int groups = (tiles + t - 1) / t;
+    if (t > 1 && (tiles + groups - 1) / groups < t) continue;      // smaller units make as many groups
+    const double a_sm = (double)units_of(p, t) / p.sms, full = std::floor(a_sm / 3.0), rest = a_sm - 3.0 * full;
+    const double time = cost[t - 1] * (full + (rest > 0.0 ? 0.5 + rest / 6.0 : 0.0));
+    if (t == 1 || time < least) {
+      best = t;
+      least = time;
+    }
+  }
+  return best;
+}
+
 template <int T, bool kE4m3, bool kPrecise>
-cudaError_t launch_split(BlockDecodeParams p, const TmaMaps& maps, cudaStream_t stream) {
+cudaError_t launch_split(const BlockDecodeParams& p, const TmaMaps& maps, cudaStream_t stream) {
   const auto kern = block_split_kernel<T, kE4m3, kPrecise>;
   const int smem = (int)sizeof(BlockSmem<T, kPrecise>) + 1024;     // + alignment slack
-  // per device: the blocks that the GPU holds at once; the shared-memory limit is raised
-  // with the first call
-  static std::atomic<int> slots_cache[kMaxDevices], sms_cache[kMaxDevices];
+  static_assert((sizeof(BlockSmem<T, kPrecise>) + 2048) * kPerSm <= 228 * 1024,
+                "with the slack and the reserve of a block");
+  // the shared-memory limit is raised with the first call on a device
+  static std::atomic<bool> raised[kMaxDevices];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const bool cached = dev >= 0 && dev < kMaxDevices;
-  int slots = cached ? slots_cache[dev].load() : 0, sms = cached ? sms_cache[dev].load() : 0;
-  if (slots <= 0 || sms <= 0) {
-    int per_sm = 0;
+  if (!cached || !raised[dev].load()) {
     if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreadsB, smem)) != cudaSuccess) return e;
-    slots = sms * (per_sm > 0 ? per_sm : 1);
-    if (cached) {
-      slots_cache[dev].store(slots);
-      sms_cache[dev].store(sms);
-    }
+    if (cached) raised[dev].store(true);
   }
-  p.sms = sms;
-  return launch_pdl(kern, dim3((unsigned)std::min<int64_t>(block_decode_units(p), slots)), dim3(kThreadsB),
-                    (size_t)smem, stream, p, maps);
+  const int64_t units = units_of(p, T), slots = (int64_t)p.sms * kPerSm;
+  return launch_pdl(kern, dim3((unsigned)std::min(units, slots)), dim3(kThreadsB), (size_t)smem, stream, p, maps);
 }
 template <bool kE4m3>
 cudaError_t launch_split(const BlockDecodeParams& p, const TmaMaps& maps, cudaStream_t stream) {
-  const bool precise = p.q_type == KATTN_F32;
-  if (p.R <= 8) return precise ? launch_split<1, kE4m3, true>(p, maps, stream) : launch_split<1, kE4m3, false>(p, maps, stream);
-  return precise ? launch_split<2, kE4m3, true>(p, maps, stream) : launch_split<2, kE4m3, false>(p, maps, stream);
+  const int tiles = unit_tiles(p);
+  if (p.q_type == KATTN_F32) {
+    switch (tiles) {
+      case 1: return launch_split<1, kE4m3, true>(p, maps, stream);
+      case 2: return launch_split<2, kE4m3, true>(p, maps, stream);
+      case 3: return launch_split<3, kE4m3, true>(p, maps, stream);
+      default: return launch_split<4, kE4m3, true>(p, maps, stream);
+    }
+  }
+  switch (tiles) {
+    case 1: return launch_split<1, kE4m3, false>(p, maps, stream);
+    case 2: return launch_split<2, kE4m3, false>(p, maps, stream);
+    case 3: return launch_split<3, kE4m3, false>(p, maps, stream);
+    case 4: return launch_split<4, kE4m3, false>(p, maps, stream);
+    default: return launch_split<5, kE4m3, false>(p, maps, stream);
+  }
 }
 
 template <int W>
@@ -793,10 +1043,7 @@ cudaError_t launch_merge(const BlockDecodeParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-int64_t block_decode_units(const BlockDecodeParams& p) {
-  const int rows = p.R <= 8 ? 8 : 16;
-  return (int64_t)p.B * block_windows(p.max_ctx + p.M - 1) * p.c.Hkv * ((p.R + rows - 1) / rows);
-}
+int64_t block_decode_units(const BlockDecodeParams& p) { return units_of(p, 1); }
 
 size_t block_decode_workspace_bytes(int B, int M, int Hq, int max_ctx) {
   // Hkv * block_stride(R) <= Hq * (M * (d + 2) + 3) whatever Hkv is
@@ -809,7 +1056,19 @@ void set_block_decode_workspace(BlockDecodeParams& p, void* workspace) {
   p.nwin_max = block_windows(p.max_ctx + p.M - 1);
 }
 
-cudaError_t launch_decode_blocks(const BlockDecodeParams& p, int code_type, cudaStream_t stream) {
+cudaError_t launch_decode_blocks(const BlockDecodeParams& params, int code_type, cudaStream_t stream) {
+  BlockDecodeParams p = params;
+  static std::atomic<int> sms_cache[kMaxDevices];
+  int dev = 0;
+  cudaError_t dev_error = cudaGetDevice(&dev);
+  if (dev_error != cudaSuccess) return dev_error;
+  const bool cached = dev >= 0 && dev < kMaxDevices;
+  p.sms = cached ? sms_cache[dev].load() : 0;
+  if (p.sms <= 0) {
+    dev_error = cudaDeviceGetAttribute(&p.sms, cudaDevAttrMultiProcessorCount, dev);
+    if (dev_error != cudaSuccess) return dev_error;
+    if (cached) sms_cache[dev].store(p.sms);
+  }
   TmaMaps maps;
   const int64_t rows = (int64_t)p.c.Hkv * p.c.cap_rows;
   if (!encode_plane_map(&maps.k, p.c.k, rows) || !encode_plane_map(&maps.v, p.c.v, rows))

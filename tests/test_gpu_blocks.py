@@ -492,6 +492,21 @@ def test_scales_and_scores_of_any_size(dtype):
 
 
 @gpu
+@pytest.mark.parametrize("M,g", [(2, 12), (8, 4), (5, 8), (6, 8), (8, 7), (8, 8), (3, 7), (1, 16)])
+@pytest.mark.parametrize("dtype,code", [("bfloat16", "int8"), ("float16", "e4m3"), ("float32", "int8"),
+                                        ("float32", "e4m3")])
+def test_units_of_any_size_give_the_same_bytes(M, g, dtype, code):
+    # the limit max_ctx chooses how many rows go together (a large one: many); lengths that
+    # leave warps of a block without keys, end inside steps, and move references late
+    c, table, ctx, q = attend_inputs(5, M, 2 * g, 2, [40, 700, 513, 1200, 97], 32, 64, code, dtype,
+                                     seed=M * 10 + g, gain=6.0)
+    few = attend(c, table, ctx, q)
+    check_attend(c, table, ctx, q, few)
+    for limit in (4000, 20000, 60000):
+        assert same(few, attend(c, table, ctx, q, max_ctx=limit)), limit
+
+
+@gpu
 @pytest.mark.parametrize("dtype,code", [("bfloat16", "int8"), ("float32", "e4m3")])
 def test_columns_and_batches_have_the_bytes_of_a_row_alone(dtype, code):
     import torch
