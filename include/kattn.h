@@ -664,8 +664,9 @@ int kattn_read_blocks(const void* k, const float* k_scale, const void* v, const 
  * kattn_decode the query is not quantized.  q, out: q_type (a kattn_dtype) [B][M][Hq][d],
  * 16-byte aligned.
  *   Queries: a row enters scaled by a power of two, its largest element in [2^14, 2^15),
- *   as f16 (bf16 exact down to 2^-28 of the largest; f16 exact) or, float32, as f16 hi +
- *   lo (22 bits, or 2^-39 of the largest).  Products are exact, sums float32.
+ *   as f16 (16-bit queries are exact down to 2^-28 of the row's largest element, and held
+ *   to 2^-39 of it below) or, float32, as f16 hi + lo (22 bits, or 2^-39 of the largest).
+ *   Products are exact, sums float32.
  *   Weights: relative to the row's reference, held as f16 (11 bits; float32 queries: hi +
  *   lo, 22 bits) with steps of 2^-33 of the reference's at the smallest, and summed up as
  *   they are held.  Values, row sums and the output before its one rounding are float32.
@@ -675,9 +676,9 @@ int kattn_read_blocks(const void* k, const float* k_scale, const void* v, const 
  * pool sets KATTN_DEVERR_BAD_PAGE and reads page 0: the sequence's outputs are then
  * unspecified.  A bounded wait for a copy that runs out sets KATTN_DEVERR_TIMEOUT; rows it
  * concerns are then not written, or unspecified.
- * e4m3 codes that are no numbers, and scales that are not finite, do not reach rows that
- * see no key of their 32-key step (codes) or block (scales); they are taken as 0 in steps
- * that some column does not see whole.
+ * e4m3 codes that are no numbers, and v_scales that are not finite, do not reach rows that
+ * see no key of their 32-key step: in a step that some column does not see whole they are
+ * taken as 0.
  * Limits on M, g * M, B and sizes, and sm_scale, as in kattn_decode.
  * Deterministic; the bytes of out[b][j][h] depend only on the row's own query and keys, so
  * column j equals an M = 1 call with ctx_len + j on the same cache, in any batch.

@@ -869,7 +869,7 @@ def append_blocks(k_new, v_new, cu_rows, start, k, k_scale, v, v_scale, block_ta
     workspace = _error_word(workspace, k, index)
     _launch("kattn_append_blocks", index, k_new.data_ptr(), v_new.data_ptr(), x_type, n, Hkv, d, k_stride,
             v_stride, cu_rows.data_ptr(), start.data_ptr(), B, k.data_ptr(), k_scale.data_ptr(), v.data_ptr(),
-            v_scale.data_ptr(), code, cap, block_rows, block_table.data_ptr(), block_table.shape[1], page_rows,
+            v_scale.data_ptr(), code, cap, block_rows, block_table.data_ptr(), block_table.shape[1], int(page_rows),
             table_ptr, n_positions, rot_dim, int(interleaved), q_ptr, Hq, q_stride, q_out_ptr, q_out_stride,
             workspace.data_ptr(), workspace.numel())
     return q_out
@@ -894,6 +894,7 @@ def read_blocks(k, k_scale, v, v_scale, block_table, page_rows: int, cu_rows, st
     index = _device_of(k, "k")
     code, Hkv, cap, d, block_rows = _block_cache(k, k_scale, v, v_scale, index)
     B = _spans(cu_rows, start, block_table, index)
+    n_rows = int(n_rows)
     if n_rows < 0:
         raise ValueError("n_rows must not be negative")
     if out_k is not None or out_v is not None:
@@ -912,7 +913,7 @@ def read_blocks(k, k_scale, v, v_scale, block_table, page_rows: int, cu_rows, st
         raise ValueError("out_k and out_v must have shape [n_rows][Hkv][128]")
     workspace = _error_word(workspace, k, index)
     _launch("kattn_read_blocks", index, k.data_ptr(), k_scale.data_ptr(), v.data_ptr(), v_scale.data_ptr(),
-            code, Hkv, d, cap, block_rows, block_table.data_ptr(), block_table.shape[1], page_rows,
+            code, Hkv, d, cap, block_rows, block_table.data_ptr(), block_table.shape[1], int(page_rows),
             cu_rows.data_ptr(), start.data_ptr(), B, n_rows, out_k.data_ptr(), out_v.data_ptr(), out_type,
             workspace.data_ptr(), workspace.numel())
     return out_k, out_v
@@ -977,8 +978,8 @@ def decode_blocks(q, k, k_scale, v, v_scale, block_table, page_rows: int, ctx_le
     else:
         _check(workspace, torch.uint8, index, "workspace", 1)
     _launch("kattn_decode_blocks", index, q.data_ptr(), q_type, k.data_ptr(), k_scale.data_ptr(), v.data_ptr(),
-            v_scale.data_ptr(), code, cap, block_rows, block_table.data_ptr(), block_table.shape[1], page_rows,
-            ctx_len.data_ptr(), B, M, Hq, Hkv, d, max_ctx, sm_scale, out.data_ptr(), workspace.data_ptr(),
+            v_scale.data_ptr(), code, cap, block_rows, block_table.data_ptr(), block_table.shape[1], int(page_rows),
+            ctx_len.data_ptr(), B, M, Hq, Hkv, d, int(max_ctx), float(sm_scale), out.data_ptr(), workspace.data_ptr(),
             workspace.numel())
     return out
 

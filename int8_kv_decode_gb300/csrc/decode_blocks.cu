@@ -47,6 +47,10 @@ namespace {
 constexpr int kWarpsB = 4, kThreadsB = kWarpsB * 32;
 constexpr float kTop = 9.0f;                      // weights are 2^9 at the reference
 constexpr float kMoveAt = 15.0f;                  // and reach 2^15 before it moves
+// A row whose reference is larger than this takes its scores as they are rounded, x = (S c)
+// - m: x = S c - m in one rounding may be far off at the largest, whose own rounding made m.
+// (Every step of a unit with such a row goes the way of a step that moves references.)
+constexpr float kLarge = 1048576.0f;
 
 // Windows of 512 keys sit at fixed positions, so that a row's bytes depend on its own keys
 // alone.  (Windows of 1024 from key 4096 on: 103 us instead of 99, 64 sequences of 512 to
@@ -527,6 +531,7 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
         sm.failed = 1;
       }
     };
+    bool large = false;                           // some row's reference passes kLarge
     int flying = 0;                               // after giving up: copies on their way (1: K, 2: V, by parity)
 
 #pragma unroll 1
@@ -588,22 +593,31 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
         const float2 f = *reinterpret_cast<const float2*>(&sm.factor[n][2 * c]);
         const float2 cf = f2_mul(f, make_float2(ksb, ksb));
         float2 x[2][2];                           // [half][key g | g + 8]
-        auto scores = [&](float2 ref) {
+        auto scores = [&](float2 ref, bool rounded) {
           const float2 down = make_float2(-ref.x, -ref.y);
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
             for (int k2 = 0; k2 < 2; ++k2)
               x[hf][k2] = f2_fma(make_float2(s[n][hf][2 * k2], s[n][hf][2 * k2 + 1]), cf, down);
+          if (rounded) {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+              for (int k2 = 0; k2 < 2; ++k2) {
+                if (fabsf(ref.x) > kLarge) x[hf][k2].x = __fsub_rn(__fmul_rn(s[n][hf][2 * k2], cf.x), ref.x);
+                if (fabsf(ref.y) > kLarge) x[hf][k2].y = __fsub_rn(__fmul_rn(s[n][hf][2 * k2 + 1], cf.y), ref.y);
+              }
+          }
           if (edge) hide_keys(x, t0 + g, keys_of(n, 0), keys_of(n, 1));
         };
-        scores(m[n]);                             // (a reference of -inf: +inf, above the limit)
+        scores(m[n], false);                      // (a reference of -inf: +inf, above the limit)
         auto largest = [&]() -> float2 {
           return make_float2(fmaxf(fmaxf(x[0][0].x, x[0][1].x), fmaxf(x[1][0].x, x[1][1].x)),
                              fmaxf(fmaxf(x[0][0].y, x[0][1].y), fmaxf(x[1][0].y, x[1][1].y)));
         };
         const float2 most = largest();
-        if (__any_sync(0xffffffffu, most.x > kMoveAt || most.y > kMoveAt)) {
+        if (__any_sync(0xffffffffu, most.x > kMoveAt || most.y > kMoveAt) || large) {
           // A row's reference moves, to where its largest score has the weight 2^kTop.  (Which
           // rows move goes by the sums that asked for it, so it depends on the row alone.)
           auto row_most = [&](float2 v) -> float2 {
@@ -614,8 +628,9 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
             }
             return v;
           };
-          const float2 over = row_most(most);
-          scores(make_float2(0.0f, 0.0f));
+          scores(m[n], true);
+          const float2 over = row_most(largest());
+          scores(make_float2(0.0f, 0.0f), false);
           const float2 top = row_most(largest());
           auto move = [&](float over, float top, float& ref) -> float {    // the factor of what is summed up
             if (!(over > kMoveAt)) return 1.0f;
@@ -625,6 +640,8 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
             return by;
           };
           const float2 al = make_float2(move(over.x, top.x, m[n].x), move(over.y, top.y, m[n].y));
+          large |= __any_sync(0xffffffffu, (fabsf(m[n].x) > kLarge && m[n].x > -INFINITY) ||
+                                               (fabsf(m[n].y) > kLarge && m[n].y > -INFINITY));
           l[n] = f2_mul(l[n], al);
           if (i == 0) {                           // (nothing is summed up yet)
           } else if constexpr (S::kTensor) {
@@ -649,7 +666,13 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
               o[md][n][0] = a0.x; o[md][n][1] = a0.y; o[md][n][2] = a1.x; o[md][n][3] = a1.y;
             }
           }
-          scores(m[n]);
+          scores(m[n], true);
+          // (a reference past 2^27 may lie 16 below the largest)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int k2 = 0; k2 < 2; ++k2)
+              x[hf][k2] = make_float2(fminf(x[hf][k2].x, kMoveAt), fminf(x[hf][k2].y, kMoveAt));
         }
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
@@ -998,21 +1021,35 @@ int unit_tiles(const BlockDecodeParams& p) {
 }
 
 template <int T, bool kE4m3, bool kPrecise>
+cudaError_t raise_limit() {
+  return cudaFuncSetAttribute(block_split_kernel<T, kE4m3, kPrecise>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)sizeof(BlockSmem<T, kPrecise>) + 1024);
+}
+// Every kernel loaded and allowed its shared memory, with the first call on a device: a later
+// call of other sizes may be captured.
+cudaError_t prepare_device() {
+  const cudaError_t e[] = {
+      raise_limit<1, false, false>(), raise_limit<2, false, false>(), raise_limit<3, false, false>(),
+      raise_limit<4, false, false>(), raise_limit<5, false, false>(), raise_limit<1, false, true>(),
+      raise_limit<2, false, true>(),  raise_limit<3, false, true>(),  raise_limit<4, false, true>(),
+      raise_limit<1, true, false>(),  raise_limit<2, true, false>(),  raise_limit<3, true, false>(),
+      raise_limit<4, true, false>(),  raise_limit<5, true, false>(),  raise_limit<1, true, true>(),
+      raise_limit<2, true, true>(),   raise_limit<3, true, true>(),   raise_limit<4, true, true>()};
+  for (const cudaError_t x : e)
+    if (x != cudaSuccess) return x;
+  cudaFuncAttributes a;
+  cudaError_t x = cudaFuncGetAttributes(&a, block_merge_kernel<2>);
+  if (x == cudaSuccess) x = cudaFuncGetAttributes(&a, block_merge_kernel<4>);
+  if (x == cudaSuccess) x = cudaFuncGetAttributes(&a, block_merge_kernel<16>);
+  return x;
+}
+
+template <int T, bool kE4m3, bool kPrecise>
 cudaError_t launch_split(const BlockDecodeParams& p, const TmaMaps& maps, cudaStream_t stream) {
   const auto kern = block_split_kernel<T, kE4m3, kPrecise>;
   const int smem = (int)sizeof(BlockSmem<T, kPrecise>) + 1024;     // + alignment slack
   static_assert((sizeof(BlockSmem<T, kPrecise>) + 2048) * kPerSm <= 228 * 1024,
                 "with the slack and the reserve of a block");
-  // the shared-memory limit is raised with the first call on a device
-  static std::atomic<bool> raised[kMaxDevices];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const bool cached = dev >= 0 && dev < kMaxDevices;
-  if (!cached || !raised[dev].load()) {
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-    if (cached) raised[dev].store(true);
-  }
   const int64_t units = units_of(p, T), slots = (int64_t)p.sms * kPerSm;
   return launch_pdl(kern, dim3((unsigned)std::min(units, slots)), dim3(kThreadsB), (size_t)smem, stream, p, maps);
 }
@@ -1066,6 +1103,7 @@ cudaError_t launch_decode_blocks(const BlockDecodeParams& params, int code_type,
   p.sms = cached ? sms_cache[dev].load() : 0;
   if (p.sms <= 0) {
     dev_error = cudaDeviceGetAttribute(&p.sms, cudaDevAttrMultiProcessorCount, dev);
+    if (dev_error == cudaSuccess) dev_error = prepare_device();
     if (dev_error != cudaSuccess) return dev_error;
     if (cached) sms_cache[dev].store(p.sms);
   }

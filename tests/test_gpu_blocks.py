@@ -356,6 +356,67 @@ def test_bad_spans_and_pages_are_skipped():
 
 
 @gpu
+def test_rows_of_no_sequence_and_queries_in_place():
+    # rows before the first sequence and behind the last are left as they are, in a call with
+    # its queries turned in place inside the fused rows
+    import torch
+    import int8_kv_decode_gb300 as K
+    c = Cache(2, 6, 64, 32, "int8")
+    table = tables([100, 70], 64, 6)
+    ang = torch_angles(128, 96)
+    y = torch.randn((80, 7, D), device="cuda").bfloat16()
+    before, cu, start = y.clone(), [3, 63, 70], [40, 63]
+    pos = np.zeros(80, np.int64)
+    pos[3:63], pos[63:70] = np.arange(40, 100), np.arange(63, 70)
+    want = K.rope(y[:, :3].contiguous(), i32(pos), ang)
+    for i, (a, b) in enumerate(((3, 63), (63, 70))):
+        rows = before[a:b].float().cpu().numpy()
+        k = oracle.blocks.rotate(rows[:, 3:5], ang.cpu().numpy()[pos[a:b]], False)
+        oracle.blocks.append(c.host, "k", k, start[i], table[i], 64)
+        oracle.blocks.append(c.host, "v", rows[:, 5:], start[i], table[i], 64)
+    got = K.append_blocks(y[:, 3:5], y[:, 5:], i32(cu), i32(start), *c.args, i32(table), 64, table=ang,
+                          q=y[:, :3], q_out=y[:, :3], workspace=c.ws)
+    assert got.data_ptr() == y.data_ptr() and K.get_device_status(c.ws) == 0
+    c.check()
+    assert same(y[3:70, :3], want[3:70]) and same(y[:, 3:], before[:, 3:])
+    assert same(y[:3], before[:3]) and same(y[70:], before[70:])
+
+
+@gpu
+def test_offsets_past_32_bits():
+    # a plane of more than 2^31 bytes and values: the last pages written, read, copied and
+    # attended to
+    import torch
+    import int8_kv_decode_gb300 as K
+    pages, page, R = 36000, 512, 64                          # 18.4 M rows of 128: 2.4 GB in each plane
+    k = torch.zeros((1, pages * page, D), dtype=torch.int8, device="cuda")
+    v = torch.zeros_like(k)
+    ks = torch.zeros((1, pages * page // R), device="cuda")
+    vs = torch.zeros_like(ks)
+    host = {"R": R, "e4m3": False, "k": np.zeros((1, 1024, D)), "v": np.zeros((1, 1024, D)),
+            "ks": np.zeros((1, 16), np.float32), "vs": np.zeros((1, 16), np.float32)}
+    r = np.random.default_rng(0)
+    x = r.standard_normal((700, 1, D)).astype(np.float32)
+    t = torch.from_numpy(x).cuda()
+    table, far = np.array([[1, 0]]), i32([[pages - 1, pages - 2]])
+    for n in ("k", "v"):
+        oracle.blocks.append(host, n, x, 0, table[0], page)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    K.append_blocks(t, t, i32([0, 700]), i32([0]), k, ks, v, vs, far, page, workspace=ws)
+    back, _ = K.read_blocks(k, ks, v, vs, far, page, i32([0, 700]), i32([0]), 700, dtype=torch.float32, workspace=ws)
+    rows = oracle.blocks.rows_of(table[0], page, np.arange(700))
+    want = oracle.blocks.values(host, "k", rows).transpose(1, 0, 2)
+    assert (np.abs(back.cpu().numpy() - want) <= 2.0 ** -24 * np.abs(want)).all()
+    q = torch.randn((1, 1, 4, D), device="cuda")
+    out = K.decode_blocks(q, k, ks, v, vs, far, page, i32([700]), 700)
+    from types import SimpleNamespace
+    check_attend(SimpleNamespace(host=host, page=page), table, np.array([700]), q, out)
+    K.copy_pages(k, ks, v, vs, i32([pages - 1, pages - 2]), i32([0, pages - 3]), page, workspace=ws)
+    assert same(out, K.decode_blocks(q, k, ks, v, vs, i32([[0, pages - 3]]), page, i32([700]), 700))
+    assert K.get_device_status(ws) == 0
+
+
+@gpu
 def test_copy_pages_of_a_block_scaled_cache():
     import torch
     import int8_kv_decode_gb300 as K
@@ -504,6 +565,20 @@ def test_units_of_any_size_give_the_same_bytes(M, g, dtype, code):
     check_attend(c, table, ctx, q, few)
     for limit in (4000, 20000, 60000):
         assert same(few, attend(c, table, ctx, q, max_ctx=limit)), limit
+
+
+@gpu
+@pytest.mark.parametrize("dtype,code", [("bfloat16", "int8"), ("float32", "e4m3")])
+@pytest.mark.parametrize("gain", [1e3, 1e6, 1e9, 1e12])
+def test_scores_of_any_size(dtype, code, gain):
+    # scores whose float32 neighbours lie whole powers of two apart: a key then takes all of
+    # a row's weight, unless others lie within the scores' rounding (the tolerance grows with
+    # the size of the scores and leaves those rows to the finiteness alone)
+    c, table, ctx, q = attend_inputs(4, 2, 8, 2, [5, 130, 600, 1500], 32, 64, code, dtype, seed=12, gain=gain)
+    got = attend(c, table, ctx, q)
+    check_attend(c, table, ctx, q, got)
+    assert same(got, attend(c, table, ctx, q, max_ctx=60000))
+    assert same(got[:, 1:], attend(c, table, ctx + 1, q[:, 1:].contiguous()))
 
 
 @gpu
