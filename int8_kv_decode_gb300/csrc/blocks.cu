@@ -4,6 +4,12 @@
 // s = max |x| / 127 (int8) or / 448 (e4m3) over the block's rows.  Rows come in over
 // time: where new rows need a larger scale than the block has, the rows that stay are
 // coded again under the new one, code' = round(code * (s_old / s)).
+//
+// What bounds them.  Writing 7 prompts of 300 to 2500 rows (7851 in all; 32 query and 4 kv
+// heads, bf16; 157 MB, 23 us at the measured copy rate): 28 us, 5.5 TB/s, by issue (70%):
+// unpacking, turning and coding are some 30 instructions an element and lane.  A row for each
+// of 64 sequences: 5 us, the chain of loads span, page, scale.  Reading 150k rows of 4 heads as
+// bf16 (463 MB, 68 us): 75 us, 6.2 TB/s; 700 rows: 4.2 us, latency.
 #include <algorithm>
 #include <type_traits>
 
@@ -19,15 +25,15 @@ __device__ __forceinline__ int64_t table_keys(const BlockCache& c) {
 }
 // The rows of a sequence and its first key; whether the rows lie in the call's and the
 // keys in the table's row.
-struct Span {
+struct RowSpan {
   int b, c0, n, start;
   bool valid;
 };
-__device__ __forceinline__ Span make_span(const SpanParams& s, int b, int c0, int c1, int start, int64_t most) {
+__device__ __forceinline__ RowSpan make_span(const SpanParams& s, int b, int c0, int c1, int start, int64_t most) {
   const bool rises = c0 >= 0 && c0 <= c1 && c1 <= s.rows;
   return {b, c0, rises ? c1 - c0 : 0, start, rises && start >= 0 && (int64_t)start + (c1 - c0) <= most};
 }
-__device__ __forceinline__ Span span_of(const SpanParams& s, int b, int64_t most) {
+__device__ __forceinline__ RowSpan span_of(const SpanParams& s, int b, int64_t most) {
   return make_span(s, b, ld_fresh(s.cu + b), ld_fresh(s.cu + b + 1), ld_fresh(s.start + b), most);
 }
 __device__ __forceinline__ void flag_bad_spans(const SpanParams& s, int64_t most) {
@@ -39,7 +45,7 @@ __device__ __forceinline__ void flag_bad_spans(const SpanParams& s, int64_t most
 // none), by a whole warp: 64 of them a step.  The last step's loads hold its span too, so
 // that a call of up to 64 sequences goes to memory once.
 template <typename Key>
-__device__ __forceinline__ Span find_span(const SpanParams& s, int64_t t, int64_t most, int lane, Key key) {
+__device__ __forceinline__ RowSpan find_span(const SpanParams& s, int64_t t, int64_t most, int lane, Key key) {
   int lo = 0, n = s.B;
   auto count = [&](int step, int x, int y) {      // those of lo + i step, i < 64, i step < n; x, y: cu of lane, lane + 32
     const int i = lane * step, j = (lane + 32) * step;
@@ -121,7 +127,7 @@ __global__ void __launch_bounds__(kBlock * 4) append_kernel(const AppendParams p
     turn_heads<T, T, kInter>(static_cast<const T*>(p.q) + row * p.q_stride + h0 * kD,
                              static_cast<T*>(p.q_out) + row * p.q_out_stride + h0 * kD,
                              min(kTurnHeads, p.Hq - h0), p.table, p.half, lane, [&](bool& know) {
-      const Span s = find_span(p.s, row, most, lane, [](int, int cu) { return (int64_t)cu; });
+      const RowSpan s = find_span(p.s, row, most, lane, [](int, int cu) { return (int64_t)cu; });
       know = s.valid;
       return row < s.c0 || row >= s.c0 + s.n ? -1 : know ? s.start + row - s.c0 : 0;   // (-1: no sequence's row)
     });
@@ -133,7 +139,7 @@ __global__ void __launch_bounds__(kBlock * 4) append_kernel(const AppendParams p
   const int plane = (int)(blockIdx.x - unit * (2u * p.c.Hkv));
   const bool is_k = plane < p.c.Hkv;
   const int h = is_k ? plane : plane - p.c.Hkv;
-  const Span span = find_span(p.s, unit, most, lane, [](int i, int cu) { return (int64_t)(cu / R) + 2 * i; });
+  const RowSpan span = find_span(p.s, unit, most, lane, [](int i, int cu) { return (int64_t)(cu / R) + 2 * i; });
   if (!span.valid || span.n == 0) return;
   const int b = span.b;
   const int st = span.start, n = span.n;
@@ -258,7 +264,7 @@ __global__ void __launch_bounds__(256, 4) read_kernel(const ReadParams p) {
     }
     const int c0 = __shfl_sync(0xffffffffu, begins, k), c1 = __shfl_sync(0xffffffffu, ends, k);
     const int st = __shfl_sync(0xffffffffu, starts, k);
-    Span s = make_span(p.s, b0 + k, c0, c1, st, most);
+    RowSpan s = make_span(p.s, b0 + k, c0, c1, st, most);
     if (c1 <= r) {                                // (k = 31: further on)
       int b = b0 + k;
       while (b + 1 < p.s.B && r >= ld_fresh(p.s.cu + b + 1)) ++b;

@@ -33,7 +33,7 @@
 // MB, 39 us): 55 us, split 52, of which the second MMAs for hi + lo take tensor pipe to 34%.
 // With more rows, issue and the latency of a step's chain at 12 warps a multiprocessor (870
 // instructions a step at T = 2, 320 of them to make f16 of the codes; 1500 at T = 5): 16
-// sequences of 1k to 4k keys, 40 rows a head, 34 us; 64 of them 81 us.  One sequence of 257
+// sequences of 1k to 4k keys, 40 rows a head, 34 us; 64 of them 77 us.  One sequence of 257
 // keys: 6.1 us, latency alone.
 #include <cmath>
 
@@ -711,7 +711,8 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
       }
       const float2 gain = make_float2(vsb, vsb);
       const uint32_t va = vbuf + (uint32_t)((lane & 15) * kD + (((lane >> 4) ^ (lane & 7)) << 4));
-#pragma unroll
+      constexpr int kUnrollV = S::kTensor ? 1 : 4;        // (fewer instructions to fetch: 1%)
+#pragma unroll kUnrollV
       for (int q = 0; q < 8; q += 2) {
         uint32_t vw[2][4];
         ldsm_x4_trans<0>(vw[0], va ^ (uint32_t)(q << 4));
@@ -974,6 +975,44 @@ __global__ void __launch_bounds__(32 * W) block_merge_kernel(const BlockDecodePa
   store_out2(p.out, p.q_type, at + 2, __fdiv_rn(O.z, l), __fdiv_rn(O.w, l));
 }
 
+// Rows of at most kSums windows: a warp each, all its windows on their way at once.  The same
+// sums: each of the sixteen has one window.
+constexpr int kRowsOfMerge = 4;
+__global__ void __launch_bounds__(32 * kRowsOfMerge) block_merge_short_kernel(const BlockDecodeParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * kRowsOfMerge + (threadIdx.x >> 5);
+  const int b = (int)(row / (p.M * p.Hq)), at = (int)(row - (int64_t)b * p.M * p.Hq), j = at / p.Hq, head = at - j * p.Hq;
+  if (b >= p.B) return;
+  const int ctx = __ldcg(p.ctx_len + b), R = p.R;
+  const int kh = head / p.g, rr = j * p.g + head - kh * p.g;
+  const size_t stride = (size_t)p.c.Hkv * block_stride(R);
+  const float* base = p.partials + ((size_t)b * p.nwin_max * p.c.Hkv + kh) * block_stride(R);
+  const float* mlcol = base + (size_t)R * kD + 2 * rr;
+  const float* ocol = base + (size_t)rr * kD + 4 * lane;
+  const bool valid = context_valid(p, ctx) && block_windows(ctx + p.M - 1) > 1;
+  griddep_wait();                                 // every partial is in place
+  if (!valid) return;
+  const int ns = block_windows(ctx + j);
+  float4 v[kSums];
+#pragma unroll
+  for (int s = 0; s < kSums; ++s)
+    v[s] = s < ns ? __ldcg(reinterpret_cast<const float4*>(ocol + s * stride)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const float2 st = lane < ns ? __ldcg(reinterpret_cast<const float2*>(mlcol + lane * stride))
+                              : make_float2(-INFINITY, 0.0f);
+  const float w = fast_exp2(__fsub_rn(st.x, warp_max(st.x)));
+  const float l = warp_sum(__fmul_rn(w, st.y));
+  float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int s = 0; s < kSums; ++s) {
+    const float wn = __shfl_sync(0xffffffffu, w, s);
+    const float4 x = make_float4(__fmul_rn(wn, v[s].x), __fmul_rn(wn, v[s].y), __fmul_rn(wn, v[s].z), __fmul_rn(wn, v[s].w));
+    O = s == 0 ? x : make_float4(__fadd_rn(O.x, x.x), __fadd_rn(O.y, x.y), __fadd_rn(O.z, x.z), __fadd_rn(O.w, x.w));
+  }
+  const int64_t to = row * kD + 4 * lane;
+  store_out2(p.out, p.q_type, to, __fdiv_rn(O.x, l), __fdiv_rn(O.y, l));
+  store_out2(p.out, p.q_type, to + 2, __fdiv_rn(O.z, l), __fdiv_rn(O.w, l));
+}
+
 // ------------------------------------------------------------------- host
 // Units of T tiles that a call has at most.
 int64_t units_of(const BlockDecodeParams& p, int T) {
@@ -987,20 +1026,22 @@ int64_t units_of(const BlockDecodeParams& p, int T) {
 // and 24 us with three of them there (two thirds of that alone), from this table (us a call,
 // bf16 queries, int8 codes, 32 query and 4 kv heads; in brackets what the rule takes):
 //   sequences x keys, columns    at most 1      2       3       4       5 tiles
-//    1 x 100, 8                    [5.0]      6.6     8.2     9.6     9.6
-//    1 x 512, 5                    [8.6]     10.5    13.4    13.4    16.8
-//    1 x 4096, 5                  [10.3]     11.4    14.2    14.3    17.4
-//    4 x 1k..4k, 5                 13.3     [15.9]   18.5    18.4    18.5
-//   16 x 1k..4k, 3                 25.6      27.2   [24.6]   24.6    24.6
-//   16 x 1k..4k, 5                 34.7      35.8    38.3    38.2   [34.3]
-//   16 x 1k..4k, 8                 49.4      40.1    50.9   [46.9]   46.9
-//   64 x 1k..4k, 2                 54.9     [42.1]
-//   64 x 1k..4k, 5                123       108     102     102     [83]
-//   64 x 1k..4k, 8                190       145     149    [130]    130
-//   16 x 16k..32k, 5              277       204     185     186    [150]
-//    1 x 64k, 8                    71       [64]     66      62      62
-//   90 x 100..500, 8               46        39      44     [40]     40
-// (All 64 rows as one unit of 8 tiles, two blocks a multiprocessor: 143 us for 64 x 1k..4k.)
+//    1 x 100, 8                    [5.2]      6.9     8.9    10.1
+//    1 x 512, 5                    [8.8]     10.9    13.6             18.0
+//    1 x 4096, 5                  [10.6]     12.0    14.9             19.1
+//    4 x 1k..4k, 5                 14.5     [16.6]   19.1             20.2
+//   16 x 1k..4k, 3                 25.9      27.2   [25.0]
+//   16 x 1k..4k, 5                 33.9      35.7    37.7            [33.7]
+//   16 x 1k..4k, 8                 46.9     [38.0]   48.9    44.4
+//   64 x 1k..4k, 2                 51.6     [40.4]
+//   64 x 1k..4k, 3                 72.9      71.8   [53.3]
+//   64 x 1k..4k, 5                115       103      94              [77]
+//   64 x 1k..4k, 8                177       137     136    [118]
+//   16 x 16k..32k, 5              280       215     190             [154]
+//    1 x 64k, 8                    73       [66]     68      64
+//   90 x 100..500, 8               47        41      46     [40]
+// (All 64 rows as one unit of 8 tiles, two blocks a multiprocessor: 143 us for 64 x 1k..4k, 8,
+// when 4 tiles took 130.)
 // Units are counted from max_ctx, as the host does not know the lengths.
 int unit_tiles(const BlockDecodeParams& p) {
   const int tiles = (p.R + 7) / 8, most = std::min(tiles, p.q_type == KATTN_F32 ? 4 : 5);
@@ -1040,6 +1081,7 @@ cudaError_t prepare_device() {
   cudaFuncAttributes a;
   cudaError_t x = cudaFuncGetAttributes(&a, block_merge_kernel<2>);
   if (x == cudaSuccess) x = cudaFuncGetAttributes(&a, block_merge_kernel<4>);
+  if (x == cudaSuccess) x = cudaFuncGetAttributes(&a, block_merge_short_kernel);
   if (x == cudaSuccess) x = cudaFuncGetAttributes(&a, block_merge_kernel<16>);
   return x;
 }
@@ -1114,9 +1156,15 @@ cudaError_t launch_decode_blocks(const BlockDecodeParams& params, int code_type,
   const cudaError_t e = code_type == KATTN_E4M3 ? launch_split<true>(p, maps, stream)
                                                 : launch_split<false>(p, maps, stream);
   if (e != cudaSuccess || p.nwin_max <= 1) return e;
-  // Warps a row, by the windows that it may have: 2 of 120k to 131k keys, 8 rows on each
-  // of 4 heads, take 56 us with 16 and 63 with 4; 16 sequences of 1k to 4k keys, 40 rows a
-  // head, 37.9 us with 2 and 38.5 with 4; 64 of 512 to 32768 keys 96 us with 2, 4 or 8.
+  // Warps a row, by the windows that it may have: 64 sequences of 1k to 4k keys, 5 columns 77
+  // us a call with one (the short form), 86 with 2; 16 sequences 34 and 36; 2 of 120k to 131k
+  // keys, 8 rows on each of 4 heads, 56 us with 16 and 63 with 4; 64 of 512 to 32768 keys 96
+  // us with 2, 4 or 8.
+  if (p.nwin_max <= kSums) {
+    const int64_t rows = (int64_t)p.B * p.M * p.Hq;
+    return launch_pdl(block_merge_short_kernel, dim3((unsigned)((rows + kRowsOfMerge - 1) / kRowsOfMerge)),
+                      dim3(32 * kRowsOfMerge), 0, stream, p);
+  }
   if (p.nwin_max <= 32) return launch_merge<2>(p, stream);
   if (p.nwin_max <= 128) return launch_merge<4>(p, stream);
   return launch_merge<16>(p, stream);

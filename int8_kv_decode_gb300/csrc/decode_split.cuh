@@ -331,6 +331,13 @@ __device__ __forceinline__ int swz(int row, int chunk) {
 
 // Programmatic dependent launch: wait until the preceding grid has finished
 // and its writes are visible / let the next grid begin its launch.
+__device__ __forceinline__ void griddep_wait() {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+}
+__device__ __forceinline__ void griddep_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+}
+
 // Plain bulk copy global -> shared (16-byte aligned, size a multiple of 16).
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
                                           uint64_t* bar) {
@@ -1053,6 +1060,25 @@ decode_fast_kernel(const DecodeParams p, const __grid_constant__ TmaMaps maps) {
     }
     prod_ok = produce();
   }
+}
+
+// Launch with programmatic stream serialization: the kernel may start while
+// the previous one on the stream drains; it waits (griddepcontrol.wait)
+// before it reads anything that one wrote.
+template <typename... Params, typename... Args>
+cudaError_t launch_pdl(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem,
+                       cudaStream_t stream, Args... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 constexpr int kMaxDevices = 64;

@@ -1,7 +1,9 @@
 // Rotary positions of query and key heads, and the table of their angles.
 //
 // A warp takes eight heads of a row, two at a time: the row's angles are loaded once for
-// them.  Bound by memory: an element is read and written once, for three operations.
+// them.  Bound by memory: an element is read and written once, for three operations.  8192
+// rows of 36 bf16 heads to float32 (231 MB, 34.0 us at the measured copy rate): 34.6 us; 16 rows:
+// 1.7 us, a launch.
 #include <algorithm>
 
 #include "blocks_internal.cuh"

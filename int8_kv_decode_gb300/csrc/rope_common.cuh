@@ -2,10 +2,18 @@
 // channels a lane in two runs of four, so that both channels of a pair are the lane's.
 #pragma once
 
+#include "decode_split.cuh"      // programmatic launches
 #include "quant_common.cuh"
 
 namespace kattn {
 namespace {
+
+// A load, after griddep_wait, of what a kernel before may have written while this one had
+// started: a plain one, as the read-only path takes its data for constant since the start.
+template <typename T>
+__device__ __forceinline__ T ld_fresh(const T* p) {
+  return *p;
+}
 
 // Where the two runs of lane l (of 16) begin, and whether its channels are rotated.
 //   half layout: channel i < half turns with channel i + half, by angle i: the runs are
