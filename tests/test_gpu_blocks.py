@@ -724,3 +724,140 @@ def test_streams_graphs_and_devices():
             res.append(r)
     torch.cuda.synchronize()
     assert same(res[0], want) and same(res[1], want)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("sm_scale", [-0.11, 0.5])
+def test_other_scales_of_the_scores(dtype, sm_scale):
+    # a negative one is the positive one with the queries' signs turned
+    c, table, ctx, q = attend_inputs(3, 2, 8, 2, [33, 600, 1], 32, 64, "int8", dtype, seed=15)
+    got = attend(c, table, ctx, q, sm_scale=sm_scale)
+    check_attend(c, table, ctx, q if sm_scale > 0 else -q, got, sm_scale=abs(sm_scale))
+
+
+@gpu
+@pytest.mark.parametrize("M,g,dtype", [(1, 4, "bfloat16"), (3, 7, "float32"), (5, 8, "float16")])
+def test_queries_that_are_no_numbers_stay_in_their_row(M, g, dtype):
+    import torch
+    for ctx in (1, 32, 500, 9000):
+        c, table, n, q = attend_inputs(2, M, 2 * g, 2, ctx, 32, 64, "int8", dtype, seed=16)
+        want = attend(c, table, n, q)
+        for bad in (float("nan"), float("inf")):
+            x = q.clone()
+            x[0, M - 1, g - 1, 5] = bad
+            got = attend(c, table, n, x)
+            assert torch.isnan(got[0, M - 1, g - 1]).all()
+            got[0, M - 1, g - 1] = want[0, M - 1, g - 1]
+            assert same(want, got), (ctx, bad)
+
+
+@gpu
+def test_one_call_of_many_sequences_is_many_calls_of_few():
+    # so many that the search for a row's sequence goes three steps, runs of them empty
+    import torch
+    import int8_kv_decode_gb300 as K
+    r = np.random.default_rng(3)
+    B, per = 5000, 50
+    lens = r.integers(0, 3, B)
+    lens[700:1400] = 0
+    lens[4990:] = 0
+    start = r.integers(0, 30, B)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    n = int(cu[-1])
+    caches = [Cache(1, B, 32, 32, "int8") for _ in range(2)]
+    table = i32(r.permutation(B)[:, None])
+    x = torch.randn((n, 3, D), device="cuda")
+    ang = K.rope_table(64)
+
+    def run(c, a, b):
+        rows = x[cu[a]:cu[b]]
+        args = (i32(cu[a:b + 1] - cu[a]), i32(start[a:b]))
+        turned = K.append_blocks(rows[:, 1:2], rows[:, 2:], *args, *c.args, table[a:b], 32, table=ang,
+                                 q=rows[:, :1], workspace=c.ws)
+        back = K.read_blocks(*c.args, table[a:b], 32, *args, int(cu[b] - cu[a]), workspace=c.ws)
+        return (turned, *back)
+
+    whole = run(caches[0], 0, B)
+    parts = [run(caches[1], a, a + per) for a in range(0, B, per) if cu[a + per] > cu[a]]
+    for i, t in enumerate(whole):
+        assert same(t, torch.cat([p[i] for p in parts]))
+    for a, b in zip(caches[0].args, caches[1].args):
+        assert same(a, b)
+    assert K.get_device_status(caches[0].ws) == 0
+
+
+@gpu
+def test_only_keys_or_only_values_read_back():
+    import torch
+    import int8_kv_decode_gb300 as K
+    from int8_kv_decode_gb300 import _lib
+    c = Cache(3, 4, 64, 32, "int8")
+    table = i32(tables([120, 70], 64, 4, spare=0))
+    cu, start = i32([0, 90, 130]), i32([20, 30])
+    want = K.read_blocks(*c.args, table, 64, cu, start, 140, dtype=torch.float32, workspace=c.ws)
+    for one in (0, 1):
+        out = torch.full((140, 3, D), 7.0, device="cuda")
+        ptr = [None, None]
+        ptr[one] = out.data_ptr()
+        k, ks, v, vs = c.args
+        status = _lib.load().kattn_read_blocks(
+            k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), 0, 3, D, k.shape[1], 32, table.data_ptr(),
+            table.shape[1], 64, cu.data_ptr(), start.data_ptr(), 2, 140, *ptr, 0, c.ws.data_ptr(), c.ws.numel(),
+            torch.cuda.current_stream().cuda_stream)
+        assert status == 0 and K.get_device_status(c.ws) == 0
+        assert same(out[:130], want[one][:130]) and (out[130:] == 7.0).all()
+
+
+@gpu
+def test_captures_with_other_work_before_and_beside():
+    # a step whose rows come from a copy, a fill and another stream's kernel in the capture,
+    # and whose outputs another stream takes
+    import torch
+    import int8_kv_decode_gb300 as K
+    c, table, ctx, q = attend_inputs(3, 1, 8, 2, [40, 300, 900], 32, 64, "int8", "bfloat16", seed=17)
+    tab, cu, start, length = i32(table), i32(np.arange(4)), i32(ctx - 1), i32(ctx)
+    ang = K.rope_table(1000)
+    src = torch.randn((3, 12, D), device="cuda").bfloat16()
+    rows, qout, out = torch.zeros_like(src), torch.empty_like(q), torch.empty_like(q)
+    both = torch.empty((2, *out.shape), device="cuda", dtype=out.dtype)
+    side = torch.cuda.Stream()
+    ws = K.alloc_blocks_workspace(3, 1, 8, 900)
+
+    def step():
+        main = torch.cuda.current_stream()
+        rows.zero_()
+        rows[:, :8].copy_(src[:, :8])
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            torch.add(src[:, 8:], 1.0, out=rows[:, 8:])
+        main.wait_stream(side)
+        K.append_blocks(rows[:, 8:10], rows[:, 10:], cu, start, *c.args, tab, 64, table=ang, q=rows[:, :8],
+                        q_out=qout.view(3, 8, D), workspace=ws)
+        K.decode_blocks(qout, *c.args, tab, 64, length, 900, out=out, workspace=ws)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            both[0].copy_(out)
+        K.decode_blocks(qout, *c.args, tab, 64, length, 900, out=both[1], workspace=ws)
+        main.wait_stream(side)
+
+    step()
+    torch.cuda.synchronize()
+    state = [t.clone() for t in c.args]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        src.normal_()
+        for t, s in zip(c.args, state):
+            t.copy_(s)
+        step()
+        want = [t.clone() for t in (out, both, qout, *c.args)]
+        out.zero_()
+        both.zero_()
+        for t, s in zip(c.args, state):
+            t.copy_(s)
+        graph.replay()
+        assert all(same(a, b) for a, b in zip(want, (out, both, qout, *c.args)))
+        assert same(both[0], both[1])
+    assert K.get_device_status(ws) == 0
