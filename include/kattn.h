@@ -588,7 +588,7 @@ int kattn_rope_table(const double* freq, int n_positions, int rot_dim, float* ta
  * they must not overlap.
  * positions: int32 [n_rows] on the device.  A row of a negative position (padding) is
  * not written; a position at or past n_positions gives NaN.
- * n_rows or n_heads 0 is a no-op. */
+ * n_heads at most 2^23.  n_rows or n_heads 0 is a no-op. */
 int kattn_rope(const void* x, int x_type, int n_rows, int n_heads, int d, int64_t x_stride,
                const int32_t* positions, const float* table, int n_positions, int rot_dim,
                int interleaved, void* out, int out_type, int64_t out_stride, void* stream);

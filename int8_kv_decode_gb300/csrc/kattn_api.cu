@@ -337,6 +337,9 @@ int set_spans(SpanParams& s, const int32_t* cu_rows, const int32_t* start, int B
   return KATTN_OK;
 }
 
+constexpr int64_t kMaxUnits = INT32_MAX / 4;      // of a decode call, counted in int32
+constexpr int kMaxHeads = 1 << 23;                // of a row: the kernels count its channels in int32
+
 // Heads of 128 channels at rows of `stride` elements, taken four elements at a time.
 int check_heads(const void* x, int type, int64_t stride, int heads) {
   if (stride < (int64_t)heads * kD) return KATTN_ERR_INVALID_ARG;
@@ -791,6 +794,7 @@ int kattn_rope(const void* x, int x_type, int n_rows, int n_heads, int d, int64_
   if (!is_dtype(x_type) || (out_type != x_type && out_type != KATTN_F32)) return KATTN_ERR_INVALID_ARG;
   if (n_rows < 0 || n_heads < 0) return KATTN_ERR_INVALID_ARG;
   if (d != KATTN_HEAD_DIM) return KATTN_ERR_UNSUPPORTED;
+  if (n_heads > kMaxHeads) return KATTN_ERR_UNSUPPORTED;
   if ((int64_t)n_rows * ((n_heads + 3) / 4) > INT32_MAX) return KATTN_ERR_UNSUPPORTED;   // one grid axis
   if (n_rows == 0 || n_heads == 0) return KATTN_OK;
   int st = check_rope_table(table, n_positions, rot_dim, interleaved);
@@ -836,13 +840,14 @@ int kattn_append_blocks(const void* k_new, const void* v_new, int x_type, int n_
   if ((q == nullptr) != (q_out == nullptr) || (q && !table)) return KATTN_ERR_INVALID_ARG;
   if (q) {
     if (Hq < 1) return KATTN_ERR_INVALID_ARG;
+    if (Hq > kMaxHeads) return KATTN_ERR_UNSUPPORTED;
     st = check_heads(q, x_type, q_stride, Hq);
     if (st == KATTN_OK) st = check_heads(q_out, x_type, q_out_stride, Hq);
     if (st != KATTN_OK) return st;
     if (q == q_out && q_stride != q_out_stride) return KATTN_ERR_INVALID_ARG;
   }
   // one grid axis: the blocks of rows of every plane, and the queries
-  if (((int64_t)n_rows / block_rows + 2 * (int64_t)B) * 2 * n_kv + (int64_t)n_rows * ((Hq + 3) / 4) > INT32_MAX)
+  if (((int64_t)n_rows / block_rows + 2 * (int64_t)B) * 2 * n_kv + (q ? (int64_t)n_rows * ((Hq + 3) / 4) : 0) > INT32_MAX)
     return KATTN_ERR_UNSUPPORTED;
   st = set_spans(p.s, cu_rows, start, B, n_rows, workspace, workspace_bytes);
   if (st != KATTN_OK) return st;
@@ -888,8 +893,18 @@ int kattn_read_blocks(const void* k, const float* k_scale, const void* v, const 
 }
 
 size_t kattn_blocks_workspace_size(int B, int M, int Hq, int max_ctx) {
-  if (B < 1 || M < 1 || M > KATTN_MAX_M || Hq < 1 || max_ctx < 1) return 0;
-  if ((int64_t)max_ctx + M - 1 > (int64_t)INT32_MAX / 2) return 0;    // as the call refuses it
+  // 0 as well for what the call refuses, however many kv heads there are
+  if (B < 1 || B > 65535 || M < 1 || M > KATTN_MAX_M || Hq < 1 || max_ctx < 1) return 0;
+  if ((int64_t)max_ctx + M - 1 > (int64_t)INT32_MAX / 2) return 0;
+  BlockDecodeParams p{};
+  p.B = B;
+  p.M = M;
+  p.max_ctx = max_ctx;
+  p.R = 1;
+  const int64_t kv = ((int64_t)Hq * M + KATTN_MAX_ROWS - 1) / KATTN_MAX_ROWS;    // at least
+  if (kv > 65535) return 0;
+  p.c.Hkv = (int)kv;
+  if (block_decode_units(p) > kMaxUnits) return 0;
   return block_decode_workspace_bytes(B, M, Hq, max_ctx);
 }
 
@@ -902,7 +917,7 @@ int kattn_decode_blocks(const void* q, int q_type, const void* k, const float* k
   if (!is_dtype(q_type) || B < 0 || B > 65535 || M < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_ctx < 1)
     return KATTN_ERR_INVALID_ARG;
   if (!std::isfinite(sm_scale)) return KATTN_ERR_INVALID_ARG;
-  if (d != KATTN_HEAD_DIM || M > KATTN_MAX_M || (Hq / Hkv) * M > KATTN_MAX_ROWS) return KATTN_ERR_UNSUPPORTED;
+  if (d != KATTN_HEAD_DIM || M > KATTN_MAX_M || Hq / Hkv > KATTN_MAX_ROWS / M) return KATTN_ERR_UNSUPPORTED;
   if ((int64_t)max_ctx + M - 1 > (int64_t)INT32_MAX / 2) return KATTN_ERR_INVALID_ARG;
   if (B == 0) return KATTN_OK;
   BlockDecodeParams p{};
@@ -922,7 +937,7 @@ int kattn_decode_blocks(const void* q, int q_type, const void* k, const float* k
   p.R = p.g * M;
   p.max_ctx = max_ctx;
   p.sm_scale = resolve_sm_scale(sm_scale, KATTN_HEAD_DIM);
-  if (block_decode_units(p) > (int64_t)INT32_MAX / 4) return KATTN_ERR_UNSUPPORTED;   // counted in int32
+  if (block_decode_units(p) > kMaxUnits) return KATTN_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < block_decode_workspace_bytes(B, M, Hq, max_ctx))
     return KATTN_ERR_WORKSPACE;

@@ -267,3 +267,21 @@ def test_oracle_attention_against_the_row_scaled_oracle():
     out, mass, size = oracle.blocks.decode(q, c, np.array([[0, 1]]), 32, [50])
     assert np.allclose(out, want, rtol=1e-4, atol=1e-4 * mass.max())
     assert (mass >= np.abs(out) - 1e-12).all() and (size > 0).all()
+
+
+def test_sizes_whose_products_pass_32_bits(lib):
+    huge = 2 ** 31 - 1
+    # g * M = 2^32, more heads than a grid's axis numbers
+    assert call(lib.kattn_decode_blocks, DECODE, M=8, Hq=2 ** 29, Hkv=1, ws_bytes=BIG) == UNSUPPORTED
+    for heads in (huge, huge - 3, 2 ** 28):
+        wide = dict(rows=8, heads=heads, pos=FAKE + 2, xs=heads * 128 + 512, os=heads * 128 + 512)
+        assert call(lib.kattn_rope, ROPE, **wide) == UNSUPPORTED, heads
+        assert call(lib.kattn_append_blocks, APPEND, rows=8, Hq=heads, qs=heads * 128 + 512,
+                    qos=heads * 128 + 512) == UNSUPPORTED, heads
+    # a workspace for no call: 0
+    size = lib.kattn_blocks_workspace_size
+    for sizes in ((65536, 1, 8, 100), (1, 1, huge, 100), (huge, 8, huge, 2 ** 29), (65535, 8, 2 ** 22, 2 ** 29),
+                  (65535, 1, 64, 2 ** 29)):
+        assert size(*sizes) == 0, sizes
+    # the largest that a call takes: its bytes count past 32 bits
+    assert size(65535, 8, 8, 4089) == 256 + 65535 * 8 * 8 * (8 * 130 + 3) * 4
