@@ -9,7 +9,7 @@
 // heads, bf16; 157 MB, 23 us at the measured copy rate): 28 us, 5.5 TB/s, by issue (70%):
 // unpacking, turning and coding are some 30 instructions an element and lane.  A row for each
 // of 64 sequences: 5 us, the chain of loads span, page, scale.  Reading 150k rows of 4 heads as
-// bf16 (463 MB, 68 us): 75 us, 6.2 TB/s; 700 rows: 4.2 us, latency.
+// bf16 (463 MB, 68 us): 75 us, 6.2 TB/s; 700 rows: 2.5 us, latency.
 #include <algorithm>
 #include <type_traits>
 
@@ -225,14 +225,14 @@ __global__ void __launch_bounds__(kBlock * 4) append_kernel(const AppendParams p
 }
 
 // ------------------------------------------------------------------- read
-// A warp looks 32 rows up, one a lane, and takes them from one of the 2 Hkv planes of K and
-// V: all their codes are loaded before the first become values.  A lane takes as many codes
+// A warp looks 8 or 16 rows up, one a lane, and takes them from one of the 2 Hkv planes of K
+// and V: all their codes are loaded before the first become values.  A lane takes as many codes
 // of a row as make a 16-byte store, so that loads and stores of a row are whole.  The warps
 // of a block take the planes of the same rows, whose values lie side by side.
-template <typename O, bool kE4m3>
+template <typename O, bool kE4m3, int kTile>
 __global__ void __launch_bounds__(256, 4) read_kernel(const ReadParams p) {
   constexpr int kPer = 16 / sizeof(O), kLanes = kD / kPer;       // codes a lane, lanes a row
-  constexpr int kRows = 32 / kLanes, kLoads = 32 / kRows;        // rows a load, loads
+  constexpr int kRows = 32 / kLanes, kLoads = kTile / kRows;     // rows a load, loads
   using Raw = typename std::conditional<kPer == 8, uint2, uint32_t>::type;
   const int lane = threadIdx.x & 31;
   griddep_wait();
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(256, 4) read_kernel(const ReadParams p) {
   const int planes = (p.out_k ? p.c.Hkv : 0) + (p.out_v ? p.c.Hkv : 0);
   const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int tile = (int)(item / planes), plane = (int)(item - (int64_t)tile * planes);
-  const int64_t first = (int64_t)tile * 32;
+  const int64_t first = (int64_t)tile * kTile;
   if (first >= p.s.rows) return;
   const bool is_k = p.out_k && plane < p.c.Hkv;
   const int h = plane - (p.out_k && plane >= p.c.Hkv ? p.c.Hkv : 0);
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(256, 4) read_kernel(const ReadParams p) {
       while (b + 1 < p.s.B && r >= ld_fresh(p.s.cu + b + 1)) ++b;
       s = span_of(p.s, b, most);
     }
-    if (s.b < p.s.B && first + lane < p.s.rows && s.valid && r >= s.c0 && r < s.c0 + s.n) {
+    if (s.b < p.s.B && lane < kTile && first + lane < p.s.rows && s.valid && r >= s.c0 && r < s.c0 + s.n) {
       const int key = s.start + r - s.c0;
       row = row_of_key(p.c, p.s.err, page_of_key(p.c, s.b, key), key);
     }
@@ -328,13 +328,23 @@ template <typename T>
 cudaError_t launch_append(const AppendParams& p, int code_type, cudaStream_t stream) {
   return code_type == KATTN_E4M3 ? launch_append<T, true>(p, stream) : launch_append<T, false>(p, stream);
 }
+// Rows a warp: few where there are few, so that their warps share the multiprocessors and a
+// warp's chain is short (us a call with 8 / 16 / 32; bf16 rows of 4 heads: 1 row for each of 64
+// sequences 2.6 / 3.3 / 4.3, 2000 2.9 / 3.1 / 4.2, 8000 5.6 / 5.4 / 5.4, 16000 9.7 / 7.9 / 8.5,
+// 144000 78 / 72 / 71; with 4, one row 2.2 as with 8, 8000 7.7).  float32 rows fill a warp's
+// stores one by one: 8 are always best (8000 rows 7.2 / 8.0 / 8.1, 144000 112 / 116 / 118).
+template <typename O, int kTile>
+cudaError_t launch_read(const ReadParams& p, int code_type, int planes, cudaStream_t stream) {
+  const int64_t items = ((int64_t)p.s.rows + kTile - 1) / kTile * planes;
+  return launch_pdl(code_type == KATTN_E4M3 ? read_kernel<O, true, kTile> : read_kernel<O, false, kTile>,
+                    dim3((unsigned)((items + 7) / 8)), dim3(256), 0, stream, p);
+}
 template <typename O>
 cudaError_t launch_read(const ReadParams& p, int code_type, cudaStream_t stream) {
   const int planes = (p.out_k ? p.c.Hkv : 0) + (p.out_v ? p.c.Hkv : 0);
-  const int64_t items = ((int64_t)p.s.rows + 31) / 32 * planes;
-  const unsigned blocks = (unsigned)((items + 7) / 8);
-  return launch_pdl(code_type == KATTN_E4M3 ? read_kernel<O, true> : read_kernel<O, false>, dim3(blocks), dim3(256),
-                    0, stream, p);
+  if constexpr (sizeof(O) == 2)
+    if ((int64_t)p.s.rows * planes > 32768) return launch_read<O, 16>(p, code_type, planes, stream);
+  return launch_read<O, 8>(p, code_type, planes, stream);
 }
 
 }  // namespace
