@@ -31,8 +31,8 @@
 // pages, 32 query and 4 kv heads (544 MB, 80 us at the measured copy rate): 96 us a call, the
 // split alone 92 (5.9 TB/s), issue 42%.  2 sequences of 128k keys with float32 queries (267
 // MB, 39 us): 55 us, split 52, of which the second MMAs for hi + lo take tensor pipe to 34%.
-// With more rows, issue and the latency of a step's chain at 12 warps a multiprocessor (870
-// instructions a step at T = 2, 320 of them to make f16 of the codes; 1500 at T = 5): 16
+// With more rows, issue and the latency of a step's chain at 12 warps a multiprocessor (920
+// instructions a step at T = 2, 330 of them to make f16 of the codes; 1620 at T = 5): 16
 // sequences of 1k to 4k keys, 40 rows a head, 34 us; 64 of them 77 us.  One sequence of 257
 // keys: 6.1 us, latency alone.
 #include <cmath>
@@ -323,7 +323,8 @@ __device__ __forceinline__ void fill_other_rows(const BlockDecodeParams& p) {
 }
 
 // (Blocks a multiprocessor holds: with 4, 128 registers a thread, and T = 1, 99 us instead
-// of 96, 64 sequences of 512 to 32768 keys; one sequence as before.)
+// of 96, 64 sequences of 512 to 32768 keys; float32 queries, 2 of 120k to 131k keys, 60
+// instead of 55; one sequence as before.)
 template <int T, bool kE4m3, bool kPrecise>
 __global__ void __launch_bounds__(kThreadsB, kPerSm)
 block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps maps) {
