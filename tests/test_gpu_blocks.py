@@ -861,3 +861,37 @@ def test_captures_with_other_work_before_and_beside():
         assert all(same(a, b) for a, b in zip(want, (out, both, qout, *c.args)))
         assert same(both[0], both[1])
     assert K.get_device_status(ws) == 0
+
+
+@gpu
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+def test_large_reads_have_the_values_of_small_ones(code):
+    # 16-bit rows of large reads go through warps of more rows: ragged sequences, some empty,
+    # with rows between none of them, against the float32 rows rounded once and single reads
+    import torch
+    import int8_kv_decode_gb300 as K
+    r = np.random.default_rng(7)
+    B, H = 230, 5
+    lens = r.integers(0, 90, B)
+    lens[40:110] = r.integers(0, 3, 70)
+    start = r.integers(0, 128 - 90, B)
+    c = Cache(H, 2 * B, 64, 32, code, seed=5)
+    table = i32(tables([128] * B, 64, 2 * B, spare=0))
+    cu = np.concatenate([[7], 7 + np.cumsum(lens)])
+    n = int(cu[-1]) + 9
+    assert n * 2 * H > 32768
+    args = (*c.args, table, 64, i32(cu), i32(start), n)
+    wide = K.read_blocks(*args, dtype=torch.float32, workspace=c.ws)
+    for dtype in (torch.bfloat16, torch.float16):
+        out = [torch.full((n, H, D), 7.0, device="cuda", dtype=dtype) for _ in range(2)]
+        K.read_blocks(*args, out_k=out[0], out_v=out[1], workspace=c.ws)
+        for o, w in zip(out, wide):
+            assert same(o[7:n - 9], w[7:n - 9].to(dtype))
+            assert (o[:7] == 7.0).all() and (o[n - 9:] == 7.0).all()
+        for b in (0, 45, 113, B - 1):
+            m = int(lens[b])
+            alone = K.read_blocks(*c.args, table[b:b + 1], 64, i32([0, m]), i32(start[b:b + 1]), m, dtype=dtype,
+                                  workspace=c.ws)
+            for o, a in zip(out, alone):
+                assert same(o[cu[b]:cu[b + 1]], a)
+    assert K.get_device_status(c.ws) == 0
