@@ -670,6 +670,8 @@ int kattn_read_blocks(const void* k, const float* k_scale, const void* v, const 
  *   Weights: relative to the row's reference, held as f16 (11 bits; float32 queries: hi +
  *   lo, 22 bits) with steps of 2^-33 of the reference's at the smallest, and summed up as
  *   they are held.  Values, row sums and the output before its one rounding are float32.
+ *   Values may be as large as float32 holds; beside a v_scale of 2^64 or more among a row's
+ *   keys, values below 2^-126 of that one may be lost.
  * ctx_len: int32 [B] on the device.  ctx_len[b] = 0 is an empty slot: its rows are 0, and
  * nothing of it is read.  Below 0, above max_ctx, or with ceil((ctx_len[b] + M - 1) /
  * page_rows) > max_pages: NaN and KATTN_DEVERR_BAD_SEQUENCE.  A table entry outside the

@@ -22,7 +22,7 @@
 //     8 x 8 blocks in registers, to the second product, whose row sums take the weights
 //     as rounded: a weight's rounding then cancels where it dominates;
 //   * O = O + v_scale (V^T P^T): the product of a step starts at zero and enters the
-//     float32 sum with the block's scale, so scales of any range need no care.  From three
+//     float32 sum with the block's scale (a row that sees a huge one: kHuge).  From three
 //     tiles on O lies in tensor memory, each lane's columns its own store, read and written
 //     once a step: so the codes are converted once for up to 40 rows, the order of every
 //     row's operations stays that of one tile, and three blocks still fit a multiprocessor.
@@ -51,6 +51,17 @@ constexpr float kMoveAt = 15.0f;                  // and reach 2^15 before it mo
 // - m: x = S c - m in one rounding may be far off at the largest, whose own rounding made m.
 // (Every step of a unit with such a row goes the way of a step that moves references.)
 constexpr float kLarge = 1048576.0f;
+// A warp's sums O of a row are up to 2^22 times the values (128 keys of weights up to 2^15),
+// those of a long context up to 2^45 times.  So where a row sees a step of the warp's window
+// with a v_scale of kHuge or more (values up to 2^128), its sums there are taken by kDown, a
+// power of two: what it costs lies 2^126 below such values.  The sign of the row sum says so
+// where sums are joined, which bring all of them to the same side.  A row goes by the steps
+// that it sees itself, so its bytes stay its own, and those of a row with none are as they are.
+constexpr float kHuge = 0x1p64f, kDown = 0x1p-64f, kUp = 0x1p64f;
+__device__ __forceinline__ bool is_down(float l) { return (int)__float_as_uint(l) < 0; }
+__device__ __forceinline__ float mark_down(float l, bool down) {
+  return down ? __uint_as_float(__float_as_uint(l) | 0x80000000u) : l;
+}
 
 // Windows of 512 keys sit at fixed positions, so that a row's bytes depend on its own keys
 // alone.  (Windows of 1024 from key 4096 on: 103 us instead of 99, 64 sequences of 512 to
@@ -532,6 +543,8 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
         sm.failed = 1;
       }
     };
+    int first_huge = INT32_MAX;                   // first key of the warp's first step with a huge scale
+    auto goes_down = [&](int n, int e) { return first_huge < keys_of(n, e); };
     bool large = false;                           // some row's reference passes kLarge
     int flying = 0;                               // after giving up: copies on their way (1: K, 2: V, by parity)
 
@@ -539,10 +552,11 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
     for (int i = 0; i < nb; ++i) {
       const int t0 = s0 + (i * kWarpsB + warp) * kBlockBk;
       const float ksb = __shfl_sync(0xffffffffu, ks, i);
-      float vsb = __shfl_sync(0xffffffffu, vs, i);
       const int next = i + 1 < nb ? __shfl_sync(0xffffffffu, row, i + 1) : nb_n > 0 ? first_n : -1;
       const bool edge = t0 + kBlockBk > it.ctx;   // keys that some row does not see
-      if (edge && !(fabsf(vsb) < INFINITY)) vsb = 0.0f;    // (0 * inf would reach rows that see none of them)
+      // Every row sees the steps that begin before ctx.  Behind it there is one at most, the
+      // warp's last: the rows that see it go down there if its scale is the first huge one.
+      const bool lowers = t0 >= it.ctx && t0 == first_huge;
       if (!ready(kbar, ph)) {
         give_up();
         flying = 3;
@@ -618,7 +632,7 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
                              fmaxf(fmaxf(x[0][0].y, x[0][1].y), fmaxf(x[1][0].y, x[1][1].y)));
         };
         const float2 most = largest();
-        if (__any_sync(0xffffffffu, most.x > kMoveAt || most.y > kMoveAt) || large) {
+        if (__any_sync(0xffffffffu, most.x > kMoveAt || most.y > kMoveAt) || large || lowers) {
           // A row's reference moves, to where its largest score has the weight 2^kTop.  (Which
           // rows move goes by the sums that asked for it, so it depends on the row alone.)
           auto row_most = [&](float2 v) -> float2 {
@@ -644,6 +658,9 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
           large |= __any_sync(0xffffffffu, (fabsf(m[n].x) > kLarge && m[n].x > -INFINITY) ||
                                                (fabsf(m[n].y) > kLarge && m[n].y > -INFINITY));
           l[n] = f2_mul(l[n], al);
+          float2 alo = al;                        // (of O)
+          if (lowers && goes_down(n, 0)) alo.x = __fmul_rn(al.x, kDown);
+          if (lowers && goes_down(n, 1)) alo.y = __fmul_rn(al.y, kDown);
           if (i == 0) {                           // (nothing is summed up yet)
           } else if constexpr (S::kTensor) {
             uint32_t v[32];
@@ -652,7 +669,7 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
             tensor_loaded(v);
 #pragma unroll
             for (int i2 = 0; i2 < 32; i2 += 2) {
-              const float2 a0 = f2_mul(as_float2(v[i2], v[i2 + 1]), al);
+              const float2 a0 = f2_mul(as_float2(v[i2], v[i2 + 1]), alo);
               v[i2] = __float_as_uint(a0.x);
               v[i2 + 1] = __float_as_uint(a0.y);
             }
@@ -662,8 +679,8 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
           } else {
 #pragma unroll
             for (int md = 0; md < 8; ++md) {
-              const float2 a0 = f2_mul(make_float2(o[md][n][0], o[md][n][1]), al);
-              const float2 a1 = f2_mul(make_float2(o[md][n][2], o[md][n][3]), al);
+              const float2 a0 = f2_mul(make_float2(o[md][n][0], o[md][n][1]), alo);
+              const float2 a1 = f2_mul(make_float2(o[md][n][2], o[md][n][3]), alo);
               o[md][n][0] = a0.x; o[md][n][1] = a0.y; o[md][n][2] = a1.x; o[md][n][3] = a1.y;
             }
           }
@@ -702,6 +719,14 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
         }
         l[n] = f2_add(l[n], make_float2(r[0], r[1]));
       }
+      if (i == 0) {                               // (the scales are here by now)
+        if (const uint32_t huge = __ballot_sync(0xffffffffu, lane < nb && fabsf(vs) >= kHuge)) {
+          first_huge = s0 + ((__ffs(huge) - 1) * kWarpsB + warp) * kBlockBk;
+          if (first_huge < it.ctx || (huge >> lane & 1u)) vs = __fmul_rn(vs, kDown);
+        }
+      }
+      float vsb = __shfl_sync(0xffffffffu, vs, i);
+      if (edge && !(fabsf(vsb) < INFINITY)) vsb = 0.0f;    // (0 * inf would reach rows that see none of them)
       // ---- O += v_scale V^T P^T.  Row g of m-tile q is channel 16q + 2g, row g + 8 the next
       // one: a 16-bit element of the buffer is two channels of a key, so that the transposing
       // load pairs the keys 2c, 2c + 1 of both channels in a register.
@@ -782,9 +807,12 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
 #pragma unroll
     for (int n = 0; n < T; ++n)
       if (g == 0) {
+        if (first_huge != INT32_MAX)
+          l[n] = make_float2(mark_down(l[n].x, goes_down(n, 0)), mark_down(l[n].y, goes_down(n, 1)));
         sm.ml[warp][n][2 * c] = make_float2(m[n].x, l[n].x);
         sm.ml[warp][n][2 * c + 1] = make_float2(m[n].y, l[n].y);
       }
+    bool special = false;                         // a warp of the block has huge scales, or found no copy
 #pragma unroll 1
     for (int n0 = 0; n0 < T; n0 += S::kJoin) {
       if constexpr (S::kTensor) {
@@ -805,17 +833,42 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
           for (int md = 0; md < 8; ++md)
             sm.o[warp][n][md][lane] = make_float4(o[md][n][0], o[md][n][1], o[md][n][2], o[md][n][3]);
       }
-      __syncthreads();
-      if (sm.failed) {                            // give the copies on their way a bounded chance, and leave
-        if (lane == 0) {
-          if (flying == 0 && ahead) flying = 3;
-          if (flying & 1) mbar_wait_bounded(&sm.full[warp][0], ph);
-          if (flying & 2) mbar_wait_bounded(&sm.full[warp][1], ph);
-          if (flying & 4) mbar_wait_bounded(&sm.full[warp][0], ph ^ 1u);
+      if (n0 == 0) special = __syncthreads_or(flying != 0 || first_huge != INT32_MAX);
+      else __syncthreads();
+      if (special) {
+        if (sm.failed) {                          // give the copies on their way a bounded chance, and leave
+          if (lane == 0) {
+            if (flying == 0 && ahead) flying = 3;
+            if (flying & 1) mbar_wait_bounded(&sm.full[warp][0], ph);
+            if (flying & 2) mbar_wait_bounded(&sm.full[warp][1], ph);
+            if (flying & 4) mbar_wait_bounded(&sm.full[warp][0], ph ^ 1u);
+          }
+          __syncwarp();
+          leave();
+          return;
         }
-        __syncwarp();
-        leave();
-        return;
+        // a row that goes down in one warp goes down in all
+#pragma unroll 1
+        for (int t = 0; t < S::kJoin; ++t) {
+          bool down[2] = {false, false}, own[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            for (int w = 0; w < kWarpsB; ++w) down[e] |= is_down(sm.ml[w][n0 + t][2 * c + e].y);
+            own[e] = is_down(sm.ml[warp][n0 + t][2 * c + e].y);
+          }
+          const float fx = down[0] && !own[0] ? kDown : 1.0f, fy = down[1] && !own[1] ? kDown : 1.0f;
+          for (int md = 0; md < 8; ++md) {
+            float4& x = sm.o[warp][t][md][lane];
+            x = make_float4(__fmul_rn(x.x, fx), __fmul_rn(x.y, fy), __fmul_rn(x.z, fx), __fmul_rn(x.w, fy));
+          }
+          __syncthreads();                        // (every sign is read)
+          if (g == 0)
+            for (int e = 0; e < 2; ++e) {
+              float& sum = sm.ml[warp][n0 + t][2 * c + e].y;
+              sum = mark_down(sum, down[e]);
+            }
+        }
+        __syncthreads();
       }
 #pragma unroll
       for (int t = 0; t < S::kJoin; ++t) {
@@ -854,7 +907,8 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
           if (whole) {
             const int j = column(rr);
             const int64_t at = (((int64_t)it.b * M + j) * p.Hq + it.kh * p.g + rr - j * p.g) * kD + 16 * md + 2 * g;
-            store_out2(p.out, p.q_type, at, __fdiv_rn(y0, lr[e]), __fdiv_rn(y1, lr[e]));
+            const float by = is_down(lr[e]) ? __fmul_rn(lr[e], -kDown) : lr[e];
+            store_out2(p.out, p.q_type, at, __fdiv_rn(y0, by), __fdiv_rn(y1, by));
           } else {
             *reinterpret_cast<float2*>(part + (size_t)rr * kD + 16 * md + 2 * g) = make_float2(y0, y1);
             if (warp == 0 && d == 0 && g == 0)
@@ -888,8 +942,9 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
 // Joins the windows of a row: W warps; the windows k, k + 16, ... are summed with the
 // weights 2^(m_s - max m), for k = 0 .. 15, and the sixteen sums are added in order, so the
 // order depends on neither W nor other rows.  A window in which a draft column's row sees
-// no key has m = -inf and weight 0.  Bound by the trips to L2 that depend on one another
-// (references, then 4 W windows a trip).
+// no key has m = -inf and weight 0.  From the first 64 windows on of which one went down, all
+// sums are on that side.  Bound by the trips to L2 that depend on one another (references,
+// then 4 W windows a trip).
 constexpr int kSums = 16, kBatchB = 4, kChunk = 64;
 
 template <int W>
@@ -936,11 +991,22 @@ __global__ void __launch_bounds__(32 * W) block_merge_kernel(const BlockDecodePa
   float4 acc[kOwn];
 #pragma unroll
   for (int k = 0; k < kOwn; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float l = 0.0f;
+  float l = 0.0f, up = 1.0f;
   float2 a = st0, c = st1;
   for (int s0 = 0; s0 < ns; s0 += kChunk) {       // lane n weighs windows s0 + n and s0 + 32 + n
-    const float w0 = fast_exp2(__fsub_rn(a.x, mx)), w1 = fast_exp2(__fsub_rn(c.x, mx));   // (-inf: 0)
-    l = __fmaf_rn(w1, c.y, __fmaf_rn(w0, a.y, l));
+    float w0 = fast_exp2(__fsub_rn(a.x, mx)), w1 = fast_exp2(__fsub_rn(c.x, mx));   // (-inf: 0)
+    l = __fmaf_rn(w1, fabsf(c.y), __fmaf_rn(w0, fabsf(a.y), l));
+    if (up != 1.0f || __any_sync(0xffffffffu, is_down(a.y) || is_down(c.y))) {
+      if (up == 1.0f) {
+        up = kUp;
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k)
+          acc[k] = make_float4(__fmul_rn(acc[k].x, kDown), __fmul_rn(acc[k].y, kDown), __fmul_rn(acc[k].z, kDown),
+                               __fmul_rn(acc[k].w, kDown));
+      }
+      if (!is_down(a.y)) w0 = __fmul_rn(w0, kDown);
+      if (!is_down(c.y)) w1 = __fmul_rn(w1, kDown);
+    }
     a = stats(s0 + kChunk + lane);                // the next chunk's
     c = stats(s0 + kChunk + 32 + lane);
 #pragma unroll
@@ -972,8 +1038,8 @@ __global__ void __launch_bounds__(32 * W) block_merge_kernel(const BlockDecodePa
     O = make_float4(__fadd_rn(O.x, x.x), __fadd_rn(O.y, x.y), __fadd_rn(O.z, x.z), __fadd_rn(O.w, x.w));
   }
   const int64_t at = (((int64_t)b * p.M + j) * p.Hq + head) * kD + 4 * lane;
-  store_out2(p.out, p.q_type, at, __fdiv_rn(O.x, l), __fdiv_rn(O.y, l));
-  store_out2(p.out, p.q_type, at + 2, __fdiv_rn(O.z, l), __fdiv_rn(O.w, l));
+  store_out2(p.out, p.q_type, at, __fmul_rn(__fdiv_rn(O.x, l), up), __fmul_rn(__fdiv_rn(O.y, l), up));
+  store_out2(p.out, p.q_type, at + 2, __fmul_rn(__fdiv_rn(O.z, l), up), __fmul_rn(__fdiv_rn(O.w, l), up));
 }
 
 // Rows of at most kSums windows: a warp each, all its windows on their way at once.  The same
@@ -1000,8 +1066,11 @@ __global__ void __launch_bounds__(32 * kRowsOfMerge) block_merge_short_kernel(co
     v[s] = s < ns ? __ldcg(reinterpret_cast<const float4*>(ocol + s * stride)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   const float2 st = lane < ns ? __ldcg(reinterpret_cast<const float2*>(mlcol + lane * stride))
                               : make_float2(-INFINITY, 0.0f);
-  const float w = fast_exp2(__fsub_rn(st.x, warp_max(st.x)));
-  const float l = warp_sum(__fmul_rn(w, st.y));
+  float w = fast_exp2(__fsub_rn(st.x, warp_max(st.x)));
+  const float l = warp_sum(__fmul_rn(w, fabsf(st.y)));
+  const bool low_side = __any_sync(0xffffffffu, is_down(st.y));
+  if (low_side && !is_down(st.y)) w = __fmul_rn(w, kDown);
+  const float up = low_side ? kUp : 1.0f;
   float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
   for (int s = 0; s < kSums; ++s) {
@@ -1010,8 +1079,8 @@ __global__ void __launch_bounds__(32 * kRowsOfMerge) block_merge_short_kernel(co
     O = s == 0 ? x : make_float4(__fadd_rn(O.x, x.x), __fadd_rn(O.y, x.y), __fadd_rn(O.z, x.z), __fadd_rn(O.w, x.w));
   }
   const int64_t to = row * kD + 4 * lane;
-  store_out2(p.out, p.q_type, to, __fdiv_rn(O.x, l), __fdiv_rn(O.y, l));
-  store_out2(p.out, p.q_type, to + 2, __fdiv_rn(O.z, l), __fdiv_rn(O.w, l));
+  store_out2(p.out, p.q_type, to, __fmul_rn(__fdiv_rn(O.x, l), up), __fmul_rn(__fdiv_rn(O.y, l), up));
+  store_out2(p.out, p.q_type, to + 2, __fmul_rn(__fdiv_rn(O.z, l), up), __fmul_rn(__fdiv_rn(O.w, l), up));
 }
 
 // ------------------------------------------------------------------- host

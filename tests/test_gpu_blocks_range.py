@@ -1,0 +1,92 @@
+"""Values at the ends of float32's range through decode_blocks.
+
+Tolerances are those of test_gpu_blocks.py; what is left beside them is a share of the
+row's own largest value (the tail) and float32's least steps, never a fixed number.
+"""
+
+import numpy as np
+import pytest
+
+import oracle
+from test_gpu_blocks import HALF_STEP, attend, attend_inputs, built, same, tolerance  # noqa: F401
+
+gpu = pytest.mark.gpu
+
+
+def set_scales(c, name, a):
+    import torch
+    c.host[name] = a.astype(np.float32)
+    getattr(c, name).copy_(torch.from_numpy(c.host[name]))
+
+
+def check_row_by_row(c, table, ctx, q, got):
+    """As check_attend, with a tail of the row's own values: 2 * keys * 2^-34 of the largest
+    |V| that it sees, and 2^-146 for results below float32's normal numbers (a float32 sum of
+    weights up to 2^15 times such values, divided by 2^9 or more, is off by single steps of
+    2^-149)."""
+    dtype = str(q.dtype).replace("torch.", "")
+    want, mass, size = oracle.blocks.decode(q.float().cpu().numpy(), c.host, table, c.page, ctx)
+    got = got.float().cpu().numpy().astype(np.float64)
+    assert np.isfinite(got).all()
+    top = np.zeros(mass.shape[:3])
+    B, M, Hq = top.shape
+    for b in range(B):
+        for j in range(M):
+            V = oracle.blocks.values(c.host, "v", oracle.blocks.rows_of(table[b], c.page, np.arange(ctx[b] + j)))
+            top[b, j] = np.repeat(np.abs(V).max((1, 2)), Hq // V.shape[0])
+    lim = tolerance(dtype, size)[..., None] * mass + (2 * (np.asarray(ctx) + M)[:, None, None] * 2.0 ** -34 * top)[..., None]
+    lim = lim + HALF_STEP[dtype] * (np.abs(want) + lim) + (2.0 ** -25 if dtype == "float16" else 2.0 ** -146)
+    worst = (np.abs(got - want) / lim).max()
+    assert worst <= 1, worst
+
+
+# Scales of V: all near the top of the range (values to 1e37 and more), all near its bottom,
+# over the whole of it from block to block, and ordinary ones with single blocks at the top.
+def value_scales(kind, shape, r):
+    if kind == "large":
+        return 10.0 ** r.uniform(34.5, 35.5, shape)
+    if kind == "largest":
+        return np.full(shape, 7e35)                          # 448 times that is 3.1e38
+    if kind == "tiny":
+        return 10.0 ** r.uniform(-37.5, -36.5, shape)
+    if kind == "small":
+        return 10.0 ** r.uniform(-31, -29, shape)
+    if kind == "any":
+        return 10.0 ** r.uniform(-34, 35, shape)
+    return np.where(r.random(shape) < 0.1, 1e35, 1.0) * r.uniform(0.5, 1.5, shape)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["large", "largest", "tiny", "small", "any", "single"])
+@pytest.mark.parametrize("dtype,code", [("bfloat16", "int8"), ("float32", "e4m3"), ("bfloat16", "e4m3")])
+@pytest.mark.parametrize("M,g,ctx", [(1, 4, [1, 33, 500, 9000]), (3, 7, [5, 510, 1500]), (5, 8, [700, 64]),
+                                     (2, 24, [40, 2000])])
+def test_value_scales_of_any_size(kind, dtype, code, M, g, ctx):
+    c, table, ctx, q = attend_inputs(len(ctx), M, 2 * g, 2, ctx, 32, 64, code, dtype, seed=M + g)
+    r = np.random.default_rng(M * 100 + g)
+    set_scales(c, "vs", value_scales(kind, c.host["vs"].shape, r))
+    got = attend(c, table, ctx, q)
+    check_row_by_row(c, table, ctx, q, got)
+    # the bytes of a row: under any limit, in any batch, as the only column
+    assert same(got, attend(c, table, ctx, q, max_ctx=60000))
+    for b in range(len(ctx)):
+        assert same(got[b:b + 1], attend(c, table[b:b + 1], ctx[b:b + 1], q[b:b + 1].contiguous(), max_ctx=9000))
+    for j in range(M):
+        assert same(got[:, j:j + 1], attend(c, table, ctx + j, q[:, j:j + 1].contiguous()))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("M,g", [(2, 4), (4, 8), (5, 8)])
+def test_large_values_that_a_column_does_not_see(dtype, M, g):
+    # a block of draft rows with the largest scales behind contexts of the smallest
+    c, table, ctx, q = attend_inputs(3, M, 2 * g, 2, [96, 640, 1600], 32, 64, "int8", dtype, seed=3)
+    set_scales(c, "vs", c.host["vs"] * np.float32(2.0 ** -118))
+    want = attend(c, table, ctx, q)
+    scales = c.host["vs"].copy()
+    for b in range(3):
+        scales[:, int(oracle.blocks.rows_of(table[b], 64, [int(ctx[b])])[0]) // 32] = 1e35
+    set_scales(c, "vs", scales)
+    got = attend(c, table, ctx, q)
+    assert same(want[:, 0], got[:, 0])
+    check_row_by_row(c, table, ctx, q, got)
