@@ -681,7 +681,8 @@ int kattn_read_blocks(const void* k, const float* k_scale, const void* v, const 
  * e4m3 codes that are no numbers, and v_scales that are not finite, do not reach rows that
  * see no key of their 32-key step: in a step that some column does not see whole they are
  * taken as 0.
- * A query row with elements that are not finite gives a row of NaN and changes no other.
+ * A query row with elements that are not finite gives a row of NaN and changes no other.  A
+ * key whose e4m3 codes or k_scale are no numbers gives NaN in the rows that see it.
  * Limits on M, g * M, B and sizes, and sm_scale, as in kattn_decode.
  * Deterministic; the bytes of out[b][j][h] depend only on the row's own query and keys, so
  * column j equals an M = 1 call with ctx_len + j on the same cache, in any batch.

@@ -287,6 +287,13 @@ __device__ __forceinline__ uint32_t numbers_only(uint32_t w) {
   return w & ~__vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
 }
 
+// The smaller; NaN if x is.  (fminf gives the other one.)
+__device__ __forceinline__ float min_or_nan(float x, float y) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
@@ -685,12 +692,13 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
             }
           }
           scores(m[n], true);
-          // (a reference past 2^27 may lie 16 below the largest)
+          // (a reference past 2^27 may lie 16 below the largest; a score that is no number stays
+          // one, as in a step that moves none)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
             for (int k2 = 0; k2 < 2; ++k2)
-              x[hf][k2] = make_float2(fminf(x[hf][k2].x, kMoveAt), fminf(x[hf][k2].y, kMoveAt));
+              x[hf][k2] = make_float2(min_or_nan(x[hf][k2].x, kMoveAt), min_or_nan(x[hf][k2].y, kMoveAt));
         }
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {

@@ -1,4 +1,5 @@
-"""Values at the ends of float32's range through decode_blocks.
+"""Values at the ends of float32's range, and values that are no numbers, through the
+operators on block-scaled caches.
 
 Tolerances are those of test_gpu_blocks.py; what is left beside them is a share of the
 row's own largest value (the tail) and float32's least steps, never a fixed number.
@@ -90,3 +91,39 @@ def test_large_values_that_a_column_does_not_see(dtype, M, g):
     got = attend(c, table, ctx, q)
     assert same(want[:, 0], got[:, 0])
     check_row_by_row(c, table, ctx, q, got)
+
+
+# ------------------------------------------------------------- no numbers
+
+@gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("M,g,gain", [(1, 4, 1.5), (1, 4, 40.0), (3, 7, 6.0), (5, 8, 1.5)])
+def test_keys_that_are_no_numbers_reach_the_rows_that_see_them(dtype, M, g, gain):
+    # an e4m3 NaN in one key, in steps that move references and in steps that do not; the
+    # rows of the other head keep their bytes
+    import torch
+    c, table, ctx, q = attend_inputs(2, M, 2 * g, 2, [1500, 700], 32, 64, "e4m3", dtype, seed=8, gain=gain)
+    want = attend(c, table, ctx, q)
+    keys = c.k.view(torch.uint8).clone()
+    for t in (0, 5, 31, 130, 300, 520, 699, 700 + M - 2):
+        row = int(oracle.blocks.rows_of(table[1], 64, [t])[0])
+        c.k.view(torch.uint8)[1, row, 77] = 0x7f
+        got = attend(c, table, ctx, q)
+        for j in range(M):
+            if t < 700 + j:
+                assert torch.isnan(got[1, j, g:].float()).all(), (t, j)
+            else:
+                assert same(got[1, j], want[1, j]), (t, j)
+        assert same(got[0], want[0]) and same(got[1, :, :g], want[1, :, :g])
+        assert same(got, attend(c, table, ctx, q, max_ctx=60000))
+        c.k.view(torch.uint8).copy_(keys)
+    # every key of a warp's first step, and of a whole first window
+    for keys_of in (np.arange(32), np.arange(512)):
+        c.k.view(torch.uint8)[1, oracle.blocks.rows_of(table[1], 64, keys_of)] = 0xff
+        got = attend(c, table, ctx, q)
+        assert torch.isnan(got[1, :, g:].float()).all() and same(got[0], want[0])
+        c.k.view(torch.uint8).copy_(keys)
+    # a scale that is no number
+    c.ks[1, int(oracle.blocks.rows_of(table[1], 64, [32])[0]) // 32] = float("nan")
+    got = attend(c, table, ctx, q)
+    assert torch.isnan(got[1, :, g:].float()).all() and same(got[0], want[0]) and same(got[1, :, :g], want[1, :, :g])
