@@ -91,6 +91,8 @@ enum kattn_p_mode {
                                           does not match the table */
 #define KATTN_DEVERR_NO_PAGES 0x8u     /* kattn_reserve_pages, kattn_fork_sequences:
                                           the pool has too few free pages */
+#define KATTN_DEVERR_NOT_FINITE 0x10u  /* kattn_append_blocks: a new row with elements
+                                          that are not finite */
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* kattn_status_string(int status);
@@ -625,8 +627,10 @@ int kattn_rope(const void* x, int x_type, int n_rows, int n_heads, int d, int64_
  *            round(c * (s_old / s))
  *   codes  = round(x / s), 0 where s = 0;  the block's scale = s
  * round is to the nearest, ties to even, clamped to +-127, or the nearest e4m3 value,
- * saturating; every product and quotient is rounded to float32 once.  Rows of the block
- * behind the last new one are dead: their codes are left as they were, under the new
+ * saturating; every product and quotient is rounded to float32 once.  Elements of x that are
+ * not finite set KATTN_DEVERR_NOT_FINITE: the maximum is that of the others; an infinite one
+ * gets the code +-top, a NaN the code 0, or e4m3's NaN (where s = 0, 0 as all).  Rows of the
+ * block behind the last new one are dead: their codes are left as they were, under the new
  * scale.  (So the codes of a block depend on how its rows came in: a row written under a
  * small scale is coded again as larger ones follow, each time with half a step of the
  * new scale.)  A block that several sequences of the call touch, as in a shared page, is

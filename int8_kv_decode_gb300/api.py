@@ -21,6 +21,7 @@ DEVERR_BAD_SEQUENCE = 0x1
 DEVERR_TIMEOUT = 0x2
 DEVERR_BAD_PAGE = 0x4
 DEVERR_NO_PAGES = 0x8
+DEVERR_NOT_FINITE = 0x10
 
 
 def _stream(device) -> int:
@@ -829,7 +830,8 @@ def append_blocks(k_new, v_new, cu_rows, start, k, k_scale, v, v_scale, block_ta
     v_scale [Hkv][cap/block_rows] float32 (block_rows 32, 64 or 128), block_table int32
     [B][max_pages].  table (rope_table()): K rows are turned by their key's position
     before they are coded, and so are the queries q [rows][Hq][128], into q_out (may be
-    q).  workspace: any workspace of the library, for the error bits.
+    q).  Elements that are not finite set DEVERR_NOT_FINITE and do not enter a block's
+    scale.  workspace: any workspace of the library, for the error bits.
     (kattn_append_blocks)
     """
     if workspace is not None and (q is None or q_out is not None):

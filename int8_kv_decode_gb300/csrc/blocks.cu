@@ -104,7 +104,17 @@ __device__ __forceinline__ void code_values(uint32_t w, float* f) {
 // blocks that sequence b touches are the units floor(cu[b] / R) + 2 b + j: at most floor(n /
 // R) + 2 for its n rows, so units of different sequences never meet, and the grid is known
 // without the lengths.  Queries, if any, are turned by further blocks of threads.
+// The maximum keeps a NaN, so a block of rows that are not all finite is known by it: its
+// scale is then taken again from the finite elements, as an infinite scale would code every
+// row of the block to 0, those that stay among them.
 constexpr int kRowsPerWarp = 8;
+
+// The largest absolute value, or NaN.
+__device__ __forceinline__ float max_abs_or_nan(float x, float y, float z) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
 
 template <typename T, int kBlock, bool kE4m3, bool kInter>
 __global__ void __launch_bounds__(kBlock * 4) append_kernel(const AppendParams p, const unsigned kv_blocks) {
@@ -179,21 +189,39 @@ __global__ void __launch_bounds__(kBlock * 4) append_kernel(const AppendParams p
     if (turns_k && run.turns && r >= lo && r < hi)
       turn<kInter>(load_angles(p.table, key0 + r, p.half, l), fa[i], fb[i]);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(fa[i][e]), fabsf(fb[i][e])));
+    for (int e = 0; e < 4; ++e) amax = max_abs_or_nan(amax, fa[i][e], fb[i][e]);
   }
-  amax = warp_max_abs(amax);
-  if (lane == 0) s_max[warp] = amax;
-  __syncthreads();
-  amax = warp_max_abs(lane < kWarps ? s_max[lane] : 0.0f);
+  auto block_max = [&](float v) {                 // (a NaN is the largest: warp_max_abs goes by the bits)
+    v = warp_max_abs(v);
+    if (lane == 0) s_max[warp] = v;
+    __syncthreads();
+    return warp_max_abs(lane < kWarps ? s_max[lane] : 0.0f);
+  };
+  amax = block_max(amax);
+  const bool odd = !(amax < INFINITY);            // elements that are not finite
+  if (odd) {
+    amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kRowsPerWarp / 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = fabsf(fa[i][e]), y = fabsf(fb[i][e]);
+        amax = fmaxf(amax, fmaxf(x < INFINITY ? x : 0.0f, y < INFINITY ? y : 0.0f));
+      }
+    __syncthreads();                              // (the maxima are read)
+    amax = block_max(amax);
+    if (threadIdx.x == 0) atomicOr(p.s.err, KATTN_DEVERR_NOT_FINITE);
+  }
   const float own = __fdiv_rn(amax, kE4m3 ? 448.0f : 127.0f);
   const float s = fmaxf(own, was);
   if (threadIdx.x == 0) *scale = s;
   const float inv = __frcp_rn(s);
+  const bool divide = odd || scale_divides(s);
 #pragma unroll
   for (int i = 0; i < kRowsPerWarp / 2; ++i) {
     const int r = r0 + 2 * i + side;
     if (r < lo || r >= hi) continue;
-    const Codes<4> ca = codes_of(fa[i], s, inv, kE4m3), cb = codes_of(fb[i], s, inv, kE4m3);
+    const Codes<4> ca = codes_of(fa[i], s, inv, kE4m3, divide), cb = codes_of(fb[i], s, inv, kE4m3, divide);
     *reinterpret_cast<Codes<4>*>(codes + r * kD + run.a) = ca;
     *reinterpret_cast<Codes<4>*>(codes + r * kD + run.b) = cb;
   }

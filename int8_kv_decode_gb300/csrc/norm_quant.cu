@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormParams p, c
         inv = __frcp_rn(s0);
         if (in && c < p.d && c % 128 == 0) p.scales[row * (p.d / 128) + c / 128] = __fmul_rn(s0, r);
       }
-      const Codes<VEC> out = codes_of<VEC>(z[v], s0, inv, e4m3);
+      const Codes<VEC> out = codes_of<VEC>(z[v], s0, inv, e4m3, scale_divides(s0));
       if (in && c < p.d) *reinterpret_cast<Codes<VEC>*>(p.codes + row * p.d + c) = out;
     }
   }

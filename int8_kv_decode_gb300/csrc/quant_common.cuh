@@ -96,11 +96,14 @@ __device__ __forceinline__ uint8_t code_of(float z, float s0, bool e4m3) {
 //   e4m3  borders at the middle of two values of 4 significant bits: the low 20
 //         bits of t's mantissa are then 0x80000; further than 4 steps is safe.
 //         Below 2^-6 the grid is coarser: those divide.
-// Elements near a border, and s0 whose reciprocal may overflow, divide.
+// Elements near a border divide, and all of them where `divide` is true: with s0 whose
+// reciprocal may overflow, and with elements that are not finite, which become +-127 (NaN: 0)
+// or saturate (NaN: NaN).
+__device__ __forceinline__ bool scale_divides(float s0) { return !(s0 > 1e-30f); }
 template <int VEC>
-__device__ __forceinline__ Codes<VEC> codes_of(const float (&z)[VEC], float s0, float inv, bool e4m3) {
+__device__ __forceinline__ Codes<VEC> codes_of(const float (&z)[VEC], float s0, float inv, bool e4m3, bool divide) {
   Codes<VEC> c;
-  bool near = !(s0 > 1e-30f);
+  bool near = divide;
   if (!e4m3) {
     const float magic = 12582912.0f;              // 1.5 * 2^23: the sum's low byte is rint(t)
     float far = 0.0f;

@@ -34,7 +34,8 @@ def rotate(x, cs, interleaved, dtype=F):
 def round_codes(u, e4m3):
     if e4m3:
         return np.asarray(e4m3_grid(u), np.float64)
-    return np.clip(np.rint(u), -127, 127).astype(np.float64) + 0.0     # (an integer has no -0)
+    u = np.where(np.isnan(u), 0, u)                                    # (an integer has no NaN)
+    return np.clip(np.rint(u), -127, 127).astype(np.float64) + 0.0     # (and no -0)
 
 
 def rows_of(table, page, keys):
@@ -43,7 +44,8 @@ def rows_of(table, page, keys):
 
 
 def append(cache, name, x, start, table, page):
-    """The rows x [n][Hkv][128] (float32) of one sequence, as keys start, start + 1, ..."""
+    """The rows x [n][Hkv][128] (float32) of one sequence, as keys start, start + 1, ...
+    Elements that are not finite do not enter a block's scale."""
     R, e4m3 = cache["R"], cache["e4m3"]
     top = F(448 if e4m3 else 127)
     x = np.asarray(x, F)
@@ -53,7 +55,7 @@ def append(cache, name, x, start, table, page):
         at = rows_of(table, page, np.arange(key0, hi))
         new = x[lo - start:hi - start].transpose(1, 0, 2)
         for h in range(x.shape[1]):
-            s = np.divide(np.abs(new[h]).max(), top, dtype=F)
+            s = np.divide(np.where(np.isfinite(new[h]), np.abs(new[h]), F(0)).max(), top, dtype=F)
             if lo > key0:
                 was = cache[name + "s"][h, at[0] // R]
                 if s > was:

@@ -9,7 +9,8 @@ import numpy as np
 import pytest
 
 import oracle
-from test_gpu_blocks import HALF_STEP, attend, attend_inputs, built, same, tolerance  # noqa: F401
+from test_gpu_blocks import (Cache, D, HALF_STEP, attend, attend_inputs, built, dtype_of, i32, same, tables,  # noqa: F401
+                             tolerance, torch_angles)
 
 gpu = pytest.mark.gpu
 
@@ -127,3 +128,52 @@ def test_keys_that_are_no_numbers_reach_the_rows_that_see_them(dtype, M, g, gain
     c.ks[1, int(oracle.blocks.rows_of(table[1], 64, [32])[0]) // 32] = float("nan")
     got = attend(c, table, ctx, q)
     assert torch.isnan(got[1, :, g:].float()).all() and same(got[0], want[0]) and same(got[1, :, :g], want[1, :, :g])
+
+
+@gpu
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("rot", [None, 64])
+def test_rows_that_are_not_finite_do_not_spoil_their_block(code, dtype, rot):
+    import torch
+    import int8_kv_decode_gb300 as K
+    c = Cache(2, 6, 64, 32, code, seed=2)
+    start, lens = [20, 0], [50, 33]                          # the first goes on inside a block
+    table = tables([70, 33], 64, 6)
+    r = np.random.default_rng(1)
+    kn, vn = (torch.from_numpy(r.standard_normal((83, 2, D)).astype(np.float32)).cuda().to(dtype_of(dtype))
+              for _ in "kv")
+    for x in (kn, vn):
+        x[2, 0, 3], x[3, 0, 5], x[4, 0, 100] = float("inf"), float("nan"), -float("inf")
+        x[13, 1, 6] = float("nan")                           # beside a finite neighbour near a border
+        x[50:82, 1, 9] = float("inf")                        # in every row of a block
+        x[82, 0] = float("nan")                              # a block of nothing else
+    ang = torch_angles(80, rot) if rot else None
+    cu = np.array([0, 50, 83])
+    K.append_blocks(kn, vn, i32(cu), i32(start), *c.args, i32(table), 64, table=ang, workspace=c.ws)
+    assert K.get_device_status(c.ws) == K.DEVERR_NOT_FINITE
+    pos = np.concatenate([np.arange(s, s + n) for s, n in zip(start, lens)])
+    with np.errstate(invalid="ignore"):
+        kh = kn.float().cpu().numpy()
+        kh = oracle.blocks.rotate(kh, ang.cpu().numpy()[pos], False) if rot else kh
+        for b in range(2):
+            for name, x in (("k", kh), ("v", vn.float().cpu().numpy())):
+                oracle.blocks.append(c.host, name, x[cu[b]:cu[b + 1]], start[b], table[b], 64)
+    for name in ("k", "v"):
+        got = getattr(c, name).float().cpu().numpy()
+        assert np.array_equal(got, c.host[name].astype(np.float32), equal_nan=True), name
+        assert same(getattr(c, name + "s"), torch.from_numpy(c.host[name + "s"])), name
+        assert np.isfinite(c.host[name + "s"]).all()
+    # finite rows flag nothing
+    K.append_blocks(kn[5:12], vn[5:12], i32([0, 7, 7]), i32([0, 0]), *c.args, i32(table), 64, workspace=c.ws)
+    assert K.get_device_status(c.ws) == 0
+
+
+def test_the_error_bit_is_the_headers():
+    import os
+    import re
+    import int8_kv_decode_gb300 as K
+    with open(os.path.join(os.path.dirname(__file__), "..", "include", "kattn.h"), encoding="utf-8") as f:
+        bit = int(re.search(r"#define KATTN_DEVERR_NOT_FINITE (0x[0-9a-f]+)u", f.read()).group(1), 16)
+    assert bit == K.DEVERR_NOT_FINITE
+    assert bit & (K.DEVERR_BAD_SEQUENCE | K.DEVERR_TIMEOUT | K.DEVERR_BAD_PAGE | K.DEVERR_NO_PAGES) == 0
