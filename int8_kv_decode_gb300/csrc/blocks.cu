@@ -26,12 +26,12 @@ __device__ __forceinline__ int64_t table_keys(const BlockCache& c) {
 // The rows of a sequence and its first key; whether the rows lie in the call's and the
 // keys in the table's row.
 struct RowSpan {
-  int b, c0, n, start;
+  int b, c0, c1, n, start;                        // n: its rows, none where they leave the call's
   bool valid;
 };
 __device__ __forceinline__ RowSpan make_span(const SpanParams& s, int b, int c0, int c1, int start, int64_t most) {
   const bool rises = c0 >= 0 && c0 <= c1 && c1 <= s.rows;
-  return {b, c0, rises ? c1 - c0 : 0, start, rises && start >= 0 && (int64_t)start + (c1 - c0) <= most};
+  return {b, c0, c1, rises ? c1 - c0 : 0, start, rises && start >= 0 && (int64_t)start + (c1 - c0) <= most};
 }
 __device__ __forceinline__ RowSpan span_of(const SpanParams& s, int b, int64_t most) {
   return make_span(s, b, ld_fresh(s.cu + b), ld_fresh(s.cu + b + 1), ld_fresh(s.start + b), most);
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kBlock * 4) append_kernel(const AppendParams p
                              min(kTurnHeads, p.Hq - h0), p.table, p.half, lane, [&](bool& know) {
       const RowSpan s = find_span(p.s, row, most, lane, [](int, int cu) { return (int64_t)cu; });
       know = s.valid;
-      return row < s.c0 || row >= s.c0 + s.n ? -1 : know ? s.start + row - s.c0 : 0;   // (-1: no sequence's row)
+      return row < s.c0 || row >= s.c1 ? -1 : know ? s.start + row - s.c0 : 0;   // (-1: no sequence's row)
     });
     return;
   }

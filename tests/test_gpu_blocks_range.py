@@ -177,3 +177,33 @@ def test_the_error_bit_is_the_headers():
         bit = int(re.search(r"#define KATTN_DEVERR_NOT_FINITE (0x[0-9a-f]+)u", f.read()).group(1), 16)
     assert bit == K.DEVERR_NOT_FINITE
     assert bit & (K.DEVERR_BAD_SEQUENCE | K.DEVERR_TIMEOUT | K.DEVERR_BAD_PAGE | K.DEVERR_NO_PAGES) == 0
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_queries_of_sequences_that_leave_the_call_are_nan(dtype):
+    import torch
+    import int8_kv_decode_gb300 as K
+    c = Cache(2, 8, 32, 32, "int8")
+    table = tables([64, 64, 64], 32, 8, spare=0)
+    x = torch.randn((30, 2, D), device="cuda").to(dtype_of(dtype))
+    q = torch.randn((30, 9, D), device="cuda").to(dtype_of(dtype))
+    ang = torch_angles(64, 128)
+
+    def run(cu):
+        out = torch.full_like(q, 7.0)
+        K.append_blocks(x, x, i32(cu), i32([0, 0, 0]), *c.args, i32(table), 32, table=ang, q=q, q_out=out,
+                        workspace=c.ws)
+        return out, K.get_device_status(c.ws)
+
+    good, st = run([0, 10, 20, 30])
+    assert st == 0
+    got, st = run([0, 10, 20, 31])                           # one row behind the arrays
+    assert st == K.DEVERR_BAD_SEQUENCE
+    assert same(got[:20], good[:20]) and torch.isnan(got[20:].float()).all()
+    got, st = run([-5, 10, 20, 30])                          # rows before them
+    assert st == K.DEVERR_BAD_SEQUENCE
+    assert same(got[10:], good[10:]) and torch.isnan(got[:10].float()).all()
+    got, st = run([2, 10, 20, 28])                           # rows of no sequence stay
+    assert st == 0 and (got[:2] == 7.0).all() and (got[28:] == 7.0).all()
+    assert same(got[10:20], good[10:20])
