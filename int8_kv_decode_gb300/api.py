@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import warnings
 
 import torch
 
@@ -472,16 +473,32 @@ def _launch(name, index, *args):
 _plain = None        # the compiled calls (bind.cpp), once loaded
 
 
+class _NoBinding:
+    """In the place of the compiled calls: every call goes by the checks here."""
+
+    @staticmethod
+    def rope(*args):
+        return None
+
+    append_blocks = read_blocks = decode_blocks = rope
+
+
 def _load_plain():
     """The module of the calls whose every argument is plainly right; each returns the
     library's status, or None for a call that the checks here have to look at."""
     global _plain
+    lib = _lib.load()
     try:
         from . import _bind
+        built_for = getattr(_bind, "torch_version", None)
+        if built_for != torch.__version__:
+            raise ImportError(f"built for torch {built_for}, this is {torch.__version__}")
     except ImportError as e:
-        raise RuntimeError("the binding module is missing or of another build: build it first "
-                           "(python -c 'import __graft_entry__ as g; g.build()')") from e
-    lib = _lib.load()
+        warnings.warn(f"the compiled binding (_bind) is not used: {e}.  Calls go to the library "
+                      "all the same, each about 10 us later; build() makes the binding.",
+                      RuntimeWarning, stacklevel=3)
+        _plain = _NoBinding
+        return _plain
     _bind.setup(*(ctypes.cast(getattr(lib, "kattn_" + n), ctypes.c_void_p).value
                   for n in ("rope", "append_blocks", "read_blocks", "decode_blocks")))
     _plain = _bind

@@ -84,9 +84,18 @@ def _run(cmd, verbose):
 
 
 # The checks and calls of the block-scaled operators in one step from Python (bind.cpp), a
-# module against the torch and Python that run this; the stamp names them.
+# module against the torch and Python that run this; the stamp names them.  The library needs
+# neither: it is built and linked without torch, and api.py calls it without this module.
 BIND = os.path.join(PKG, "_bind.so")
 _STAMP = os.path.join(BUILD, "bind.stamp")
+
+
+def _has_torch() -> bool:
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return False
+    return True
 
 
 def _bind_stamp() -> str:
@@ -94,8 +103,12 @@ def _bind_stamp() -> str:
     return f"{sys.version} {torch.__version__} {torch.__file__}"
 
 
+def _bind_outdated() -> bool:
+    return _stale(BIND, [os.path.join(CSRC, "bind.cpp"), os.path.join(INCLUDE, "kattn.h"), __file__])
+
+
 def _bind_stale() -> bool:
-    if _stale(BIND, [os.path.join(CSRC, "bind.cpp"), os.path.join(INCLUDE, "kattn.h"), __file__]):
+    if _bind_outdated():
         return True
     try:
         with open(_STAMP, encoding="utf-8") as f:
@@ -114,7 +127,8 @@ def _build_bind(verbose: bool) -> None:
     cmd = ["g++", "-shared", "-O2", "-std=c++17", "-fPIC", os.path.join(CSRC, "bind.cpp"), "-o", tmp,
            "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", os.path.join(base, "include"),
            "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
-           "-I", os.path.join(cuda, "include"), "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
+           "-I", os.path.join(cuda, "include"), f"-DKATTN_TORCH_VERSION=\"{torch.__version__}\"",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
            "-lc10"]
     _run(cmd, verbose)
     os.replace(tmp, BIND)
@@ -123,8 +137,8 @@ def _build_bind(verbose: bool) -> None:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Compile and link libkattn.so and the binding module; returns the library's path.
-    Rebuilds what is stale."""
+    """Compile and link libkattn.so and, where there is torch, the binding module; returns
+    the library's path.  Rebuilds what is stale."""
     nvcc = nvcc_path()
     os.makedirs(BUILD, exist_ok=True)
     headers = _headers()
@@ -140,17 +154,20 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
                 cmd += ["-Xptxas", "-v"]
             jobs.append(cmd)
     outputs = []
-    bind = force or _bind_stale()
+    binding = None
+    bind = _has_torch() and (force or _bind_stale())
+    if not bind and os.path.exists(BIND) and _bind_outdated():
+        os.remove(BIND)                           # (its calls may not be the library's any more)
     if jobs or bind:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
             binding = ex.submit(_build_bind, verbose) if bind else None
             outputs = list(ex.map(lambda c: _run(c, verbose), jobs))
-            if binding:
-                binding.result()
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + ".tmp"
         _run([nvcc, "-shared", "-o", tmp] + ARCH + objs + ["-cudart", "static"], verbose)
         os.replace(tmp, LIB)
+    if binding:
+        binding.result()                          # (a failure of its own, once the library is there)
     if ptxas_verbose:
         for out in outputs:
             print(out)

@@ -1,5 +1,5 @@
 """Values at the ends of float32's range, and values that are no numbers, through the
-operators on block-scaled caches.
+operators on block-scaled caches; the Python calls without the compiled binding.
 
 Tolerances are those of test_gpu_blocks.py; what is left beside them is a share of the
 row's own largest value (the tail) and float32's least steps, never a fixed number.
@@ -207,3 +207,36 @@ def test_queries_of_sequences_that_leave_the_call_are_nan(dtype):
     got, st = run([2, 10, 20, 28])                           # rows of no sequence stay
     assert st == 0 and (got[:2] == 7.0).all() and (got[28:] == 7.0).all()
     assert same(got[10:20], good[10:20])
+
+
+# ----------------------------------------------- without the compiled binding
+
+@gpu
+def test_calls_without_the_compiled_binding(monkeypatch):
+    import sys
+    import torch
+    import int8_kv_decode_gb300 as K
+    from int8_kv_decode_gb300 import api
+
+    def run():
+        c, table, ctx, q = attend_inputs(2, 2, 8, 2, [100, 300], dtype="bfloat16", seed=1)
+        ang = torch_angles(400, 128)
+        x = torch.randn((9, 12, D), device="cuda", generator=torch.Generator("cuda").manual_seed(3)).bfloat16()
+        got = [K.rope(x, i32(np.arange(9)), ang, out=torch.empty_like(x))]
+        q_out = torch.empty_like(x[:, :8])
+        K.append_blocks(x[:, 8:10], x[:, 10:], i32([0, 5, 9]), i32([96, 1]), *c.args, i32(table), c.page, table=ang,
+                        q=x[:, :8], q_out=q_out, workspace=c.ws)
+        back = [torch.empty((9, 2, D), device="cuda") for _ in "kv"]
+        K.read_blocks(*c.args, i32(table), c.page, i32([0, 5, 9]), i32([96, 1]), 9, out_k=back[0], out_v=back[1],
+                      workspace=c.ws)
+        out = attend(c, table, ctx, q, out=torch.empty_like(q), workspace=K.alloc_blocks_workspace(2, 2, 8, 300))
+        assert K.get_device_status(c.ws) == 0
+        return got + [q_out] + back + [out]
+
+    want = run()
+    monkeypatch.setattr(api, "_plain", None)
+    monkeypatch.setitem(sys.modules, "int8_kv_decode_gb300._bind", None)       # its import fails
+    monkeypatch.delattr(K, "_bind", raising=False)
+    with pytest.warns(RuntimeWarning, match="binding"):
+        got = run()
+    assert all(same(a, b) for a, b in zip(want, got))
