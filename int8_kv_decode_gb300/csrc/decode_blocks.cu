@@ -880,52 +880,51 @@ block_split_kernel(const BlockDecodeParams p, const __grid_constant__ TmaMaps ma
       }
 #pragma unroll
       for (int t = 0; t < S::kJoin; ++t) {
-      const int n = n0 + t;
-      // weights 2^(m_w - m) of the warps, for rows 2c and 2c + 1
-      float4 st[kWarpsB];                         // m, l of both rows
+        const int n = n0 + t;
+        // weights 2^(m_w - m) of the warps, for rows 2c and 2c + 1
+        float4 st[kWarpsB];                       // m, l of both rows
 #pragma unroll
-      for (int w = 0; w < kWarpsB; ++w) st[w] = *reinterpret_cast<const float4*>(&sm.ml[w][n][2 * c]);
-      float mr[2], lr[2], wt[2][kWarpsB];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        auto ref = [&](int w) { return e ? st[w].z : st[w].x; };
-        auto sum = [&](int w) { return e ? st[w].w : st[w].y; };
-        mr[e] = fmaxf(fmaxf(ref(0), ref(1)), fmaxf(ref(2), ref(3)));
-#pragma unroll
-        for (int w = 0; w < kWarpsB; ++w)
-          wt[e][w] = mr[e] == -INFINITY ? 0.0f : fast_exp2(__fsub_rn(ref(w), mr[e]));
-        lr[e] = __fadd_rn(__fmaf_rn(wt[e][1], sum(1), __fmul_rn(wt[e][0], sum(0))),
-                          __fmaf_rn(wt[e][3], sum(3), __fmul_rn(wt[e][2], sum(2))));
-      }
-#pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        const int md = 2 * warp + d;
-        float4 x[kWarpsB];
-#pragma unroll
-        for (int w = 0; w < kWarpsB; ++w) x[w] = sm.o[w][t][md][lane];
-        auto join = [&](const float (&wt)[kWarpsB], float a0, float a1, float a2, float a3) {
-          return __fadd_rn(__fmaf_rn(wt[1], a1, __fmul_rn(wt[0], a0)), __fmaf_rn(wt[3], a3, __fmul_rn(wt[2], a2)));
-        };
+        for (int w = 0; w < kWarpsB; ++w) st[w] = *reinterpret_cast<const float4*>(&sm.ml[w][n][2 * c]);
+        float mr[2], lr[2], wt[2][kWarpsB];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int rr = it.rg * kUnitRows + 8 * n + 2 * c + e;
-          if (rr >= R) continue;
-          const float y0 = e ? join(wt[1], x[0].y, x[1].y, x[2].y, x[3].y) : join(wt[0], x[0].x, x[1].x, x[2].x, x[3].x);
-          const float y1 = e ? join(wt[1], x[0].w, x[1].w, x[2].w, x[3].w) : join(wt[0], x[0].z, x[1].z, x[2].z, x[3].z);
-          if (whole) {
-            const int j = column(rr);
-            const int64_t at = (((int64_t)it.b * M + j) * p.Hq + it.kh * p.g + rr - j * p.g) * kD + 16 * md + 2 * g;
-            const float by = is_down(lr[e]) ? __fmul_rn(lr[e], -kDown) : lr[e];
-            store_out2(p.out, p.q_type, at, __fdiv_rn(y0, by), __fdiv_rn(y1, by));
-          } else {
-            *reinterpret_cast<float2*>(part + (size_t)rr * kD + 16 * md + 2 * g) = make_float2(y0, y1);
-            if (warp == 0 && d == 0 && g == 0)
-              *reinterpret_cast<float2*>(part + (size_t)R * kD + 2 * rr) = make_float2(mr[e], lr[e]);
+          auto ref = [&](int w) { return e ? st[w].z : st[w].x; };
+          auto sum = [&](int w) { return e ? st[w].w : st[w].y; };
+          mr[e] = fmaxf(fmaxf(ref(0), ref(1)), fmaxf(ref(2), ref(3)));
+#pragma unroll
+          for (int w = 0; w < kWarpsB; ++w)
+            wt[e][w] = mr[e] == -INFINITY ? 0.0f : fast_exp2(__fsub_rn(ref(w), mr[e]));
+          lr[e] = __fadd_rn(__fmaf_rn(wt[e][1], sum(1), __fmul_rn(wt[e][0], sum(0))),
+                            __fmaf_rn(wt[e][3], sum(3), __fmul_rn(wt[e][2], sum(2))));
+        }
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          const int md = 2 * warp + d;
+          float4 x[kWarpsB];
+#pragma unroll
+          for (int w = 0; w < kWarpsB; ++w) x[w] = sm.o[w][t][md][lane];
+          auto join = [&](const float (&wt)[kWarpsB], float a0, float a1, float a2, float a3) {
+            return __fadd_rn(__fmaf_rn(wt[1], a1, __fmul_rn(wt[0], a0)), __fmaf_rn(wt[3], a3, __fmul_rn(wt[2], a2)));
+          };
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int rr = it.rg * kUnitRows + 8 * n + 2 * c + e;
+            if (rr >= R) continue;
+            const float y0 = e ? join(wt[1], x[0].y, x[1].y, x[2].y, x[3].y) : join(wt[0], x[0].x, x[1].x, x[2].x, x[3].x);
+            const float y1 = e ? join(wt[1], x[0].w, x[1].w, x[2].w, x[3].w) : join(wt[0], x[0].z, x[1].z, x[2].z, x[3].z);
+            if (whole) {
+              const int j = column(rr);
+              const int64_t at = (((int64_t)it.b * M + j) * p.Hq + it.kh * p.g + rr - j * p.g) * kD + 16 * md + 2 * g;
+              const float by = is_down(lr[e]) ? __fmul_rn(lr[e], -kDown) : lr[e];
+              store_out2(p.out, p.q_type, at, __fdiv_rn(y0, by), __fdiv_rn(y1, by));
+            } else {
+              *reinterpret_cast<float2*>(part + (size_t)rr * kD + 16 * md + 2 * g) = make_float2(y0, y1);
+              if (warp == 0 && d == 0 && g == 0)
+                *reinterpret_cast<float2*>(part + (size_t)R * kD + 2 * rr) = make_float2(mr[e], lr[e]);
+            }
           }
         }
       }
-    }
-
     }
 
     // ---- next item
