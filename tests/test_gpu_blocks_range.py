@@ -94,6 +94,28 @@ def test_large_values_that_a_column_does_not_see(dtype, M, g):
     check_row_by_row(c, table, ctx, q, got)
 
 
+@gpu
+@pytest.mark.parametrize("at", [100, 35000, 69900])
+def test_a_large_block_in_a_long_context(at):
+    # more windows than the join of a row weighs at a time, by every number of warps
+    c, table, ctx, q = attend_inputs(2, 2, 4, 1, [70000, 20000], 32, 64, "int8", "float32", seed=6)
+    scales = c.host["vs"].copy()
+    scales[:, int(oracle.blocks.rows_of(table[0], 64, [at])[0]) // 32] = 1e35
+    want = attend(c, table, ctx, q)
+    set_scales(c, "vs", scales)
+    got = attend(c, table, ctx, q)
+    check_row_by_row(c, table, ctx, q, got)
+    assert same(want[1], got[1])
+    assert same(got, attend(c, table, ctx, q, max_ctx=200000))
+    # a window with the block alone, and a row that begins and ends with it
+    c, table, ctx, q = attend_inputs(1, 1, 4, 1, [600], 32, 64, "int8", "float32", seed=7)
+    set_scales(c, "vs", np.full(c.host["vs"].shape, 1e-30 if at == 100 else 1.0))
+    scales = c.host["vs"].copy()
+    scales[:, int(oracle.blocks.rows_of(table[0], 64, [at % 600])[0]) // 32] = 1e35
+    set_scales(c, "vs", scales)
+    check_row_by_row(c, table, ctx, q, attend(c, table, ctx, q))
+
+
 # ------------------------------------------------------------- no numbers
 
 @gpu
