@@ -959,7 +959,7 @@ def decode_blocks(q, k, k_scale, v, v_scale, block_table, page_rows: int, ctx_le
 
     q [B][M][Hq][128] float32, bfloat16 or float16 (not quantized); column j of sequence
     b sees the keys t < ctx_len[b] + j (int32 [B]; 0: an empty slot, whose rows are 0).
-    Cache and table as append_blocks().  workspace: a uint8 tensor of
+    max_ctx: a limit on ctx_len; one near the batch's longest is fastest.  Cache and table as append_blocks().  workspace: a uint8 tensor of
     blocks_workspace_size(...) bytes, its first 256 zeroed before its first use,
     allocated here with torch if None.  (kattn_decode_blocks)
     """

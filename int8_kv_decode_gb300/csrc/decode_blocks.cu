@@ -9,7 +9,7 @@
 // of the rows (query heads x draft columns) that read the head; T = 1 to 5 (unit_tiles).
 // Warp w takes the steps of 32 keys w, w + 4, ..., so a short window is shared by all four as
 // well, and the warps' sums come together in shared memory: one partial a window.  (A warp
-// per window of 256 keys took 122 us where this takes 96, 64 sequences of 512 to 32768 keys:
+// per window of 256 keys took 122 us where this takes 97, 64 sequences of 512 to 32768 keys:
 // more partials, larger shares of work per warp.)  A warp's K and V rows come by TMA into a
 // buffer each, refilled for the step that follows as soon as its products are issued.  Per step
 //   * S^T = K Q^T on f16 MMAs: the codes are exact in f16, and so are bf16 and f16
@@ -20,7 +20,10 @@
 //   * weights 2^x; the reference m of a row moves only where a weight would pass 2^15;
 //   * the weights go to f16 (float32 queries: hi + lo) and, through a transposition of
 //     8 x 8 blocks in registers, to the second product, whose row sums take the weights
-//     as rounded: a weight's rounding then cancels where it dominates;
+//     as rounded: a weight's rounding then cancels where it dominates.  11 bits, as hi + lo
+//     doubles that product's MMAs: beside the output's own rounding they add nothing to see in
+//     bf16 (1.68e-3 relative on 64 long contexts, where float32 weights give 1.67e-3), and a
+//     third in f16 (2.7e-4, 2.1e-4); a call that wants more takes float32 queries;
 //   * O = O + v_scale (V^T P^T): the product of a step starts at zero and enters the
 //     float32 sum with the block's scale (a row that sees a huge one: kHuge).  From three
 //     tiles on O lies in tensor memory, each lane's columns its own store, read and written
@@ -28,13 +31,13 @@
 //     row's operations stays that of one tile, and three blocks still fit a multiprocessor.
 //
 // What bounds it.  Up to 8 rows a head, HBM: 64 sequences of 512 to 32768 keys over 64-row
-// pages, 32 query and 4 kv heads (544 MB, 80 us at the measured copy rate): 96 us a call, the
-// split alone 92 (5.9 TB/s), issue 42%.  2 sequences of 128k keys with float32 queries (267
-// MB, 39 us): 55 us, split 52, of which the second MMAs for hi + lo take tensor pipe to 34%.
+// pages, 32 query and 4 kv heads (544 MB, 80 us at the measured copy rate): 97 us a call, the
+// split alone 90 (6.0 TB/s), issue 42%.  2 sequences of 128k keys with float32 queries (267
+// MB, 39 us): 56 us, split 49, of which the second MMAs for hi + lo take tensor pipe to 34%.
 // With more rows, issue and the latency of a step's chain at 12 warps a multiprocessor (920
 // instructions a step at T = 2, 330 of them to make f16 of the codes; 1620 at T = 5): 16
-// sequences of 1k to 4k keys, 40 rows a head, 34 us; 64 of them 77 us.  One sequence of 257
-// keys: 6.1 us, latency alone.
+// sequences of 1k to 4k keys, 40 rows a head, 34 us; 64 of them 78 us.  One sequence of 257
+// keys: 6.2 us, latency alone.
 #include <cmath>
 
 #include "blocks_internal.cuh"
@@ -57,6 +60,8 @@ constexpr float kLarge = 1048576.0f;
 // power of two: what it costs lies 2^126 below such values.  The sign of the row sum says so
 // where sums are joined, which bring all of them to the same side.  A row goes by the steps
 // that it sees itself, so its bytes stay its own, and those of a row with none are as they are.
+// (Looking for such scales: 0.4% of 64 sequences of 512 to 32768 keys, 1.6% of 64 of 1k to 4k
+// with 5 columns; a scale for each row in the loop took 3%.)
 constexpr float kHuge = 0x1p64f, kDown = 0x1p-64f, kUp = 0x1p64f;
 __device__ __forceinline__ bool is_down(float l) { return (int)__float_as_uint(l) < 0; }
 __device__ __forceinline__ float mark_down(float l, bool down) {
@@ -1119,7 +1124,13 @@ int64_t units_of(const BlockDecodeParams& p, int T) {
 //   90 x 100..500, 8               47        41      46     [40]
 // (All 64 rows as one unit of 8 tiles, two blocks a multiprocessor: 143 us for 64 x 1k..4k, 8,
 // when 4 tiles took 130.)
-// Units are counted from max_ctx, as the host does not know the lengths.
+// The costs are those of bf16 queries and int8 codes.  e4m3 takes as long (16 x 1k..4k, 5:
+// 34.3 us); with float32 queries, whose MMAs are twice as many, they were not taken one by one
+// (16 x 1k..4k, 5: 47.5; 64 of them 125).  The scales that kHuge looks for came later: up to
+// 2% more than here.
+// Units are counted from max_ctx, as the host does not know the lengths.  With a limit of
+// 131072, in brackets with the batch's own: 1 x 4096 keys, 5 columns 26.6 us [11.1]; 16 x
+// 1k..4k, 5 61 [34]; 64 x 1k..4k, 1, 2 and 5 columns 55 [33], 85 [41] and 190 [78].
 int unit_tiles(const BlockDecodeParams& p) {
   const int tiles = (p.R + 7) / 8, most = std::min(tiles, p.q_type == KATTN_F32 ? 4 : 5);
   static const int cost[5] = {7, 11, 15, 20, 24};
