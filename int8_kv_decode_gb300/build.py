@@ -130,7 +130,12 @@ def _build_bind(verbose: bool) -> None:
            "-I", os.path.join(cuda, "include"), f"-DKATTN_TORCH_VERSION=\"{torch.__version__}\"",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
            "-lc10"]
-    _run(cmd, verbose)
+    try:
+        _run(cmd, verbose)
+    except RuntimeError:
+        if os.path.exists(BIND):
+            os.remove(BIND)                       # (of an earlier source)
+        raise
     os.replace(tmp, BIND)
     with open(_STAMP, "w", encoding="utf-8") as f:
         f.write(_bind_stamp())

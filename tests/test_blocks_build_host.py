@@ -28,6 +28,24 @@ def test_the_library_builds_without_torch():
     assert r.stdout.strip().endswith("libkattn.so")
 
 
+def test_a_binding_that_does_not_compile_leaves_the_library(tmp_path):
+    # the library is linked all the same, the error is raised, and no older binding is left
+    r = run(f"import os, shutil, runpy; p = {str(tmp_path)!r}\n"
+            "for d in ('include', 'int8_kv_decode_gb300'):\n"
+            "    shutil.copytree(d, os.path.join(p, d), copy_function=shutil.copy2)\n"
+            "q = os.path.join(p, 'int8_kv_decode_gb300')\n"
+            "os.remove(os.path.join(q, 'libkattn.so'))\n"
+            "open(os.path.join(q, 'csrc', 'bind.cpp'), 'a').write('#error no')\n"
+            "m = runpy.run_path(os.path.join(q, 'build.py'))\n"
+            "try:\n"
+            "    m['build']()\n"
+            "except RuntimeError as e:\n"
+            "    print('raised' if 'bind.cpp' in str(e) else e)\n"
+            "print(os.path.exists(os.path.join(q, 'libkattn.so')), os.path.exists(os.path.join(q, '_bind.so')))\n")
+    assert r.returncode == 0, r.stdout
+    assert r.stdout.split() == ["raised", "True", "False"], r.stdout
+
+
 HIDDEN = ("import sys; sys.modules['int8_kv_decode_gb300._bind'] = None\n"
           "import warnings, torch, int8_kv_decode_gb300 as K\n")
 
